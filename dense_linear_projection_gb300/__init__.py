@@ -20,7 +20,7 @@ from ._build import build, library_path
 __all__ = [
     "PROJ_OK", "PROJ_ERR_INVALID_ARG", "PROJ_ERR_UNSUPPORTED", "PROJ_ERR_MISALIGNED",
     "PROJ_ERR_OUT_OF_MEMORY", "PROJ_ERR_CUDA", "PROJ_ERR_DEVICE_TIMEOUT",
-    "PROJ_BF16", "PROJ_F32", "PROJ_W_NK", "PROJ_W_KN",
+    "PROJ_BF16", "PROJ_F32", "PROJ_E4M3", "PROJ_W_NK", "PROJ_W_KN",
     "PROJ_KERNEL_NONE", "PROJ_KERNEL_FILL", "PROJ_KERNEL_TC",
     "ProjError", "lib", "build", "library_path", "EXPORTED_SYMBOLS",
     "proj_plan_compute", "proj_plan_segments", "proj_plan_reduction_order", "proj_create",
@@ -32,11 +32,14 @@ __all__ = [
     "proj_packed_weight_bytes", "proj_pack_weights", "proj_run_packed", "proj_run_host_packed",
     "proj_set_activation", "proj_run_fused", "PROJ_ACT_NONE", "PROJ_ACT_GELU", "PROJ_ACT_SWIGLU",
     "Projection",
+    "proj_q4_packed_bytes", "proj_q4_create", "proj_q4_pack", "proj_q4_run", "proj_q4_destroy",
+    "proj_kv_create", "proj_kv_append", "proj_kv_attend", "proj_kv_device_status", "proj_kv_destroy",
+    "Q4Projection", "PagedKV", "rope_table",
 ]
 
 PROJ_OK, PROJ_ERR_INVALID_ARG, PROJ_ERR_UNSUPPORTED, PROJ_ERR_MISALIGNED = 0, 1, 2, 3
 PROJ_ERR_OUT_OF_MEMORY, PROJ_ERR_CUDA, PROJ_ERR_DEVICE_TIMEOUT = 4, 5, 6
-PROJ_BF16, PROJ_F32 = 0, 1
+PROJ_BF16, PROJ_F32, PROJ_E4M3 = 0, 1, 2
 PROJ_W_NK, PROJ_W_KN = 0, 1
 PROJ_KERNEL_NONE, PROJ_KERNEL_FILL, PROJ_KERNEL_TC = 0, 1, 2
 PROJ_OVERLAP_NONE, PROJ_OVERLAP_PROLOGUE, PROJ_OVERLAP_WEIGHTS = 0, 1, 2
@@ -49,6 +52,8 @@ EXPORTED_SYMBOLS = (
     "proj_packed_weight_bytes", "proj_pack_weights", "proj_run_packed", "proj_run_host_packed",
     "proj_set_activation", "proj_run_fused", "proj_noalloc_device_status",
     "proj_noalloc_selftest_wait_timeout",
+    "proj_q4_packed_bytes", "proj_q4_create", "proj_q4_pack", "proj_q4_run", "proj_q4_destroy",
+    "proj_kv_create", "proj_kv_append", "proj_kv_attend", "proj_kv_device_status", "proj_kv_destroy",
 )
 
 
@@ -80,6 +85,12 @@ class Segment(ctypes.Structure):
     def as_tuple(self):
         return (self.tile, self.tile_m, self.tile_n, self.k_block_begin, self.k_block_end,
                 self.slot, self.split)
+
+
+class KvDesc(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int64) for name in (
+        "num_pages", "page_stride", "token_stride", "head_stride", "max_sequences")] + [
+        (name, ctypes.c_int32) for name in ("page_size", "q_heads", "kv_heads", "head_dim", "kv_dtype")]
 
 
 def _plan_struct(plan: dict) -> PlanDesc:
@@ -130,6 +141,17 @@ def lib() -> ctypes.CDLL:
     L.proj_run_host_packed.argtypes = [vp, vp, vp, vp, vp, vp]
     L.proj_set_activation.argtypes = [vp, i32]
     L.proj_run_fused.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp]
+    L.proj_q4_packed_bytes.argtypes = [i64, i64, i64, i32, ctypes.POINTER(ctypes.c_size_t)]
+    L.proj_q4_create.argtypes = [ctypes.POINTER(vp), i64, i64, i64, i64, i32, i32, i32, vp]
+    L.proj_q4_pack.argtypes = [vp, vp, vp, vp, vp, vp]
+    L.proj_q4_run.argtypes = [vp, i64, vp, vp, vp, vp, vp]
+    L.proj_q4_destroy.argtypes = [vp]
+    L.proj_kv_create.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(KvDesc), vp]
+    L.proj_kv_append.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, vp, vp, i64, i64, vp, i64, ctypes.c_int32, i32,
+                                 vp, vp, vp, vp, vp, i64, vp]
+    L.proj_kv_attend.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, ctypes.c_float, vp, i64, vp, vp]
+    L.proj_kv_device_status.argtypes = [vp, vp]
+    L.proj_kv_destroy.argtypes = [vp]
     for name in EXPORTED_SYMBOLS:
         if name != "proj_status_string":
             getattr(L, name).restype = st
@@ -314,6 +336,64 @@ def proj_set_trace(h: int, buf=None, nbytes: int = 0) -> None:
     _check(lib().proj_set_trace(h, _ptr(buf), int(nbytes)), "proj_set_trace")
 
 
+def proj_q4_packed_bytes(N: int, K: int, group: int, has_zeros: bool = False) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().proj_q4_packed_bytes(N, K, group, int(bool(has_zeros)), ctypes.byref(out)), "proj_q4_packed_bytes")
+    return int(out.value)
+
+
+def proj_q4_create(max_tokens: int, N: int, K: int, group: int, has_zeros: bool = False, y_dtype: int = PROJ_BF16,
+                   has_bias: bool = False, stream=None) -> int:
+    h = ctypes.c_void_p()
+    _check(lib().proj_q4_create(ctypes.byref(h), max_tokens, N, K, group, int(bool(has_zeros)), y_dtype,
+                                int(bool(has_bias)), _stream(stream)), "proj_q4_create")
+    return h.value
+
+
+def proj_q4_pack(h: int, codes, scales, zeros, packed, stream=None) -> None:
+    _check(lib().proj_q4_pack(h, _ptr(codes), _ptr(scales), _ptr(zeros), _ptr(packed), _stream(stream)), "proj_q4_pack")
+
+
+def proj_q4_run(h: int, M: int, X, packed, bias, Y, stream=None) -> None:
+    _check(lib().proj_q4_run(h, M, _ptr(X), _ptr(packed), _ptr(bias), _ptr(Y), _stream(stream)), "proj_q4_run")
+
+
+def proj_q4_destroy(h: Optional[int]) -> None:
+    _check(lib().proj_q4_destroy(h), "proj_q4_destroy")
+
+
+def proj_kv_create(desc: KvDesc, stream=None) -> int:
+    h = ctypes.c_void_p()
+    _check(lib().proj_kv_create(ctypes.byref(h), ctypes.byref(desc), _stream(stream)), "proj_kv_create")
+    return h.value
+
+
+def proj_kv_append(h: int, tokens: int, q, q_stride: int, k, v, kv_stride: int, positions, seq_ids, page_table,
+                   sequences: int, table_width: int, rope, rope_positions: int, rot_dim: int, interleaved: bool,
+                   k_scale, v_scale, k_cache, v_cache, q_out, q_out_stride: int, stream=None) -> None:
+    _check(lib().proj_kv_append(h, tokens, _ptr(q), q_stride, _ptr(k), _ptr(v), kv_stride, _ptr(positions),
+                                _ptr(seq_ids), _ptr(page_table), sequences, table_width, _ptr(rope), rope_positions,
+                                rot_dim, int(bool(interleaved)), _ptr(k_scale), _ptr(v_scale), _ptr(k_cache),
+                                _ptr(v_cache), _ptr(q_out), q_out_stride, _stream(stream)), "proj_kv_append")
+
+
+def proj_kv_attend(h: int, sequences: int, q, q_stride: int, k_cache, v_cache, k_scale, v_scale, page_table,
+                   table_width: int, seq_lens, window: int, scale: float, out, out_stride: int, lse,
+                   stream=None) -> None:
+    _check(lib().proj_kv_attend(h, sequences, _ptr(q), q_stride, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                                _ptr(v_scale), _ptr(page_table), table_width, _ptr(seq_lens), window, scale,
+                                _ptr(out), out_stride, _ptr(lse), _stream(stream)), "proj_kv_attend")
+
+
+def proj_kv_device_status(h: int, stream=None) -> int:
+    """Raw status (PROJ_ERR_INVALID_ARG once after a kernel met an index out of range); does not raise."""
+    return int(lib().proj_kv_device_status(h, _stream(stream)))
+
+
+def proj_kv_destroy(h: Optional[int]) -> None:
+    _check(lib().proj_kv_destroy(h), "proj_kv_destroy")
+
+
 # ---------------------------------------------------------------- convenience
 class Projection:
     """A planned projection for one shape; call it with PyTorch tensors.
@@ -381,6 +461,218 @@ class Projection:
     def close(self) -> None:
         if self.handle:
             proj_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _require(ok: bool, what: str) -> None:
+    if not ok:
+        raise ProjError(PROJ_ERR_INVALID_ARG, what)
+
+
+class Q4Projection:
+    """A planned projection with 4-bit weights; call it with PyTorch tensors.
+
+    ``max_tokens`` bounds the rows of ``X`` ([M, K] bf16).  :meth:`pack` takes
+    the stored form: ``codes`` [N, K/2] uint8 (even k in the low four bits),
+    ``scales`` [N, K/group] bf16 and, with ``has_zeros``, ``zeros`` [N, K/group]
+    uint8.  Packed weights run with every handle of the same N, K, group and
+    ``has_zeros``.
+    """
+
+    def __init__(self, max_tokens: int, N: int, K: int, group: int = 128, has_zeros: bool = False,
+                 y_dtype: int = PROJ_BF16, has_bias: bool = False, stream=None):
+        self.handle = None
+        import torch
+        self.N, self.K, self.group, self.has_zeros = N, K, group, bool(has_zeros)
+        self.has_bias = bool(has_bias)
+        self._dtype = torch.float32 if y_dtype == PROJ_F32 else torch.bfloat16
+        self.handle = proj_q4_create(max_tokens, N, K, group, has_zeros, y_dtype, has_bias, stream)
+
+    def pack(self, codes, scales, zeros=None, stream=None):
+        """The packed weights (uint8 CUDA tensor), made on the given or current stream."""
+        import torch
+        groups = self.K // self.group
+        _require(codes.dtype == torch.uint8 and tuple(codes.shape) == (self.N, self.K // 2) and codes.is_contiguous(),
+                 "codes: contiguous uint8 [N, K/2]")
+        _require(scales.dtype == torch.bfloat16 and tuple(scales.shape) == (self.N, groups) and scales.is_contiguous(),
+                 "scales: contiguous bf16 [N, K/group]")
+        _require((zeros is not None) == self.has_zeros, "zeros: given if and only if has_zeros")
+        if zeros is not None:
+            _require(zeros.dtype == torch.uint8 and tuple(zeros.shape) == (self.N, groups) and zeros.is_contiguous(),
+                     "zeros: contiguous uint8 [N, K/group]")
+        packed = torch.empty(max(16, proj_q4_packed_bytes(self.N, self.K, self.group, self.has_zeros)),
+                             dtype=torch.uint8, device=codes.device)
+        if stream is None:
+            stream = torch.cuda.current_stream(codes.device)
+        proj_q4_pack(self.handle, codes, scales, zeros, packed, stream)
+        return packed
+
+    def __call__(self, X, packed, bias=None, out=None, stream=None):
+        import torch
+        M = X.shape[0]
+        _require(X.dtype == torch.bfloat16 and X.dim() == 2 and X.shape[1] == self.K and X.is_contiguous(),
+                 "X: contiguous bf16 [M, K]")
+        _require(bias is None or (bias.dtype == torch.bfloat16 and tuple(bias.shape) == (self.N,) and
+                                  bias.is_contiguous()), "bias: contiguous bf16 [N]")
+        if out is None:
+            out = torch.empty((M, self.N), dtype=self._dtype, device=X.device)
+        else:
+            _require(out.dtype == self._dtype and tuple(out.shape) == (M, self.N) and out.is_contiguous(),
+                     "out: contiguous [M, N] of y_dtype")
+        if stream is None:
+            stream = torch.cuda.current_stream(X.device)
+        proj_q4_run(self.handle, M, X, packed, bias, out, stream)
+        return out
+
+    def close(self) -> None:
+        if self.handle:
+            proj_q4_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
+    """Rotary table [positions, rot_dim] fp32: cosines, then sines, of
+    position · base^(−2j/rot_dim), computed in 64 bits and rounded once."""
+    import torch
+    half = rot_dim // 2
+    rate = base ** (-torch.arange(half, dtype=torch.float64, device=device) / max(1, half))
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * rate[None, :]
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+class PagedKV:
+    """A paged key-value cache: :meth:`append` new tokens, :meth:`attend` over it.
+
+    ``k_cache``, ``v_cache``: [pages, page_size, kv_heads, head_dim] bf16 or
+    float8_e4m3fn CUDA tensors of the same strides; a view with heads before
+    tokens in memory works as well, head_dim has to be contiguous.  With 8-bit
+    elements ``k_scale``, ``v_scale`` ([kv_heads] fp32) say what one unit
+    stands for.  The tensors stay the caller's; the handle owns scratch for
+    sequences that several thread blocks share.
+    """
+
+    def __init__(self, k_cache, v_cache, q_heads: int, max_sequences: int, k_scale=None, v_scale=None, stream=None):
+        self.handle = None
+        import torch
+        _require(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.stride() == v_cache.stride() and
+                 k_cache.dtype == v_cache.dtype, "k_cache, v_cache: 4-D, of one shape, type and strides")
+        _require(k_cache.shape[3] <= 1 or k_cache.stride(3) == 1, "k_cache, v_cache: head_dim contiguous")
+        pages, page_size, kv_heads, head_dim = k_cache.shape
+        if k_cache.dtype == torch.bfloat16:
+            kv_dtype = PROJ_BF16
+        elif k_cache.dtype == torch.float8_e4m3fn:
+            kv_dtype = PROJ_E4M3
+        else:
+            raise ProjError(PROJ_ERR_UNSUPPORTED, "k_cache, v_cache: bf16 or float8_e4m3fn")
+        for s in (k_scale, v_scale):
+            _require(s is None or (kv_dtype == PROJ_E4M3 and s.dtype == torch.float32 and
+                                   tuple(s.shape) == (kv_heads,) and s.is_contiguous()),
+                     "k_scale, v_scale: contiguous fp32 [kv_heads], for an 8-bit cache")
+        self.k_cache, self.v_cache, self.k_scale, self.v_scale = k_cache, v_cache, k_scale, v_scale
+        self.q_heads, self.kv_heads, self.head_dim, self.page_size = q_heads, kv_heads, head_dim, page_size
+        self._bf16, self._i32, self._f32 = torch.bfloat16, torch.int32, torch.float32
+        self._torch = torch
+        s = k_cache.stride()
+        desc = KvDesc(pages, s[0], s[1], s[2], max_sequences, page_size, q_heads, kv_heads, head_dim, kv_dtype)
+        self.handle = proj_kv_create(desc, stream)
+
+    def _rows(self, x, heads: int, what: str) -> int:
+        """Checks [tokens, heads, head_dim] rows with contiguous heads; the row stride."""
+        s = x.stride()
+        _require(x.dtype == self._bf16 and x.dim() == 3 and x.shape[1] == heads and x.shape[2] == self.head_dim and
+                 s[2] == 1 and (heads == 1 or s[1] == self.head_dim),
+                 f"{what}: bf16 [tokens, {heads}, {self.head_dim}] with contiguous heads")
+        return s[0] if x.shape[0] > 1 else heads * self.head_dim
+
+    def _ints(self, x, dims: int, what: str) -> None:
+        _require(x.dtype == self._i32 and x.dim() == dims and x.is_contiguous(), f"{what}: contiguous int32, {dims}-D")
+
+    def append(self, q, k, v, positions, page_table, seq_ids=None, rope=None, interleaved: bool = False, q_out=None,
+               stream=None):
+        """Rotate ``q`` and ``k`` ([tokens, heads, head_dim] bf16, rows of any
+        stride) at ``positions`` (int32 [tokens], negative: padding) and write
+        ``k`` and ``v`` to the cache; returns the rotated queries (``q_out``,
+        which may be ``q``; None when ``q`` is None).  ``page_table``: int32
+        [sequences, pages of a sequence]; ``seq_ids``: int32 [tokens], default
+        0, 1, 2, …; ``rope``: :func:`rope_table`'s form, or None for no
+        rotation."""
+        torch = self._torch
+        tokens = k.shape[0]
+        kv_stride = self._rows(k, self.kv_heads, "k")
+        _require(self._rows(v, self.kv_heads, "v") == kv_stride and v.shape[0] == tokens, "v: rows as k's")
+        self._ints(positions, 1, "positions")
+        self._ints(page_table, 2, "page_table")
+        _require(positions.shape[0] == tokens, "positions: one for each token")
+        if seq_ids is not None:
+            self._ints(seq_ids, 1, "seq_ids")
+            _require(seq_ids.shape[0] == tokens, "seq_ids: one for each token")
+        rot_dim = 0
+        if rope is not None:
+            _require(rope.dtype == self._f32 and rope.dim() == 2 and rope.is_contiguous(),
+                     "rope: contiguous fp32 [positions, rot_dim]")
+            rot_dim = rope.shape[1]
+        q_stride = q_out_stride = 0
+        if q is not None:
+            q_stride = self._rows(q, self.q_heads, "q")
+            _require(q.shape[0] == tokens, "q: one row for each token")
+            if q_out is None:
+                q_out = torch.empty((tokens, self.q_heads, self.head_dim), dtype=self._bf16, device=q.device)
+            q_out_stride = self._rows(q_out, self.q_heads, "q_out")
+            _require(q_out.shape[0] == tokens, "q_out: one row for each token")
+        else:
+            _require(q_out is None, "q_out: only with q")
+        if stream is None:
+            stream = torch.cuda.current_stream(k.device)
+        proj_kv_append(self.handle, tokens, q, q_stride, k, v, kv_stride, positions, seq_ids, page_table,
+                       page_table.shape[0], page_table.shape[1], rope, 0 if rope is None else rope.shape[0], rot_dim,
+                       interleaved, self.k_scale, self.v_scale, self.k_cache, self.v_cache, q_out, q_out_stride,
+                       stream)
+        return q_out
+
+    def attend(self, q, page_table, seq_lens, scale: Optional[float] = None, window: int = 0, out=None,
+               return_lse: bool = False, stream=None):
+        """Attention of ``q`` ([sequences, q_heads, head_dim] bf16) over each
+        sequence's first ``seq_lens`` (int32 [sequences]) cached tokens, or the
+        last ``window`` of them; ``scale`` is 1/√head_dim by default.  Returns
+        ``out`` ([sequences, q_heads, head_dim] bf16), with the fp32 log sums
+        [sequences, q_heads] beside it when ``return_lse``."""
+        torch = self._torch
+        n = q.shape[0]
+        q_stride = self._rows(q, self.q_heads, "q")
+        self._ints(page_table, 2, "page_table")
+        self._ints(seq_lens, 1, "seq_lens")
+        _require(page_table.shape[0] == n and seq_lens.shape[0] == n, "page_table, seq_lens: one row for each sequence")
+        if out is None:
+            out = torch.empty((n, self.q_heads, self.head_dim), dtype=self._bf16, device=q.device)
+        out_stride = self._rows(out, self.q_heads, "out")
+        _require(out.shape[0] == n, "out: one row for each sequence")
+        lse = torch.empty((n, self.q_heads), dtype=self._f32, device=q.device) if return_lse else None
+        if stream is None:
+            stream = torch.cuda.current_stream(q.device)
+        if scale is None:
+            scale = self.head_dim ** -0.5
+        proj_kv_attend(self.handle, n, q, q_stride, self.k_cache, self.v_cache, self.k_scale, self.v_scale, page_table,
+                       page_table.shape[1], seq_lens, window, scale, out, out_stride, lse, stream)
+        return (out, lse) if return_lse else out
+
+    def status(self, stream=None) -> int:
+        return proj_kv_device_status(self.handle, stream)
+
+    def close(self) -> None:
+        if self.handle:
+            proj_kv_destroy(self.handle)
             self.handle = None
 
     def __del__(self):

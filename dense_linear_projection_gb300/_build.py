@@ -17,10 +17,12 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 SOURCES = ["proj_api.cu", "planner.cpp", "kernel_tc_lean.cu", "kernel_tc_fused.cu", "kernel_tc_pair.cu",
-           "kernel_tc_pair_fused.cu"]
+           "kernel_tc_pair_fused.cu", "q4_api.cu", "kv_api.cu"]
 HEADERS = [os.path.join(CSRC, "proj_internal.h"), os.path.join(CSRC, "proj_kernel.cuh"),
            os.path.join(CSRC, "proj_aux.cuh"), os.path.join(CSRC, "proj_launch.h"),
-           os.path.join(INCLUDE, "proj.h")]
+           os.path.join(CSRC, "proj_host.h"), os.path.join(CSRC, "q4_internal.h"),
+           os.path.join(CSRC, "q4_kernels.cuh"), os.path.join(CSRC, "kv_internal.h"),
+           os.path.join(CSRC, "kv_kernels.cuh"), os.path.join(INCLUDE, "proj.h")]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]

@@ -1,0 +1,247 @@
+// Device code of the paged key-value cache: append with the rotary position,
+// and attention of one new token of each sequence.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "kv_internal.h"
+#include "proj_kernel.cuh"
+
+namespace projgb {
+namespace dev {
+
+__device__ __forceinline__ float e4m3_to_float(uint8_t b) {
+    return __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)));
+}
+
+// Length of sequence b, checked against the page table.
+__device__ __forceinline__ int64_t checked_length(const KvCacheView &c, const int32_t *seq_lens, int64_t b,
+                                                  int *status) {
+    int64_t n = seq_lens[b];
+    const int64_t most = c.table_width * c.page_size;
+    if (n < 0 || n > most) {
+        atomicOr(status, kKvErrLength);
+        n = n < 0 ? 0 : most;
+    }
+    return n;
+}
+
+// Offset of a token's head in the cache, or -1 for a page outside it.
+__device__ __forceinline__ int64_t token_offset(const KvCacheView &c, int64_t b, int64_t t, int head, int *status) {
+    const int32_t page = c.table[b * c.table_width + t / c.page_size];
+    if (page < 0 || page >= c.num_pages) {
+        atomicOr(status, kKvErrPage);
+        return -1;
+    }
+    return page * c.page_stride + (t % c.page_size) * c.token_stride + head * c.head_stride;
+}
+
+template <bool kE4m3>
+__device__ __forceinline__ float cache_element(const void *cache, int64_t at) {
+    if constexpr (kE4m3)
+        return e4m3_to_float(static_cast<const uint8_t *>(cache)[at]);
+    else
+        return bf16_bits_to_float(static_cast<const uint16_t *>(cache)[at]);
+}
+
+// One warp per sequence and query head, one token at a time.
+template <bool kE4m3>
+__global__ void kv_attend_kernel(KvAttendParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const KvCacheView &c = p.cache;
+    const int lane = threadIdx.x & 31;
+    const int64_t row = blockIdx.x * static_cast<int64_t>(blockDim.x / 32) + threadIdx.x / 32;
+    if (row >= p.sequences * p.q_heads) return;
+    const int64_t b = row / p.q_heads;
+    const int h = static_cast<int>(row % p.q_heads), hk = h / (p.q_heads / c.kv_heads);
+    const float ks = p.k_scale ? p.k_scale[hk] : 1.f, vs = p.v_scale ? p.v_scale[hk] : 1.f;
+    constexpr int kPer = kKvMaxDim / 32;
+    float q[kPer], o[kPer];
+    for (int i = 0; i < kPer; ++i) {
+        const int d = lane + 32 * i;
+        q[i] = d < c.head_dim ? bf16_bits_to_float(p.q[b * p.q_stride + h * c.head_dim + d]) * p.scale * ks : 0.f;
+        o[i] = 0.f;
+    }
+    const int64_t n = checked_length(c, p.seq_lens, b, p.status);
+    float m = -INFINITY, l = 0.f;
+    for (int64_t t = p.window > 0 && n > p.window ? n - p.window : 0; t < n; ++t) {
+        const int64_t at = token_offset(c, b, t, hk, p.status);
+        if (at < 0) continue;
+        float s = 0.f;
+        for (int i = 0; i < kPer; ++i) {
+            const int d = lane + 32 * i;
+            if (d < c.head_dim) s += q[i] * cache_element<kE4m3>(p.k_cache, at + d);
+        }
+        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+        const float top = fmaxf(m, s);
+        const float keep = m == -INFINITY ? 0.f : expf(m - top), w = expf(s - top);
+        l = l * keep + w;
+        m = top;
+        for (int i = 0; i < kPer; ++i) {
+            const int d = lane + 32 * i;
+            if (d < c.head_dim) o[i] = o[i] * keep + w * cache_element<kE4m3>(p.v_cache, at + d);
+        }
+    }
+    for (int i = 0; i < kPer; ++i) {
+        const int d = lane + 32 * i;
+        if (d < c.head_dim)
+            reinterpret_cast<__nv_bfloat16 *>(p.out)[b * p.out_stride + h * c.head_dim + d] =
+                __float2bfloat16_rn(l > 0.f ? o[i] / l * vs : 0.f);
+    }
+    if (p.lse && lane == 0) p.lse[row] = l > 0.f ? m + logf(l) : -INFINITY;
+}
+
+// Append.  A unit is 16 elements of one head of one token: eight rotary pairs
+// (kVec: two 16-byte loads, either 8 + 8 elements of the two halves or 16 in a
+// row), or 16 elements that are only copied.  A thread takes the same unit of
+// several heads, so its cosines and sines are read once.  The rotation uses
+// separate fp32 products and sums (no fused multiply-add): the value rounded to
+// the cache's type is the formula's own.  Bytes bound it: each row is read and
+// written once.
+constexpr int kAppendThreads = 256;
+
+__device__ __forceinline__ void load8(const uint16_t *from, float *x) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(from);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ uint8_t to_e4m3(float x, float scale) {
+    const float y = fminf(fmaxf(__fdiv_rn(x, scale), -448.f), 448.f);
+    // fmaxf and fminf drop a NaN; the cache keeps it.
+    return __nv_cvt_float_to_fp8(x != x ? x : y, __NV_SATFINITE, __NV_E4M3);
+}
+
+// Elements [at, at + 8) of a head, as bf16 or e4m3.
+template <bool kE4m3>
+__device__ __forceinline__ void store8(void *to, int64_t at, const float *x, float scale) {
+    if constexpr (kE4m3) {
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i / 4] |= static_cast<uint32_t>(to_e4m3(x[i], scale)) << (8 * (i % 4));
+        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(to) + at) = make_uint2(w[0], w[1]);
+    } else {
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(to) + at) =
+            make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+    }
+}
+
+template <bool kE4m3>
+__device__ __forceinline__ void store1(void *to, int64_t at, float x, float scale) {
+    if constexpr (kE4m3)
+        static_cast<uint8_t *>(to)[at] = to_e4m3(x, scale);
+    else
+        static_cast<__nv_bfloat16 *>(to)[at] = __float2bfloat16_rn(x);
+}
+
+__device__ __forceinline__ void rotate(float &a, float &b, float cos, float sin) {
+    const float u = __fsub_rn(__fmul_rn(a, cos), __fmul_rn(b, sin));
+    b = __fadd_rn(__fmul_rn(b, cos), __fmul_rn(a, sin));
+    a = u;
+}
+
+template <bool kE4m3, bool kInterleaved, bool kVec>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvAppendParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const KvCacheView &c = p.cache;
+    const int64_t token = blockIdx.x;
+    const int half = p.rot_dim / 2;
+    const int pair_units = (half + 7) / 8, units = pair_units + (c.head_dim - p.rot_dim + 15) / 16;
+    const int slots = kAppendThreads / units;  // heads a block takes at a time
+    const int unit = threadIdx.x % units, slot = threadIdx.x / units;
+    if (slot >= slots) return;
+    const int64_t pos = p.positions[token];
+    const int64_t seq = p.seq_ids ? p.seq_ids[token] : token;
+    if (pos < 0) return;
+    int bad = 0;
+    if (pos >= c.table_width * c.page_size || (p.rope && pos >= p.rope_positions)) bad |= kKvErrPosition;
+    if (seq < 0 || seq >= p.sequences) bad |= kKvErrSequence;
+    int64_t page = 0;
+    if (!bad) {
+        page = c.table[seq * c.table_width + pos / c.page_size];
+        if (page < 0 || page >= c.num_pages) bad |= kKvErrPage;
+    }
+    if (bad) {
+        if (unit == 0 && slot == 0 && blockIdx.y == 0) atomicOr(p.status, bad);
+        return;
+    }
+    const int64_t place = page * c.page_stride + (pos % c.page_size) * c.token_stride;
+    const bool rotary = unit < pair_units;
+    const int j0 = 8 * unit;  // first rotary pair
+    const int d0 = p.rot_dim + 16 * (unit - pair_units);  // first copied element
+    float cos[8], sin[8];
+    if (rotary) {
+        const float *r = p.rope + pos * p.rot_dim;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            cos[i] = j0 + i < half ? r[j0 + i] : 1.f;
+            sin[i] = j0 + i < half ? r[half + j0 + i] : 0.f;
+        }
+    }
+    const int heads = p.q_heads + 2 * c.kv_heads;
+    for (int h = slot + blockIdx.y * slots; h < heads; h += slots * gridDim.y) {
+        const bool is_q = h < p.q_heads, is_v = h >= p.q_heads + c.kv_heads;
+        const int head = is_q ? h : h - p.q_heads - (is_v ? c.kv_heads : 0);
+        const uint16_t *from = (is_q ? p.q + token * p.q_stride : (is_v ? p.v : p.k) + token * p.kv_stride) +
+                               static_cast<int64_t>(head) * c.head_dim;
+        void *to = is_q ? p.q_out : is_v ? p.v_cache : p.k_cache;
+        const int64_t at = is_q ? token * p.q_out_stride + static_cast<int64_t>(head) * c.head_dim : place + head * c.head_stride;
+        const float *scales = is_v ? p.v_scale : p.k_scale;
+        const float scale = kE4m3 && !is_q && scales ? scales[head] : 1.f;
+        if constexpr (kVec) {
+            // First elements of the unit's two runs of eight.
+            const int e0 = !rotary ? d0 : kInterleaved ? 2 * j0 : j0;
+            const int e1 = rotary && !kInterleaved ? half + j0 : e0 + 8;
+            float a[8], b[8];
+            load8(from + e0, a);
+            load8(from + e1, b);
+            if (rotary && !is_v) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if constexpr (kInterleaved) {
+                        float *x = i < 4 ? a + 2 * i : b + 2 * (i - 4);
+                        rotate(x[0], x[1], cos[i], sin[i]);
+                    } else {
+                        rotate(a[i], b[i], cos[i], sin[i]);
+                    }
+                }
+            }
+            if (is_q) {
+                store8<false>(to, at + e0, a, 1.f);
+                store8<false>(to, at + e1, b, 1.f);
+            } else {
+                store8<kE4m3>(to, at + e0, a, scale);
+                store8<kE4m3>(to, at + e1, b, scale);
+            }
+        } else {
+            for (int i = 0; i < 8; ++i) {
+                const int e0 = !rotary ? d0 + 2 * i : kInterleaved ? 2 * (j0 + i) : j0 + i;
+                const int e1 = rotary && !kInterleaved ? half + j0 + i : e0 + 1;
+                if (rotary ? j0 + i >= half : e0 >= c.head_dim) break;
+                float a = bf16_bits_to_float(from[e0]), b = bf16_bits_to_float(from[e1]);
+                if (rotary && !is_v) rotate(a, b, cos[i], sin[i]);
+                if (is_q) {
+                    store1<false>(to, at + e0, a, 1.f);
+                    store1<false>(to, at + e1, b, 1.f);
+                } else {
+                    store1<kE4m3>(to, at + e0, a, scale);
+                    store1<kE4m3>(to, at + e1, b, scale);
+                }
+            }
+        }
+    }
+}
+
+}  // namespace dev
+}  // namespace projgb

@@ -13,10 +13,41 @@
 
 #include "proj.h"
 #include "proj_aux.cuh"
+#include "proj_host.h"
 #include "proj_internal.h"
 #include "proj_launch.h"
 
 using namespace projgb;
+
+namespace projgb {
+
+// Host-side fault injection for tests (PROJ_FAULT, read once per process): a
+// comma-separated list of "alloc" (every device allocation of the library
+// fails as out of memory), "encode" (every tensor-map encoding fails) and
+// "launch" (every kernel launch fails before it is queued).  The failure is
+// made on the host: nothing faulty reaches the device.
+int fault_mask() {
+    static const int mask = [] {
+        int m = 0;
+        if (const char *e = std::getenv("PROJ_FAULT")) {
+            if (std::strstr(e, "alloc")) m |= kFaultAlloc;
+            if (std::strstr(e, "encode")) m |= kFaultEncode;
+            if (std::strstr(e, "launch")) m |= kFaultLaunch;
+        }
+        return m;
+    }();
+    return mask;
+}
+
+cudaError_t dev_malloc(void **p, size_t bytes) {
+    if (fault_mask() & kFaultAlloc) {
+        *p = nullptr;
+        return cudaErrorMemoryAllocation;
+    }
+    return cudaMalloc(p, bytes);
+}
+
+}  // namespace projgb
 
 struct proj_plan_s {
     int device = 0;
@@ -63,39 +94,6 @@ struct proj_plan_s {
 namespace {
 
 constexpr int64_t kDefaultWaitLimitNs = 1000000000LL;  // 1 s
-
-cudaStream_t as_stream(void *s) { return static_cast<cudaStream_t>(s); }
-
-// Host-side fault injection for tests (PROJ_FAULT, read once per process): a
-// comma-separated list of "alloc" (every device allocation of the library
-// fails as out of memory), "encode" (every tensor-map encoding fails) and
-// "launch" (every kernel launch fails before it is queued).  The failure is
-// made on the host: nothing faulty reaches the device.
-constexpr int kFaultAlloc = 1, kFaultEncode = 2, kFaultLaunch = 4;
-
-int fault_mask() {
-    static const int mask = [] {
-        int m = 0;
-        if (const char *e = std::getenv("PROJ_FAULT")) {
-            if (std::strstr(e, "alloc")) m |= kFaultAlloc;
-            if (std::strstr(e, "encode")) m |= kFaultEncode;
-            if (std::strstr(e, "launch")) m |= kFaultLaunch;
-        }
-        return m;
-    }();
-    return mask;
-}
-
-bool launch_faulted() { return (fault_mask() & kFaultLaunch) != 0; }
-
-// Every device allocation of the library goes through here.
-cudaError_t dev_malloc(void **p, size_t bytes) {
-    if (fault_mask() & kFaultAlloc) {
-        *p = nullptr;
-        return cudaErrorMemoryAllocation;
-    }
-    return cudaMalloc(p, bytes);
-}
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -311,8 +309,6 @@ int y_vec_of(const void *Y, int64_t N, int y_dtype) {
     const int64_t row_bytes = N * (y_dtype == PROJ_F32 ? 4 : 2);
     return (row_bytes % 16 == 0) && (reinterpret_cast<uintptr_t>(Y) % 16 == 0);
 }
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // The kernel instance a plan runs on: CTA pairs or single CTAs, with or
 // without the fused epilogue.

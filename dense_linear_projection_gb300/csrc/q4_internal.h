@@ -1,0 +1,63 @@
+// Packed 4-bit weights: layout shared by the packing kernel, the projection
+// kernel and the host.
+//
+// Weight rows are cut into tiles of 64 (four row blocks of 16) and K into
+// blocks of 64.  One (row block, k-block) is 512 bytes: lane l of a warp takes
+// 16 bytes, the A operands of four tensor-core steps (16 rows × 16 K each) in
+// the lane's own register layout.  With r = l / 4 and j = l % 4, step i covers
+// rows r and r + 8 and the four K positions q4_k_of(j, i) .. + 3.  (Which K
+// positions share a step is free, as X is read by the same rule; this one gives
+// a lane 16 contiguous bytes of X for two steps, and keeps a step within a
+// group of 32.)  Register t of a step holds nibbles t and t + 4 of its word,
+// stored rotated left by 3 so that a rotation by 4·t alone brings them to bits
+// 3..6 of each half, where OR-ing 0x4180 makes them the bf16 numbers 16 + q.
+//
+//   codes   [row tile][k-block][row block 0..3][lane] 16 bytes
+//   scales  [row tile][group][row block][r = 0..7] bf16 of rows r, r + 8
+//   zeros   [row tile][group][row block][r] four bits of rows r, r + 8
+//
+// Rows past N and K past its end have code 8 and scale 0.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include <cuda_runtime.h>
+
+#include "proj_internal.h"
+
+namespace projgb {
+
+constexpr int kQ4TileRows = 64;
+
+PROJ_HD int q4_k_of(int j, int i) { return (i >> 1) * 32 + j * 8 + (i & 1) * 4; }
+
+struct Q4Shape {
+    int64_t row_tiles, k_blocks, groups, groups_padded;
+    int64_t codes_bytes, scales_bytes, zeros_bytes;
+};
+
+inline Q4Shape q4_shape(int64_t N, int64_t K, int64_t group, bool has_zeros) {
+    Q4Shape s;
+    s.row_tiles = (N + kQ4TileRows - 1) / kQ4TileRows;
+    s.k_blocks = (K + 63) / 64;
+    s.groups = K / group;
+    s.groups_padded = group <= 64 ? s.k_blocks * (64 / group) : s.groups;  // 128: K is whole groups
+    s.codes_bytes = s.row_tiles * s.k_blocks * 2048;
+    s.scales_bytes = s.row_tiles * s.groups_padded * 128;
+    s.zeros_bytes = has_zeros ? s.row_tiles * s.groups_padded * 32 : 0;
+    return s;
+}
+
+struct Q4Params {
+    int64_t M, N, K, k_blocks, groups_padded;
+    int32_t group, y_f32;
+    const uint16_t *X;
+    const uint4 *codes;
+    const uint32_t *scales;
+    const uint8_t *zeros;  // nullptr: 8
+    const uint16_t *bias;
+    void *Y;
+};
+
+}  // namespace projgb

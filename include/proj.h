@@ -74,7 +74,9 @@ typedef enum proj_status {
     PROJ_ERR_DEVICE_TIMEOUT = 6  /* a bounded device-side wait ran out */
 } proj_status_t;
 
-typedef enum proj_dtype { PROJ_BF16 = 0, PROJ_F32 = 1 } proj_dtype_t;
+/* PROJ_E4M3 (8-bit floating, 4 exponent and 3 mantissa bits) is a type of a
+ * paged key-value cache only. */
+typedef enum proj_dtype { PROJ_BF16 = 0, PROJ_F32 = 1, PROJ_E4M3 = 2 } proj_dtype_t;
 
 typedef enum proj_wlayout { PROJ_W_NK = 0, PROJ_W_KN = 1 } proj_wlayout_t;
 
@@ -502,6 +504,126 @@ const char *proj_status_string(proj_status_t s);
  * the wait did not give up).  No fault, trap or hang is involved.
  */
 proj_status_t proj_selftest_wait_timeout(int64_t limit_ns, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Projections with 4-bit weights.
+ *
+ *   Y[m, n] = Σ_k X[m, k] · s[n, g] · (q[n, k] − z[n, g])  (+ bias[n]),  g = ⌊k / group⌋
+ *
+ * q are codes 0..15, s bf16 scales, z zero points 0..15 (8 everywhere when
+ * the weights have none).  q − z is exact in bf16; products and sums are fp32
+ * (the scale multiplies a group's fp32 sum, so the dequantised weight itself is
+ * never rounded), and Y is rounded once.  For the token counts of a decode
+ * step: any M ≥ 0 runs, in passes over the weights of 32 tokens each.
+ *
+ * Stored form (device, read by proj_q4_pack only):
+ *   codes   [N, K/2] bytes: byte j of a row holds k = 2j in its low and
+ *           k = 2j + 1 in its high four bits;
+ *   scales  [N, K/group] bf16;   zeros [N, K/group] bytes (low four bits
+ *           used), or NULL for handles without zero points.
+ * Packed form (caller-owned device memory, 16-byte aligned,
+ *   proj_q4_packed_bytes): the same codes in the order in which the kernel's
+ *   lanes take them, then the scales, then the zero points.  It depends on N,
+ *   K, group and has_zeros alone: every handle with those runs it.
+ *
+ * proj_q4_create: max_tokens is the largest M of a run (it sizes the scratch).
+ *   group 32, 64 or 128 (else PROJ_ERR_UNSUPPORTED), K a multiple of it (else
+ *   PROJ_ERR_INVALID_ARG); N of any size; K = 0 gives Y = bias or 0.
+ * proj_q4_run: X [M, K] bf16 (16-byte aligned), bias [N] bf16 or NULL as
+ *   created, Y [M, N] of y_dtype; 0 ≤ M ≤ max_tokens.  Asynchronous, no
+ *   allocation, can be captured in a graph.  One handle must not run on two
+ *   streams at the same time.
+ */
+typedef struct proj_q4_s *proj_q4_handle_t;
+
+proj_status_t proj_q4_packed_bytes(int64_t N, int64_t K, int64_t group, int has_zeros, size_t *bytes);
+proj_status_t proj_q4_create(proj_q4_handle_t *out, int64_t max_tokens, int64_t N, int64_t K, int64_t group,
+                             int has_zeros, proj_dtype_t y_dtype, int has_bias, void *stream);
+proj_status_t proj_q4_pack(proj_q4_handle_t h, const void *codes, const void *scales, const void *zeros,
+                           void *packed, void *stream);
+proj_status_t proj_q4_run(proj_q4_handle_t h, int64_t M, const void *X, const void *packed, const void *bias,
+                          void *Y, void *stream);
+proj_status_t proj_q4_destroy(proj_q4_handle_t h);
+
+/* ---------------------------------------------------------------------------
+ * A paged key-value cache: appending new tokens, and attention of one new
+ * token of each sequence over it.
+ *
+ * The cache of one layer is two arrays of pages.  Token t of a sequence lies
+ * in page table[sequence][⌊t / page_size⌋] at place t mod page_size; its key
+ * of head h starts at
+ *   k_cache + page · page_stride + place · token_stride + h · head_stride
+ * (strides in elements; head_dim elements are contiguous), its value at the
+ * same place of v_cache.  So pages with tokens first or heads first, and keys
+ * and values in one allocation, are all described by the strides.
+ * kv_dtype PROJ_BF16, or PROJ_E4M3: an element then stands for
+ * scale[h] · e4m3, with fp32 scales [kv_heads] on the device (NULL: 1).
+ *
+ * proj_kv_create: head_dim a multiple of 16 up to 256, q_heads a multiple of
+ *   kv_heads, page_size ≥ 1; strides whole 16-byte multiples (else
+ *   PROJ_ERR_MISALIGNED).  max_sequences bounds the sequences of one
+ *   proj_kv_attend.  A handle owns scratch for joining split sequences and a
+ *   status word; one handle may serve every layer whose cache has its
+ *   geometry, but must not run on two streams at the same time.
+ *
+ * proj_kv_append: for token i of `tokens`, at position p = positions[i] of
+ *   sequence seq_ids[i] (i itself when seq_ids is NULL): the first rot_dim
+ *   elements of each head of q and k are rotated,
+ *     (u, v) = (a·cos − b·sin, b·cos + a·sin)
+ *   for pair j = (a, b): elements (j, j + rot_dim/2), or (2j, 2j + 1) when
+ *   `interleaved`; rope[p] holds the rot_dim/2 cosines, then the sines, fp32.
+ *   k and v go to the cache, q to q_out (which may be q).  The rotation is
+ *   fp32, rounded once to the type written; e4m3 values are x / scale,
+ *   clamped to ±448.  rope NULL: no rotation.  q NULL: keys and values only.
+ *   q, k, v, q_out: bf16 rows of heads × head_dim, rows *_stride elements
+ *   apart (a q·k·v projection's output is read in place).  A token with
+ *   p < 0 is padding: nothing of it is read or written.
+ *   Two tokens of one call must not name the same place.
+ *
+ * proj_kv_attend: for each sequence b and query head h (key head
+ *   ⌊h · kv_heads / q_heads⌋), over its tokens t in [max(0, n − window), n),
+ *   n = seq_lens[b] (window 0: all n):
+ *     out[b,h] = Σ_t softmax_t(scale · q[b,h]·k_t) · v_t,
+ *     lse[b,h] = log Σ_t e^(scale · q[b,h]·k_t)   (lse fp32 [B, q_heads], or NULL).
+ *   n = 0 gives out = 0 and lse = −∞.  The weights and sums are fp32; out is bf16, rounded once.
+ *   The sequences' tokens are dealt out evenly over the GPU and joined in a
+ *   fixed order: reruns are bit-identical.
+ *
+ * Asynchronous, no allocation, can be captured in a graph.  What only the
+ * device can see is checked there: a position past the page table or the
+ * rope table, a sequence id or a page outside its array, a length below zero
+ * or past the page table.  Such a token is skipped (attention leaves it out)
+ * and proj_kv_device_status then returns PROJ_ERR_INVALID_ARG once.
+ */
+typedef struct proj_kv_s *proj_kv_handle_t;
+
+typedef struct proj_kv_desc {
+    int64_t num_pages;      /* pages in k_cache and in v_cache */
+    int64_t page_stride;    /* elements between pages, tokens of a page, heads of a token */
+    int64_t token_stride;
+    int64_t head_stride;
+    int64_t max_sequences;
+    int32_t page_size;      /* tokens a page */
+    int32_t q_heads;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t kv_dtype;       /* PROJ_BF16 or PROJ_E4M3 */
+} proj_kv_desc_t;
+
+proj_status_t proj_kv_create(proj_kv_handle_t *out, const proj_kv_desc_t *desc, void *stream);
+proj_status_t proj_kv_append(proj_kv_handle_t h, int64_t tokens, const void *q, int64_t q_stride,
+                             const void *k, const void *v, int64_t kv_stride, const int32_t *positions,
+                             const int32_t *seq_ids, const int32_t *page_table, int64_t sequences,
+                             int64_t table_width, const float *rope, int64_t rope_positions, int32_t rot_dim,
+                             int interleaved, const float *k_scale, const float *v_scale, void *k_cache,
+                             void *v_cache, void *q_out, int64_t q_out_stride, void *stream);
+proj_status_t proj_kv_attend(proj_kv_handle_t h, int64_t sequences, const void *q, int64_t q_stride,
+                             const void *k_cache, const void *v_cache, const float *k_scale,
+                             const float *v_scale, const int32_t *page_table, int64_t table_width,
+                             const int32_t *seq_lens, int64_t window, float scale, void *out,
+                             int64_t out_stride, float *lse, void *stream);
+proj_status_t proj_kv_device_status(proj_kv_handle_t h, void *stream);
+proj_status_t proj_kv_destroy(proj_kv_handle_t h);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,237 @@
+"""Attention of one new token of each sequence over the paged cache, against 64 bits (the bounds
+are derived in kv_util.attention64)."""
+import math
+
+import pytest
+
+import kv_util as ku
+
+pytestmark = pytest.mark.gpu
+
+
+def case(lens, heads, kv_heads, dim, page, dtype="bf16", layout="tokens_first", seed=0, unused=0):
+    import torch
+    import dense_linear_projection_gb300 as dlp
+    pages = sum(-(-n // page) for n in lens) + 3
+    k, v = ku.make_cache(pages, page, kv_heads, dim, dtype, layout, seed)
+    table = ku.make_table(lens, page, pages, seed, unused=unused)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed + 1)
+    q = torch.randn((len(lens), heads, dim), generator=g, device="cuda").to(torch.bfloat16)
+    scales = [torch.rand(kv_heads, generator=g, device="cuda") + 0.5 for _ in "kv"] if dtype == "e4m3" else [None, None]
+    kv = dlp.PagedKV(k, v, heads, max_sequences=len(lens), k_scale=scales[0], v_scale=scales[1])
+    return kv, q, table, torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+
+def run(lens, heads, kv_heads, dim, page, window=0, scale=None, **more):
+    import torch
+    kv, q, table, lens_dev = case(lens, heads, kv_heads, dim, page, **more)
+    out, lse = kv.attend(q, table, lens_dev, scale=scale, window=window, return_lse=True)
+    ref = ku.attention64(q, kv.k_cache, kv.v_cache, table, lens, page, scale or dim ** -0.5, window, kv.k_scale, kv.v_scale)
+    what = f"lens={lens[:8]} heads={heads}/{kv_heads} dim={dim} page={page} window={window} {more}"
+    ku.check_attention(out, lse, ref, what)
+    again, lse2 = kv.attend(q, table, lens_dev, scale=scale, window=window, return_lse=True)
+    assert torch.equal(again, out) and torch.equal(lse2, lse), what
+    import dense_linear_projection_gb300 as dlp
+    assert kv.status() == dlp.PROJ_OK
+
+
+@pytest.mark.parametrize("lens", [[1], [0], [2, 0, 1], [15, 16, 17], [63, 64, 65], [127, 128, 129], [1000, 0, 3, 4097],
+                                  [37] * 33, [20000], [1, 9000, 1, 1]], ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_lengths(lens, dtype):
+    run(lens, 16, 4, 128, 16, dtype=dtype)
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (8, 8), (2, 1), (6, 2), (14, 2), (16, 2), (32, 2), (20, 1), (96, 2), (64, 8), (40, 40)])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_head_groups(heads, kv_heads, dtype):
+    run([300, 5, 77], heads, kv_heads, 64, 16, dtype=dtype)
+
+
+@pytest.mark.parametrize("dim", [16, 32, 48, 64, 80, 96, 128, 144, 192, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_head_dims(dim, dtype):
+    run([200, 33], 8, 2, dim, 16, dtype=dtype)
+
+
+@pytest.mark.parametrize("page", [1, 2, 3, 7, 16, 17, 64, 100, 300])
+@pytest.mark.parametrize("layout", ["tokens_first", "heads_first", "together"])
+def test_pages_and_layouts(page, layout):
+    run([301, 2, 64], 8, 2, 64, page, layout=layout)
+    run([301, 2, 64], 8, 2, 64, page, layout=layout, dtype="e4m3")
+
+
+@pytest.mark.parametrize("window", [1, 15, 16, 100, 300, 5000])
+def test_windows(window):
+    run([301, 0, 16, 2000, 1], 8, 4, 128, 16, window=window)
+    run([301, 0, 16, 2000, 1], 8, 4, 128, 16, window=window, dtype="e4m3")
+
+
+def test_scales():
+    for scale in (1.0, -0.2, 1e-6, 0.0):
+        import torch
+        kv, q, table, lens = case([70, 9], 8, 2, 64, 16)
+        out, lse = kv.attend(q, table, lens, scale=scale, return_lse=True)
+        ref = ku.attention64(q, kv.k_cache, kv.v_cache, table, [70, 9], 16, scale)
+        ku.check_attention(out, lse, ref, f"scale={scale}")
+
+
+def test_wide_logits():
+    # Logits hundreds apart: one token takes all the weight, wherever it is.
+    import torch
+    kv, q, table, lens = case([500] * 4, 8, 2, 64, 16)
+    q *= 40
+    out, lse = kv.attend(q, table, lens, return_lse=True)
+    ku.check_attention(out, lse, ku.attention64(q, kv.k_cache, kv.v_cache, table, [500] * 4, 16, 64 ** -0.5), "wide")
+
+
+def test_extreme_queries_over_8_bits():
+    # Queries of any bf16 size: the 8-bit path must not lose or overflow them.
+    import torch
+    kv, q, table, lens = case([100] * 2, 4, 2, 64, 16, dtype="e4m3")
+    for size in (1e30, 1e-30):
+        x = (q.float() * size).to(torch.bfloat16)
+        out, lse = kv.attend(x, table, lens, scale=0.125 / size, return_lse=True)
+        ref = ku.attention64(x, kv.k_cache, kv.v_cache, table, [100] * 2, 16, 0.125 / size, 0, kv.k_scale, kv.v_scale)
+        ku.check_attention(out, lse, ref, f"size={size}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("window", [0, 20])
+def test_nothing_outside_the_sequences_is_used(dtype, window):
+    # Every place no sequence sees holds NaN, and the table's unused entries are no pages at all.
+    import torch
+    import dense_linear_projection_gb300 as dlp
+    lens, page, dim = [45, 0, 130, 1], 16, 64
+    kv, q, table, lens_dev = case(lens, 8, 2, dim, page, dtype=dtype, unused=-7)
+    ref = ku.attention64(q, kv.k_cache, kv.v_cache, table, lens, page, dim ** -0.5, window, kv.k_scale, kv.v_scale)
+    seen = torch.zeros(kv.k_cache.shape[:2], dtype=torch.bool, device="cuda")
+    for b, n in enumerate(lens):
+        t = torch.arange(max(0, n - window) if window else 0, n, device="cuda")
+        seen[table[b].long()[t // page], t % page] = True
+        if window:  # pages wholly before the window are not read either
+            table[b, :max(0, n - window) // page] = 1 << 30
+    for c in (kv.k_cache, kv.v_cache):
+        raw = c.view(torch.uint8) if dtype == "e4m3" else c
+        raw[~seen] = 0x7F if dtype == "e4m3" else math.nan
+    out, lse = kv.attend(q, table, lens_dev, window=window, return_lse=True)
+    ku.check_attention(out, lse, ref, "poisoned")
+    assert kv.status() == dlp.PROJ_OK
+
+
+def test_strided_queries_and_outputs():
+    # Queries inside the rows of a query, key and value projection, outputs inside wider rows.
+    import torch
+    kv, q, table, lens = case([90, 33, 4], 8, 2, 64, 16)
+    rows = torch.randn((3, 12, 64), device="cuda").to(torch.bfloat16)
+    rows[:, :8] = q
+    wide = torch.full((3, 11, 64), 7.0, device="cuda", dtype=torch.bfloat16)
+    out = kv.attend(rows[:, :8], table, lens, out=wide[:, :8])
+    assert torch.equal(out, kv.attend(q, table, lens)) and (wide[:, 8:] == 7).all()
+
+
+def test_cache_offsets_past_31_bits():
+    # Pages far apart: element offsets above 2³¹ in each array.
+    import torch
+    import dense_linear_projection_gb300 as dlp
+    lens, page, hk, dim = [700], 16, 2, 64
+    stride = 1 << 26
+    base = [torch.empty(stride * 43 + page * hk * dim, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    k, v = (x.as_strided((44, page, hk, dim), (stride, hk * dim, dim, 1)) for x in base)
+    for x in (k, v):
+        x.copy_(torch.randn(x.shape, device="cuda"))
+    table = torch.randperm(44).to(torch.int32)[None].cuda()
+    q = torch.randn((1, 8, dim), device="cuda").to(torch.bfloat16)
+    kv = dlp.PagedKV(k, v, 8, 1)
+    out, lse = kv.attend(q, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), return_lse=True)
+    ku.check_attention(out, lse, ku.attention64(q, k, v, table, lens, page, dim ** -0.5), "far pages")
+
+
+def test_streams_graphs_and_shrinking_lengths():
+    # A captured call follows the lengths and tables that the buffers hold at replay.
+    import torch
+    lens = [800, 40, 1500, 0]
+    kv, q, table, lens_dev = case(lens, 16, 2, 128, 16)
+    ref = kv.attend(q, table, lens_dev)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = kv.attend(q, table, lens_dev)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(other, ref)
+    g, out = torch.cuda.CUDAGraph(), torch.empty_like(ref)
+    with torch.cuda.graph(g):
+        kv.attend(q, table, lens_dev, out=out)
+    for now in ([800, 40, 1500, 0], [1, 0, 1499, 5], [0, 0, 0, 0], [799, 39, 3, 0]):
+        now[3] = min(now[3], 0)  # the last sequence has no pages of its own
+        lens_dev.copy_(torch.tensor(now, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        ku.check_attention(out, None, ku.attention64(q, kv.k_cache, kv.v_cache, table, now, 16, 128 ** -0.5), str(now))
+
+
+def test_bad_pages_and_lengths_are_reported_and_left_out():
+    import torch
+    import dense_linear_projection_gb300 as dlp
+    lens, page = [100, 64], 16
+    kv, q, table, lens_dev = case(lens, 8, 2, 64, page)
+    good = table.clone()
+    table[0, 2], table[1, 0] = kv.k_cache.shape[0], -1
+    out, lse = kv.attend(q, table, lens_dev, return_lse=True)
+    assert kv.status() == dlp.PROJ_ERR_INVALID_ARG and kv.status() == dlp.PROJ_OK
+    keep = lambda b, t: (t // page != 2) if b == 0 else (t // page != 0)  # noqa: E731
+    ref = ku.attention64(q, kv.k_cache, kv.v_cache, good, lens, page, 64 ** -0.5, keep=keep)
+    ku.check_attention(out, lse, ref, "bad pages")
+    # A sequence whose every page is bad is an empty row.
+    table.fill_(-1)
+    out, lse = kv.attend(q, table, lens_dev, return_lse=True)
+    assert (out == 0).all() and (lse == -math.inf).all() and kv.status() == dlp.PROJ_ERR_INVALID_ARG
+    # Lengths past the table (cut to it) and below zero (an empty row).
+    full = good.shape[1] * page
+    pages = torch.randperm(kv.k_cache.shape[0], device="cuda").to(torch.int32)[:good.shape[1]]
+    both = pages.expand(2, -1).contiguous()
+    out, lse = kv.attend(q, both, torch.tensor([full + 9, -3], dtype=torch.int32, device="cuda"), return_lse=True)
+    assert kv.status() == dlp.PROJ_ERR_INVALID_ARG
+    ku.check_attention(out, lse, ku.attention64(q, kv.k_cache, kv.v_cache, both, [full, 0], page, 64 ** -0.5), "bad lengths")
+
+
+def test_empty_batch_and_empty_table():
+    import torch
+    kv, q, table, lens = case([5, 5], 8, 2, 64, 16)
+    assert kv.attend(q[:0], table[:0], lens[:0]).shape == (0, 8, 64)
+    out, lse = kv.attend(q, torch.empty((2, 0), dtype=torch.int32, device="cuda"), torch.zeros_like(lens), return_lse=True)
+    assert (out == 0).all() and (lse == -math.inf).all()
+
+
+def test_refusals():
+    import torch
+    import dense_linear_projection_gb300 as dlp
+    kv, q, table, lens = case([50, 20], 8, 2, 64, 16)
+    k, v = kv.k_cache, kv.v_cache
+    invalid, unsupported, misaligned = dlp.PROJ_ERR_INVALID_ARG, dlp.PROJ_ERR_UNSUPPORTED, dlp.PROJ_ERR_MISALIGNED
+    for what, status in [
+        (lambda: kv.attend(torch.cat([q, q]), torch.cat([table, table]), torch.cat([lens, lens])), invalid),
+        (lambda: kv.attend(q.float(), table, lens), invalid),
+        (lambda: kv.attend(q[:, :4], table, lens), invalid),
+        (lambda: kv.attend(q, table.long(), lens), invalid),
+        (lambda: kv.attend(q, table[:1], lens), invalid),
+        (lambda: kv.attend(q, table, lens[:1]), invalid),
+        (lambda: kv.attend(q, table, lens, window=-1), invalid),
+        (lambda: kv.attend(q, table, lens, scale=math.nan), invalid),
+        (lambda: dlp.PagedKV(k, v, 7, 2), invalid),                                  # heads not a multiple
+        (lambda: dlp.PagedKV(k, v[:1], 8, 2), invalid),
+        (lambda: dlp.PagedKV(k.float(), v.float(), 8, 2), unsupported),
+        (lambda: dlp.PagedKV(k[..., :40], v[..., :40], 8, 2), unsupported),
+        (lambda: dlp.PagedKV(*ku.make_cache(4, 16, 1, 272), 1, 2), unsupported),
+        (lambda: dlp.PagedKV(k, v, 8, 2, k_scale=torch.ones(2, device="cuda")), invalid),
+        (lambda: dlp.proj_kv_attend(kv.handle, 2, q.data_ptr() + 2, 512, k, v, None, None, table, table.shape[1], lens, 0,
+                                    1.0, q, 512, None), misaligned),
+        (lambda: dlp.proj_kv_attend(kv.handle, 2, q, 512, None, v, None, None, table, table.shape[1], lens, 0, 1.0, q,
+                                    512, None), invalid),
+        (lambda: dlp.proj_kv_attend(None, 2, q, 512, k, v, None, None, table, table.shape[1], lens, 0, 1.0, q, 512,
+                                    None), invalid),
+    ]:
+        with pytest.raises(dlp.ProjError) as e:
+            what()
+        assert e.value.status == status
