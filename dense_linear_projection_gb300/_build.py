@@ -22,7 +22,8 @@ HEADERS = [os.path.join(CSRC, "proj_internal.h"), os.path.join(CSRC, "proj_kerne
            os.path.join(CSRC, "proj_aux.cuh"), os.path.join(CSRC, "proj_launch.h"),
            os.path.join(CSRC, "proj_host.h"), os.path.join(CSRC, "q4_internal.h"),
            os.path.join(CSRC, "q4_kernels.cuh"), os.path.join(CSRC, "kv_internal.h"),
-           os.path.join(CSRC, "kv_kernels.cuh"), os.path.join(INCLUDE, "proj.h")]
+           os.path.join(CSRC, "kv_append.cuh"), os.path.join(CSRC, "kv_attend.cuh"),
+           os.path.join(INCLUDE, "proj.h")]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]

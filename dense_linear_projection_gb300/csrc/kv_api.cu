@@ -5,8 +5,9 @@
 #include <cmath>
 #include <new>
 
+#include "kv_append.cuh"
+#include "kv_attend.cuh"
 #include "kv_internal.h"
-#include "kv_kernels.cuh"
 #include "proj.h"
 #include "proj_host.h"
 
@@ -16,8 +17,12 @@ struct proj_kv_s {
     proj_kv_desc_t d{};
     int sm_count = 0;
     int elem = 2;  // bytes of a cache element
-    void *scratch = nullptr;
+    int chunk_heads = 0, chunks = 0;  // rows of a key head: query heads of each, and how many
+    int grid = 0;                     // CTAs of an attention launch at most
+    void *scratch = nullptr;          // status word, counters, partial results
     int *status = nullptr;
+    uint32_t *counters = nullptr;
+    float *partials = nullptr;
 };
 
 namespace {
@@ -74,6 +79,35 @@ proj_status_t launch_append(const KvAppendParams &p, dim3 grid, bool interleaved
                : launch(dev::kv_append_kernel<kE4m3, false, false>, grid, t, 0, stream, p);
 }
 
+// The attention kernel's instance for a head width and a row's heads.
+using AttendKernel = void (*)(KvAttendParams);
+struct AttendInstance {
+    AttendKernel kernel;
+    int smem, per_sm, part;  // shared memory, CTAs an SM, floats of a partial result
+};
+
+template <bool kE4m3, int kDim, int kNT>
+AttendInstance instance_of() {
+    using Shape = dev::AttendShape<kE4m3, kDim, kNT>;
+    return {dev::kv_attend_kernel<kE4m3, kDim, kNT>, Shape::kSmem, Shape::kPerSm, Shape::kHeads * (kDim + 2)};
+}
+
+// Rows of at most 8 query heads, or 16 where the group is larger and the
+// accumulators of 16 fit the registers (heads up to 128 wide).
+template <bool kE4m3>
+AttendInstance instance_for(int head_dim, int chunk_heads) {
+    if (head_dim <= 64) return chunk_heads <= 8 ? instance_of<kE4m3, 64, 1>() : instance_of<kE4m3, 64, 2>();
+    if (head_dim <= 128) return chunk_heads <= 8 ? instance_of<kE4m3, 128, 1>() : instance_of<kE4m3, 128, 2>();
+    return instance_of<kE4m3, 256, 1>();
+}
+
+AttendInstance instance_for(const proj_kv_s *h) {
+    return h->d.kv_dtype == PROJ_E4M3 ? instance_for<true>(h->d.head_dim, h->chunk_heads)
+                                      : instance_for<false>(h->d.head_dim, h->chunk_heads);
+}
+
+size_t rounded(size_t bytes) { return (bytes + 255) / 256 * 256; }
+
 }  // namespace
 
 extern "C" {
@@ -102,14 +136,28 @@ proj_status_t proj_kv_create(proj_kv_handle_t *out, const proj_kv_desc_t *desc, 
     h->d = d;
     h->sm_count = prop.multiProcessorCount;
     h->elem = elem;
-    const size_t bytes = 256;
+    const int group = d.q_heads / d.kv_heads, most = d.head_dim <= 128 ? 16 : 8;
+    h->chunks = (group + most - 1) / most;
+    h->chunk_heads = (group + h->chunks - 1) / h->chunks;
+    const AttendInstance a = instance_for(h);
+    if (cudaFuncSetAttribute(a.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, a.smem) != cudaSuccess) {
+        cudaGetLastError();
+        delete h;
+        return PROJ_ERR_CUDA;
+    }
+    h->grid = h->sm_count * a.per_sm;
+    const size_t counters = rounded(static_cast<size_t>(d.max_sequences) * d.kv_heads * h->chunks * 4);
+    const size_t clear = 256 + counters;
+    const size_t bytes = clear + static_cast<size_t>(h->grid) * 2 * a.part * 4;
     if (dev_malloc(&h->scratch, bytes) != cudaSuccess) {
         cudaGetLastError();
         delete h;
         return PROJ_ERR_OUT_OF_MEMORY;
     }
     h->status = static_cast<int *>(h->scratch);
-    if (cudaMemsetAsync(h->scratch, 0, bytes, as_stream(stream)) != cudaSuccess ||
+    h->counters = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(h->scratch) + 256);
+    h->partials = reinterpret_cast<float *>(static_cast<uint8_t *>(h->scratch) + clear);
+    if (cudaMemsetAsync(h->scratch, 0, clear, as_stream(stream)) != cudaSuccess ||
         cudaStreamSynchronize(as_stream(stream)) != cudaSuccess) {
         cudaGetLastError();
         cudaFree(h->scratch);
@@ -208,9 +256,19 @@ proj_status_t proj_kv_attend(proj_kv_handle_t h, int64_t sequences, const void *
     p.out = static_cast<uint16_t *>(out);
     p.lse = lse;
     p.status = h->status;
-    const dim3 grid(static_cast<unsigned>((sequences * d.q_heads + 7) / 8));
-    return d.kv_dtype == PROJ_E4M3 ? launch(dev::kv_attend_kernel<true>, grid, 256, 0, stream, p)
-                                   : launch(dev::kv_attend_kernel<false>, grid, 256, 0, stream, p);
+    p.group = d.q_heads / d.kv_heads;
+    p.chunk_heads = h->chunk_heads;
+    p.chunks = h->chunks;
+    p.units = d.kv_heads * h->chunks;
+    p.partials = h->partials;
+    p.counters = h->counters;
+    // No more CTAs than there can be tiles (one where every length is zero).
+    int64_t tiles = (table_width * d.page_size + kKvTile - 1) / kKvTile;
+    if (window > 0 && window / kKvTile + 2 < tiles) tiles = window / kKvTile + 2;
+    const int64_t want = sequences * p.units * (tiles > 0 ? tiles : 1);
+    const AttendInstance a = instance_for(h);
+    return launch(a.kernel, dim3(static_cast<unsigned>(want < h->grid ? want : h->grid)), kKvThreads,
+                  static_cast<size_t>(a.smem), stream, p);
 }
 
 proj_status_t proj_kv_device_status(proj_kv_handle_t h, void *stream) {

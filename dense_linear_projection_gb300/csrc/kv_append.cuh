@@ -1,5 +1,4 @@
-// Device code of the paged key-value cache: append with the rotary position,
-// and attention of one new token of each sequence.
+// Device code of the paged key-value cache's append: rotary position and write.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -9,88 +8,6 @@
 
 namespace projgb {
 namespace dev {
-
-__device__ __forceinline__ float e4m3_to_float(uint8_t b) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)));
-}
-
-// Length of sequence b, checked against the page table.
-__device__ __forceinline__ int64_t checked_length(const KvCacheView &c, const int32_t *seq_lens, int64_t b,
-                                                  int *status) {
-    int64_t n = seq_lens[b];
-    const int64_t most = c.table_width * c.page_size;
-    if (n < 0 || n > most) {
-        atomicOr(status, kKvErrLength);
-        n = n < 0 ? 0 : most;
-    }
-    return n;
-}
-
-// Offset of a token's head in the cache, or -1 for a page outside it.
-__device__ __forceinline__ int64_t token_offset(const KvCacheView &c, int64_t b, int64_t t, int head, int *status) {
-    const int32_t page = c.table[b * c.table_width + t / c.page_size];
-    if (page < 0 || page >= c.num_pages) {
-        atomicOr(status, kKvErrPage);
-        return -1;
-    }
-    return page * c.page_stride + (t % c.page_size) * c.token_stride + head * c.head_stride;
-}
-
-template <bool kE4m3>
-__device__ __forceinline__ float cache_element(const void *cache, int64_t at) {
-    if constexpr (kE4m3)
-        return e4m3_to_float(static_cast<const uint8_t *>(cache)[at]);
-    else
-        return bf16_bits_to_float(static_cast<const uint16_t *>(cache)[at]);
-}
-
-// One warp per sequence and query head, one token at a time.
-template <bool kE4m3>
-__global__ void kv_attend_kernel(KvAttendParams p) {
-    griddep_launch_dependents();
-    griddep_wait();
-    const KvCacheView &c = p.cache;
-    const int lane = threadIdx.x & 31;
-    const int64_t row = blockIdx.x * static_cast<int64_t>(blockDim.x / 32) + threadIdx.x / 32;
-    if (row >= p.sequences * p.q_heads) return;
-    const int64_t b = row / p.q_heads;
-    const int h = static_cast<int>(row % p.q_heads), hk = h / (p.q_heads / c.kv_heads);
-    const float ks = p.k_scale ? p.k_scale[hk] : 1.f, vs = p.v_scale ? p.v_scale[hk] : 1.f;
-    constexpr int kPer = kKvMaxDim / 32;
-    float q[kPer], o[kPer];
-    for (int i = 0; i < kPer; ++i) {
-        const int d = lane + 32 * i;
-        q[i] = d < c.head_dim ? bf16_bits_to_float(p.q[b * p.q_stride + h * c.head_dim + d]) * p.scale * ks : 0.f;
-        o[i] = 0.f;
-    }
-    const int64_t n = checked_length(c, p.seq_lens, b, p.status);
-    float m = -INFINITY, l = 0.f;
-    for (int64_t t = p.window > 0 && n > p.window ? n - p.window : 0; t < n; ++t) {
-        const int64_t at = token_offset(c, b, t, hk, p.status);
-        if (at < 0) continue;
-        float s = 0.f;
-        for (int i = 0; i < kPer; ++i) {
-            const int d = lane + 32 * i;
-            if (d < c.head_dim) s += q[i] * cache_element<kE4m3>(p.k_cache, at + d);
-        }
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        const float top = fmaxf(m, s);
-        const float keep = m == -INFINITY ? 0.f : expf(m - top), w = expf(s - top);
-        l = l * keep + w;
-        m = top;
-        for (int i = 0; i < kPer; ++i) {
-            const int d = lane + 32 * i;
-            if (d < c.head_dim) o[i] = o[i] * keep + w * cache_element<kE4m3>(p.v_cache, at + d);
-        }
-    }
-    for (int i = 0; i < kPer; ++i) {
-        const int d = lane + 32 * i;
-        if (d < c.head_dim)
-            reinterpret_cast<__nv_bfloat16 *>(p.out)[b * p.out_stride + h * c.head_dim + d] =
-                __float2bfloat16_rn(l > 0.f ? o[i] / l * vs : 0.f);
-    }
-    if (p.lse && lane == 0) p.lse[row] = l > 0.f ? m + logf(l) : -INFINITY;
-}
 
 // Append.  A unit is 16 elements of one head of one token: eight rotary pairs
 // (kVec: two 16-byte loads, either 8 + 8 elements of the two halves or 16 in a

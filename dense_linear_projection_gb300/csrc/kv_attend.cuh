@@ -1,0 +1,626 @@
+// Device code of attention of one new token of each sequence over the paged
+// key-value cache.
+//
+// Mathematics.  For one sequence and one key head, the G query heads that share
+// it, and tokens t: x[t,h] = scale·log2(e)·q[h]·k[t];  with a running maximum m,
+// l = Σ 2^(x − m) and o = Σ 2^(x − m)·v[t].  Two parts (m, l, o), (m', l', o')
+// join with M = max(m, m'): l·2^(m − M) + l'·2^(m' − M), and o likewise; out =
+// o / l, lse = ln 2·(M + log2 l).
+//
+// What bounds it: the bytes of K and V, each read once for all G heads.  So
+//   * a warp works alone on 16 tokens at a time, with a ring of shared-memory
+//     stages of its own filled by 16-byte asynchronous copies, and waits for no
+//     other warp until its row ends;
+//   * both products are swapped: X[tokens, heads] = K·Qᵀ and Oᵀ[dim, heads] =
+//     Vᵀ·P, so K and V are the 16-row operand of the tensor-core step and the
+//     heads its 8 columns: a group of up to 8 heads costs one step per 16 tokens
+//     × 16 elements, and a wider group a second one on the same operand.
+//   * the tokens of all sequences and key heads, in tiles of kKvTile, form one
+//     line that the CTAs share evenly: CTA c takes tiles [c·T/C, (c+1)·T/C).  A
+//     row that several CTAs share is joined by the one that arrives last, in CTA
+//     order, from fp32 partial results in scratch.
+//
+// Precision: fp32 logits, weights and sums.  The weights enter the second
+// product as two 16-bit parts (high + low): in one bf16 part their rounding
+// would double the error of a bf16 output.  An e4m3 cache is converted to fp16
+// (exact); the queries then are fp16 too, scaled by a power of two per head so
+// that no bf16 query overflows or vanishes.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "kv_internal.h"
+#include "proj_kernel.cuh"
+
+namespace projgb {
+namespace dev {
+
+template <bool kE4m3, int kDim, int kNT>
+struct AttendShape {
+    static constexpr int kElem = kE4m3 ? 1 : 2;
+    static constexpr int kRow = kDim * kElem;         // bytes of a token's row in a stage
+    static constexpr int kChunks = kRow / 16;         // 16-byte chunks of a row
+    static constexpr int kStage = 2 * kKvStep * kRow;  // keys, then values
+    static constexpr int kHeads = 8 * kNT;
+    static constexpr int kJoin = kKvWarps * kHeads * kDim * 4;  // the warps' sums, fp32
+    static constexpr int kSmall = kKvWarps * kHeads * 8 + 64;   // their maxima and sums of weights; flags
+    // Two CTAs an SM (one for 256-wide heads): while one joins its warps, the
+    // other streams.
+    static constexpr int kPerSm = kDim > 128 ? 1 : 2;
+    static constexpr int kBudget = (kPerSm == 2 ? 113 : 226) * 1024 - kJoin - kSmall;
+    static constexpr int kFit = kBudget / (kKvWarps * kStage);
+    static constexpr int kStages = kFit > 8 ? 8 : kFit;
+    static constexpr int kSmem = kKvWarps * kStages * kStage + kJoin + kSmall;
+    static_assert(kStages >= 2, "a stage to read and one to fill");
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t to, const void *from, bool fill) {
+    // fill = false: no byte is read, the 16 bytes become zero.
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(fill ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// D += A·B: 16 rows, 8 columns, 16 deep.
+template <bool kHalf>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    if constexpr (kHalf)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+            "%2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, "
+            "%1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+    return h;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two weights as 16-bit high parts and what the high parts leave.
+template <bool kHalf>
+__device__ __forceinline__ void split2(float a, float b, uint32_t &high, uint32_t &low) {
+    if constexpr (kHalf) {
+        const __half2 h = __floats2half2_rn(a, b);
+        const float2 f = __half22float2(h);
+        const __half2 r = __floats2half2_rn(a - f.x, b - f.y);
+        high = *reinterpret_cast<const uint32_t *>(&h);
+        low = *reinterpret_cast<const uint32_t *>(&r);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        const float2 f = __bfloat1622float2(h);
+        const __nv_bfloat162 r = __floats2bfloat162_rn(a - f.x, b - f.y);
+        high = *reinterpret_cast<const uint32_t *>(&h);
+        low = *reinterpret_cast<const uint32_t *>(&r);
+    }
+}
+
+// Byte offset of chunk c of row r in an operand of a stage: the chunks of
+// eight consecutive rows at one column fall in eight different 16-byte banks.
+template <int kRow>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    if constexpr (kRow >= 128) return r * kRow + ((c ^ (r & 7)) << 4);
+    return r * kRow + ((c ^ ((r >> 1) & 3)) << 4);  // 64-byte rows, two to a 128-byte line
+}
+
+// A place on the line of tiles: sequence b, whose tiles begin at `base` and
+// number `tiles` for each of the `units` (key head, chunk of query heads).
+struct AttendCursor {
+    int64_t base = 0, tiles = 0;
+    int b = 0;
+    int low = 0, n = 0;  // the tokens attended are [low, n)
+};
+
+struct AttendSegment {
+    int unit, first, last;  // tokens [first, last) of the cursor's sequence; last <= n
+    int64_t row_begin;      // the row's first tile on the line
+};
+
+__device__ __forceinline__ void read_length(const KvAttendParams &p, int b, AttendCursor &c) {
+    const int64_t most = p.cache.table_width * p.cache.page_size;
+    int n = p.seq_lens[b];
+    if (n < 0 || n > most) {
+        atomicOr(p.status, kKvErrLength);
+        n = n < 0 ? 0 : static_cast<int>(most);
+    }
+    c.n = n;
+    c.low = p.window > 0 && n > p.window ? n - static_cast<int>(p.window) : 0;
+    c.tiles = (n - (c.low & ~(kKvStep - 1)) + kKvTile - 1) / kKvTile;
+}
+
+// Moves the cursor to the sequence that holds tile `pos` (which exists).
+__device__ __forceinline__ void seek(const KvAttendParams &p, AttendCursor &c, int64_t pos) {
+    while (pos >= c.base + c.tiles * p.units) {
+        c.base += c.tiles * p.units;
+        ++c.b;
+        read_length(p, c.b, c);
+    }
+}
+
+// The part of tile range [pos, end) that lies in pos's row.
+__device__ __forceinline__ AttendSegment segment_at(const KvAttendParams &p, const AttendCursor &c, int64_t pos,
+                                                    int64_t end) {
+    AttendSegment s;
+    s.unit = static_cast<int>((pos - c.base) / c.tiles);
+    s.row_begin = c.base + s.unit * c.tiles;
+    const int64_t k0 = pos - s.row_begin, k1 = end - s.row_begin < c.tiles ? end - s.row_begin : c.tiles;
+    const int start = c.low & ~(kKvStep - 1);
+    s.first = start + static_cast<int>(k0) * kKvTile;
+    s.last = k1 == c.tiles ? c.n : start + static_cast<int>(k1) * kKvTile;
+    return s;
+}
+
+template <bool kE4m3, int kDim, int kNT>
+__global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPerSm) kv_attend_kernel(KvAttendParams p) {
+    using Shape = AttendShape<kE4m3, kDim, kNT>;
+    constexpr int kHeads = Shape::kHeads, kStages = Shape::kStages, kRow = Shape::kRow;
+    constexpr int kSteps = kDim / 16;  // 16-wide steps over a head
+    extern __shared__ __align__(1024) uint8_t smem[];
+    griddep_launch_dependents();
+    const KvCacheView &cache = p.cache;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, j = lane & 3;
+    const uint32_t ring = smem_u32(smem) + warp * kStages * Shape::kStage;
+    float *join = reinterpret_cast<float *>(smem + kKvWarps * kStages * Shape::kStage);  // [warp][dim][head]
+    float *join_m = join + kKvWarps * kHeads * kDim;                                     // [warp][head]
+    float *join_l = join_m + kKvWarps * kHeads;
+    int *flag = reinterpret_cast<int *>(join_l + kKvWarps * kHeads);
+
+    // Chunks past head_dim stay zero: no copy ever writes them.
+    if (cache.head_dim < kDim) {
+        for (int at = tid * 16; at < kKvWarps * kStages * Shape::kStage; at += kKvThreads * 16)
+            *reinterpret_cast<uint4 *>(smem + at) = make_uint4(0u, 0u, 0u, 0u);
+        __syncthreads();
+    }
+    griddep_wait();
+
+    // The line of tiles: every thread sums a run of sequences, and a scan over
+    // the threads gives the total and where this CTA's first tile lies.
+    const int B = static_cast<int>(p.sequences);
+    const int run = (B + kKvThreads - 1) / kKvThreads;
+    AttendCursor cur;  // the warp's place in computing
+    int64_t pos, end, total, ctas;
+    {
+        int64_t *sums = reinterpret_cast<int64_t *>(join);  // [threads] inclusive, before the first join
+        int64_t mine = 0;
+        for (int b = tid * run; b < B && b < (tid + 1) * run; ++b) {
+            AttendCursor c;
+            read_length(p, b, c);
+            mine += c.tiles * p.units;
+        }
+        int64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t other = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += other;
+        }
+        sums[tid] = incl;
+        __syncthreads();
+        int64_t before = 0;
+        for (int w = 0; w < warp; ++w) before += sums[32 * w + 31];
+        __syncthreads();
+        sums[tid] = incl + before;
+        __syncthreads();
+        total = sums[kKvThreads - 1];
+        ctas = total < gridDim.x ? total : gridDim.x;  // those that have a tile: each at least one
+        pos = blockIdx.x < ctas ? total * blockIdx.x / ctas : total;
+        end = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : total;
+        int low = 0, high = kKvThreads - 1;  // first thread whose inclusive sum is past pos
+        while (low < high) {
+            const int mid = (low + high) / 2;
+            if (sums[mid] > pos)
+                high = mid;
+            else
+                low = mid + 1;
+        }
+        if (pos < end) {
+            cur.base = low > 0 ? sums[low - 1] : 0;
+            cur.b = low * run;
+            read_length(p, cur.b, cur);
+            seek(p, cur, pos);
+        }
+        __syncthreads();  // `sums` is the join buffer
+    }
+
+    // Sequences without tokens have no tiles: their rows are written here.
+    for (int b = blockIdx.x; b < B; b += gridDim.x) {
+        AttendCursor c;
+        read_length(p, b, c);
+        if (c.n > 0) continue;
+        for (int i = tid; i < p.q_heads * cache.head_dim; i += kKvThreads) p.out[b * p.out_stride + i] = 0;
+        if (p.lse)
+            for (int h = tid; h < p.q_heads; h += kKvThreads) p.lse[static_cast<int64_t>(b) * p.q_heads + h] = -INFINITY;
+    }
+    if (pos >= end) return;
+
+    // ---- loading: a cursor of its own, up to kStages - 1 steps ahead.
+    AttendCursor lcur = cur;
+    int64_t lpos = pos;
+    AttendSegment lseg = segment_at(p, lcur, lpos, end);
+    int ltok = lseg.first + warp * kKvStep;  // first token of the step to load next
+    bool lmore = true;
+    int64_t lhead = 0;  // the row's head in the cache
+    int lpage = -1;     // page of token ltok + lane (lanes 0..15), -1: not attended
+    int lplace = 0;
+    auto settle = [&]() {  // moves to the next step that exists and asks for its pages
+        while (ltok >= lseg.last) {
+            lpos += (lseg.last == lcur.n ? lcur.tiles - (lpos - lseg.row_begin)
+                                         : (lseg.last - (lcur.low & ~(kKvStep - 1))) / kKvTile - (lpos - lseg.row_begin));
+            if (lpos >= end) {
+                lmore = false;
+                return;
+            }
+            seek(p, lcur, lpos);
+            lseg = segment_at(p, lcur, lpos, end);
+            ltok = lseg.first + warp * kKvStep;
+        }
+        lhead = static_cast<int64_t>(lseg.unit / p.chunks) * cache.head_stride;
+        const int t = ltok + (lane & 15);
+        lpage = -1;
+        if (t >= lcur.low && t < lseg.last) {
+            const uint32_t q = static_cast<uint32_t>(t) / static_cast<uint32_t>(cache.page_size);
+            lplace = t - static_cast<int>(q) * cache.page_size;
+            lpage = __ldg(cache.table + lcur.b * cache.table_width + q);
+            if (lpage < 0 || lpage >= cache.num_pages) {
+                atomicOr(p.status, kKvErrPage);
+                lpage = -1;
+            }
+        }
+    };
+    settle();
+    uint32_t valid[kStages];  // tokens of each stage that are attended, a bit each
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) valid[s] = 0;
+    const int row_chunks = cache.head_dim * Shape::kElem / 16;
+    auto load = [&](int slot) {
+        uint32_t bits = 0;
+        if (lmore) {
+            const bool ok = lpage >= 0;
+            bits = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+            const int64_t offset =
+                ok ? lpage * cache.page_stride + lplace * cache.token_stride + lhead : 0;
+            const uint32_t to = ring + slot * Shape::kStage;
+            const uint8_t *kc = static_cast<const uint8_t *>(p.k_cache), *vc = static_cast<const uint8_t *>(p.v_cache);
+            constexpr int kRowsAtOnce = 32 / (Shape::kChunks < 32 ? Shape::kChunks : 32);
+#pragma unroll
+            for (int i = 0; i < kKvStep / kRowsAtOnce; ++i) {
+                const int r = i * kRowsAtOnce + lane / Shape::kChunks, c = lane % Shape::kChunks;
+                const int64_t at = __shfl_sync(0xffffffffu, offset, r) * Shape::kElem + c * 16;
+                const bool fill = (bits >> r) & 1u;
+                if (c < row_chunks) {
+                    const uint32_t d = to + chunk_at<kRow>(r, c);
+                    cp_async16(d, kc + (fill ? at : 0), fill);
+                    cp_async16(d + kKvStep * kRow, vc + (fill ? at : 0), fill);
+                }
+            }
+            ltok += kKvWarps * kKvStep;
+            settle();
+        }
+#pragma unroll
+        for (int s = 0; s < kStages; ++s)
+            if (s == slot) valid[s] = bits;
+        cp_async_commit();
+    };
+    int slot_in = 0, slot = 0;
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) load(slot_in++);
+
+    // ---- computing, row by row.
+    while (pos < end) {
+        seek(p, cur, pos);
+        const AttendSegment seg = segment_at(p, cur, pos, end);
+        const int hk = seg.unit / p.chunks, chunk = seg.unit % p.chunks;
+        const int head0 = hk * p.group + chunk * p.chunk_heads;
+        const int heads = min(p.chunk_heads, p.group - chunk * p.chunk_heads);
+        const int tiles = static_cast<int>((seg.last == cur.n ? cur.tiles : (seg.last - (cur.low & ~(kKvStep - 1))) / kKvTile) -
+                                           (pos - seg.row_begin));
+
+        // Queries as the second operand: column (head) g, rows (elements) of lane j.
+        uint32_t qf[kNT][kSteps][2];
+        float factor[kNT][2];  // logit to exponent of two, of this lane's heads 2j, 2j + 1
+#pragma unroll
+        for (int t = 0; t < kNT; ++t) {
+            const uint16_t *q = p.q + cur.b * p.q_stride + static_cast<int64_t>(head0 + 8 * t + g) * cache.head_dim;
+            const bool there = 8 * t + g < heads;
+            const float scale = p.scale * 1.4426950408889634f;
+            if constexpr (!kE4m3) {
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    const bool in = there && 16 * k < cache.head_dim;
+                    qf[t][k][0] = in ? *reinterpret_cast<const uint32_t *>(q + 16 * k + 2 * j) : 0u;
+                    qf[t][k][1] = in ? *reinterpret_cast<const uint32_t *>(q + 16 * k + 8 + 2 * j) : 0u;
+                }
+                factor[t][0] = factor[t][1] = scale;
+            } else {
+                // Elements 4j .. 4j + 3 of each 16, as the keys come (below).
+                uint2 raw[kSteps];
+                uint32_t top = 0;  // largest magnitude, as bf16 bits
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    raw[k] = there && 16 * k < cache.head_dim ? *reinterpret_cast<const uint2 *>(q + 16 * k + 4 * j)
+                                                              : make_uint2(0u, 0u);
+                    top = max(max(top, raw[k].x & 0x7fffu), (raw[k].x >> 16) & 0x7fffu);
+                    top = max(max(top, raw[k].y & 0x7fffu), (raw[k].y >> 16) & 0x7fffu);
+                }
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // 2^-e brings the largest to [1, 2): e within ±126 keeps both powers normal numbers.
+                const int e = min(126, max(-126, static_cast<int>(top >> 7) - 127));
+                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    const uint32_t w[2] = {raw[k].x, raw[k].y};
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const __half2 h = __floats2half2_rn(__uint_as_float(w[i] << 16) * down,
+                                                            __uint_as_float(w[i] & 0xffff0000u) * down);
+                        qf[t][k][i] = *reinterpret_cast<const uint32_t *>(&h);
+                    }
+                }
+                const float up = scale * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) *
+                                 (p.k_scale ? p.k_scale[hk] : 1.f);
+                factor[t][0] = __shfl_sync(0xffffffffu, up, 8 * j);
+                factor[t][1] = __shfl_sync(0xffffffffu, up, 8 * j + 4);
+            }
+        }
+
+        float m[kNT][2], l[kNT][2], o[kNT][kSteps][4];
+#pragma unroll
+        for (int t = 0; t < kNT; ++t) {
+            m[t][0] = m[t][1] = -INFINITY;
+            l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+            for (int d = 0; d < kSteps; ++d) o[t][d][0] = o[t][d][1] = o[t][d][2] = o[t][d][3] = 0.f;
+        }
+
+        for (int tok = seg.first + warp * kKvStep; tok < seg.last; tok += kKvWarps * kKvStep) {
+            cp_async_wait<kStages - 2>();
+            __syncwarp();
+            uint32_t bits = 0;
+#pragma unroll
+            for (int s = 0; s < kStages; ++s)
+                if (s == slot) bits = valid[s];
+            load(slot_in == kStages ? 0 : slot_in);
+            slot_in = slot_in == kStages ? 1 : slot_in + 1;
+            const uint32_t ks = ring + slot * Shape::kStage, vs = ks + kKvStep * kRow;
+            slot = slot + 1 == kStages ? 0 : slot + 1;
+
+            float x[kNT][4];
+#pragma unroll
+            for (int t = 0; t < kNT; ++t) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
+            if constexpr (!kE4m3) {
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    uint32_t a[4];
+                    ldsm_x4(a, ks + chunk_at<kRow>(lane & 15, 2 * k + (lane >> 4)));
+#pragma unroll
+                    for (int t = 0; t < kNT; ++t) mma16816<false>(x[t], a[0], a[1], a[2], a[3], qf[t][k][0], qf[t][k][1]);
+                }
+            } else {
+                // A 16-byte chunk holds 16 elements: lane j of a row receives
+                // elements 4j .. 4j + 3, so the first pair stands at the
+                // step's rows 2j, 2j + 1 and the second at rows 2j + 8, + 9.
+#pragma unroll
+                for (int k = 0; k < kSteps; k += 2) {
+                    uint32_t a[4];
+                    ldsm_x4(a, ks + chunk_at<kRow>(lane & 15, k + (lane >> 4)));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t up = a[2 * i], dn = a[2 * i + 1];
+                        const uint32_t a0 = e4m3x2_to_half2(up), a2 = e4m3x2_to_half2(up >> 16);
+                        const uint32_t a1 = e4m3x2_to_half2(dn), a3 = e4m3x2_to_half2(dn >> 16);
+#pragma unroll
+                        for (int t = 0; t < kNT; ++t)
+                            mma16816<true>(x[t], a0, a1, a2, a3, qf[t][k + i][0], qf[t][k + i][1]);
+                    }
+                }
+            }
+
+            // x: tokens g (0, 1) and g + 8 (2, 3), heads 2j and 2j + 1.
+            uint32_t high[kNT][2], low[kNT][2];
+#pragma unroll
+            for (int t = 0; t < kNT; ++t) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[t][i] *= factor[t][i & 1];
+                    if (bits != 0xffffu && !((bits >> (g + 8 * (i >> 1))) & 1u)) x[t][i] = -INFINITY;
+                }
+                float keep[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float top = fmaxf(x[t][h], x[t][2 + h]);
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                    top = fmaxf(top, m[t][h]);
+                    const float base = top == -INFINITY ? 0.f : top;  // no token yet: every weight is 0
+                    keep[h] = exp2_fast(m[t][h] - base);
+                    m[t][h] = top;
+                    x[t][h] = exp2_fast(x[t][h] - base);
+                    x[t][2 + h] = exp2_fast(x[t][2 + h] - base);
+                    l[t][h] = l[t][h] * keep[h] + x[t][h] + x[t][2 + h];
+                }
+                if (__any_sync(0xffffffffu, keep[0] != 1.f || keep[1] != 1.f)) {
+#pragma unroll
+                    for (int d = 0; d < kSteps; ++d) {
+                        o[t][d][0] *= keep[0];
+                        o[t][d][1] *= keep[1];
+                        o[t][d][2] *= keep[0];
+                        o[t][d][3] *= keep[1];
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t hi, lo;
+                    split2<kE4m3>(x[t][2 * i], x[t][2 * i + 1], hi, lo);
+                    high[t][i] = transpose8x8(hi);
+                    low[t][i] = transpose8x8(lo);
+                }
+            }
+            if constexpr (!kE4m3) {
+#pragma unroll
+                for (int d = 0; d < kSteps; ++d) {
+                    uint32_t a[4];
+                    ldsm_x4_t(a, vs + chunk_at<kRow>((lane & 7) + ((lane >> 4) << 3), 2 * d + ((lane >> 3) & 1)));
+#pragma unroll
+                    for (int t = 0; t < kNT; ++t) {
+                        mma16816<false>(o[t][d], a[0], a[1], a[2], a[3], high[t][0], high[t][1]);
+                        mma16816<false>(o[t][d], a[0], a[1], a[2], a[3], low[t][0], low[t][1]);
+                    }
+                }
+            } else {
+                // Transposed in pairs of elements: a lane receives elements
+                // 2g, 2g + 1 of tokens 2j, 2j + 1.  Rows 0..7 of the step take
+                // the even elements, rows 8..15 the odd ones.
+#pragma unroll
+                for (int d = 0; d < kSteps; d += 2) {
+                    uint32_t a[4];
+                    ldsm_x4_t(a, vs + chunk_at<kRow>((lane & 7) + (((lane >> 3) & 1) << 3), d + (lane >> 4)));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t lo8 = __byte_perm(a[2 * i], 0, 0x3120), hi8 = __byte_perm(a[2 * i + 1], 0, 0x3120);
+                        const uint32_t a0 = e4m3x2_to_half2(lo8), a1 = e4m3x2_to_half2(lo8 >> 16);
+                        const uint32_t a2 = e4m3x2_to_half2(hi8), a3 = e4m3x2_to_half2(hi8 >> 16);
+#pragma unroll
+                        for (int t = 0; t < kNT; ++t) {
+                            mma16816<true>(o[t][d + i], a0, a1, a2, a3, high[t][0], high[t][1]);
+                            mma16816<true>(o[t][d + i], a0, a1, a2, a3, low[t][0], low[t][1]);
+                        }
+                    }
+                }
+            }
+        }
+
+        // Join the warps.
+#pragma unroll
+        for (int t = 0; t < kNT; ++t) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int s = 4; s < 32; s <<= 1) l[t][h] += __shfl_xor_sync(0xffffffffu, l[t][h], s);
+                if (g == 0) {
+                    join_m[warp * kHeads + 8 * t + 2 * j + h] = m[t][h];
+                    join_l[warp * kHeads + 8 * t + 2 * j + h] = l[t][h];
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < kSteps; ++d) {
+                float *to = join + warp * kHeads * kDim + 8 * t + 2 * j;
+                const int d0 = 16 * d + (kE4m3 ? 2 * g : g), d1 = 16 * d + (kE4m3 ? 2 * g + 1 : g + 8);
+                *reinterpret_cast<float2 *>(to + d0 * kHeads) = make_float2(o[t][d][0], o[t][d][1]);
+                *reinterpret_cast<float2 *>(to + d1 * kHeads) = make_float2(o[t][d][2], o[t][d][3]);
+            }
+        }
+        __syncthreads();
+        constexpr int kPer = kHeads * kDim / kKvThreads, kDimStep = kKvThreads / kHeads;
+        const int h = tid % kHeads, d0 = tid / kHeads;
+        float M = -INFINITY, L = 0.f, w[kKvWarps], acc[kPer];
+#pragma unroll
+        for (int i = 0; i < kKvWarps; ++i) M = fmaxf(M, join_m[i * kHeads + h]);
+        const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int i = 0; i < kKvWarps; ++i) {
+            w[i] = exp2_fast(join_m[i * kHeads + h] - base);
+            L += w[i] * join_l[i * kHeads + h];
+        }
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            acc[k] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kKvWarps; ++i)
+                acc[k] += w[i] * join[(i * kDim + d0 + k * kDimStep) * kHeads + h];
+        }
+
+        bool write = true;
+        if (tiles != cur.tiles) {
+            // Other CTAs own the rest of the row: leave this part in scratch,
+            // and join all parts if the others are there already.
+            constexpr int kPart = kHeads * (kDim + 2);
+            const int64_t C = ctas, T = total;
+            const int64_t row_end = seg.row_begin + cur.tiles;
+            const int64_t c0 = ((seg.row_begin + 1) * C - 1) / T, c1 = (row_end * C - 1) / T;  // first and last owner
+            const int64_t c0_slot = T * c0 / C < seg.row_begin ? 1 : 0;  // the row is the last of its first owner's
+            const int64_t mine = blockIdx.x * int64_t(2) + (blockIdx.x == c0 ? c0_slot : 0);
+            float *part = p.partials + mine * kPart;
+            if (d0 == 0) {
+                __stcg(part + h, M);
+                __stcg(part + kHeads + h, L);
+            }
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) __stcg(part + (2 + d0 + k * kDimStep) * kHeads + h, acc[k]);
+            __threadfence();
+            __syncthreads();
+            uint32_t *counter = p.counters + static_cast<int64_t>(cur.b) * p.units + seg.unit;
+            if (tid == 0) *flag = atomicAdd(counter, 1u) == static_cast<uint32_t>(c1 - c0);
+            __syncthreads();
+            write = *flag != 0;
+            if (write) {
+                __threadfence();
+                if (tid == 0) *counter = 0;
+                M = -INFINITY;
+                for (int64_t c = c0; c <= c1; ++c)
+                    M = fmaxf(M, __ldcg(p.partials + (2 * c + (c == c0 ? c0_slot : 0)) * kPart + h));
+                const float all = M == -INFINITY ? 0.f : M;
+                L = 0.f;
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+                for (int64_t c = c0; c <= c1; ++c) {
+                    const float *from = p.partials + (2 * c + (c == c0 ? c0_slot : 0)) * kPart;
+                    const float f = exp2_fast(__ldcg(from + h) - all);
+                    L += f * __ldcg(from + kHeads + h);
+#pragma unroll
+                    for (int k = 0; k < kPer; ++k) acc[k] += f * __ldcg(from + (2 + d0 + k * kDimStep) * kHeads + h);
+                }
+            }
+        }
+        if (write && h < heads) {
+            const float by = (L > 0.f ? 1.f / L : 0.f) * (kE4m3 && p.v_scale ? p.v_scale[hk] : 1.f);
+            __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(p.out) + cur.b * p.out_stride +
+                                 static_cast<int64_t>(head0 + h) * cache.head_dim;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k)
+                if (d0 + k * kDimStep < cache.head_dim) out[d0 + k * kDimStep] = __float2bfloat16_rn(acc[k] * by);
+            if (p.lse && d0 == 0)
+                p.lse[static_cast<int64_t>(cur.b) * p.q_heads + head0 + h] =
+                    L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        }
+        __syncthreads();  // the join buffer and the flag are free again
+        pos += tiles;
+    }
+    cp_async_wait<0>();
+}
+
+}  // namespace dev
+}  // namespace projgb

@@ -9,6 +9,10 @@
 namespace projgb {
 
 constexpr int kKvMaxDim = 256;
+constexpr int kKvWarps = 4;                        // warps of an attention CTA
+constexpr int kKvThreads = 32 * kKvWarps;
+constexpr int kKvStep = 16;                        // tokens a warp takes at a time
+constexpr int kKvTile = kKvWarps * kKvStep;        // unit of the work shared between CTAs
 
 // Bits of the cache handle's status word: what a kernel found out of range.
 constexpr int kKvErrPosition = 1 << 0;  // position past the page table or the rope table
@@ -53,6 +57,12 @@ struct KvAttendParams {
     int64_t window;
     float scale;
     int32_t q_heads;
+    int32_t group;        // query heads of a key head
+    int32_t chunk_heads;  // of which a row takes this many at most
+    int32_t chunks;       // rows of a key head
+    int32_t units;        // kv_heads · chunks: rows of a sequence
+    float *partials;      // [CTA][first, last row][2 + dim][heads]
+    uint32_t *counters;   // [sequence][unit], zero between runs
     uint16_t *out;
     float *lse;
     int *status;
