@@ -20,7 +20,7 @@ SOURCES = ["proj_api.cu", "planner.cpp", "kernel_tc_lean.cu", "kernel_tc_fused.c
            "kernel_tc_pair_fused.cu", "q4_api.cu", "kv_api.cu"]
 HEADERS = [os.path.join(CSRC, "proj_internal.h"), os.path.join(CSRC, "proj_kernel.cuh"),
            os.path.join(CSRC, "proj_aux.cuh"), os.path.join(CSRC, "proj_launch.h"),
-           os.path.join(CSRC, "proj_host.h"), os.path.join(CSRC, "q4_internal.h"),
+           os.path.join(CSRC, "proj_host.h"), os.path.join(CSRC, "proj_warp.cuh"), os.path.join(CSRC, "q4_internal.h"),
            os.path.join(CSRC, "q4_kernels.cuh"), os.path.join(CSRC, "kv_internal.h"),
            os.path.join(CSRC, "kv_append.cuh"), os.path.join(CSRC, "kv_attend.cuh"),
            os.path.join(INCLUDE, "proj.h")]

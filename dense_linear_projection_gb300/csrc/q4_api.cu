@@ -31,6 +31,31 @@ int pack_blocks(int64_t items, int sm_count) {
     return static_cast<int>(want < int64_t(sm_count) * 16 ? want : int64_t(sm_count) * 16);
 }
 
+using Q4Kernel = void (*)(Q4Params);
+struct Q4Instance {
+    Q4Kernel kernel;
+    int row_tiles, k_steps, red;  // of a CTA; bytes of its join
+};
+
+template <int kNT>
+Q4Instance instance_nt(int64_t group, bool zeros) {
+    using Tile = dev::Q4Tile<kNT>;
+    Q4Kernel k;
+    if (group == 128)
+        k = zeros ? dev::q4_kernel<kNT, 1, true> : dev::q4_kernel<kNT, 1, false>;
+    else if (group == 64)
+        k = zeros ? dev::q4_kernel<kNT, 2, true> : dev::q4_kernel<kNT, 2, false>;
+    else
+        k = zeros ? dev::q4_kernel<kNT, 4, true> : dev::q4_kernel<kNT, 4, false>;
+    return {k, Tile::kRT, Tile::kKW, Tile::kRed};
+}
+
+Q4Instance instance_for(int64_t M, int64_t group, bool zeros) {
+    return M <= 8 ? instance_nt<1>(group, zeros) : M <= 16 ? instance_nt<2>(group, zeros) : instance_nt<4>(group, zeros);
+}
+
+constexpr int kSmemMost = 100 * 1024;
+
 }  // namespace
 
 extern "C" {
@@ -60,6 +85,12 @@ proj_status_t proj_q4_create(proj_q4_handle_t *out, int64_t max_tokens, int64_t 
     if (cudaGetDevice(&device) != cudaSuccess || cudaGetDeviceProperties(&prop, device) != cudaSuccess)
         return PROJ_ERR_CUDA;
     if (prop.major != 10 || prop.minor != 3) return PROJ_ERR_UNSUPPORTED;  // built for sm_103a
+    for (int64_t m = 8; m <= kQ4MaxTokens; m *= 2)
+        if (cudaFuncSetAttribute(instance_for(m, group, has_zeros != 0).kernel,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) != cudaSuccess) {
+            cudaGetLastError();
+            return PROJ_ERR_CUDA;
+        }
     proj_q4_s *h = new (std::nothrow) proj_q4_s();
     if (!h) return PROJ_ERR_OUT_OF_MEMORY;
     h->max_tokens = max_tokens;
@@ -109,9 +140,9 @@ proj_status_t proj_q4_run(proj_q4_handle_t h, int64_t M, const void *X, const vo
     p.M = M;
     p.N = h->N;
     p.K = h->K;
+    p.row_tiles = h->shape.row_tiles;
     p.k_blocks = h->shape.k_blocks;
     p.groups_padded = h->shape.groups_padded;
-    p.group = static_cast<int32_t>(h->group);
     p.y_f32 = h->y_dtype == PROJ_F32;
     p.X = static_cast<const uint16_t *>(X);
     p.codes = reinterpret_cast<const uint4 *>(at);
@@ -119,9 +150,42 @@ proj_status_t proj_q4_run(proj_q4_handle_t h, int64_t M, const void *X, const vo
     p.zeros = h->has_zeros ? at + h->shape.codes_bytes + h->shape.scales_bytes : nullptr;
     p.bias = static_cast<const uint16_t *>(bias);
     p.Y = Y;
-    const dim3 grid(static_cast<unsigned>((h->N + 7) / 8), static_cast<unsigned>(M < 32 ? M : 32));
-    dev::q4_kernel<<<grid, 256, 0, as_stream(stream)>>>(p);
-    return cudaGetLastError() == cudaSuccess ? PROJ_OK : PROJ_ERR_CUDA;
+
+    const Q4Instance q = instance_for(M, h->group, h->has_zeros != 0);
+    const int64_t tiles = (p.row_tiles + q.row_tiles - 1) / q.row_tiles;
+    const int64_t passes = (M + kQ4MaxTokens - 1) / kQ4MaxTokens;
+    // CTAs of one K range: enough that about three CTAs stand on every SM and
+    // share the memory's bandwidth evenly, while every warp has a step.
+    const int64_t steps = (p.k_blocks + 1) / 2;
+    int64_t splits = 3 * int64_t(h->sm_count) / tiles;
+    if (splits > steps / q.k_steps) splits = steps / q.k_steps;
+    p.splits = static_cast<int32_t>(splits < 1 ? 1 : splits > kQ4MaxSplits ? kQ4MaxSplits : splits);
+    const int tokens = static_cast<int>(M < kQ4MaxTokens ? M : kQ4MaxTokens);
+    const int groups = static_cast<int>(128 / h->group);
+    const int stage = kQ4Warps * (4096 + groups * (128 + (h->has_zeros ? 32 : 0))) + q.k_steps * tokens * kQ4XPitch;
+    p.stages = 3 * stage <= 56 * 1024 ? 3 : 2;
+    int smem = p.stages * stage;
+    if (smem < q.red) smem = q.red;
+
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.splits), static_cast<unsigned>(passes));
+    cfg.blockDim = dim3(kQ4Threads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = as_stream(stream);
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.splits);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.splits > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, q.kernel, p) != cudaSuccess) {
+        cudaGetLastError();
+        return PROJ_ERR_CUDA;
+    }
+    return PROJ_OK;
 }
 
 proj_status_t proj_q4_destroy(proj_q4_handle_t h) {

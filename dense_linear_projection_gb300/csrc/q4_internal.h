@@ -29,6 +29,11 @@
 namespace projgb {
 
 constexpr int kQ4TileRows = 64;
+constexpr int kQ4Warps = 4, kQ4Threads = 32 * kQ4Warps;
+constexpr int kQ4MaxTokens = 32;  // tokens of one pass over the weights
+constexpr int kQ4MaxSplits = 8;   // CTAs of a cluster that share a K range (the portable cluster size)
+constexpr int kQ4XPitch = 320;    // bytes between tokens of X in a stage: 128 K, and 64 bytes that
+                                  // put the next token's 16-byte chunks on the other banks
 
 PROJ_HD int q4_k_of(int j, int i) { return (i >> 1) * 32 + j * 8 + (i & 1) * 4; }
 
@@ -50,8 +55,10 @@ inline Q4Shape q4_shape(int64_t N, int64_t K, int64_t group, bool has_zeros) {
 }
 
 struct Q4Params {
-    int64_t M, N, K, k_blocks, groups_padded;
-    int32_t group, y_f32;
+    int64_t M, N, K, row_tiles, k_blocks, groups_padded;
+    int32_t y_f32;
+    int32_t splits;  // CTAs of a cluster
+    int32_t stages;  // of the ring: 2, 3 or 4
     const uint16_t *X;
     const uint4 *codes;
     const uint32_t *scales;

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "proj_kernel.cuh"
+#include "proj_warp.cuh"
 #include "q4_internal.h"
 
 namespace projgb {
@@ -60,44 +61,259 @@ __global__ void q4_pack_scales_kernel(const uint16_t *scales, const uint8_t *zer
     }
 }
 
-// One warp per weight row and token.
-__global__ void q4_kernel(Q4Params p) {
+// ---- the projection
+//
+// Mathematics: Y[m,n] = Σ_g s[n,g]·Σ_{k in g} x[m,k]·(q[n,k] − z[n,g]).  The
+// bf16 number 16 + q comes from two bit operations on the packed word and
+// (16 + q) − (16 + z) is exact, so the tensor core multiplies X by exact
+// integers; a group's fp32 sum is then scaled into the row's fp32 sum.
+//
+// The product is swapped (weight rows are the 16-row operand, up to 8·kNT
+// tokens its columns).  What bounds it is the stream of codes, and for small
+// token counts the instructions that turn a code into an operand: about 11 per
+// 8 codes of a lane.  A warp owns 64 rows × 128 K at a time, in a ring of
+// shared-memory stages filled by 16-byte asynchronous copies.  A CTA of four
+// warps covers kRT row tiles × kKW K steps (more tokens: more rows to a CTA,
+// since the CTA's copies of X grow with them); the S CTAs of a cluster share the
+// K range of the same rows.  Sums join in a fixed order: the kKW warps in shared
+// memory, then the cluster's CTAs through distributed shared memory.
+template <int kNT>
+struct Q4Tile {
+    static constexpr int kRT = kNT == 1 ? 1 : 2;  // row tiles of a CTA
+    static constexpr int kKW = kQ4Warps / kRT;    // K steps at a time
+    static constexpr int kPitch = kRT * 64 + 4;   // floats of a token's rows while joining: conflict-free
+    static constexpr int kRed = kKW * 8 * kNT * kPitch * 4;
+};
+
+__device__ __forceinline__ uint32_t bf16x2_sub(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t at) {
+    uint32_t v;
+    asm volatile("{\n\t.reg .u8 b;\n\tld.shared.u8 b, [%1];\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
+// kGroups: groups of a 128-wide K step (1, 2 or 4).
+template <int kNT, int kGroups, bool kZeros>
+__global__ void __launch_bounds__(kQ4Threads, kNT == 1 ? 4 : kNT == 2 ? 3 : 2) q4_kernel(const Q4Params p) {
+    using Tile = Q4Tile<kNT>;
+    constexpr int kRT = Tile::kRT, kKW = Tile::kKW;
+    extern __shared__ __align__(128) uint8_t smem[];
     griddep_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rt = warp % kRT, kw = warp / kRT;
+    const int g = lane >> 2, j = lane & 3;
+    const int rank = static_cast<int>(blockIdx.x % p.splits);
+    const int64_t tile0 = blockIdx.x / p.splits * kRT;  // the CTA's first row tile
+    const int64_t tile = tile0 + rt;
+    const bool rows_there = tile < p.row_tiles;
+    const int64_t m0 = blockIdx.y * int64_t(kQ4MaxTokens);
+    const int M = static_cast<int>(p.M - m0 < kQ4MaxTokens ? p.M - m0 : kQ4MaxTokens);
+
+    // A stage: each warp's codes, scales and zero points, then X for each K step.
+    constexpr int kScaleBytes = kGroups * 128, kZeroBytes = kZeros ? kGroups * 32 : 0;
+    constexpr int kWarpBytes = 4096 + kScaleBytes + kZeroBytes;
+    const int x_bytes = M * kQ4XPitch;
+    const int stage_bytes = kQ4Warps * kWarpBytes + kKW * x_bytes;
+    const uint32_t base = smem_u32(smem);
+    const uint32_t my_w = base + warp * kWarpBytes, my_x = base + kQ4Warps * kWarpBytes + kw * x_bytes;
+
+    const int64_t steps = (p.k_blocks + 1) / 2;
+    const int64_t step0 = steps * rank / p.splits + kw, step1 = steps * (rank + 1) / p.splits;
+
+    float acc[4][kNT][4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int t = 0; t < kNT; ++t) acc[r][t][0] = acc[r][t][1] = acc[r][t][2] = acc[r][t][3] = 0.f;
+
+    const uint8_t *codes = reinterpret_cast<const uint8_t *>(p.codes) + tile * p.k_blocks * 2048;
+    const uint8_t *scales = reinterpret_cast<const uint8_t *>(p.scales) + tile * p.groups_padded * 128;
+    const uint8_t *zeros = p.zeros + (kZeros ? tile * p.groups_padded * 32 : 0);
+    const uint8_t *x = reinterpret_cast<const uint8_t *>(p.X + m0 * p.K);
+    auto load = [&](int64_t step, int slot) {
+        if (step < step1) {
+            const uint32_t w = my_w + slot * stage_bytes, xs = my_x + slot * stage_bytes;
+            if (rows_there) {
+                const int blocks = step * 2 + 1 < p.k_blocks ? 8 : 4;  // 512-byte blocks that exist
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    cp_async16(w + i * 512 + lane * 16, codes + step * 4096 + (i < blocks ? i * 512 + lane * 16 : 0), i < blocks);
+                if (lane < kGroups * 8) {
+                    const bool in = step * kGroups + lane / 8 < p.groups_padded;
+                    cp_async16(w + 4096 + lane * 16, scales + (in ? step * kScaleBytes + lane * 16 : 0), in);
+                }
+                if (kZeros && lane < kGroups * 2) {
+                    const bool in = step * kGroups + lane / 2 < p.groups_padded;
+                    cp_async16(w + 4096 + kScaleBytes + lane * 16, zeros + (in ? step * kZeroBytes + lane * 16 : 0), in);
+                }
+            }
+            for (int at = rt * 32 + lane; at < M * 16; at += 32 * kRT) {
+                const int m = at >> 4, c = at & 15;
+                const bool in = step * 128 + c * 8 < p.K;
+                cp_async16(xs + m * kQ4XPitch + c * 16, x + (in ? (m * p.K + step * 128 + c * 8) * 2 : 0), in);
+            }
+        }
+        cp_async_commit();
+    };
+    // The warps that share a step's X.
+    auto meet = [&]() {
+        if constexpr (kRT == 1)
+            __syncwarp();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + kw), "n"(32 * kRT) : "memory");
+    };
+
     griddep_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t n = blockIdx.x * static_cast<int64_t>(blockDim.x / 32) + threadIdx.x / 32;
-    if (n >= p.N) return;
-    const int64_t tile = n / kQ4TileRows;
-    const int rb = static_cast<int>(n % kQ4TileRows) / 16, half = static_cast<int>(n % 16) / 8, r = static_cast<int>(n % 8);
-    for (int64_t m = blockIdx.y; m < p.M; m += gridDim.y) {
-        float acc = 0.f;
-        for (int64_t kb = lane; kb < p.k_blocks; kb += 32) {
-            for (int j = 0; j < 4; ++j) {
-                const uint4 v = p.codes[((tile * p.k_blocks + kb) * 4 + rb) * 32 + r * 4 + j];
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const int stages = p.stages;
+    for (int s = 0; s < stages - 1; ++s) load(step0 + s * kKW, s);
+    int slot = 0, slot_in = stages - 1;
+    for (int64_t step = step0; step < step1; step += kKW) {
+        if (stages == 2)
+            cp_async_wait<0>();
+        else if (stages == 3)
+            cp_async_wait<1>();
+        else
+            cp_async_wait<2>();
+        meet();
+        load(step + (stages - 1) * kKW, slot_in);
+        if (++slot_in == stages) slot_in = 0;
+        const uint32_t w = my_w + slot * stage_bytes, xs = my_x + slot * stage_bytes;
+        if (++slot == stages) slot = 0;
+
+        float part[4][kNT][4];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            // X as the second operand: column (token) g; columns past M repeat the last token and are dropped.
+            uint32_t b[kNT][8];
+#pragma unroll
+            for (int t = 0; t < kNT; ++t) {
+                const uint32_t at = xs + min(8 * t + g, M - 1) * kQ4XPitch + kb * 128 + j * 16;
+                const uint4 lo = lds128(at), hi = lds128(at + 64);
+                b[t][0] = lo.x, b[t][1] = lo.y, b[t][2] = lo.z, b[t][3] = lo.w;
+                b[t][4] = hi.x, b[t][5] = hi.y, b[t][6] = hi.z, b[t][7] = hi.w;
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const uint4 v = lds128(w + kb * 2048 + r * 512 + lane * 16);
+                const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int64_t k0 = kb * 64 + q4_k_of(j, i);
-                    if (k0 >= p.K) continue;
-                    const int64_t at = ((tile * p.groups_padded + k0 / p.group) * 4 + rb) * 8 + r;
-                    const float s = bf16_bits_to_float(static_cast<uint16_t>(p.scales[at] >> (16 * half)));
-                    const float z = p.zeros ? static_cast<float>((p.zeros[at] >> (4 * half)) & 15) : 8.f;
-                    const uint32_t raw = __funnelshift_r(w[i], w[i], 3) >> (4 * half);
-                    const uint16_t *x = p.X + m * p.K + k0;
-                    acc += s * (bf16_bits_to_float(x[0]) * (static_cast<float>(raw & 15) - z) +
-                                bf16_bits_to_float(x[1]) * (static_cast<float>((raw >> 16) & 15) - z) +
-                                bf16_bits_to_float(x[2]) * (static_cast<float>((raw >> 8) & 15) - z) +
-                                bf16_bits_to_float(x[3]) * (static_cast<float>((raw >> 24) & 15) - z));
+                    const int k32 = kb * 2 + i / 2;                  // 32-wide part of the step
+                    const int group = k32 * kGroups / 4;
+                    const bool first = (i & 1) == 0 && k32 % (4 / kGroups) == 0;
+                    const bool last = (i & 1) == 1 && (k32 + 1) % (4 / kGroups) == 0;
+                    uint32_t z0 = 0x41C041C0u, z1 = 0x41C041C0u;  // 16 + 8
+                    if constexpr (kZeros) {
+                        const uint32_t z = lds8(w + 4096 + kScaleBytes + group * 32 + r * 8 + g);
+                        z0 = 0x41804180u | ((z & 15u) * 0x00080008u);
+                        z1 = 0x41804180u | ((z >> 4) * 0x00080008u);
+                    }
+                    uint32_t a[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t turned = q ? __funnelshift_r(word[i], word[i], 4 * q) : word[i];
+                        a[q] = bf16x2_sub((turned & 0x00780078u) | 0x41804180u, q & 1 ? z1 : z0);
+                    }
+                    float s0 = 0.f, s1 = 0.f;
+                    if (last) {
+                        const uint32_t s = lds32(w + 4096 + group * 128 + r * 32 + g * 4);
+                        s0 = __uint_as_float(s << 16);
+                        s1 = __uint_as_float(s & 0xffff0000u);
+                    }
+#pragma unroll
+                    for (int t = 0; t < kNT; ++t) {
+                        float(&d)[4] = part[r][t];
+                        if (first) d[0] = d[1] = d[2] = d[3] = 0.f;
+                        mma16816<false>(d, a[0], a[1], a[2], a[3], b[t][2 * i], b[t][2 * i + 1]);
+                        if (last) {
+                            acc[r][t][0] += s0 * d[0];
+                            acc[r][t][1] += s0 * d[1];
+                            acc[r][t][2] += s1 * d[2];
+                            acc[r][t][3] += s1 * d[3];
+                        }
+                    }
                 }
             }
         }
-        for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-        if (lane == 0) {
-            if (p.bias) acc += bf16_bits_to_float(p.bias[n]);
-            if (p.y_f32)
-                static_cast<float *>(p.Y)[m * p.N + n] = acc;
-            else
-                static_cast<__nv_bfloat16 *>(p.Y)[m * p.N + n] = __float2bfloat16_rn(acc);
+    }
+
+    // Join: [K step][token][row] in shared memory (the stages are done with).
+    cp_async_wait<0>();
+    __syncthreads();
+    float *red = reinterpret_cast<float *>(smem);
+    constexpr int kPitch = Tile::kPitch, kPlane = 8 * kNT * kPitch;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int t = 0; t < kNT; ++t) {
+            float *to = red + kw * kPlane + (8 * t + 2 * j) * kPitch + rt * 64 + r * 16 + g;
+            to[0] = acc[r][t][0];
+            to[kPitch] = acc[r][t][1];
+            to[8] = acc[r][t][2];
+            to[kPitch + 8] = acc[r][t][3];
         }
+    __syncthreads();
+    constexpr int kRows = 64 * kRT;
+    const int64_t n0 = tile0 * 64;
+    auto store = [&](int m, int row, float y) {
+        const int64_t n = n0 + row;
+        if (n >= p.N) return;
+        if (p.bias) y += bf16_bits_to_float(p.bias[n]);
+        if (p.y_f32)
+            static_cast<float *>(p.Y)[(m0 + m) * p.N + n] = y;
+        else
+            static_cast<__nv_bfloat16 *>(p.Y)[(m0 + m) * p.N + n] = __float2bfloat16_rn(y);
+    };
+    for (int e = tid; e < M * kRows; e += kQ4Threads) {
+        float *at = red + (e / kRows) * kPitch + e % kRows;
+        float y = at[0];
+#pragma unroll
+        for (int k = 1; k < kKW; ++k) y += at[k * kPlane];
+        if (p.splits == 1)
+            store(e / kRows, e % kRows, y);
+        else
+            at[0] = y;
+    }
+    if (p.splits > 1) {
+        __syncthreads();
+        cluster_arrive();
+        cluster_wait();
+        // Each CTA finishes a share of the elements, adding the ranks in order.
+        const int all = M * kRows, e1 = all * (rank + 1) / p.splits;
+        for (int e = all * rank / p.splits + tid; e < e1; e += kQ4Threads) {
+            const uint32_t at = base + ((e / kRows) * kPitch + e % kRows) * 4;
+            float part[kQ4MaxSplits];
+#pragma unroll
+            for (int s = 0; s < kQ4MaxSplits; ++s)
+                if (s < p.splits) part[s] = ld_cluster_f32(map_to_rank(at, s));
+            float y = part[0];
+#pragma unroll
+            for (int s = 1; s < kQ4MaxSplits; ++s)
+                if (s < p.splits) y += part[s];
+            store(e / kRows, e % kRows, y);
+        }
+        cluster_arrive();  // no CTA leaves while another reads its sums
+        cluster_wait();
     }
 }
 
