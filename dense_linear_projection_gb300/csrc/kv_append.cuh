@@ -5,6 +5,7 @@
 
 #include "kv_internal.h"
 #include "proj_kernel.cuh"
+#include "proj_warp.cuh"
 
 namespace projgb {
 namespace dev {
@@ -26,11 +27,6 @@ __device__ __forceinline__ void load8(const uint16_t *from, float *x) {
         x[2 * i] = __uint_as_float(w[i] << 16);
         x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
-}
-
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
 __device__ __forceinline__ uint8_t to_e4m3(float x, float scale) {

@@ -2,10 +2,16 @@
 // matrix loads and transposes, and the 16×8×16 tensor-core step.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <stdint.h>
 
 namespace projgb {
 namespace dev {
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t to, const void *from, bool fill) {
     // fill = false: no byte is read, the 16 bytes become zero.

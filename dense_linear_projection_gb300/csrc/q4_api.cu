@@ -2,6 +2,7 @@
 // launches.  See include/proj.h for the contract.
 #include <cuda_runtime.h>
 
+#include <cstdlib>
 #include <new>
 
 #include "proj.h"
@@ -144,6 +145,7 @@ proj_status_t proj_q4_run(proj_q4_handle_t h, int64_t M, const void *X, const vo
     p.k_blocks = h->shape.k_blocks;
     p.groups_padded = h->shape.groups_padded;
     p.y_f32 = h->y_dtype == PROJ_F32;
+    p.y_vec = h->N % 4 == 0 && reinterpret_cast<uintptr_t>(Y) % (p.y_f32 ? 16 : 8) == 0;
     p.X = static_cast<const uint16_t *>(X);
     p.codes = reinterpret_cast<const uint4 *>(at);
     p.scales = reinterpret_cast<const uint32_t *>(at + h->shape.codes_bytes);
@@ -160,10 +162,12 @@ proj_status_t proj_q4_run(proj_q4_handle_t h, int64_t M, const void *X, const vo
     int64_t splits = 3 * int64_t(h->sm_count) / tiles;
     if (splits > steps / q.k_steps) splits = steps / q.k_steps;
     p.splits = static_cast<int32_t>(splits < 1 ? 1 : splits > kQ4MaxSplits ? kQ4MaxSplits : splits);
+    if (const char *e = getenv("Q4S")) p.splits = atoi(e);
     const int tokens = static_cast<int>(M < kQ4MaxTokens ? M : kQ4MaxTokens);
     const int groups = static_cast<int>(128 / h->group);
     const int stage = kQ4Warps * (4096 + groups * (128 + (h->has_zeros ? 32 : 0))) + q.k_steps * tokens * kQ4XPitch;
     p.stages = 3 * stage <= 56 * 1024 ? 3 : 2;
+    if (const char *e = getenv("Q4T")) p.stages = atoi(e);
     int smem = p.stages * stage;
     if (smem < q.red) smem = q.red;
 

@@ -8,9 +8,9 @@
 // rows r and r + 8 and the four K positions q4_k_of(j, i) .. + 3.  (Which K
 // positions share a step is free, as X is read by the same rule; this one gives
 // a lane 16 contiguous bytes of X for two steps, and keeps a step within a
-// group of 32.)  Register t of a step holds nibbles t and t + 4 of its word,
-// stored rotated left by 3 so that a rotation by 4·t alone brings them to bits
-// 3..6 of each half, where OR-ing 0x4180 makes them the bf16 numbers 16 + q.
+// group of 32.)  A step's word holds, in each half (even K low, odd K high):
+// nibble 0 row r, K + 0/1; nibble 1 row r, K + 2/3; nibbles 2 and 3 the same of
+// row r + 8.
 //
 //   codes   [row tile][k-block][row block 0..3][lane] 16 bytes
 //   scales  [row tile][group][row block][r = 0..7] bf16 of rows r, r + 8
@@ -57,6 +57,7 @@ inline Q4Shape q4_shape(int64_t N, int64_t K, int64_t group, bool has_zeros) {
 struct Q4Params {
     int64_t M, N, K, row_tiles, k_blocks, groups_padded;
     int32_t y_f32;
+    int32_t y_vec;   // Y's rows start on four-element boundaries: four at a time
     int32_t splits;  // CTAs of a cluster
     int32_t stages;  // of the ring: 2, 3 or 4
     const uint16_t *X;

@@ -29,13 +29,12 @@ __global__ void q4_pack_codes_kernel(const uint8_t *codes, uint4 *P, int64_t N, 
                 uint32_t four = 0x8888u;
                 if (n < N && k0 < K)  // K is a multiple of 32: the four codes are all in range
                     four = codes[n * (K / 2) + k0 / 2] | (static_cast<uint32_t>(codes[n * (K / 2) + k0 / 2 + 1]) << 8);
-                // Nibbles t and t + 4 become the low and high halves of operand register t.
-                raw |= (four & 15u) << (4 * half);
-                raw |= ((four >> 4) & 15u) << (4 * half + 16);
-                raw |= ((four >> 8) & 15u) << (4 * half + 8);
-                raw |= ((four >> 12) & 15u) << (4 * half + 24);
+                raw |= (four & 15u) << (8 * half);
+                raw |= ((four >> 4) & 15u) << (8 * half + 16);
+                raw |= ((four >> 8) & 15u) << (8 * half + 4);
+                raw |= ((four >> 12) & 15u) << (8 * half + 20);
             }
-            w[i] = __funnelshift_l(raw, raw, 3);
+            w[i] = raw;
         }
         P[e] = make_uint4(w[0], w[1], w[2], w[3]);
     }
@@ -63,20 +62,30 @@ __global__ void q4_pack_scales_kernel(const uint16_t *scales, const uint8_t *zer
 
 // ---- the projection
 //
-// Mathematics: Y[m,n] = Σ_g s[n,g]·Σ_{k in g} x[m,k]·(q[n,k] − z[n,g]).  The
-// bf16 number 16 + q comes from two bit operations on the packed word and
-// (16 + q) − (16 + z) is exact, so the tensor core multiplies X by exact
-// integers; a group's fp32 sum is then scaled into the row's fp32 sum.
+// Mathematics: Y[m,n] = Σ_g s[n,g]·(Σ_{k in g} q[n,k]·x[m,k] − z[n,g]·Σ_{k in g} x[m,k]).
+//
+// Codes as operands.  A bf16 number with exponent field 0 and mantissa q is
+// q·2^-133 (a subnormal), and the scale goes on evenly into exponent field 1:
+// the 16 bits 0000'0000'qqqq'0000 are q·2^-129 for every q of four bits.  So one
+// AND makes a pair of codes a pair of exact bf16 numbers, in either of two
+// nibbles of each half word, and one fused multiply-add makes it
+// (q − z)·2^-7, exact: nine instructions for eight codes.  The tensor core
+// multiplies X as it is by these; a group's fp32 sum is scaled into the row's
+// fp32 sum, and the 2^7 is taken back when the row is written.
 //
 // The product is swapped (weight rows are the 16-row operand, up to 8·kNT
 // tokens its columns).  What bounds it is the stream of codes, and for small
-// token counts the instructions that turn a code into an operand: about 11 per
-// 8 codes of a lane.  A warp owns 64 rows × 128 K at a time, in a ring of
-// shared-memory stages filled by 16-byte asynchronous copies.  A CTA of four
-// warps covers kRT row tiles × kKW K steps (more tokens: more rows to a CTA,
-// since the CTA's copies of X grow with them); the S CTAs of a cluster share the
-// K range of the same rows.  Sums join in a fixed order: the kKW warps in shared
-// memory, then the cluster's CTAs through distributed shared memory.
+// token counts the instructions per code.  A warp owns 64 rows × 128 K at a
+// time, in a ring of shared-memory stages filled by 16-byte asynchronous copies.
+// A CTA of four warps covers kRT row tiles × kKW K steps (more tokens: more rows
+// to a CTA, since the CTA's copies of X grow with them); the S CTAs of a cluster
+// share the K range of the same rows.  Sums join in a fixed order: the kKW warps
+// in shared memory, then the cluster's CTAs through distributed shared memory.
+constexpr uint32_t kQ4Unit = 0x7E807E80u;      // 2^126, twice: codes that stand for q·2^-133
+constexpr uint32_t kQ4UnitHigh = 0x7C807C80u;  // 2^122: for q·2^-129
+constexpr uint32_t kQ4UnitMinus = 0xFE80FE80u;
+constexpr float kQ4Restore = 128.f;
+
 template <int kNT>
 struct Q4Tile {
     static constexpr int kRT = kNT == 1 ? 1 : 2;  // row tiles of a CTA
@@ -85,15 +94,25 @@ struct Q4Tile {
     static constexpr int kRed = kKW * 8 * kNT * kPitch * 4;
 };
 
-__device__ __forceinline__ uint32_t bf16x2_sub(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
     return v;
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t at) {
@@ -106,9 +125,12 @@ __device__ __forceinline__ uint32_t lds8(uint32_t at) {
     asm volatile("{\n\t.reg .u8 b;\n\tld.shared.u8 b, [%1];\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(v) : "r"(at) : "memory");
     return v;
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_addr)
+                 : "memory");
     return v;
 }
 
@@ -139,6 +161,10 @@ __global__ void __launch_bounds__(kQ4Threads, kNT == 1 ? 4 : kNT == 2 ? 3 : 2) q
 
     const int64_t steps = (p.k_blocks + 1) / 2;
     const int64_t step0 = steps * rank / p.splits + kw, step1 = steps * (rank + 1) / p.splits;
+
+    uint32_t x_row[kNT];  // this lane's place in a step's X
+#pragma unroll
+    for (int t = 0; t < kNT; ++t) x_row[t] = min(8 * t + g, M - 1) * kQ4XPitch + j * 16;
 
     float acc[4][kNT][4];
 #pragma unroll
@@ -200,59 +226,77 @@ __global__ void __launch_bounds__(kQ4Threads, kNT == 1 ? 4 : kNT == 2 ? 3 : 2) q
         const uint32_t w = my_w + slot * stage_bytes, xs = my_x + slot * stage_bytes;
         if (++slot == stages) slot = 0;
 
-        float part[4][kNT][4];
+        // X as the second operand: column (token) g; columns past M repeat the
+        // last token and are dropped.
+        uint32_t b[kNT][16];
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            // X as the second operand: column (token) g; columns past M repeat the last token and are dropped.
-            uint32_t b[kNT][8];
+        for (int t = 0; t < kNT; ++t)
 #pragma unroll
-            for (int t = 0; t < kNT; ++t) {
-                const uint32_t at = xs + min(8 * t + g, M - 1) * kQ4XPitch + kb * 128 + j * 16;
-                const uint4 lo = lds128(at), hi = lds128(at + 64);
-                b[t][0] = lo.x, b[t][1] = lo.y, b[t][2] = lo.z, b[t][3] = lo.w;
-                b[t][4] = hi.x, b[t][5] = hi.y, b[t][6] = hi.z, b[t][7] = hi.w;
+            for (int h = 0; h < 4; ++h) {
+                const uint4 v = lds128(xs + x_row[t] + h * 64);
+                b[t][4 * h] = v.x, b[t][4 * h + 1] = v.y, b[t][4 * h + 2] = v.z, b[t][4 * h + 3] = v.w;
             }
+        // Row blocks together: enough independent chains of tensor-core steps
+        // to cover their latency.
+        constexpr int kTogether = kNT == 1 ? 4 : kNT == 2 ? 2 : 1;
+        constexpr int kWords = 8 / kGroups;  // tensor-core steps of a group
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const uint4 v = lds128(w + kb * 2048 + r * 512 + lane * 16);
-                const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+        for (int r0 = 0; r0 < 4; r0 += kTogether) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k32 = kb * 2 + i / 2;                  // 32-wide part of the step
-                    const int group = k32 * kGroups / 4;
-                    const bool first = (i & 1) == 0 && k32 % (4 / kGroups) == 0;
-                    const bool last = (i & 1) == 1 && (k32 + 1) % (4 / kGroups) == 0;
-                    uint32_t z0 = 0x41C041C0u, z1 = 0x41C041C0u;  // 16 + 8
+            for (int group = 0; group < kGroups; ++group) {
+                float part[kTogether][kNT][4], s[kTogether][2];
+                uint32_t z[kTogether][2], word[kTogether][kWords];
+#pragma unroll
+                for (int r = 0; r < kTogether; ++r) {
+#pragma unroll
+                    for (int i = 0; i < kWords; i += (kWords < 4 ? 2 : 4)) {
+                        const int at = group * kWords + i;  // steps 4·kb + (0..3) share a 16-byte piece
+                        const uint32_t from = w + (at / 4) * 2048 + (r0 + r) * 512 + lane * 16;
+                        if constexpr (kWords >= 4) {
+                            const uint4 v = lds128(from);
+                            word[r][i] = v.x, word[r][i + 1] = v.y, word[r][i + 2] = v.z, word[r][i + 3] = v.w;
+                        } else {
+                            const uint2 v = lds64(from + (at % 4) * 4);
+                            word[r][i] = v.x, word[r][i + 1] = v.y;
+                        }
+                    }
+                    const uint32_t two = lds32(w + 4096 + group * 128 + (r0 + r) * 32 + g * 4);
+                    s[r][0] = __uint_as_float(two << 16);
+                    s[r][1] = __uint_as_float(two & 0xffff0000u);
                     if constexpr (kZeros) {
-                        const uint32_t z = lds8(w + 4096 + kScaleBytes + group * 32 + r * 8 + g);
-                        z0 = 0x41804180u | ((z & 15u) * 0x00080008u);
-                        z1 = 0x41804180u | ((z >> 4) * 0x00080008u);
+                        const uint32_t both = lds8(w + 4096 + kScaleBytes + group * 32 + (r0 + r) * 8 + g);
+                        z[r][0] = bf16x2_mul((both & 15u) * 0x00010001u, kQ4UnitMinus);
+                        z[r][1] = bf16x2_mul((both >> 4) * 0x00010001u, kQ4UnitMinus);
+                    } else {
+                        z[r][0] = z[r][1] = 0xBD80BD80u;  // −8·2^-7
                     }
-                    uint32_t a[4];
+                }
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint32_t turned = q ? __funnelshift_r(word[i], word[i], 4 * q) : word[i];
-                        a[q] = bf16x2_sub((turned & 0x00780078u) | 0x41804180u, q & 1 ? z1 : z0);
-                    }
-                    float s0 = 0.f, s1 = 0.f;
-                    if (last) {
-                        const uint32_t s = lds32(w + 4096 + group * 128 + r * 32 + g * 4);
-                        s0 = __uint_as_float(s << 16);
-                        s1 = __uint_as_float(s & 0xffff0000u);
-                    }
+                for (int i = 0; i < kWords; ++i) {
+                    const int at = group * kWords + i;
 #pragma unroll
-                    for (int t = 0; t < kNT; ++t) {
-                        float(&d)[4] = part[r][t];
-                        if (first) d[0] = d[1] = d[2] = d[3] = 0.f;
-                        mma16816<false>(d, a[0], a[1], a[2], a[3], b[t][2 * i], b[t][2 * i + 1]);
-                        if (last) {
-                            acc[r][t][0] += s0 * d[0];
-                            acc[r][t][1] += s0 * d[1];
-                            acc[r][t][2] += s1 * d[2];
-                            acc[r][t][3] += s1 * d[3];
+                    for (int r = 0; r < kTogether; ++r) {
+                        const uint32_t now = word[r][i], next = now >> 8;
+                        const uint32_t a0 = bf16x2_fma(now & 0x000f000fu, kQ4Unit, z[r][0]);
+                        const uint32_t a1 = bf16x2_fma(next & 0x000f000fu, kQ4Unit, z[r][1]);
+                        const uint32_t a2 = bf16x2_fma(now & 0x00f000f0u, kQ4UnitHigh, z[r][0]);
+                        const uint32_t a3 = bf16x2_fma(next & 0x00f000f0u, kQ4UnitHigh, z[r][1]);
+#pragma unroll
+                        for (int t = 0; t < kNT; ++t) {
+                            if (i == 0) part[r][t][0] = part[r][t][1] = part[r][t][2] = part[r][t][3] = 0.f;
+                            mma16816<false>(part[r][t], a0, a1, a2, a3, b[t][2 * at], b[t][2 * at + 1]);
                         }
                     }
                 }
+#pragma unroll
+                for (int r = 0; r < kTogether; ++r)
+#pragma unroll
+                    for (int t = 0; t < kNT; ++t) {
+                        acc[r0 + r][t][0] += s[r][0] * part[r][t][0];
+                        acc[r0 + r][t][1] += s[r][0] * part[r][t][1];
+                        acc[r0 + r][t][2] += s[r][1] * part[r][t][2];
+                        acc[r0 + r][t][3] += s[r][1] * part[r][t][3];
+                    }
             }
         }
     }
@@ -273,44 +317,64 @@ __global__ void __launch_bounds__(kQ4Threads, kNT == 1 ? 4 : kNT == 2 ? 3 : 2) q
             to[kPitch + 8] = acc[r][t][3];
         }
     __syncthreads();
-    constexpr int kRows = 64 * kRT;
+    // Four rows at a time.
+    constexpr uint32_t kQuads = 16 * kRT;
+    const uint32_t quads = M * kQuads;
     const int64_t n0 = tile0 * 64;
-    auto store = [&](int m, int row, float y) {
-        const int64_t n = n0 + row;
-        if (n >= p.N) return;
-        if (p.bias) y += bf16_bits_to_float(p.bias[n]);
-        if (p.y_f32)
-            static_cast<float *>(p.Y)[(m0 + m) * p.N + n] = y;
-        else
-            static_cast<__nv_bfloat16 *>(p.Y)[(m0 + m) * p.N + n] = __float2bfloat16_rn(y);
-    };
-    for (int e = tid; e < M * kRows; e += kQ4Threads) {
-        float *at = red + (e / kRows) * kPitch + e % kRows;
-        float y = at[0];
+    auto store = [&](uint32_t e, float4 v) {
+        const int64_t n = n0 + (e % kQuads) * 4, at = (m0 + e / kQuads) * p.N + n;
+        float y[4] = {v.x * kQ4Restore, v.y * kQ4Restore, v.z * kQ4Restore, v.w * kQ4Restore};
+        if (p.bias) {
 #pragma unroll
-        for (int k = 1; k < kKW; ++k) y += at[k * kPlane];
+            for (int i = 0; i < 4; ++i)
+                if (n + i < p.N) y[i] += bf16_bits_to_float(p.bias[n + i]);
+        }
+        if (p.y_vec && n < p.N) {  // N is a multiple of 4
+            if (p.y_f32)
+                *reinterpret_cast<float4 *>(static_cast<float *>(p.Y) + at) = make_float4(y[0], y[1], y[2], y[3]);
+            else
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.Y) + at) =
+                    make_uint2(bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (n + i >= p.N) break;
+                if (p.y_f32)
+                    static_cast<float *>(p.Y)[at + i] = y[i];
+                else
+                    static_cast<__nv_bfloat16 *>(p.Y)[at + i] = __float2bfloat16_rn(y[i]);
+            }
+        }
+    };
+    for (uint32_t e = tid; e < quads; e += kQ4Threads) {
+        float4 *at = reinterpret_cast<float4 *>(red + (e / kQuads) * kPitch + (e % kQuads) * 4);
+        float4 y = *at;
+#pragma unroll
+        for (int k = 1; k < kKW; ++k) {
+            const float4 o = at[k * kPlane / 4];
+            y.x += o.x, y.y += o.y, y.z += o.z, y.w += o.w;
+        }
         if (p.splits == 1)
-            store(e / kRows, e % kRows, y);
+            store(e, y);
         else
-            at[0] = y;
+            *at = y;
     }
     if (p.splits > 1) {
-        __syncthreads();
         cluster_arrive();
         cluster_wait();
         // Each CTA finishes a share of the elements, adding the ranks in order.
-        const int all = M * kRows, e1 = all * (rank + 1) / p.splits;
-        for (int e = all * rank / p.splits + tid; e < e1; e += kQ4Threads) {
-            const uint32_t at = base + ((e / kRows) * kPitch + e % kRows) * 4;
-            float part[kQ4MaxSplits];
+        const uint32_t e1 = quads * (rank + 1) / p.splits;
+        for (uint32_t e = quads * rank / p.splits + tid; e < e1; e += kQ4Threads) {
+            const uint32_t at = base + ((e / kQuads) * kPitch + (e % kQuads) * 4) * 4;
+            float4 part[kQ4MaxSplits];
 #pragma unroll
             for (int s = 0; s < kQ4MaxSplits; ++s)
-                if (s < p.splits) part[s] = ld_cluster_f32(map_to_rank(at, s));
-            float y = part[0];
+                if (s < p.splits) part[s] = ld_cluster_f4(map_to_rank(at, s));
+            float4 y = part[0];
 #pragma unroll
             for (int s = 1; s < kQ4MaxSplits; ++s)
-                if (s < p.splits) y += part[s];
-            store(e / kRows, e % kRows, y);
+                if (s < p.splits) y.x += part[s].x, y.y += part[s].y, y.z += part[s].z, y.w += part[s].w;
+            store(e, y);
         }
         cluster_arrive();  // no CTA leaves while another reads its sums
         cluster_wait();

@@ -181,6 +181,20 @@ def test_infinities_and_nan_stay_in_their_rows():
     assert torch.equal(Y[3].isnan(), ref[3].isnan()) and torch.equal(Y[3] == math.inf, ref[3] == math.inf)
 
 
+@pytest.mark.parametrize("sizes", [(1e-30,), (1e-20,), (1e5,), (1e12,), (1e25,), (1.0, 1e30), (1e-30, 1.0), (1e-25, 1e25)], ids=str)
+@pytest.mark.parametrize("M", [1, 6, 16, 32])
+def test_activations_of_any_size(M, sizes):
+    # Every size of activation that fp32 sums can hold, and sizes that change along K or between tokens.
+    import torch
+    proj, P, X, _, W = run(M, 70, 512, 64, True, False, True, seed=11)
+    size = torch.tensor(sizes, device="cuda", dtype=torch.float64)
+    for at in (torch.arange(512, device="cuda") // 64 % len(sizes), torch.arange(512, device="cuda") // 5 % len(sizes)):
+        x = (X.double() * size[at][None]).to(torch.bfloat16)
+        check(proj(x, P), x, W, None, f"{sizes} along K")
+    x = (X.double() * size[torch.arange(M, device="cuda") % len(sizes)][:, None]).to(torch.bfloat16)
+    check(proj(x, P), x, W, None, f"{sizes} between tokens")
+
+
 def test_refusals():
     import torch
     import dense_linear_projection_gb300 as dlp
