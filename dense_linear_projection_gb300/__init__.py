@@ -470,9 +470,19 @@ class Projection:
             pass
 
 
+def _refuse(what: str):
+    raise ProjError(PROJ_ERR_INVALID_ARG, what)
+
+
 def _require(ok: bool, what: str) -> None:
     if not ok:
-        raise ProjError(PROJ_ERR_INVALID_ARG, what)
+        _refuse(what)
+
+
+def _raw_stream(stream, device: int) -> int:
+    """The given stream's handle, or that of the device's current stream."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 class Q4Projection:
@@ -489,10 +499,13 @@ class Q4Projection:
                  y_dtype: int = PROJ_BF16, has_bias: bool = False, stream=None):
         self.handle = None
         import torch
+        self._torch = torch
         self.N, self.K, self.group, self.has_zeros = N, K, group, bool(has_zeros)
         self.has_bias = bool(has_bias)
         self._dtype = torch.float32 if y_dtype == PROJ_F32 else torch.bfloat16
         self.handle = proj_q4_create(max_tokens, N, K, group, has_zeros, y_dtype, has_bias, stream)
+        self._bytes = max(16, proj_q4_packed_bytes(N, K, group, has_zeros))
+        self._run = lib().proj_q4_run
 
     def pack(self, codes, scales, zeros=None, stream=None):
         """The packed weights (uint8 CUDA tensor), made on the given or current stream."""
@@ -506,28 +519,31 @@ class Q4Projection:
         if zeros is not None:
             _require(zeros.dtype == torch.uint8 and tuple(zeros.shape) == (self.N, groups) and zeros.is_contiguous(),
                      "zeros: contiguous uint8 [N, K/group]")
-        packed = torch.empty(max(16, proj_q4_packed_bytes(self.N, self.K, self.group, self.has_zeros)),
-                             dtype=torch.uint8, device=codes.device)
-        if stream is None:
-            stream = torch.cuda.current_stream(codes.device)
-        proj_q4_pack(self.handle, codes, scales, zeros, packed, stream)
+        device = codes.get_device()
+        _require(device >= 0 and scales.get_device() == device and (zeros is None or zeros.get_device() == device),
+                 "codes, scales, zeros: on one CUDA device")
+        packed = torch.empty(self._bytes, dtype=torch.uint8, device=codes.device)
+        proj_q4_pack(self.handle, codes, scales, zeros, packed, _raw_stream(stream, device))
         return packed
 
     def __call__(self, X, packed, bias=None, out=None, stream=None):
-        import torch
-        M = X.shape[0]
-        _require(X.dtype == torch.bfloat16 and X.dim() == 2 and X.shape[1] == self.K and X.is_contiguous(),
-                 "X: contiguous bf16 [M, K]")
-        _require(bias is None or (bias.dtype == torch.bfloat16 and tuple(bias.shape) == (self.N,) and
-                                  bias.is_contiguous()), "bias: contiguous bf16 [N]")
+        torch, dtype, shape, device = self._torch, self._dtype, X.shape, X.get_device()
+        if X.dtype is not torch.bfloat16 or len(shape) != 2 or shape[1] != self.K or not X.is_contiguous() or device < 0:
+            _refuse("X: contiguous bf16 CUDA [M, K]")
+        M, N = shape[0], self.N
+        if packed.dtype is not torch.uint8 or packed.numel() != self._bytes or packed.get_device() != device:
+            _refuse("packed: what pack() returned, on X's device")
+        if bias is not None and (bias.dtype is not torch.bfloat16 or bias.shape != (N,) or not bias.is_contiguous() or
+                                 bias.get_device() != device):
+            _refuse("bias: contiguous bf16 [N], on X's device")
         if out is None:
-            out = torch.empty((M, self.N), dtype=self._dtype, device=X.device)
-        else:
-            _require(out.dtype == self._dtype and tuple(out.shape) == (M, self.N) and out.is_contiguous(),
-                     "out: contiguous [M, N] of y_dtype")
-        if stream is None:
-            stream = torch.cuda.current_stream(X.device)
-        proj_q4_run(self.handle, M, X, packed, bias, out, stream)
+            out = torch.empty((M, N), dtype=dtype, device=X.device)
+        elif out.dtype is not dtype or out.shape != (M, N) or not out.is_contiguous() or out.get_device() != device:
+            _refuse("out: contiguous [M, N] of y_dtype, on X's device")
+        status = self._run(self.handle, M, X.data_ptr(), packed.data_ptr(), None if bias is None else bias.data_ptr(),
+                           out.data_ptr(), _raw_stream(stream, device))
+        if status:
+            raise ProjError(status, "proj_q4_run")
         return out
 
     def close(self) -> None:
@@ -580,24 +596,27 @@ class PagedKV:
             _require(s is None or (kv_dtype == PROJ_E4M3 and s.dtype == torch.float32 and
                                    tuple(s.shape) == (kv_heads,) and s.is_contiguous()),
                      "k_scale, v_scale: contiguous fp32 [kv_heads], for an 8-bit cache")
+        device = k_cache.get_device()
+        _require(device >= 0 and all(x is None or x.get_device() == device for x in (v_cache, k_scale, v_scale)),
+                 "k_cache, v_cache, k_scale, v_scale: on one CUDA device")
         self.k_cache, self.v_cache, self.k_scale, self.v_scale = k_cache, v_cache, k_scale, v_scale
         self.q_heads, self.kv_heads, self.head_dim, self.page_size = q_heads, kv_heads, head_dim, page_size
-        self._bf16, self._i32, self._f32 = torch.bfloat16, torch.int32, torch.float32
-        self._torch = torch
+        self._torch, self._device, self._scale = torch, device, head_dim ** -0.5
         s = k_cache.stride()
         desc = KvDesc(pages, s[0], s[1], s[2], max_sequences, page_size, q_heads, kv_heads, head_dim, kv_dtype)
         self.handle = proj_kv_create(desc, stream)
+        self._append, self._attend = lib().proj_kv_append, lib().proj_kv_attend
 
-    def _rows(self, x, heads: int, what: str) -> int:
-        """Checks [tokens, heads, head_dim] rows with contiguous heads; the row stride."""
-        s = x.stride()
-        _require(x.dtype == self._bf16 and x.dim() == 3 and x.shape[1] == heads and x.shape[2] == self.head_dim and
-                 s[2] == 1 and (heads == 1 or s[1] == self.head_dim),
-                 f"{what}: bf16 [tokens, {heads}, {self.head_dim}] with contiguous heads")
-        return s[0] if x.shape[0] > 1 else heads * self.head_dim
+    def _rows(self, x, n: int, heads: int) -> int:
+        """The row stride of bf16 [n, heads, head_dim] with contiguous heads on the cache's device; -1: not that."""
+        s, d = x.stride(), self.head_dim
+        if (x.dtype is not self._torch.bfloat16 or x.shape != (n, heads, d) or s[2] != 1 or
+                (heads > 1 and s[1] != d) or x.get_device() != self._device):
+            return -1
+        return s[0] if n > 1 else heads * d
 
-    def _ints(self, x, dims: int, what: str) -> None:
-        _require(x.dtype == self._i32 and x.dim() == dims and x.is_contiguous(), f"{what}: contiguous int32, {dims}-D")
+    def _ints(self, x) -> bool:
+        return x.dtype is self._torch.int32 and x.is_contiguous() and x.get_device() == self._device
 
     def append(self, q, k, v, positions, page_table, seq_ids=None, rope=None, interleaved: bool = False, q_out=None,
                stream=None):
@@ -608,37 +627,47 @@ class PagedKV:
         [sequences, pages of a sequence]; ``seq_ids``: int32 [tokens], default
         0, 1, 2, …; ``rope``: :func:`rope_table`'s form, or None for no
         rotation."""
-        torch = self._torch
-        tokens = k.shape[0]
-        kv_stride = self._rows(k, self.kv_heads, "k")
-        _require(self._rows(v, self.kv_heads, "v") == kv_stride and v.shape[0] == tokens, "v: rows as k's")
-        self._ints(positions, 1, "positions")
-        self._ints(page_table, 2, "page_table")
-        _require(positions.shape[0] == tokens, "positions: one for each token")
-        if seq_ids is not None:
-            self._ints(seq_ids, 1, "seq_ids")
-            _require(seq_ids.shape[0] == tokens, "seq_ids: one for each token")
-        rot_dim = 0
+        torch, tokens = self._torch, k.shape[0]
+        kv_stride = self._rows(k, tokens, self.kv_heads)
+        if kv_stride < 0 or self._rows(v, tokens, self.kv_heads) != kv_stride:
+            _refuse("k, v: bf16 [tokens, kv_heads, head_dim] with contiguous heads and one row stride, on the cache's device")
+        if not self._ints(positions) or positions.shape != (tokens,):
+            _refuse("positions: contiguous int32 [tokens], on the cache's device")
+        table = page_table.shape
+        if not self._ints(page_table) or len(table) != 2:
+            _refuse("page_table: contiguous int32 [sequences, pages], on the cache's device")
+        if seq_ids is not None and (not self._ints(seq_ids) or seq_ids.shape != (tokens,)):
+            _refuse("seq_ids: contiguous int32 [tokens], on the cache's device")
+        rope_ptr, rope_rows, rot_dim = None, 0, 0
         if rope is not None:
-            _require(rope.dtype == self._f32 and rope.dim() == 2 and rope.is_contiguous(),
-                     "rope: contiguous fp32 [positions, rot_dim]")
-            rot_dim = rope.shape[1]
-        q_stride = q_out_stride = 0
+            if (rope.dtype is not torch.float32 or rope.dim() != 2 or not rope.is_contiguous() or
+                    rope.get_device() != self._device):
+                _refuse("rope: contiguous fp32 [positions, rot_dim], on the cache's device")
+            rope_ptr, (rope_rows, rot_dim) = rope.data_ptr(), rope.shape
+        q_ptr, q_out_ptr, q_stride, q_out_stride = None, None, 0, 0
         if q is not None:
-            q_stride = self._rows(q, self.q_heads, "q")
-            _require(q.shape[0] == tokens, "q: one row for each token")
+            q_stride = self._rows(q, tokens, self.q_heads)
+            if q_stride < 0:
+                _refuse("q: bf16 [tokens, q_heads, head_dim] with contiguous heads, on the cache's device")
             if q_out is None:
-                q_out = torch.empty((tokens, self.q_heads, self.head_dim), dtype=self._bf16, device=q.device)
-            q_out_stride = self._rows(q_out, self.q_heads, "q_out")
-            _require(q_out.shape[0] == tokens, "q_out: one row for each token")
-        else:
-            _require(q_out is None, "q_out: only with q")
-        if stream is None:
-            stream = torch.cuda.current_stream(k.device)
-        proj_kv_append(self.handle, tokens, q, q_stride, k, v, kv_stride, positions, seq_ids, page_table,
-                       page_table.shape[0], page_table.shape[1], rope, 0 if rope is None else rope.shape[0], rot_dim,
-                       interleaved, self.k_scale, self.v_scale, self.k_cache, self.v_cache, q_out, q_out_stride,
-                       stream)
+                q_out = torch.empty((tokens, self.q_heads, self.head_dim), dtype=torch.bfloat16, device=q.device)
+                q_out_stride = self.q_heads * self.head_dim
+            else:
+                q_out_stride = self._rows(q_out, tokens, self.q_heads)
+                if q_out_stride < 0:
+                    _refuse("q_out: as q")
+            q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
+        elif q_out is not None:
+            _refuse("q_out: only with q")
+        ks, vs = self.k_scale, self.v_scale
+        status = self._append(self.handle, tokens, q_ptr, q_stride, k.data_ptr(), v.data_ptr(), kv_stride,
+                              positions.data_ptr(), None if seq_ids is None else seq_ids.data_ptr(),
+                              page_table.data_ptr(), table[0], table[1], rope_ptr, rope_rows, rot_dim,
+                              1 if interleaved else 0, None if ks is None else ks.data_ptr(),
+                              None if vs is None else vs.data_ptr(), self.k_cache.data_ptr(), self.v_cache.data_ptr(),
+                              q_out_ptr, q_out_stride, _raw_stream(stream, self._device))
+        if status:
+            raise ProjError(status, "proj_kv_append")
         return q_out
 
     def attend(self, q, page_table, seq_lens, scale: Optional[float] = None, window: int = 0, out=None,
@@ -648,23 +677,31 @@ class PagedKV:
         last ``window`` of them; ``scale`` is 1/√head_dim by default.  Returns
         ``out`` ([sequences, q_heads, head_dim] bf16), with the fp32 log sums
         [sequences, q_heads] beside it when ``return_lse``."""
-        torch = self._torch
-        n = q.shape[0]
-        q_stride = self._rows(q, self.q_heads, "q")
-        self._ints(page_table, 2, "page_table")
-        self._ints(seq_lens, 1, "seq_lens")
-        _require(page_table.shape[0] == n and seq_lens.shape[0] == n, "page_table, seq_lens: one row for each sequence")
+        torch, n, heads = self._torch, q.shape[0], self.q_heads
+        q_stride = self._rows(q, n, heads)
+        if q_stride < 0:
+            _refuse("q: bf16 [sequences, q_heads, head_dim] with contiguous heads, on the cache's device")
+        table = page_table.shape
+        if not self._ints(page_table) or len(table) != 2 or table[0] != n:
+            _refuse("page_table: contiguous int32 [sequences, pages], on the cache's device")
+        if not self._ints(seq_lens) or seq_lens.shape != (n,):
+            _refuse("seq_lens: contiguous int32 [sequences], on the cache's device")
         if out is None:
-            out = torch.empty((n, self.q_heads, self.head_dim), dtype=self._bf16, device=q.device)
-        out_stride = self._rows(out, self.q_heads, "out")
-        _require(out.shape[0] == n, "out: one row for each sequence")
-        lse = torch.empty((n, self.q_heads), dtype=self._f32, device=q.device) if return_lse else None
-        if stream is None:
-            stream = torch.cuda.current_stream(q.device)
-        if scale is None:
-            scale = self.head_dim ** -0.5
-        proj_kv_attend(self.handle, n, q, q_stride, self.k_cache, self.v_cache, self.k_scale, self.v_scale, page_table,
-                       page_table.shape[1], seq_lens, window, scale, out, out_stride, lse, stream)
+            out = torch.empty((n, heads, self.head_dim), dtype=torch.bfloat16, device=q.device)
+            out_stride = heads * self.head_dim
+        else:
+            out_stride = self._rows(out, n, heads)
+            if out_stride < 0:
+                _refuse("out: as q")
+        lse = torch.empty((n, heads), dtype=torch.float32, device=q.device) if return_lse else None
+        ks, vs = self.k_scale, self.v_scale
+        status = self._attend(self.handle, n, q.data_ptr(), q_stride, self.k_cache.data_ptr(), self.v_cache.data_ptr(),
+                              None if ks is None else ks.data_ptr(), None if vs is None else vs.data_ptr(),
+                              page_table.data_ptr(), table[1], seq_lens.data_ptr(), window,
+                              self._scale if scale is None else scale, out.data_ptr(), out_stride,
+                              None if lse is None else lse.data_ptr(), _raw_stream(stream, self._device))
+        if status:
+            raise ProjError(status, "proj_kv_attend")
         return (out, lse) if return_lse else out
 
     def status(self, stream=None) -> int:

@@ -35,7 +35,7 @@ int pack_blocks(int64_t items, int sm_count) {
 using Q4Kernel = void (*)(Q4Params);
 struct Q4Instance {
     Q4Kernel kernel;
-    int row_tiles, k_steps, red;  // of a CTA; bytes of its join
+    int warps, per_sm, row_tiles, k_steps, red;  // of a CTA; bytes of its join
 };
 
 template <int kNT>
@@ -48,14 +48,14 @@ Q4Instance instance_nt(int64_t group, bool zeros) {
         k = zeros ? dev::q4_kernel<kNT, 2, true> : dev::q4_kernel<kNT, 2, false>;
     else
         k = zeros ? dev::q4_kernel<kNT, 4, true> : dev::q4_kernel<kNT, 4, false>;
-    return {k, Tile::kRT, Tile::kKW, Tile::kRed};
+    return {k, Tile::kWarps, Tile::kPerSm, Tile::kRT, Tile::kKW, Tile::kRed};
 }
 
 Q4Instance instance_for(int64_t M, int64_t group, bool zeros) {
     return M <= 8 ? instance_nt<1>(group, zeros) : M <= 16 ? instance_nt<2>(group, zeros) : instance_nt<4>(group, zeros);
 }
 
-constexpr int kSmemMost = 100 * 1024;
+constexpr int kSmemOfSm = 228 * 1024;  // shared memory of an SM, 1 KiB of it reserved for each CTA
 
 }  // namespace
 
@@ -88,7 +88,7 @@ proj_status_t proj_q4_create(proj_q4_handle_t *out, int64_t max_tokens, int64_t 
     if (prop.major != 10 || prop.minor != 3) return PROJ_ERR_UNSUPPORTED;  // built for sm_103a
     for (int64_t m = 8; m <= kQ4MaxTokens; m *= 2)
         if (cudaFuncSetAttribute(instance_for(m, group, has_zeros != 0).kernel,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) != cudaSuccess) {
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOfSm - 1024) != cudaSuccess) {
             cudaGetLastError();
             return PROJ_ERR_CUDA;
         }
@@ -156,17 +156,19 @@ proj_status_t proj_q4_run(proj_q4_handle_t h, int64_t M, const void *X, const vo
     const Q4Instance q = instance_for(M, h->group, h->has_zeros != 0);
     const int64_t tiles = (p.row_tiles + q.row_tiles - 1) / q.row_tiles;
     const int64_t passes = (M + kQ4MaxTokens - 1) / kQ4MaxTokens;
-    // CTAs of one K range: enough that about three CTAs stand on every SM and
-    // share the memory's bandwidth evenly, while every warp has a step.
+    // CTAs of one K range: as many as stand on the GPU at once, while every
+    // warp has a step.
     const int64_t steps = (p.k_blocks + 1) / 2;
-    int64_t splits = 3 * int64_t(h->sm_count) / tiles;
+    int64_t splits = q.per_sm * int64_t(h->sm_count) / tiles;
     if (splits > steps / q.k_steps) splits = steps / q.k_steps;
     p.splits = static_cast<int32_t>(splits < 1 ? 1 : splits > kQ4MaxSplits ? kQ4MaxSplits : splits);
     if (const char *e = getenv("Q4S")) p.splits = atoi(e);
     const int tokens = static_cast<int>(M < kQ4MaxTokens ? M : kQ4MaxTokens);
     const int groups = static_cast<int>(128 / h->group);
-    const int stage = kQ4Warps * (4096 + groups * (128 + (h->has_zeros ? 32 : 0))) + q.k_steps * tokens * kQ4XPitch;
-    p.stages = 3 * stage <= 56 * 1024 ? 3 : 2;
+    const int stage = q.warps * (4096 + groups * (128 + (h->has_zeros ? 32 : 0))) + q.k_steps * tokens * kQ4XPitch;
+    const int fit = (kSmemOfSm / q.per_sm - 1024) / stage;
+    const int most = q.warps * q.per_sm > 8 ? 2 : 3;
+    p.stages = fit < 2 ? 2 : fit < most ? fit : most;
     if (const char *e = getenv("Q4T")) p.stages = atoi(e);
     int smem = p.stages * stage;
     if (smem < q.red) smem = q.red;
@@ -174,7 +176,7 @@ proj_status_t proj_q4_run(proj_q4_handle_t h, int64_t M, const void *X, const vo
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.splits), static_cast<unsigned>(passes));
-    cfg.blockDim = dim3(kQ4Threads);
+    cfg.blockDim = dim3(static_cast<unsigned>(32 * q.warps));
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = as_stream(stream);
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

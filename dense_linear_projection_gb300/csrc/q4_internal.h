@@ -29,7 +29,6 @@
 namespace projgb {
 
 constexpr int kQ4TileRows = 64;
-constexpr int kQ4Warps = 4, kQ4Threads = 32 * kQ4Warps;
 constexpr int kQ4MaxTokens = 32;  // tokens of one pass over the weights
 constexpr int kQ4MaxSplits = 8;   // CTAs of a cluster that share a K range (the portable cluster size)
 constexpr int kQ4XPitch = 320;    // bytes between tokens of X in a stage: 128 K, and 64 bytes that

@@ -88,8 +88,10 @@ constexpr float kQ4Restore = 128.f;
 
 template <int kNT>
 struct Q4Tile {
-    static constexpr int kRT = kNT == 1 ? 1 : 2;  // row tiles of a CTA
-    static constexpr int kKW = kQ4Warps / kRT;    // K steps at a time
+    static constexpr int kWarps = kNT == 4 ? 4 : 8, kThreads = 32 * kWarps;
+    static constexpr int kPerSm = kNT == 2 ? 1 : 2;  // CTAs an SM: 16 warps at 8 tokens, 8 above (registers)
+    static constexpr int kRT = kNT == 4 ? 2 : 1;     // row tiles of a CTA
+    static constexpr int kKW = kWarps / kRT;      // K steps at a time
     static constexpr int kPitch = kRT * 64 + 4;   // floats of a token's rows while joining: conflict-free
     static constexpr int kRed = kKW * 8 * kNT * kPitch * 4;
 };
@@ -136,7 +138,7 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
 
 // kGroups: groups of a 128-wide K step (1, 2 or 4).
 template <int kNT, int kGroups, bool kZeros>
-__global__ void __launch_bounds__(kQ4Threads, kNT == 1 ? 4 : kNT == 2 ? 3 : 2) q4_kernel(const Q4Params p) {
+__global__ void __launch_bounds__(Q4Tile<kNT>::kThreads, Q4Tile<kNT>::kPerSm) q4_kernel(const Q4Params p) {
     using Tile = Q4Tile<kNT>;
     constexpr int kRT = Tile::kRT, kKW = Tile::kKW;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -155,12 +157,12 @@ __global__ void __launch_bounds__(kQ4Threads, kNT == 1 ? 4 : kNT == 2 ? 3 : 2) q
     constexpr int kScaleBytes = kGroups * 128, kZeroBytes = kZeros ? kGroups * 32 : 0;
     constexpr int kWarpBytes = 4096 + kScaleBytes + kZeroBytes;
     const int x_bytes = M * kQ4XPitch;
-    const int stage_bytes = kQ4Warps * kWarpBytes + kKW * x_bytes;
+    const int stage_bytes = Tile::kWarps * kWarpBytes + kKW * x_bytes;
     const uint32_t base = smem_u32(smem);
-    const uint32_t my_w = base + warp * kWarpBytes, my_x = base + kQ4Warps * kWarpBytes + kw * x_bytes;
+    const uint32_t my_w = base + warp * kWarpBytes, my_x = base + Tile::kWarps * kWarpBytes + kw * x_bytes;
 
     const int64_t steps = (p.k_blocks + 1) / 2;
-    const int64_t step0 = steps * rank / p.splits + kw, step1 = steps * (rank + 1) / p.splits;
+    const int step0 = static_cast<int>(steps * rank / p.splits) + kw, step1 = static_cast<int>(steps * (rank + 1) / p.splits);
 
     uint32_t x_row[kNT];  // this lane's place in a step's X
 #pragma unroll
@@ -172,32 +174,51 @@ __global__ void __launch_bounds__(kQ4Threads, kNT == 1 ? 4 : kNT == 2 ? 3 : 2) q
 #pragma unroll
         for (int t = 0; t < kNT; ++t) acc[r][t][0] = acc[r][t][1] = acc[r][t][2] = acc[r][t][3] = 0.f;
 
-    const uint8_t *codes = reinterpret_cast<const uint8_t *>(p.codes) + tile * p.k_blocks * 2048;
-    const uint8_t *scales = reinterpret_cast<const uint8_t *>(p.scales) + tile * p.groups_padded * 128;
-    const uint8_t *zeros = p.zeros + (kZeros ? tile * p.groups_padded * 32 : 0);
-    const uint8_t *x = reinterpret_cast<const uint8_t *>(p.X + m0 * p.K);
-    auto load = [&](int64_t step, int slot) {
+    // Loading: pointers to this lane's next step.
+    const uint8_t *codes = reinterpret_cast<const uint8_t *>(p.codes) + (tile * p.k_blocks + step0 * 2) * 2048 + lane * 16;
+    const uint8_t *scales = reinterpret_cast<const uint8_t *>(p.scales) + (tile * p.groups_padded + step0 * kGroups) * 128 + lane * 16;
+    const uint8_t *zeros = kZeros ? p.zeros + (tile * p.groups_padded + step0 * kGroups) * 32 + lane * 16 : nullptr;
+    const int x_first = (rt * 32 + lane) / 16, x_chunk = lane % 16;  // first of the tokens this lane copies; its 8 K of the step
+    const uint8_t *x = reinterpret_cast<const uint8_t *>(p.X + (m0 + x_first) * p.K + step0 * 128 + x_chunk * 8);
+    const int64_t x_next = 2 * kRT * p.K * 2;  // bytes to the lane's next token
+    const int whole = static_cast<int>((p.K / 128 < step1 ? p.K / 128 : step1));  // steps below it lie inside K
+    auto load = [&](int step, int slot) {
         if (step < step1) {
-            const uint32_t w = my_w + slot * stage_bytes, xs = my_x + slot * stage_bytes;
-            if (rows_there) {
-                const int blocks = step * 2 + 1 < p.k_blocks ? 8 : 4;  // 512-byte blocks that exist
+            const uint32_t w = my_w + slot * stage_bytes + lane * 16;
+            uint32_t to = my_x + slot * stage_bytes + x_first * kQ4XPitch + x_chunk * 16;
+            const uint8_t *from = x;
+            if (step < whole) {
+                if (rows_there) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    cp_async16(w + i * 512 + lane * 16, codes + step * 4096 + (i < blocks ? i * 512 + lane * 16 : 0), i < blocks);
-                if (lane < kGroups * 8) {
-                    const bool in = step * kGroups + lane / 8 < p.groups_padded;
-                    cp_async16(w + 4096 + lane * 16, scales + (in ? step * kScaleBytes + lane * 16 : 0), in);
+                    for (int i = 0; i < 8; ++i) cp_async16(w + i * 512, codes + i * 512);
+                    if (lane < kGroups * 8) cp_async16(w + 4096, scales);
+                    if (kZeros && lane < kGroups * 2) cp_async16(w + 4096 + kScaleBytes, zeros);
                 }
-                if (kZeros && lane < kGroups * 2) {
-                    const bool in = step * kGroups + lane / 2 < p.groups_padded;
-                    cp_async16(w + 4096 + kScaleBytes + lane * 16, zeros + (in ? step * kZeroBytes + lane * 16 : 0), in);
+                for (int m = x_first; m < M; m += 2 * kRT, to += 2 * kRT * kQ4XPitch, from += x_next) cp_async16(to, from);
+            } else {
+                // K ends inside the step: the blocks of codes and the groups
+                // that exist, and zeros for the rest.
+                const int blocks = step * 2 + 1 < p.k_blocks ? 8 : 4;
+                if (rows_there) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) cp_async16(w + i * 512, i < blocks ? codes + i * 512 : codes, i < blocks);
+                    if (lane < kGroups * 8) {
+                        const bool in = step * kGroups + lane / 8 < p.groups_padded;
+                        cp_async16(w + 4096, in ? scales : codes, in);
+                    }
+                    if (kZeros && lane < kGroups * 2) {
+                        const bool in = step * kGroups + lane / 2 < p.groups_padded;
+                        cp_async16(w + 4096 + kScaleBytes, in ? zeros : codes, in);
+                    }
                 }
+                const bool in = step * 128 + x_chunk * 8 < p.K;
+                for (int m = x_first; m < M; m += 2 * kRT, to += 2 * kRT * kQ4XPitch, from += x_next)
+                    cp_async16(to, in ? from : codes, in);
             }
-            for (int at = rt * 32 + lane; at < M * 16; at += 32 * kRT) {
-                const int m = at >> 4, c = at & 15;
-                const bool in = step * 128 + c * 8 < p.K;
-                cp_async16(xs + m * kQ4XPitch + c * 16, x + (in ? (m * p.K + step * 128 + c * 8) * 2 : 0), in);
-            }
+            codes += kKW * 4096;
+            scales += kKW * kScaleBytes;
+            if (kZeros) zeros += kKW * kZeroBytes;
+            x += kKW * 256;
         }
         cp_async_commit();
     };
@@ -213,7 +234,7 @@ __global__ void __launch_bounds__(kQ4Threads, kNT == 1 ? 4 : kNT == 2 ? 3 : 2) q
     const int stages = p.stages;
     for (int s = 0; s < stages - 1; ++s) load(step0 + s * kKW, s);
     int slot = 0, slot_in = stages - 1;
-    for (int64_t step = step0; step < step1; step += kKW) {
+    for (int step = step0; step < step1; step += kKW) {
         if (stages == 2)
             cp_async_wait<0>();
         else if (stages == 3)
@@ -244,25 +265,10 @@ __global__ void __launch_bounds__(kQ4Threads, kNT == 1 ? 4 : kNT == 2 ? 3 : 2) q
         for (int r0 = 0; r0 < 4; r0 += kTogether) {
 #pragma unroll
             for (int group = 0; group < kGroups; ++group) {
-                float part[kTogether][kNT][4], s[kTogether][2];
-                uint32_t z[kTogether][2], word[kTogether][kWords];
+                float part[kTogether][kNT][4];
+                uint32_t z[kTogether][2];
 #pragma unroll
                 for (int r = 0; r < kTogether; ++r) {
-#pragma unroll
-                    for (int i = 0; i < kWords; i += (kWords < 4 ? 2 : 4)) {
-                        const int at = group * kWords + i;  // steps 4·kb + (0..3) share a 16-byte piece
-                        const uint32_t from = w + (at / 4) * 2048 + (r0 + r) * 512 + lane * 16;
-                        if constexpr (kWords >= 4) {
-                            const uint4 v = lds128(from);
-                            word[r][i] = v.x, word[r][i + 1] = v.y, word[r][i + 2] = v.z, word[r][i + 3] = v.w;
-                        } else {
-                            const uint2 v = lds64(from + (at % 4) * 4);
-                            word[r][i] = v.x, word[r][i + 1] = v.y;
-                        }
-                    }
-                    const uint32_t two = lds32(w + 4096 + group * 128 + (r0 + r) * 32 + g * 4);
-                    s[r][0] = __uint_as_float(two << 16);
-                    s[r][1] = __uint_as_float(two & 0xffff0000u);
                     if constexpr (kZeros) {
                         const uint32_t both = lds8(w + 4096 + kScaleBytes + group * 32 + (r0 + r) * 8 + g);
                         z[r][0] = bf16x2_mul((both & 15u) * 0x00010001u, kQ4UnitMinus);
@@ -271,22 +277,48 @@ __global__ void __launch_bounds__(kQ4Threads, kNT == 1 ? 4 : kNT == 2 ? 3 : 2) q
                         z[r][0] = z[r][1] = 0xBD80BD80u;  // −8·2^-7
                     }
                 }
+                constexpr int kPiece = kWords < 4 ? 2 : 4;  // words of one load
 #pragma unroll
-                for (int i = 0; i < kWords; ++i) {
-                    const int at = group * kWords + i;
+                for (int i0 = 0; i0 < kWords; i0 += kPiece) {
+                    uint32_t word[kTogether][kPiece];
 #pragma unroll
                     for (int r = 0; r < kTogether; ++r) {
-                        const uint32_t now = word[r][i], next = now >> 8;
-                        const uint32_t a0 = bf16x2_fma(now & 0x000f000fu, kQ4Unit, z[r][0]);
-                        const uint32_t a1 = bf16x2_fma(next & 0x000f000fu, kQ4Unit, z[r][1]);
-                        const uint32_t a2 = bf16x2_fma(now & 0x00f000f0u, kQ4UnitHigh, z[r][0]);
-                        const uint32_t a3 = bf16x2_fma(next & 0x00f000f0u, kQ4UnitHigh, z[r][1]);
-#pragma unroll
-                        for (int t = 0; t < kNT; ++t) {
-                            if (i == 0) part[r][t][0] = part[r][t][1] = part[r][t][2] = part[r][t][3] = 0.f;
-                            mma16816<false>(part[r][t], a0, a1, a2, a3, b[t][2 * at], b[t][2 * at + 1]);
+                        const int at = group * kWords + i0;  // steps 4·kb + (0..3) share 16 bytes
+                        const uint32_t from = w + (at / 4) * 2048 + (r0 + r) * 512 + lane * 16 + (at % 4) * 4;
+                        if constexpr (kPiece == 4) {
+                            const uint4 v = lds128(from);
+                            word[r][0] = v.x, word[r][1] = v.y, word[r][2] = v.z, word[r][3] = v.w;
+                        } else {
+                            const uint2 v = lds64(from);
+                            word[r][0] = v.x, word[r][1] = v.y;
                         }
                     }
+#pragma unroll
+                    for (int i = 0; i < kPiece; ++i) {
+                        const int at = group * kWords + i0 + i;
+#pragma unroll
+                        for (int r = 0; r < kTogether; ++r) {
+                            const uint32_t now = word[r][i], next = now >> 8;
+                            const uint32_t a0 = bf16x2_fma(now & 0x000f000fu, kQ4Unit, z[r][0]);
+                            const uint32_t a1 = bf16x2_fma(next & 0x000f000fu, kQ4Unit, z[r][1]);
+                            const uint32_t a2 = bf16x2_fma(now & 0x00f000f0u, kQ4UnitHigh, z[r][0]);
+                            const uint32_t a3 = bf16x2_fma(next & 0x00f000f0u, kQ4UnitHigh, z[r][1]);
+#pragma unroll
+                            for (int t = 0; t < kNT; ++t) {
+                                if (i0 + i == 0)
+                                    mma16816_first<false>(part[r][t], a0, a1, a2, a3, b[t][2 * at], b[t][2 * at + 1]);
+                                else
+                                    mma16816<false>(part[r][t], a0, a1, a2, a3, b[t][2 * at], b[t][2 * at + 1]);
+                            }
+                        }
+                    }
+                }
+                float s[kTogether][2];
+#pragma unroll
+                for (int r = 0; r < kTogether; ++r) {
+                    const uint32_t two = lds32(w + 4096 + group * 128 + (r0 + r) * 32 + g * 4);
+                    s[r][0] = __uint_as_float(two << 16);
+                    s[r][1] = __uint_as_float(two & 0xffff0000u);
                 }
 #pragma unroll
                 for (int r = 0; r < kTogether; ++r)
@@ -346,7 +378,7 @@ __global__ void __launch_bounds__(kQ4Threads, kNT == 1 ? 4 : kNT == 2 ? 3 : 2) q
             }
         }
     };
-    for (uint32_t e = tid; e < quads; e += kQ4Threads) {
+    for (uint32_t e = tid; e < quads; e += Tile::kThreads) {
         float4 *at = reinterpret_cast<float4 *>(red + (e / kQuads) * kPitch + (e % kQuads) * 4);
         float4 y = *at;
 #pragma unroll
@@ -364,7 +396,7 @@ __global__ void __launch_bounds__(kQ4Threads, kNT == 1 ? 4 : kNT == 2 ? 3 : 2) q
         cluster_wait();
         // Each CTA finishes a share of the elements, adding the ranks in order.
         const uint32_t e1 = quads * (rank + 1) / p.splits;
-        for (uint32_t e = quads * rank / p.splits + tid; e < e1; e += kQ4Threads) {
+        for (uint32_t e = quads * rank / p.splits + tid; e < e1; e += Tile::kThreads) {
             const uint32_t at = base + ((e / kQuads) * kPitch + (e % kQuads) * 4) * 4;
             float4 part[kQ4MaxSplits];
 #pragma unroll
