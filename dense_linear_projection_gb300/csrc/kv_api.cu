@@ -21,7 +21,7 @@ struct proj_kv_s {
     int grid = 0;                     // CTAs of an attention launch at most
     void *scratch = nullptr;          // status word, counters, partial results
     int *status = nullptr;
-    uint32_t *counters = nullptr;
+    uint32_t *counters = nullptr, *group_counters = nullptr;
     float *partials = nullptr;
 };
 
@@ -83,13 +83,13 @@ proj_status_t launch_append(const KvAppendParams &p, dim3 grid, bool interleaved
 using AttendKernel = void (*)(KvAttendParams);
 struct AttendInstance {
     AttendKernel kernel;
-    int smem, per_sm, part;  // shared memory, CTAs an SM, floats of a partial result
+    int smem, per_sm, part, tile;  // shared memory, CTAs an SM, floats of a partial result, tokens of a tile
 };
 
 template <bool kE4m3, int kDim, int kNT>
 AttendInstance instance_of() {
     using Shape = dev::AttendShape<kE4m3, kDim, kNT>;
-    return {dev::kv_attend_kernel<kE4m3, kDim, kNT>, Shape::kSmem, Shape::kPerSm, Shape::kHeads * (kDim + 2)};
+    return {dev::kv_attend_kernel<kE4m3, kDim, kNT>, Shape::kSmem, Shape::kPerSm, Shape::kHeads * (kDim + 2), Shape::kTile};
 }
 
 // Rows of at most 8 query heads, or 16 where the group is larger and the
@@ -147,7 +147,8 @@ proj_status_t proj_kv_create(proj_kv_handle_t *out, const proj_kv_desc_t *desc, 
     }
     h->grid = h->sm_count * a.per_sm;
     const size_t counters = rounded(static_cast<size_t>(d.max_sequences) * d.kv_heads * h->chunks * 4);
-    const size_t clear = 256 + counters;
+    const size_t groups = rounded(static_cast<size_t>(h->grid) * 2 * 4);
+    const size_t clear = 256 + counters + groups;
     const size_t bytes = clear + static_cast<size_t>(h->grid) * 2 * a.part * 4;
     if (dev_malloc(&h->scratch, bytes) != cudaSuccess) {
         cudaGetLastError();
@@ -156,6 +157,7 @@ proj_status_t proj_kv_create(proj_kv_handle_t *out, const proj_kv_desc_t *desc, 
     }
     h->status = static_cast<int *>(h->scratch);
     h->counters = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(h->scratch) + 256);
+    h->group_counters = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(h->scratch) + 256 + counters);
     h->partials = reinterpret_cast<float *>(static_cast<uint8_t *>(h->scratch) + clear);
     if (cudaMemsetAsync(h->scratch, 0, clear, as_stream(stream)) != cudaSuccess ||
         cudaStreamSynchronize(as_stream(stream)) != cudaSuccess) {
@@ -262,11 +264,12 @@ proj_status_t proj_kv_attend(proj_kv_handle_t h, int64_t sequences, const void *
     p.units = d.kv_heads * h->chunks;
     p.partials = h->partials;
     p.counters = h->counters;
+    p.group_counters = h->group_counters;
     // No more CTAs than there can be tiles (one where every length is zero).
-    int64_t tiles = (table_width * d.page_size + kKvTile - 1) / kKvTile;
-    if (window > 0 && window / kKvTile + 2 < tiles) tiles = window / kKvTile + 2;
-    const int64_t want = sequences * p.units * (tiles > 0 ? tiles : 1);
     const AttendInstance a = instance_for(h);
+    int64_t tiles = (table_width * d.page_size + a.tile - 1) / a.tile;
+    if (window > 0 && window / a.tile + 2 < tiles) tiles = window / a.tile + 2;
+    const int64_t want = sequences * p.units * (tiles > 0 ? tiles : 1);
     return launch(a.kernel, dim3(static_cast<unsigned>(want < h->grid ? want : h->grid)), kKvThreads,
                   static_cast<size_t>(a.smem), stream, p);
 }

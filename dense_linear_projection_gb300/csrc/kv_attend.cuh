@@ -8,14 +8,14 @@
 // o / l, lse = ln 2·(M + log2 l).
 //
 // What bounds it: the bytes of K and V, each read once for all G heads.  So
-//   * a warp works alone on 16 tokens at a time, with a ring of shared-memory
+//   * a warp works alone on 16 or 32 tokens at a time, with a ring of shared-memory
 //     stages of its own filled by 16-byte asynchronous copies, and waits for no
 //     other warp until its row ends;
 //   * both products are swapped: X[tokens, heads] = K·Qᵀ and Oᵀ[dim, heads] =
 //     Vᵀ·P, so K and V are the 16-row operand of the tensor-core step and the
 //     heads its 8 columns: a group of up to 8 heads costs one step per 16 tokens
 //     × 16 elements, and a wider group a second one on the same operand.
-//   * the tokens of all sequences and key heads, in tiles of kKvTile, form one
+//   * the tokens of all sequences and key heads, in tiles of a CTA's step, form one
 //     line that the CTAs share evenly: CTA c takes tiles [c·T/C, (c+1)·T/C).  A
 //     row that several CTAs share is joined by the one that arrives last, in CTA
 //     order, from fp32 partial results in scratch.
@@ -41,7 +41,13 @@ struct AttendShape {
     static constexpr int kElem = kE4m3 ? 1 : 2;
     static constexpr int kRow = kDim * kElem;         // bytes of a token's row in a stage
     static constexpr int kChunks = kRow / 16;         // 16-byte chunks of a row
-    static constexpr int kStage = 2 * kKvStep * kRow;  // keys, then values
+    // Token blocks of 16 a step: two where a row is short, so that a step is
+    // 8 KiB or more and its two chains of tensor-core steps and shuffles overlap
+    // (an 8-bit cache of 128-wide heads ran at 66 % of the copy bandwidth with one).
+    static constexpr int kBlocks = kRow <= 128 ? 2 : 1;
+    static constexpr int kStep = 16 * kBlocks;        // tokens of a warp's step
+    static constexpr int kTile = kKvWarps * kStep;    // unit of the work shared between CTAs
+    static constexpr int kStage = 2 * kStep * kRow;   // keys, then values
     static constexpr int kHeads = 8 * kNT;
     static constexpr int kJoin = kKvWarps * kHeads * kDim * 4;  // the warps' sums, fp32
     static constexpr int kSmall = kKvWarps * kHeads * 8 + 64;   // their maxima and sums of weights; flags
@@ -103,8 +109,10 @@ struct AttendCursor {
 struct AttendSegment {
     int unit, first, last;  // tokens [first, last) of the cursor's sequence; last <= n
     int64_t row_begin;      // the row's first tile on the line
+    int64_t tiles;          // of the segment
 };
 
+template <int kStep>
 __device__ __forceinline__ void read_length(const KvAttendParams &p, int b, AttendCursor &c) {
     const int64_t most = p.cache.table_width * p.cache.page_size;
     int n = p.seq_lens[b];
@@ -114,29 +122,98 @@ __device__ __forceinline__ void read_length(const KvAttendParams &p, int b, Atte
     }
     c.n = n;
     c.low = p.window > 0 && n > p.window ? n - static_cast<int>(p.window) : 0;
-    c.tiles = (n - (c.low & ~(kKvStep - 1)) + kKvTile - 1) / kKvTile;
+    constexpr int kTile = kKvWarps * kStep;
+    c.tiles = (n - (c.low & ~(kStep - 1)) + kTile - 1) / kTile;
 }
 
 // Moves the cursor to the sequence that holds tile `pos` (which exists).
+template <int kStep>
 __device__ __forceinline__ void seek(const KvAttendParams &p, AttendCursor &c, int64_t pos) {
     while (pos >= c.base + c.tiles * p.units) {
         c.base += c.tiles * p.units;
         ++c.b;
-        read_length(p, c.b, c);
+        read_length<kStep>(p, c.b, c);
     }
 }
 
 // The part of tile range [pos, end) that lies in pos's row.
-__device__ __forceinline__ AttendSegment segment_at(const KvAttendParams &p, const AttendCursor &c, int64_t pos,
-                                                    int64_t end) {
+template <int kStep>
+__device__ __forceinline__ AttendSegment segment_at(const AttendCursor &c, int64_t pos, int64_t end) {
+    constexpr int kTile = kKvWarps * kStep;
     AttendSegment s;
     s.unit = static_cast<int>((pos - c.base) / c.tiles);
     s.row_begin = c.base + s.unit * c.tiles;
     const int64_t k0 = pos - s.row_begin, k1 = end - s.row_begin < c.tiles ? end - s.row_begin : c.tiles;
-    const int start = c.low & ~(kKvStep - 1);
-    s.first = start + static_cast<int>(k0) * kKvTile;
-    s.last = k1 == c.tiles ? c.n : start + static_cast<int>(k1) * kKvTile;
+    const int start = c.low & ~(kStep - 1);
+    s.first = start + static_cast<int>(k0) * kTile;
+    s.last = k1 == c.tiles ? c.n : start + static_cast<int>(k1) * kTile;
+    s.tiles = k1 - k0;
     return s;
+}
+
+// Joins the partial results in slots slot(0) .. slot(count - 1), in that order:
+// this thread's head h and elements d0, d0 + kDimStep, ..  Eight parts' loads
+// are in flight at a time.
+template <int kHeads, int kDim, int kPer, int kDimStep, typename Slot>
+__device__ __forceinline__ void join_parts(const float *partials, int count, Slot slot, int h, int d0, float &M, float &L,
+                                           float (&acc)[kPer]) {
+    constexpr int kPart = kHeads * (kDim + 2), kAtOnce = 64 / kPer < 8 ? 64 / kPer : 8;
+    M = -INFINITY;
+    L = 0.f;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+    for (int c = 0; c < count; c += kAtOnce) {
+        float m[kAtOnce], l[kAtOnce], o[kAtOnce][kPer];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const float *from = partials + slot(c + i < count ? c + i : c) * kPart + h;
+            m[i] = c + i < count ? __ldcg(from) : -INFINITY;
+            l[i] = __ldcg(from + kHeads);
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) o[i][k] = __ldcg(from + (2 + d0 + k * kDimStep) * kHeads);
+        }
+        float top = M;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) top = fmaxf(top, m[i]);
+        const float base = top == -INFINITY ? 0.f : top, keep = exp2_fast(M - base);
+        M = top;
+        L *= keep;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) acc[k] *= keep;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const float f = exp2_fast(m[i] - base);
+            L += f * l[i];
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) acc[k] += f * o[i][k];
+        }
+    }
+}
+
+// A thread's elements of a partial result to slot `at`, the CTA's last write
+// before it says so; true for the last of `expected` arrivals at `counter`.
+template <int kHeads, int kDim, int kPer, int kDimStep>
+__device__ __forceinline__ bool leave_part(float *partials, int64_t at, uint32_t *counter, int expected, int h, int d0, float M,
+                                           float L, const float (&acc)[kPer], int *flag) {
+    float *part = partials + at * (kHeads * (kDim + 2)) + h;
+    if (d0 == 0) {
+        __stcg(part, M);
+        __stcg(part + kHeads, L);
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) __stcg(part + (2 + d0 + k * kDimStep) * kHeads, acc[k]);
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const bool last = atomicAdd(counter, 1u) == static_cast<uint32_t>(expected - 1);
+        if (last) *counter = 0;  // as every run finds it
+        *flag = last;
+    }
+    __syncthreads();
+    const bool last = *flag != 0;
+    if (last) __threadfence();
+    __syncthreads();  // the flag is free again
+    return last;
 }
 
 template <bool kE4m3, int kDim, int kNT>
@@ -144,6 +221,7 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
     using Shape = AttendShape<kE4m3, kDim, kNT>;
     constexpr int kHeads = Shape::kHeads, kStages = Shape::kStages, kRow = Shape::kRow;
     constexpr int kSteps = kDim / 16;  // 16-wide steps over a head
+    constexpr int kStep = Shape::kStep, kBlocks = Shape::kBlocks;
     extern __shared__ __align__(1024) uint8_t smem[];
     griddep_launch_dependents();
     const KvCacheView &cache = p.cache;
@@ -174,7 +252,7 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
         int64_t mine = 0;
         for (int b = tid * run; b < B && b < (tid + 1) * run; ++b) {
             AttendCursor c;
-            read_length(p, b, c);
+            read_length<kStep>(p, b, c);
             mine += c.tiles * p.units;
         }
         int64_t incl = mine;
@@ -205,8 +283,8 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
         if (pos < end) {
             cur.base = low > 0 ? sums[low - 1] : 0;
             cur.b = low * run;
-            read_length(p, cur.b, cur);
-            seek(p, cur, pos);
+            read_length<kStep>(p, cur.b, cur);
+            seek<kStep>(p, cur, pos);
         }
         __syncthreads();  // `sums` is the join buffer
     }
@@ -214,7 +292,7 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
     // Sequences without tokens have no tiles: their rows are written here.
     for (int b = blockIdx.x; b < B; b += gridDim.x) {
         AttendCursor c;
-        read_length(p, b, c);
+        read_length<kStep>(p, b, c);
         if (c.n > 0) continue;
         for (int i = tid; i < p.q_heads * cache.head_dim; i += kKvThreads) p.out[b * p.out_stride + i] = 0;
         if (p.lse)
@@ -225,26 +303,25 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
     // ---- loading: a cursor of its own, up to kStages - 1 steps ahead.
     AttendCursor lcur = cur;
     int64_t lpos = pos;
-    AttendSegment lseg = segment_at(p, lcur, lpos, end);
-    int ltok = lseg.first + warp * kKvStep;  // first token of the step to load next
+    AttendSegment lseg = segment_at<kStep>(lcur, lpos, end);
+    int ltok = lseg.first + warp * kStep;  // first token of the step to load next
     bool lmore = true;
     int64_t lhead = 0;  // the row's head in the cache
-    int lpage = -1;     // page of token ltok + lane (lanes 0..15), -1: not attended
+    int lpage = -1;     // page of token ltok + lane % kStep, -1: not attended
     int lplace = 0;
     auto settle = [&]() {  // moves to the next step that exists and asks for its pages
         while (ltok >= lseg.last) {
-            lpos += (lseg.last == lcur.n ? lcur.tiles - (lpos - lseg.row_begin)
-                                         : (lseg.last - (lcur.low & ~(kKvStep - 1))) / kKvTile - (lpos - lseg.row_begin));
+            lpos += lseg.tiles;
             if (lpos >= end) {
                 lmore = false;
                 return;
             }
-            seek(p, lcur, lpos);
-            lseg = segment_at(p, lcur, lpos, end);
-            ltok = lseg.first + warp * kKvStep;
+            seek<kStep>(p, lcur, lpos);
+            lseg = segment_at<kStep>(lcur, lpos, end);
+            ltok = lseg.first + warp * kStep;
         }
         lhead = static_cast<int64_t>(lseg.unit / p.chunks) * cache.head_stride;
-        const int t = ltok + (lane & 15);
+        const int t = ltok + (lane & (kStep - 1));
         lpage = -1;
         if (t >= lcur.low && t < lseg.last) {
             const uint32_t q = static_cast<uint32_t>(t) / static_cast<uint32_t>(cache.page_size);
@@ -257,6 +334,7 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
         }
     };
     settle();
+    constexpr uint32_t kAll = kStep == 32 ? 0xffffffffu : 0xffffu;
     uint32_t valid[kStages];  // tokens of each stage that are attended, a bit each
 #pragma unroll
     for (int s = 0; s < kStages; ++s) valid[s] = 0;
@@ -265,24 +343,24 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
         uint32_t bits = 0;
         if (lmore) {
             const bool ok = lpage >= 0;
-            bits = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+            bits = __ballot_sync(0xffffffffu, ok) & kAll;
             const int64_t offset =
                 ok ? lpage * cache.page_stride + lplace * cache.token_stride + lhead : 0;
             const uint32_t to = ring + slot * Shape::kStage;
             const uint8_t *kc = static_cast<const uint8_t *>(p.k_cache), *vc = static_cast<const uint8_t *>(p.v_cache);
             constexpr int kRowsAtOnce = 32 / (Shape::kChunks < 32 ? Shape::kChunks : 32);
 #pragma unroll
-            for (int i = 0; i < kKvStep / kRowsAtOnce; ++i) {
+            for (int i = 0; i < kStep / kRowsAtOnce; ++i) {
                 const int r = i * kRowsAtOnce + lane / Shape::kChunks, c = lane % Shape::kChunks;
                 const int64_t at = __shfl_sync(0xffffffffu, offset, r) * Shape::kElem + c * 16;
                 const bool fill = (bits >> r) & 1u;
                 if (c < row_chunks) {
                     const uint32_t d = to + chunk_at<kRow>(r, c);
                     cp_async16(d, kc + (fill ? at : 0), fill);
-                    cp_async16(d + kKvStep * kRow, vc + (fill ? at : 0), fill);
+                    cp_async16(d + kStep * kRow, vc + (fill ? at : 0), fill);
                 }
             }
-            ltok += kKvWarps * kKvStep;
+            ltok += Shape::kTile;
             settle();
         }
 #pragma unroll
@@ -296,14 +374,11 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
 
     // ---- computing, row by row.
     while (pos < end) {
-        seek(p, cur, pos);
-        const AttendSegment seg = segment_at(p, cur, pos, end);
+        seek<kStep>(p, cur, pos);
+        const AttendSegment seg = segment_at<kStep>(cur, pos, end);
         const int hk = seg.unit / p.chunks, chunk = seg.unit % p.chunks;
         const int head0 = hk * p.group + chunk * p.chunk_heads;
         const int heads = min(p.chunk_heads, p.group - chunk * p.chunk_heads);
-        const int tiles = static_cast<int>((seg.last == cur.n ? cur.tiles : (seg.last - (cur.low & ~(kKvStep - 1))) / kKvTile) -
-                                           (pos - seg.row_begin));
-
         // Queries as the second operand: column (head) g, rows (elements) of lane j.
         uint32_t qf[kNT][kSteps][2];
         float factor[kNT][2];  // logit to exponent of two, of this lane's heads 2j, 2j + 1
@@ -362,7 +437,7 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
             for (int d = 0; d < kSteps; ++d) o[t][d][0] = o[t][d][1] = o[t][d][2] = o[t][d][3] = 0.f;
         }
 
-        for (int tok = seg.first + warp * kKvStep; tok < seg.last; tok += kKvWarps * kKvStep) {
+        for (int tok = seg.first + warp * kStep; tok < seg.last; tok += Shape::kTile) {
             cp_async_wait<kStages - 2>();
             __syncwarp();
             uint32_t bits = 0;
@@ -371,53 +446,67 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
                 if (s == slot) bits = valid[s];
             load(slot_in == kStages ? 0 : slot_in);
             slot_in = slot_in == kStages ? 1 : slot_in + 1;
-            const uint32_t ks = ring + slot * Shape::kStage, vs = ks + kKvStep * kRow;
+            const uint32_t ks = ring + slot * Shape::kStage, vs = ks + kStep * kRow;
             slot = slot + 1 == kStages ? 0 : slot + 1;
 
-            float x[kNT][4];
+            float x[kBlocks][kNT][4];
 #pragma unroll
-            for (int t = 0; t < kNT; ++t) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
+            for (int n = 0; n < kBlocks; ++n)
+#pragma unroll
+                for (int t = 0; t < kNT; ++t) x[n][t][0] = x[n][t][1] = x[n][t][2] = x[n][t][3] = 0.f;
             if constexpr (!kE4m3) {
 #pragma unroll
-                for (int k = 0; k < kSteps; ++k) {
-                    uint32_t a[4];
-                    ldsm_x4(a, ks + chunk_at<kRow>(lane & 15, 2 * k + (lane >> 4)));
+                for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-                    for (int t = 0; t < kNT; ++t) mma16816<false>(x[t], a[0], a[1], a[2], a[3], qf[t][k][0], qf[t][k][1]);
-                }
+                    for (int n = 0; n < kBlocks; ++n) {
+                        uint32_t a[4];
+                        ldsm_x4(a, ks + chunk_at<kRow>(16 * n + (lane & 15), 2 * k + (lane >> 4)));
+#pragma unroll
+                        for (int t = 0; t < kNT; ++t)
+                            mma16816<false>(x[n][t], a[0], a[1], a[2], a[3], qf[t][k][0], qf[t][k][1]);
+                    }
             } else {
                 // A 16-byte chunk holds 16 elements: lane j of a row receives
                 // elements 4j .. 4j + 3, so the first pair stands at the
                 // step's rows 2j, 2j + 1 and the second at rows 2j + 8, + 9.
 #pragma unroll
-                for (int k = 0; k < kSteps; k += 2) {
-                    uint32_t a[4];
-                    ldsm_x4(a, ks + chunk_at<kRow>(lane & 15, k + (lane >> 4)));
+                for (int k = 0; k < kSteps; k += 2)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t up = a[2 * i], dn = a[2 * i + 1];
-                        const uint32_t a0 = e4m3x2_to_half2(up), a2 = e4m3x2_to_half2(up >> 16);
-                        const uint32_t a1 = e4m3x2_to_half2(dn), a3 = e4m3x2_to_half2(dn >> 16);
+                    for (int n = 0; n < kBlocks; ++n) {
+                        uint32_t a[4];
+                        ldsm_x4(a, ks + chunk_at<kRow>(16 * n + (lane & 15), k + (lane >> 4)));
 #pragma unroll
-                        for (int t = 0; t < kNT; ++t)
-                            mma16816<true>(x[t], a0, a1, a2, a3, qf[t][k + i][0], qf[t][k + i][1]);
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t up = a[2 * i], dn = a[2 * i + 1];
+                            const uint32_t a0 = e4m3x2_to_half2(up), a2 = e4m3x2_to_half2(up >> 16);
+                            const uint32_t a1 = e4m3x2_to_half2(dn), a3 = e4m3x2_to_half2(dn >> 16);
+#pragma unroll
+                            for (int t = 0; t < kNT; ++t)
+                                mma16816<true>(x[n][t], a0, a1, a2, a3, qf[t][k + i][0], qf[t][k + i][1]);
+                        }
                     }
-                }
             }
 
-            // x: tokens g (0, 1) and g + 8 (2, 3), heads 2j and 2j + 1.
-            uint32_t high[kNT][2], low[kNT][2];
+            // x: tokens g (0, 1) and g + 8 (2, 3) of each block, heads 2j and 2j + 1.
+            uint32_t high[kBlocks][kNT][2], low[kBlocks][kNT][2];
 #pragma unroll
             for (int t = 0; t < kNT; ++t) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[t][i] *= factor[t][i & 1];
-                    if (bits != 0xffffu && !((bits >> (g + 8 * (i >> 1))) & 1u)) x[t][i] = -INFINITY;
+                for (int n = 0; n < kBlocks; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[n][t][i] *= factor[t][i & 1];
+                if (bits != kAll) {
+#pragma unroll
+                    for (int n = 0; n < kBlocks; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (!((bits >> (16 * n + g + 8 * (i >> 1))) & 1u)) x[n][t][i] = -INFINITY;
                 }
                 float keep[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float top = fmaxf(x[t][h], x[t][2 + h]);
+                    float top = fmaxf(x[0][t][h], x[0][t][2 + h]);
+                    if constexpr (kBlocks == 2) top = fmaxf(top, fmaxf(x[1][t][h], x[1][t][2 + h]));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -425,9 +514,13 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
                     const float base = top == -INFINITY ? 0.f : top;  // no token yet: every weight is 0
                     keep[h] = exp2_fast(m[t][h] - base);
                     m[t][h] = top;
-                    x[t][h] = exp2_fast(x[t][h] - base);
-                    x[t][2 + h] = exp2_fast(x[t][2 + h] - base);
-                    l[t][h] = l[t][h] * keep[h] + x[t][h] + x[t][2 + h];
+                    l[t][h] *= keep[h];
+#pragma unroll
+                    for (int n = 0; n < kBlocks; ++n) {
+                        x[n][t][h] = exp2_fast(x[n][t][h] - base);
+                        x[n][t][2 + h] = exp2_fast(x[n][t][2 + h] - base);
+                        l[t][h] += x[n][t][h] + x[n][t][2 + h];
+                    }
                 }
                 if (__any_sync(0xffffffffu, keep[0] != 1.f || keep[1] != 1.f)) {
 #pragma unroll
@@ -439,44 +532,50 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t hi, lo;
-                    split2<kE4m3>(x[t][2 * i], x[t][2 * i + 1], hi, lo);
-                    high[t][i] = transpose8x8(hi);
-                    low[t][i] = transpose8x8(lo);
-                }
+                for (int n = 0; n < kBlocks; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t hi, lo;
+                        split2<kE4m3>(x[n][t][2 * i], x[n][t][2 * i + 1], hi, lo);
+                        high[n][t][i] = transpose8x8(hi);
+                        low[n][t][i] = transpose8x8(lo);
+                    }
             }
             if constexpr (!kE4m3) {
 #pragma unroll
-                for (int d = 0; d < kSteps; ++d) {
-                    uint32_t a[4];
-                    ldsm_x4_t(a, vs + chunk_at<kRow>((lane & 7) + ((lane >> 4) << 3), 2 * d + ((lane >> 3) & 1)));
+                for (int n = 0; n < kBlocks; ++n)
 #pragma unroll
-                    for (int t = 0; t < kNT; ++t) {
-                        mma16816<false>(o[t][d], a[0], a[1], a[2], a[3], high[t][0], high[t][1]);
-                        mma16816<false>(o[t][d], a[0], a[1], a[2], a[3], low[t][0], low[t][1]);
+                    for (int d = 0; d < kSteps; ++d) {
+                        uint32_t a[4];
+                        ldsm_x4_t(a, vs + chunk_at<kRow>(16 * n + (lane & 7) + ((lane >> 4) << 3), 2 * d + ((lane >> 3) & 1)));
+#pragma unroll
+                        for (int t = 0; t < kNT; ++t) {
+                            mma16816<false>(o[t][d], a[0], a[1], a[2], a[3], high[n][t][0], high[n][t][1]);
+                            mma16816<false>(o[t][d], a[0], a[1], a[2], a[3], low[n][t][0], low[n][t][1]);
+                        }
                     }
-                }
             } else {
                 // Transposed in pairs of elements: a lane receives elements
                 // 2g, 2g + 1 of tokens 2j, 2j + 1.  Rows 0..7 of the step take
                 // the even elements, rows 8..15 the odd ones.
 #pragma unroll
-                for (int d = 0; d < kSteps; d += 2) {
-                    uint32_t a[4];
-                    ldsm_x4_t(a, vs + chunk_at<kRow>((lane & 7) + (((lane >> 3) & 1) << 3), d + (lane >> 4)));
+                for (int n = 0; n < kBlocks; ++n)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t lo8 = __byte_perm(a[2 * i], 0, 0x3120), hi8 = __byte_perm(a[2 * i + 1], 0, 0x3120);
-                        const uint32_t a0 = e4m3x2_to_half2(lo8), a1 = e4m3x2_to_half2(lo8 >> 16);
-                        const uint32_t a2 = e4m3x2_to_half2(hi8), a3 = e4m3x2_to_half2(hi8 >> 16);
+                    for (int d = 0; d < kSteps; d += 2) {
+                        uint32_t a[4];
+                        ldsm_x4_t(a, vs + chunk_at<kRow>(16 * n + (lane & 7) + (((lane >> 3) & 1) << 3), d + (lane >> 4)));
 #pragma unroll
-                        for (int t = 0; t < kNT; ++t) {
-                            mma16816<true>(o[t][d + i], a0, a1, a2, a3, high[t][0], high[t][1]);
-                            mma16816<true>(o[t][d + i], a0, a1, a2, a3, low[t][0], low[t][1]);
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t lo8 = __byte_perm(a[2 * i], 0, 0x3120), hi8 = __byte_perm(a[2 * i + 1], 0, 0x3120);
+                            const uint32_t a0 = e4m3x2_to_half2(lo8), a1 = e4m3x2_to_half2(lo8 >> 16);
+                            const uint32_t a2 = e4m3x2_to_half2(hi8), a3 = e4m3x2_to_half2(hi8 >> 16);
+#pragma unroll
+                            for (int t = 0; t < kNT; ++t) {
+                                mma16816<true>(o[t][d + i], a0, a1, a2, a3, high[n][t][0], high[n][t][1]);
+                                mma16816<true>(o[t][d + i], a0, a1, a2, a3, low[n][t][0], low[n][t][1]);
+                            }
                         }
                     }
-                }
             }
         }
 
@@ -521,44 +620,34 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
         }
 
         bool write = true;
-        if (tiles != cur.tiles) {
+        if (seg.tiles != cur.tiles) {
             // Other CTAs own the rest of the row: leave this part in scratch,
             // and join all parts if the others are there already.
-            constexpr int kPart = kHeads * (kDim + 2);
-            const int64_t C = ctas, T = total;
             const int64_t row_end = seg.row_begin + cur.tiles;
-            const int64_t c0 = ((seg.row_begin + 1) * C - 1) / T, c1 = (row_end * C - 1) / T;  // first and last owner
-            const int64_t c0_slot = T * c0 / C < seg.row_begin ? 1 : 0;  // the row is the last of its first owner's
-            const int64_t mine = blockIdx.x * int64_t(2) + (blockIdx.x == c0 ? c0_slot : 0);
-            float *part = p.partials + mine * kPart;
-            if (d0 == 0) {
-                __stcg(part + h, M);
-                __stcg(part + kHeads + h, L);
-            }
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) __stcg(part + (2 + d0 + k * kDimStep) * kHeads + h, acc[k]);
-            __threadfence();
-            __syncthreads();
+            const int c0 = static_cast<int>(((seg.row_begin + 1) * ctas - 1) / total);  // first and last owner
+            const int c1 = static_cast<int>((row_end * ctas - 1) / total);
+            const int first_slot = total * c0 / ctas < seg.row_begin ? 1 : 0;  // the row is the last of its first owner's
+            const int parts = c1 - c0 + 1, mine = static_cast<int>(blockIdx.x) - c0;
+            auto slot = [&](int part) { return int64_t(2) * (c0 + part) + (part == 0 ? first_slot : 0); };
             uint32_t *counter = p.counters + static_cast<int64_t>(cur.b) * p.units + seg.unit;
-            if (tid == 0) *flag = atomicAdd(counter, 1u) == static_cast<uint32_t>(c1 - c0);
-            __syncthreads();
-            write = *flag != 0;
-            if (write) {
-                __threadfence();
-                if (tid == 0) *counter = 0;
-                M = -INFINITY;
-                for (int64_t c = c0; c <= c1; ++c)
-                    M = fmaxf(M, __ldcg(p.partials + (2 * c + (c == c0 ? c0_slot : 0)) * kPart + h));
-                const float all = M == -INFINITY ? 0.f : M;
-                L = 0.f;
-#pragma unroll
-                for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-                for (int64_t c = c0; c <= c1; ++c) {
-                    const float *from = p.partials + (2 * c + (c == c0 ? c0_slot : 0)) * kPart;
-                    const float f = exp2_fast(__ldcg(from + h) - all);
-                    L += f * __ldcg(from + kHeads + h);
-#pragma unroll
-                    for (int k = 0; k < kPer; ++k) acc[k] += f * __ldcg(from + (2 + d0 + k * kDimStep) * kHeads + h);
+            if (parts <= kKvJoinOnce) {
+                write = leave_part<kHeads, kDim, kPer, kDimStep>(p.partials, slot(mine), counter, parts, h, d0, M, L, acc, flag);
+                if (write) join_parts<kHeads, kDim, kPer, kDimStep>(p.partials, parts, slot, h, d0, M, L, acc);
+            } else {
+                // Many parts: in groups, each joined into its first part's
+                // slot by its own last arrival, and then the groups.
+                const int g0 = mine / kKvJoinGroup * kKvJoinGroup, in_group = min(kKvJoinGroup, parts - g0);
+                write = leave_part<kHeads, kDim, kPer, kDimStep>(p.partials, slot(mine), p.group_counters + slot(g0), in_group, h,
+                                                                 d0, M, L, acc, flag);
+                if (write) {
+                    join_parts<kHeads, kDim, kPer, kDimStep>(
+                        p.partials, in_group, [&](int i) { return slot(g0 + i); }, h, d0, M, L, acc);
+                    __syncthreads();  // every thread has read the slot that is written next
+                    const int groups = (parts + kKvJoinGroup - 1) / kKvJoinGroup;
+                    write = leave_part<kHeads, kDim, kPer, kDimStep>(p.partials, slot(g0), counter, groups, h, d0, M, L, acc, flag);
+                    if (write)
+                        join_parts<kHeads, kDim, kPer, kDimStep>(
+                            p.partials, groups, [&](int i) { return slot(i * kKvJoinGroup); }, h, d0, M, L, acc);
                 }
             }
         }
@@ -574,7 +663,7 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
                     L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
         }
         __syncthreads();  // the join buffer and the flag are free again
-        pos += tiles;
+        pos += seg.tiles;
     }
     cp_async_wait<0>();
 }

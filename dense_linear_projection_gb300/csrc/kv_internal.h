@@ -11,8 +11,9 @@ namespace projgb {
 constexpr int kKvMaxDim = 256;
 constexpr int kKvWarps = 4;                        // warps of an attention CTA
 constexpr int kKvThreads = 32 * kKvWarps;
-constexpr int kKvStep = 16;                        // tokens a warp takes at a time
-constexpr int kKvTile = kKvWarps * kKvStep;        // unit of the work shared between CTAs
+// Parts of a row that one CTA joins at once; more are joined in groups first
+// (one CTA reads a part of 4 KiB in about 50 ns once its loads overlap).
+constexpr int kKvJoinOnce = 64, kKvJoinGroup = 16;
 
 // Bits of the cache handle's status word: what a kernel found out of range.
 constexpr int kKvErrPosition = 1 << 0;  // position past the page table or the rope table
@@ -62,7 +63,8 @@ struct KvAttendParams {
     int32_t chunks;       // rows of a key head
     int32_t units;        // kv_heads · chunks: rows of a sequence
     float *partials;      // [CTA][first, last row][2 + dim][heads]
-    uint32_t *counters;   // [sequence][unit], zero between runs
+    uint32_t *counters;        // [sequence][unit], zero between runs
+    uint32_t *group_counters;  // [slot of a partial result], zero between runs
     uint16_t *out;
     float *lse;
     int *status;

@@ -68,6 +68,13 @@ def test_windows(window):
     run([301, 0, 16, 2000, 1], 8, 4, 128, 16, window=window, dtype="e4m3")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,heads,kv_heads,dim", [([30000], 8, 1, 128), ([100, 40000, 3], 4, 1, 64), ([9000, 17000], 16, 1, 128), ([15000], 8, 1, 256)])
+def test_rows_of_many_parts(lens, heads, kv_heads, dim, dtype):
+    # One key head: a row is shared by up to every CTA of the launch, and its parts are joined in groups.
+    run(lens, heads, kv_heads, dim, 16, dtype=dtype)
+
+
 def test_scales():
     for scale in (1.0, -0.2, 1e-6, 0.0):
         import torch
