@@ -16,7 +16,7 @@
 //     heads its 8 columns: a group of up to 8 heads costs one step per 16 tokens
 //     × 16 elements, and a wider group a second one on the same operand.
 //   * the tokens of all sequences and key heads, in tiles of a CTA's step, form one
-//     line that the CTAs share evenly: CTA c takes tiles [c·T/C, (c+1)·T/C).  A
+//     line that the CTAs share evenly: CTA c takes places [c·T/C, (c+1)·T/C).  A
 //     row that several CTAs share is joined by the one that arrives last, in CTA
 //     order, from fp32 partial results in scratch.
 //
@@ -49,7 +49,7 @@ struct AttendShape {
     static constexpr int kTile = kKvWarps * kStep;    // unit of the work shared between CTAs
     static constexpr int kStage = 2 * kStep * kRow;   // keys, then values
     static constexpr int kHeads = 8 * kNT;
-    static constexpr int kJoin = kKvWarps * kHeads * kDim * 4;  // the warps' sums, fp32
+    static constexpr int kJoin = kKvWarps * kHeads * (kDim + 4) * 4;  // the warps' sums, fp32
     static constexpr int kSmall = kKvWarps * kHeads * 8 + 64;   // their maxima and sums of weights; flags
     // Two CTAs an SM (one for 256-wide heads): while one joins its warps, the
     // other streams.
@@ -98,18 +98,32 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     return r * kRow + ((c ^ ((r >> 1) & 3)) << 4);  // 64-byte rows, two to a 128-byte line
 }
 
-// A place on the line of tiles: sequence b, whose tiles begin at `base` and
-// number `tiles` for each of the `units` (key head, chunk of query heads).
+// a·b / c and a / b for b < 512 and c < 512 in the first: 32-bit where they fit
+// (a 64-bit division takes about 0.1 us, at the start of every row).
+__device__ __forceinline__ int64_t share_of(int64_t a, uint32_t b, uint32_t c) {
+    if (a < (int64_t(1) << 23)) return static_cast<uint32_t>(a) * b / c;
+    return a * b / c;
+}
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
+// A place on the line of work: sequence b, whose rows (one for each of the
+// `units`: key head, chunk of query heads) begin at `base`.  A row is kKvRowCost
+// places for its start and its join, which take about as long as a tile, and
+// then a place for each of its `tiles`.
 struct AttendCursor {
-    int64_t base = 0, tiles = 0;
+    int64_t base = 0, tiles = 0, span = 0;
     int b = 0;
     int low = 0, n = 0;  // the tokens attended are [low, n)
 };
 
 struct AttendSegment {
     int unit, first, last;  // tokens [first, last) of the cursor's sequence; last <= n
-    int64_t row_begin;      // the row's first tile on the line
-    int64_t tiles;          // of the segment
+    int64_t row_begin;      // the row's first place on the line
+    int64_t places;         // the segment's length on the line
+    int64_t tiles;          // of the segment: 0 where it holds only the row's start
 };
 
 template <int kStep>
@@ -124,94 +138,130 @@ __device__ __forceinline__ void read_length(const KvAttendParams &p, int b, Atte
     c.low = p.window > 0 && n > p.window ? n - static_cast<int>(p.window) : 0;
     constexpr int kTile = kKvWarps * kStep;
     c.tiles = (n - (c.low & ~(kStep - 1)) + kTile - 1) / kTile;
+    c.span = c.tiles > 0 ? c.tiles + kKvRowCost : 0;
 }
 
-// Moves the cursor to the sequence that holds tile `pos` (which exists).
+// Moves the cursor to the sequence that holds place `pos` (which exists).
 template <int kStep>
 __device__ __forceinline__ void seek(const KvAttendParams &p, AttendCursor &c, int64_t pos) {
-    while (pos >= c.base + c.tiles * p.units) {
-        c.base += c.tiles * p.units;
+    while (pos >= c.base + c.span * p.units) {
+        c.base += c.span * p.units;
         ++c.b;
         read_length<kStep>(p, c.b, c);
     }
 }
 
-// The part of tile range [pos, end) that lies in pos's row.
+// The part of places [pos, end) that lies in pos's row.
 template <int kStep>
 __device__ __forceinline__ AttendSegment segment_at(const AttendCursor &c, int64_t pos, int64_t end) {
     constexpr int kTile = kKvWarps * kStep;
     AttendSegment s;
-    s.unit = static_cast<int>((pos - c.base) / c.tiles);
-    s.row_begin = c.base + s.unit * c.tiles;
-    const int64_t k0 = pos - s.row_begin, k1 = end - s.row_begin < c.tiles ? end - s.row_begin : c.tiles;
+    s.unit = static_cast<int>(divide(pos - c.base, c.span));
+    s.row_begin = c.base + s.unit * c.span;
+    const int64_t from = pos - s.row_begin, to = end - s.row_begin < c.span ? end - s.row_begin : c.span;
+    const int64_t k0 = from > kKvRowCost ? from - kKvRowCost : 0, k1 = to > kKvRowCost ? to - kKvRowCost : 0;
     const int start = c.low & ~(kStep - 1);
     s.first = start + static_cast<int>(k0) * kTile;
     s.last = k1 == c.tiles ? c.n : start + static_cast<int>(k1) * kTile;
+    s.places = to - from;
     s.tiles = k1 - k0;
     return s;
 }
 
-// Joins the partial results in slots slot(0) .. slot(count - 1), in that order:
-// this thread's head h and elements d0, d0 + kDimStep, ..  Eight parts' loads
-// are in flight at a time.
-template <int kHeads, int kDim, int kPer, int kDimStep, typename Slot>
-__device__ __forceinline__ void join_parts(const float *partials, int count, Slot slot, int h, int d0, float &M, float &L,
-                                           float (&acc)[kPer]) {
-    constexpr int kPart = kHeads * (kDim + 2), kAtOnce = 64 / kPer < 8 ? 64 / kPer : 8;
-    M = -INFINITY;
-    L = 0.f;
+// What a thread holds of a row while it is joined: four elements of kPer heads.
+template <int kHeads, int kDim>
+struct JoinPart {
+    static constexpr int kLanes = kDim / 4;                      // threads of a head
+    static constexpr int kHeadStep = kKvThreads / kLanes;        // heads at a time
+    static constexpr int kPer = kHeads / kHeadStep;
+    static constexpr int kPitch = kDim + 4;                      // of a head in the warps' sums: conflict-free
+    static constexpr int kFloats = kHeads * (kDim + 2);          // of a partial result: maxima, sums of weights, [head][dim]
+    static_assert(kPer >= 1, "every thread has an element");
+    float m[kPer], l[kPer];
+    float4 o[kPer];
+
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-    for (int c = 0; c < count; c += kAtOnce) {
-        float m[kAtOnce], l[kAtOnce], o[kAtOnce][kPer];
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-            const float *from = partials + slot(c + i < count ? c + i : c) * kPart + h;
-            m[i] = c + i < count ? __ldcg(from) : -INFINITY;
-            l[i] = __ldcg(from + kHeads);
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) o[i][k] = __ldcg(from + (2 + d0 + k * kDimStep) * kHeads);
+        for (int k = 0; k < kPer; ++k) {
+            m[k] = -INFINITY;
+            l[k] = 0.f;
+            o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        float top = M;
+    }
+};
+
+__device__ __forceinline__ float finite_or_zero(float top) { return top == -INFINITY ? 0.f : top; }
+
+// Joins the partial results in slots slot(0) .. slot(count - 1), in that order;
+// the loads of several are in flight at a time.  Heads past `heads` are unused.
+template <int kHeads, int kDim, typename Slot>
+__device__ __forceinline__ void join_parts(const float *partials, int count, Slot slot, int heads, JoinPart<kHeads, kDim> &r) {
+    using Part = JoinPart<kHeads, kDim>;
+    constexpr int kAtOnce = 8;
+    const int h0 = threadIdx.x / Part::kLanes, d = threadIdx.x % Part::kLanes * 4;
+    r.clear();
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) top = fmaxf(top, m[i]);
-        const float base = top == -INFINITY ? 0.f : top, keep = exp2_fast(M - base);
-        M = top;
-        L *= keep;
+    for (int k = 0; k < Part::kPer; ++k) {
+        const int h = h0 + k * Part::kHeadStep;
+        if (h >= heads) break;
+        for (int c = 0; c < count; c += kAtOnce) {
+            float m[kAtOnce], l[kAtOnce];
+            float4 o[kAtOnce];
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) acc[k] *= keep;
+            for (int i = 0; i < kAtOnce; ++i) {
+                const float *from = partials + slot(c + i < count ? c + i : c) * Part::kFloats;
+                m[i] = __ldcg(from + h);
+                l[i] = __ldcg(from + kHeads + h);
+                o[i] = __ldcg(reinterpret_cast<const float4 *>(from + 2 * kHeads + h * kDim + d));
+            }
+            float top = r.m[k];
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-            const float f = exp2_fast(m[i] - base);
-            L += f * l[i];
+            for (int i = 0; i < kAtOnce; ++i) top = fmaxf(top, m[i]);
+            const float base = finite_or_zero(top), keep = exp2_fast(r.m[k] - base);
+            r.m[k] = top;
+            r.l[k] *= keep;
+            r.o[k].x *= keep, r.o[k].y *= keep, r.o[k].z *= keep, r.o[k].w *= keep;
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) acc[k] += f * o[i][k];
+            for (int i = 0; i < kAtOnce; ++i) {
+                if (c + i >= count) break;
+                const float w = exp2_fast(m[i] - base);
+                r.l[k] += w * l[i];
+                r.o[k].x += w * o[i].x, r.o[k].y += w * o[i].y, r.o[k].z += w * o[i].z, r.o[k].w += w * o[i].w;
+            }
         }
     }
 }
 
-// A thread's elements of a partial result to slot `at`, the CTA's last write
-// before it says so; true for the last of `expected` arrivals at `counter`.
-template <int kHeads, int kDim, int kPer, int kDimStep>
-__device__ __forceinline__ bool leave_part(float *partials, int64_t at, uint32_t *counter, int expected, int h, int d0, float M,
-                                           float L, const float (&acc)[kPer], int *flag) {
-    float *part = partials + at * (kHeads * (kDim + 2)) + h;
-    if (d0 == 0) {
-        __stcg(part, M);
-        __stcg(part + kHeads, L);
-    }
+// Writes this CTA's partial result to slot `at` and says so; true for the last
+// of `expected` arrivals at `counter`, which then sees all of theirs.
+template <int kHeads, int kDim>
+__device__ __forceinline__ bool leave_part(float *partials, int64_t at, uint32_t *counter, int expected, int heads,
+                                           const JoinPart<kHeads, kDim> &r, int *flag) {
+    using Part = JoinPart<kHeads, kDim>;
+    const int h0 = threadIdx.x / Part::kLanes, d = threadIdx.x % Part::kLanes * 4;
+    float *part = partials + at * Part::kFloats;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) __stcg(part + (2 + d0 + k * kDimStep) * kHeads, acc[k]);
-    __threadfence();
+    for (int k = 0; k < Part::kPer; ++k) {
+        const int h = h0 + k * Part::kHeadStep;
+        if (h >= heads) break;
+        if (d == 0) {
+            __stcg(part + h, r.m[k]);
+            __stcg(part + kHeads + h, r.l[k]);
+        }
+        __stcg(reinterpret_cast<float4 *>(part + 2 * kHeads + h * kDim + d), r.o[k]);
+    }
     __syncthreads();
     if (threadIdx.x == 0) {
+        __threadfence();  // after the barrier: covers every thread's stores
         const bool last = atomicAdd(counter, 1u) == static_cast<uint32_t>(expected - 1);
-        if (last) *counter = 0;  // as every run finds it
+        if (last) {
+            __threadfence();
+            *counter = 0;  // as every run finds it
+        }
         *flag = last;
     }
     __syncthreads();
     const bool last = *flag != 0;
-    if (last) __threadfence();
     __syncthreads();  // the flag is free again
     return last;
 }
@@ -228,8 +278,8 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, j = lane & 3;
     const uint32_t ring = smem_u32(smem) + warp * kStages * Shape::kStage;
-    float *join = reinterpret_cast<float *>(smem + kKvWarps * kStages * Shape::kStage);  // [warp][dim][head]
-    float *join_m = join + kKvWarps * kHeads * kDim;                                     // [warp][head]
+    float *join = reinterpret_cast<float *>(smem + kKvWarps * kStages * Shape::kStage);  // [warp][head][dim + 4]
+    float *join_m = join + kKvWarps * kHeads * (kDim + 4);                                    // [warp][head]
     float *join_l = join_m + kKvWarps * kHeads;
     int *flag = reinterpret_cast<int *>(join_l + kKvWarps * kHeads);
 
@@ -241,77 +291,54 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
     }
     griddep_wait();
 
-    // The line of tiles: every thread sums a run of sequences, and a scan over
-    // the threads gives the total and where this CTA's first tile lies.
+    // The line of work: every lane sums a run of sequences, and a scan over
+    // the lanes (the same in every warp: no barrier) gives the total and where
+    // this CTA's part of it begins.
     const int B = static_cast<int>(p.sequences);
-    const int run = (B + kKvThreads - 1) / kKvThreads;
+    const int run = (B + 31) / 32;
     AttendCursor cur;  // the warp's place in computing
-    int64_t pos, end, total, ctas;
+    int64_t pos, end, total;
+    uint32_t ctas;
     {
-        int64_t *sums = reinterpret_cast<int64_t *>(join);  // [threads] inclusive, before the first join
-        int64_t mine = 0;
-        for (int b = tid * run; b < B && b < (tid + 1) * run; ++b) {
+        int64_t incl = 0;
+        for (int b = lane * run; b < B && b < (lane + 1) * run; ++b) {
             AttendCursor c;
             read_length<kStep>(p, b, c);
-            mine += c.tiles * p.units;
+            incl += c.span * p.units;
         }
-        int64_t incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t other = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += other;
         }
-        sums[tid] = incl;
-        __syncthreads();
-        int64_t before = 0;
-        for (int w = 0; w < warp; ++w) before += sums[32 * w + 31];
-        __syncthreads();
-        sums[tid] = incl + before;
-        __syncthreads();
-        total = sums[kKvThreads - 1];
-        ctas = total < gridDim.x ? total : gridDim.x;  // those that have a tile: each at least one
-        pos = blockIdx.x < ctas ? total * blockIdx.x / ctas : total;
-        end = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : total;
-        int low = 0, high = kKvThreads - 1;  // first thread whose inclusive sum is past pos
-        while (low < high) {
-            const int mid = (low + high) / 2;
-            if (sums[mid] > pos)
-                high = mid;
-            else
-                low = mid + 1;
-        }
+        total = __shfl_sync(0xffffffffu, incl, 31);
+        ctas = total < gridDim.x ? static_cast<uint32_t>(total) : gridDim.x;  // those that have a place
+        pos = blockIdx.x < ctas ? share_of(total, blockIdx.x, ctas) : total;
+        end = blockIdx.x < ctas ? share_of(total, blockIdx.x + 1, ctas) : total;
         if (pos < end) {
-            cur.base = low > 0 ? sums[low - 1] : 0;
-            cur.b = low * run;
+            // First lane whose inclusive sum is past pos.
+            const int from = __ffs(__ballot_sync(0xffffffffu, incl > pos)) - 1;
+            const int64_t before = __shfl_sync(0xffffffffu, incl, from > 0 ? from - 1 : 0);
+            cur.base = from > 0 ? before : 0;
+            cur.b = from * run;
             read_length<kStep>(p, cur.b, cur);
             seek<kStep>(p, cur, pos);
         }
-        __syncthreads();  // `sums` is the join buffer
     }
-
-    // Sequences without tokens have no tiles: their rows are written here.
-    for (int b = blockIdx.x; b < B; b += gridDim.x) {
-        AttendCursor c;
-        read_length<kStep>(p, b, c);
-        if (c.n > 0) continue;
-        for (int i = tid; i < p.q_heads * cache.head_dim; i += kKvThreads) p.out[b * p.out_stride + i] = 0;
-        if (p.lse)
-            for (int h = tid; h < p.q_heads; h += kKvThreads) p.lse[static_cast<int64_t>(b) * p.q_heads + h] = -INFINITY;
-    }
-    if (pos >= end) return;
 
     // ---- loading: a cursor of its own, up to kStages - 1 steps ahead.
     AttendCursor lcur = cur;
     int64_t lpos = pos;
-    AttendSegment lseg = segment_at<kStep>(lcur, lpos, end);
+    AttendSegment lseg{};
+    bool lmore = pos < end;
+    if (lmore) lseg = segment_at<kStep>(lcur, lpos, end);
     int ltok = lseg.first + warp * kStep;  // first token of the step to load next
-    bool lmore = true;
     int64_t lhead = 0;  // the row's head in the cache
     int lpage = -1;     // page of token ltok + lane % kStep, -1: not attended
     int lplace = 0;
     auto settle = [&]() {  // moves to the next step that exists and asks for its pages
         while (ltok >= lseg.last) {
-            lpos += lseg.tiles;
+            lpos += lseg.places;
             if (lpos >= end) {
                 lmore = false;
                 return;
@@ -333,7 +360,7 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
             }
         }
     };
-    settle();
+    if (lmore) settle();
     constexpr uint32_t kAll = kStep == 32 ? 0xffffffffu : 0xffffu;
     uint32_t valid[kStages];  // tokens of each stage that are attended, a bit each
 #pragma unroll
@@ -372,39 +399,74 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) load(slot_in++);
 
-    // ---- computing, row by row.
+    // Sequences without tokens have no tiles: their rows are written here.
+    for (int b = blockIdx.x; b < B; b += gridDim.x) {
+        AttendCursor c;
+        read_length<kStep>(p, b, c);
+        if (c.n > 0) continue;
+        for (int i = tid; i < p.q_heads * cache.head_dim; i += kKvThreads) p.out[b * p.out_stride + i] = 0;
+        if (p.lse)
+            for (int h = tid; h < p.q_heads; h += kKvThreads) p.lse[static_cast<int64_t>(b) * p.q_heads + h] = -INFINITY;
+    }
+    if (pos >= end) return;
+
+    // ---- computing, row by row.  The queries of a row are asked for before
+    // the row ahead of it is joined.
+    // Second operand: column (head) g, rows (elements) of lane j.  From an 8-bit
+    // cache the elements come 4j .. 4j + 3 of each 16 (below).
+    uint2 raw[kNT][kSteps];
+    float key_scale = 1.f;
+    AttendSegment seg;
+    auto ask = [&]() {
+        for (; pos < end; pos += seg.places) {
+            seek<kStep>(p, cur, pos);
+            seg = segment_at<kStep>(cur, pos, end);
+            if (seg.tiles > 0) break;
+        }
+        if (pos >= end) return;
+        const int chunk = seg.unit % p.chunks, key_head = seg.unit / p.chunks;
+        const int heads = min(p.chunk_heads, p.group - chunk * p.chunk_heads);
+        const int64_t head0 = key_head * p.group + chunk * p.chunk_heads;
+#pragma unroll
+        for (int t = 0; t < kNT; ++t) {
+            const uint16_t *q = p.q + cur.b * p.q_stride + (head0 + 8 * t + g) * cache.head_dim;
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                const bool in = 8 * t + g < heads && 16 * k < cache.head_dim;
+                if constexpr (kE4m3) {
+                    raw[t][k] = in ? *reinterpret_cast<const uint2 *>(q + 16 * k + 4 * j) : make_uint2(0u, 0u);
+                } else {
+                    raw[t][k].x = in ? *reinterpret_cast<const uint32_t *>(q + 16 * k + 2 * j) : 0u;
+                    raw[t][k].y = in ? *reinterpret_cast<const uint32_t *>(q + 16 * k + 8 + 2 * j) : 0u;
+                }
+            }
+        }
+        if (kE4m3 && p.k_scale) key_scale = p.k_scale[key_head];
+    };
+    ask();
     while (pos < end) {
-        seek<kStep>(p, cur, pos);
-        const AttendSegment seg = segment_at<kStep>(cur, pos, end);
         const int hk = seg.unit / p.chunks, chunk = seg.unit % p.chunks;
         const int head0 = hk * p.group + chunk * p.chunk_heads;
         const int heads = min(p.chunk_heads, p.group - chunk * p.chunk_heads);
-        // Queries as the second operand: column (head) g, rows (elements) of lane j.
+        const int row_b = cur.b;
+        const int64_t row_tiles = cur.tiles, seg_tiles = seg.tiles, row_begin = seg.row_begin;
+        const int seg_unit = seg.unit;
+
         uint32_t qf[kNT][kSteps][2];
         float factor[kNT][2];  // logit to exponent of two, of this lane's heads 2j, 2j + 1
 #pragma unroll
         for (int t = 0; t < kNT; ++t) {
-            const uint16_t *q = p.q + cur.b * p.q_stride + static_cast<int64_t>(head0 + 8 * t + g) * cache.head_dim;
-            const bool there = 8 * t + g < heads;
             const float scale = p.scale * 1.4426950408889634f;
             if constexpr (!kE4m3) {
 #pragma unroll
-                for (int k = 0; k < kSteps; ++k) {
-                    const bool in = there && 16 * k < cache.head_dim;
-                    qf[t][k][0] = in ? *reinterpret_cast<const uint32_t *>(q + 16 * k + 2 * j) : 0u;
-                    qf[t][k][1] = in ? *reinterpret_cast<const uint32_t *>(q + 16 * k + 8 + 2 * j) : 0u;
-                }
+                for (int k = 0; k < kSteps; ++k) qf[t][k][0] = raw[t][k].x, qf[t][k][1] = raw[t][k].y;
                 factor[t][0] = factor[t][1] = scale;
             } else {
-                // Elements 4j .. 4j + 3 of each 16, as the keys come (below).
-                uint2 raw[kSteps];
                 uint32_t top = 0;  // largest magnitude, as bf16 bits
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k) {
-                    raw[k] = there && 16 * k < cache.head_dim ? *reinterpret_cast<const uint2 *>(q + 16 * k + 4 * j)
-                                                              : make_uint2(0u, 0u);
-                    top = max(max(top, raw[k].x & 0x7fffu), (raw[k].x >> 16) & 0x7fffu);
-                    top = max(max(top, raw[k].y & 0x7fffu), (raw[k].y >> 16) & 0x7fffu);
+                    top = max(max(top, raw[t][k].x & 0x7fffu), (raw[t][k].x >> 16) & 0x7fffu);
+                    top = max(max(top, raw[t][k].y & 0x7fffu), (raw[t][k].y >> 16) & 0x7fffu);
                 }
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -413,7 +475,7 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
                 const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k) {
-                    const uint32_t w[2] = {raw[k].x, raw[k].y};
+                    const uint32_t w[2] = {raw[t][k].x, raw[t][k].y};
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const __half2 h = __floats2half2_rn(__uint_as_float(w[i] << 16) * down,
@@ -421,8 +483,7 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
                         qf[t][k][i] = *reinterpret_cast<const uint32_t *>(&h);
                     }
                 }
-                const float up = scale * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) *
-                                 (p.k_scale ? p.k_scale[hk] : 1.f);
+                const float up = scale * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * key_scale;
                 factor[t][0] = __shfl_sync(0xffffffffu, up, 8 * j);
                 factor[t][1] = __shfl_sync(0xffffffffu, up, 8 * j + 4);
             }
@@ -579,7 +640,11 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
             }
         }
 
+        pos += seg.places;
+        ask();
+
         // Join the warps.
+        using Part = JoinPart<kHeads, kDim>;
 #pragma unroll
         for (int t = 0; t < kNT; ++t) {
 #pragma unroll
@@ -593,77 +658,89 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
             }
 #pragma unroll
             for (int d = 0; d < kSteps; ++d) {
-                float *to = join + warp * kHeads * kDim + 8 * t + 2 * j;
-                const int d0 = 16 * d + (kE4m3 ? 2 * g : g), d1 = 16 * d + (kE4m3 ? 2 * g + 1 : g + 8);
-                *reinterpret_cast<float2 *>(to + d0 * kHeads) = make_float2(o[t][d][0], o[t][d][1]);
-                *reinterpret_cast<float2 *>(to + d1 * kHeads) = make_float2(o[t][d][2], o[t][d][3]);
-            }
-        }
-        __syncthreads();
-        constexpr int kPer = kHeads * kDim / kKvThreads, kDimStep = kKvThreads / kHeads;
-        const int h = tid % kHeads, d0 = tid / kHeads;
-        float M = -INFINITY, L = 0.f, w[kKvWarps], acc[kPer];
-#pragma unroll
-        for (int i = 0; i < kKvWarps; ++i) M = fmaxf(M, join_m[i * kHeads + h]);
-        const float base = M == -INFINITY ? 0.f : M;
-#pragma unroll
-        for (int i = 0; i < kKvWarps; ++i) {
-            w[i] = exp2_fast(join_m[i * kHeads + h] - base);
-            L += w[i] * join_l[i * kHeads + h];
-        }
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            acc[k] = 0.f;
-#pragma unroll
-            for (int i = 0; i < kKvWarps; ++i)
-                acc[k] += w[i] * join[(i * kDim + d0 + k * kDimStep) * kHeads + h];
-        }
-
-        bool write = true;
-        if (seg.tiles != cur.tiles) {
-            // Other CTAs own the rest of the row: leave this part in scratch,
-            // and join all parts if the others are there already.
-            const int64_t row_end = seg.row_begin + cur.tiles;
-            const int c0 = static_cast<int>(((seg.row_begin + 1) * ctas - 1) / total);  // first and last owner
-            const int c1 = static_cast<int>((row_end * ctas - 1) / total);
-            const int first_slot = total * c0 / ctas < seg.row_begin ? 1 : 0;  // the row is the last of its first owner's
-            const int parts = c1 - c0 + 1, mine = static_cast<int>(blockIdx.x) - c0;
-            auto slot = [&](int part) { return int64_t(2) * (c0 + part) + (part == 0 ? first_slot : 0); };
-            uint32_t *counter = p.counters + static_cast<int64_t>(cur.b) * p.units + seg.unit;
-            if (parts <= kKvJoinOnce) {
-                write = leave_part<kHeads, kDim, kPer, kDimStep>(p.partials, slot(mine), counter, parts, h, d0, M, L, acc, flag);
-                if (write) join_parts<kHeads, kDim, kPer, kDimStep>(p.partials, parts, slot, h, d0, M, L, acc);
-            } else {
-                // Many parts: in groups, each joined into its first part's
-                // slot by its own last arrival, and then the groups.
-                const int g0 = mine / kKvJoinGroup * kKvJoinGroup, in_group = min(kKvJoinGroup, parts - g0);
-                write = leave_part<kHeads, kDim, kPer, kDimStep>(p.partials, slot(mine), p.group_counters + slot(g0), in_group, h,
-                                                                 d0, M, L, acc, flag);
-                if (write) {
-                    join_parts<kHeads, kDim, kPer, kDimStep>(
-                        p.partials, in_group, [&](int i) { return slot(g0 + i); }, h, d0, M, L, acc);
-                    __syncthreads();  // every thread has read the slot that is written next
-                    const int groups = (parts + kKvJoinGroup - 1) / kKvJoinGroup;
-                    write = leave_part<kHeads, kDim, kPer, kDimStep>(p.partials, slot(g0), counter, groups, h, d0, M, L, acc, flag);
-                    if (write)
-                        join_parts<kHeads, kDim, kPer, kDimStep>(
-                            p.partials, groups, [&](int i) { return slot(i * kKvJoinGroup); }, h, d0, M, L, acc);
+                float *to = join + (warp * kHeads + 8 * t + 2 * j) * Part::kPitch + 16 * d;
+                if constexpr (kE4m3) {
+                    *reinterpret_cast<float2 *>(to + 2 * g) = make_float2(o[t][d][0], o[t][d][2]);
+                    *reinterpret_cast<float2 *>(to + Part::kPitch + 2 * g) = make_float2(o[t][d][1], o[t][d][3]);
+                } else {
+                    to[g] = o[t][d][0];
+                    to[Part::kPitch + g] = o[t][d][1];
+                    to[g + 8] = o[t][d][2];
+                    to[Part::kPitch + g + 8] = o[t][d][3];
                 }
             }
         }
-        if (write && h < heads) {
-            const float by = (L > 0.f ? 1.f / L : 0.f) * (kE4m3 && p.v_scale ? p.v_scale[hk] : 1.f);
-            __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(p.out) + cur.b * p.out_stride +
-                                 static_cast<int64_t>(head0 + h) * cache.head_dim;
+        __syncthreads();
+        const int h0 = tid / Part::kLanes, d0 = tid % Part::kLanes * 4;
+        Part r;
+        r.clear();
 #pragma unroll
-            for (int k = 0; k < kPer; ++k)
-                if (d0 + k * kDimStep < cache.head_dim) out[d0 + k * kDimStep] = __float2bfloat16_rn(acc[k] * by);
-            if (p.lse && d0 == 0)
-                p.lse[static_cast<int64_t>(cur.b) * p.q_heads + head0 + h] =
-                    L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        for (int k = 0; k < Part::kPer; ++k) {
+            const int h = h0 + k * Part::kHeadStep;
+            if (h >= heads) break;
+            float warp_m[kKvWarps];
+#pragma unroll
+            for (int i = 0; i < kKvWarps; ++i) {
+                warp_m[i] = join_m[i * kHeads + h];
+                r.m[k] = fmaxf(r.m[k], warp_m[i]);
+            }
+            const float base = finite_or_zero(r.m[k]);
+#pragma unroll
+            for (int i = 0; i < kKvWarps; ++i) {
+                const float w = exp2_fast(warp_m[i] - base);
+                const float4 v = *reinterpret_cast<const float4 *>(join + (i * kHeads + h) * Part::kPitch + d0);
+                r.l[k] += w * join_l[i * kHeads + h];
+                r.o[k].x += w * v.x, r.o[k].y += w * v.y, r.o[k].z += w * v.z, r.o[k].w += w * v.w;
+            }
         }
-        __syncthreads();  // the join buffer and the flag are free again
-        pos += seg.tiles;
+
+        bool write = true;
+        if (seg_tiles != row_tiles) {
+            // Other CTAs own the rest of the row: leave this part in scratch,
+            // and join all parts if the others are there already.
+            // First and last owner of its tiles.
+            const int64_t row_first = row_begin + kKvRowCost, row_end = row_first + row_tiles;
+            const int c0 = static_cast<int>(divide((row_first + 1) * ctas - 1, total));
+            const int c1 = static_cast<int>(divide(row_end * ctas - 1, total));
+            const int parts = c1 - c0 + 1, mine = static_cast<int>(blockIdx.x) - c0;
+            // A CTA's scratch: slot 0 for a row begun by another, slot 1 for the row that it begins last.
+            auto slot = [&](int part) { return int64_t(2) * (c0 + part) + (part == 0 ? 1 : 0); };
+            uint32_t *counter = p.counters + static_cast<int64_t>(row_b) * p.units + seg_unit;
+            if (parts <= kKvJoinOnce) {
+                write = leave_part<kHeads, kDim>(p.partials, slot(mine), counter, parts, heads, r, flag);
+                if (write) join_parts<kHeads, kDim>(p.partials, parts, slot, heads, r);
+            } else {
+                // Many parts: in groups, each joined into its first part's
+                // slot by its own last arrival, and then the groups.
+                const int size = parts <= kKvJoinMany ? kKvJoinGroup : 2 * kKvJoinGroup;
+                const int g0 = mine / size * size, in_group = min(size, parts - g0);
+                write = leave_part<kHeads, kDim>(p.partials, slot(mine), p.group_counters + slot(g0), in_group, heads, r, flag);
+                if (write) {
+                    join_parts<kHeads, kDim>(p.partials, in_group, [&](int i) { return slot(g0 + i); }, heads, r);
+                    __syncthreads();  // every thread has read the slot that is written next
+                    const int groups = (parts + size - 1) / size;
+                    write = leave_part<kHeads, kDim>(p.partials, slot(g0), counter, groups, heads, r, flag);
+                    if (write)
+                        join_parts<kHeads, kDim>(p.partials, groups, [&](int i) { return slot(i * size); }, heads, r);
+                }
+            }
+        }
+        if (write) {
+            const float by = kE4m3 && p.v_scale ? p.v_scale[hk] : 1.f;
+            uint16_t *out = p.out + row_b * p.out_stride + static_cast<int64_t>(head0) * cache.head_dim + d0;
+            float *lse = p.lse ? p.lse + static_cast<int64_t>(row_b) * p.q_heads + head0 : nullptr;
+#pragma unroll
+            for (int k = 0; k < Part::kPer; ++k) {
+                const int h = h0 + k * Part::kHeadStep;
+                if (h >= heads) break;
+                const float inv = r.l[k] > 0.f ? by / r.l[k] : 0.f;
+                if (d0 < cache.head_dim)
+                    *reinterpret_cast<uint2 *>(out + h * cache.head_dim) =
+                        make_uint2(bf16_pair(r.o[k].x * inv, r.o[k].y * inv), bf16_pair(r.o[k].z * inv, r.o[k].w * inv));
+                if (lse && d0 == 0) lse[h] = r.l[k] > 0.f ? (r.m[k] + log2f(r.l[k])) * 0.6931471805599453f : -INFINITY;
+            }
+        }
+        __syncthreads();  // the join buffer is free again
     }
     cp_async_wait<0>();
 }

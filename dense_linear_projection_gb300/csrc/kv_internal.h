@@ -11,9 +11,11 @@ namespace projgb {
 constexpr int kKvMaxDim = 256;
 constexpr int kKvWarps = 4;                        // warps of an attention CTA
 constexpr int kKvThreads = 32 * kKvWarps;
-// Parts of a row that one CTA joins at once; more are joined in groups first
-// (one CTA reads a part of 4 KiB in about 50 ns once its loads overlap).
-constexpr int kKvJoinOnce = 64, kKvJoinGroup = 16;
+constexpr int kKvRowCost = 2;  // a row's start and join, in tiles (64 ragged sequences: 0, 1, 2 gave 170, 163, 161 us)
+// Parts of a row that one CTA joins at once; more are joined in groups first.
+// While the other CTAs stream, a round trip to scratch takes about 2 us and one
+// CTA keeps eight parts of 4 KiB in flight, so 38 parts took 15 us at once.
+constexpr int kKvJoinOnce = 16, kKvJoinGroup = 8, kKvJoinMany = 128;
 
 // Bits of the cache handle's status word: what a kernel found out of range.
 constexpr int kKvErrPosition = 1 << 0;  // position past the page table or the rope table
