@@ -232,6 +232,48 @@ __device__ __forceinline__ void join_parts(const float *partials, int count, Slo
     }
 }
 
+// The same by way of `ring` (shared memory of `bytes` that no copy is under way
+// to): one round trip for as many parts as it holds.
+template <int kHeads, int kDim, typename Slot>
+__device__ __forceinline__ void join_parts_in(uint8_t *ring, int bytes, const float *partials, int count, Slot slot, int heads,
+                                              JoinPart<kHeads, kDim> &r) {
+    using Part = JoinPart<kHeads, kDim>;
+    const int h0 = threadIdx.x / Part::kLanes, d = threadIdx.x % Part::kLanes * 4;
+    const int floats = 2 * kHeads + heads * kDim, at_once = bytes / (floats * 4);  // the heads in use come first
+    const uint32_t to = smem_u32(ring);
+    r.clear();
+    for (int c = 0; c < count; c += at_once) {
+        const int n = min(at_once, count - c);
+        for (int i = 0; i < n; ++i) {
+            const float *from = partials + slot(c + i) * Part::kFloats;
+            for (int x = threadIdx.x * 4; x < floats; x += kKvThreads * 4) cp_async16(to + (i * floats + x) * 4, from + x);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncthreads();
+        const float *part = reinterpret_cast<const float *>(ring);
+#pragma unroll
+        for (int k = 0; k < Part::kPer; ++k) {
+            const int h = h0 + k * Part::kHeadStep;
+            if (h >= heads) break;
+            float top = r.m[k];
+            for (int i = 0; i < n; ++i) top = fmaxf(top, part[i * floats + h]);
+            const float base = finite_or_zero(top), keep = exp2_fast(r.m[k] - base);
+            r.m[k] = top;
+            r.l[k] *= keep;
+            r.o[k].x *= keep, r.o[k].y *= keep, r.o[k].z *= keep, r.o[k].w *= keep;
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+                const float w = exp2_fast(part[i * floats + h] - base);
+                const float4 o = *reinterpret_cast<const float4 *>(part + i * floats + 2 * kHeads + h * kDim + d);
+                r.l[k] += w * part[i * floats + kHeads + h];
+                r.o[k].x += w * o.x, r.o[k].y += w * o.y, r.o[k].z += w * o.z, r.o[k].w += w * o.w;
+            }
+        }
+        __syncthreads();
+    }
+}
+
 // Writes this CTA's partial result to slot `at` and says so; true for the last
 // of `expected` arrivals at `counter`, which then sees all of theirs.
 template <int kHeads, int kDim>
@@ -706,9 +748,16 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
             // A CTA's scratch: slot 0 for a row begun by another, slot 1 for the row that it begins last.
             auto slot = [&](int part) { return int64_t(2) * (c0 + part) + (part == 0 ? 1 : 0); };
             uint32_t *counter = p.counters + static_cast<int64_t>(row_b) * p.units + seg_unit;
+            // A CTA that has no more to load joins by way of its ring.
+            auto join_all = [&](int count, auto at) {
+                if (pos >= end)
+                    join_parts_in<kHeads, kDim>(smem, kKvWarps * kStages * Shape::kStage, p.partials, count, at, heads, r);
+                else
+                    join_parts<kHeads, kDim>(p.partials, count, at, heads, r);
+            };
             if (parts <= kKvJoinOnce) {
                 write = leave_part<kHeads, kDim>(p.partials, slot(mine), counter, parts, heads, r, flag);
-                if (write) join_parts<kHeads, kDim>(p.partials, parts, slot, heads, r);
+                if (write) join_all(parts, slot);
             } else {
                 // Many parts: in groups, each joined into its first part's
                 // slot by its own last arrival, and then the groups.
@@ -716,12 +765,11 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
                 const int g0 = mine / size * size, in_group = min(size, parts - g0);
                 write = leave_part<kHeads, kDim>(p.partials, slot(mine), p.group_counters + slot(g0), in_group, heads, r, flag);
                 if (write) {
-                    join_parts<kHeads, kDim>(p.partials, in_group, [&](int i) { return slot(g0 + i); }, heads, r);
+                    join_all(in_group, [&](int i) { return slot(g0 + i); });
                     __syncthreads();  // every thread has read the slot that is written next
                     const int groups = (parts + size - 1) / size;
                     write = leave_part<kHeads, kDim>(p.partials, slot(g0), counter, groups, heads, r, flag);
-                    if (write)
-                        join_parts<kHeads, kDim>(p.partials, groups, [&](int i) { return slot(i * size); }, heads, r);
+                    if (write) join_all(groups, [&](int i) { return slot(i * size); });
                 }
             }
         }

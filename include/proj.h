@@ -577,7 +577,7 @@ proj_status_t proj_q4_destroy(proj_q4_handle_t h);
  *   clamped to ±448.  rope NULL: no rotation.  q NULL: keys and values only.
  *   q, k, v, q_out: bf16 rows of heads × head_dim, rows *_stride elements
  *   apart (a q·k·v projection's output is read in place).  A token with
- *   p < 0 is padding: nothing of it is read or written.
+ *   p < 0 is padding: nothing is written for it.
  *   Two tokens of one call must not name the same place.
  *
  * proj_kv_attend: for each sequence b and query head h (key head
