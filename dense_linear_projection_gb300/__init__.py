@@ -15,7 +15,7 @@ import json
 import os
 from typing import Optional
 
-from ._build import build, library_path
+from ._build import bind_path, build, library_path
 
 __all__ = [
     "PROJ_OK", "PROJ_ERR_INVALID_ARG", "PROJ_ERR_UNSUPPORTED", "PROJ_ERR_MISALIGNED",
@@ -479,10 +479,26 @@ def _require(ok: bool, what: str) -> None:
         _refuse(what)
 
 
-def _raw_stream(stream, device: int) -> int:
-    """The given stream's handle, or that of the device's current stream."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+_BIND = None
+
+
+def _bind():
+    """The native calls that take PyTorch tensors (csrc/bind.cpp), loaded once."""
+    global _BIND
+    if _BIND is None:
+        import importlib.machinery
+        import importlib.util
+        import torch  # noqa: F401  (the module uses its libraries)
+        lib()
+        path = bind_path()
+        if not os.path.exists(path):
+            build()
+        loader = importlib.machinery.ExtensionFileLoader("_bind", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_bind", loader))
+        loader.exec_module(module)
+        module.init(ProjError)
+        _BIND = module
+    return _BIND
 
 
 class Q4Projection:
@@ -498,14 +514,11 @@ class Q4Projection:
     def __init__(self, max_tokens: int, N: int, K: int, group: int = 128, has_zeros: bool = False,
                  y_dtype: int = PROJ_BF16, has_bias: bool = False, stream=None):
         self.handle = None
-        import torch
-        self._torch = torch
         self.N, self.K, self.group, self.has_zeros = N, K, group, bool(has_zeros)
-        self.has_bias = bool(has_bias)
-        self._dtype = torch.float32 if y_dtype == PROJ_F32 else torch.bfloat16
+        self.has_bias, self._f32 = bool(has_bias), int(y_dtype == PROJ_F32)
+        self._call = _bind().q4
         self.handle = proj_q4_create(max_tokens, N, K, group, has_zeros, y_dtype, has_bias, stream)
         self._bytes = max(16, proj_q4_packed_bytes(N, K, group, has_zeros))
-        self._run = lib().proj_q4_run
 
     def pack(self, codes, scales, zeros=None, stream=None):
         """The packed weights (uint8 CUDA tensor), made on the given or current stream."""
@@ -523,28 +536,14 @@ class Q4Projection:
         _require(device >= 0 and scales.get_device() == device and (zeros is None or zeros.get_device() == device),
                  "codes, scales, zeros: on one CUDA device")
         packed = torch.empty(self._bytes, dtype=torch.uint8, device=codes.device)
-        proj_q4_pack(self.handle, codes, scales, zeros, packed, _raw_stream(stream, device))
+        if stream is None:
+            stream = torch.cuda.current_stream(codes.device)
+        proj_q4_pack(self.handle, codes, scales, zeros, packed, stream)
         return packed
 
     def __call__(self, X, packed, bias=None, out=None, stream=None):
-        torch, dtype, shape, device = self._torch, self._dtype, X.shape, X.get_device()
-        if X.dtype is not torch.bfloat16 or len(shape) != 2 or shape[1] != self.K or not X.is_contiguous() or device < 0:
-            _refuse("X: contiguous bf16 CUDA [M, K]")
-        M, N = shape[0], self.N
-        if packed.dtype is not torch.uint8 or packed.numel() != self._bytes or packed.get_device() != device:
-            _refuse("packed: what pack() returned, on X's device")
-        if bias is not None and (bias.dtype is not torch.bfloat16 or bias.shape != (N,) or not bias.is_contiguous() or
-                                 bias.get_device() != device):
-            _refuse("bias: contiguous bf16 [N], on X's device")
-        if out is None:
-            out = torch.empty((M, N), dtype=dtype, device=X.device)
-        elif out.dtype is not dtype or out.shape != (M, N) or not out.is_contiguous() or out.get_device() != device:
-            _refuse("out: contiguous [M, N] of y_dtype, on X's device")
-        status = self._run(self.handle, M, X.data_ptr(), packed.data_ptr(), None if bias is None else bias.data_ptr(),
-                           out.data_ptr(), _raw_stream(stream, device))
-        if status:
-            raise ProjError(status, "proj_q4_run")
-        return out
+        """``Y`` [M, N] for ``X`` [M, K] bf16 (contiguous, M ≤ max_tokens) and weights from :meth:`pack`."""
+        return self._call(self.handle, self.N, self.K, self._bytes, self._f32, X, packed, bias, out, _stream(stream))
 
     def close(self) -> None:
         if self.handle:
@@ -601,22 +600,11 @@ class PagedKV:
                  "k_cache, v_cache, k_scale, v_scale: on one CUDA device")
         self.k_cache, self.v_cache, self.k_scale, self.v_scale = k_cache, v_cache, k_scale, v_scale
         self.q_heads, self.kv_heads, self.head_dim, self.page_size = q_heads, kv_heads, head_dim, page_size
-        self._torch, self._device, self._scale = torch, device, head_dim ** -0.5
+        self._scale = head_dim ** -0.5
+        self._append, self._attend = _bind().append, _bind().attend
         s = k_cache.stride()
         desc = KvDesc(pages, s[0], s[1], s[2], max_sequences, page_size, q_heads, kv_heads, head_dim, kv_dtype)
         self.handle = proj_kv_create(desc, stream)
-        self._append, self._attend = lib().proj_kv_append, lib().proj_kv_attend
-
-    def _rows(self, x, n: int, heads: int) -> int:
-        """The row stride of bf16 [n, heads, head_dim] with contiguous heads on the cache's device; -1: not that."""
-        s, d = x.stride(), self.head_dim
-        if (x.dtype is not self._torch.bfloat16 or x.shape != (n, heads, d) or s[2] != 1 or
-                (heads > 1 and s[1] != d) or x.get_device() != self._device):
-            return -1
-        return s[0] if n > 1 else heads * d
-
-    def _ints(self, x) -> bool:
-        return x.dtype is self._torch.int32 and x.is_contiguous() and x.get_device() == self._device
 
     def append(self, q, k, v, positions, page_table, seq_ids=None, rope=None, interleaved: bool = False, q_out=None,
                stream=None):
@@ -627,48 +615,9 @@ class PagedKV:
         [sequences, pages of a sequence]; ``seq_ids``: int32 [tokens], default
         0, 1, 2, …; ``rope``: :func:`rope_table`'s form, or None for no
         rotation."""
-        torch, tokens = self._torch, k.shape[0]
-        kv_stride = self._rows(k, tokens, self.kv_heads)
-        if kv_stride < 0 or self._rows(v, tokens, self.kv_heads) != kv_stride:
-            _refuse("k, v: bf16 [tokens, kv_heads, head_dim] with contiguous heads and one row stride, on the cache's device")
-        if not self._ints(positions) or positions.shape != (tokens,):
-            _refuse("positions: contiguous int32 [tokens], on the cache's device")
-        table = page_table.shape
-        if not self._ints(page_table) or len(table) != 2:
-            _refuse("page_table: contiguous int32 [sequences, pages], on the cache's device")
-        if seq_ids is not None and (not self._ints(seq_ids) or seq_ids.shape != (tokens,)):
-            _refuse("seq_ids: contiguous int32 [tokens], on the cache's device")
-        rope_ptr, rope_rows, rot_dim = None, 0, 0
-        if rope is not None:
-            if (rope.dtype is not torch.float32 or rope.dim() != 2 or not rope.is_contiguous() or
-                    rope.get_device() != self._device):
-                _refuse("rope: contiguous fp32 [positions, rot_dim], on the cache's device")
-            rope_ptr, (rope_rows, rot_dim) = rope.data_ptr(), rope.shape
-        q_ptr, q_out_ptr, q_stride, q_out_stride = None, None, 0, 0
-        if q is not None:
-            q_stride = self._rows(q, tokens, self.q_heads)
-            if q_stride < 0:
-                _refuse("q: bf16 [tokens, q_heads, head_dim] with contiguous heads, on the cache's device")
-            if q_out is None:
-                q_out = torch.empty((tokens, self.q_heads, self.head_dim), dtype=torch.bfloat16, device=q.device)
-                q_out_stride = self.q_heads * self.head_dim
-            else:
-                q_out_stride = self._rows(q_out, tokens, self.q_heads)
-                if q_out_stride < 0:
-                    _refuse("q_out: as q")
-            q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
-        elif q_out is not None:
-            _refuse("q_out: only with q")
-        ks, vs = self.k_scale, self.v_scale
-        status = self._append(self.handle, tokens, q_ptr, q_stride, k.data_ptr(), v.data_ptr(), kv_stride,
-                              positions.data_ptr(), None if seq_ids is None else seq_ids.data_ptr(),
-                              page_table.data_ptr(), table[0], table[1], rope_ptr, rope_rows, rot_dim,
-                              1 if interleaved else 0, None if ks is None else ks.data_ptr(),
-                              None if vs is None else vs.data_ptr(), self.k_cache.data_ptr(), self.v_cache.data_ptr(),
-                              q_out_ptr, q_out_stride, _raw_stream(stream, self._device))
-        if status:
-            raise ProjError(status, "proj_kv_append")
-        return q_out
+        return self._append(self.handle, self.q_heads, self.kv_heads, self.head_dim, self.k_cache, self.v_cache,
+                            self.k_scale, self.v_scale, q, k, v, positions, page_table, seq_ids, rope, interleaved,
+                            q_out, _stream(stream))
 
     def attend(self, q, page_table, seq_lens, scale: Optional[float] = None, window: int = 0, out=None,
                return_lse: bool = False, stream=None):
@@ -677,32 +626,9 @@ class PagedKV:
         last ``window`` of them; ``scale`` is 1/√head_dim by default.  Returns
         ``out`` ([sequences, q_heads, head_dim] bf16), with the fp32 log sums
         [sequences, q_heads] beside it when ``return_lse``."""
-        torch, n, heads = self._torch, q.shape[0], self.q_heads
-        q_stride = self._rows(q, n, heads)
-        if q_stride < 0:
-            _refuse("q: bf16 [sequences, q_heads, head_dim] with contiguous heads, on the cache's device")
-        table = page_table.shape
-        if not self._ints(page_table) or len(table) != 2 or table[0] != n:
-            _refuse("page_table: contiguous int32 [sequences, pages], on the cache's device")
-        if not self._ints(seq_lens) or seq_lens.shape != (n,):
-            _refuse("seq_lens: contiguous int32 [sequences], on the cache's device")
-        if out is None:
-            out = torch.empty((n, heads, self.head_dim), dtype=torch.bfloat16, device=q.device)
-            out_stride = heads * self.head_dim
-        else:
-            out_stride = self._rows(out, n, heads)
-            if out_stride < 0:
-                _refuse("out: as q")
-        lse = torch.empty((n, heads), dtype=torch.float32, device=q.device) if return_lse else None
-        ks, vs = self.k_scale, self.v_scale
-        status = self._attend(self.handle, n, q.data_ptr(), q_stride, self.k_cache.data_ptr(), self.v_cache.data_ptr(),
-                              None if ks is None else ks.data_ptr(), None if vs is None else vs.data_ptr(),
-                              page_table.data_ptr(), table[1], seq_lens.data_ptr(), window,
-                              self._scale if scale is None else scale, out.data_ptr(), out_stride,
-                              None if lse is None else lse.data_ptr(), _raw_stream(stream, self._device))
-        if status:
-            raise ProjError(status, "proj_kv_attend")
-        return (out, lse) if return_lse else out
+        return self._attend(self.handle, self.q_heads, self.kv_heads, self.head_dim, self.k_cache, self.v_cache,
+                            self.k_scale, self.v_scale, q, page_table, seq_lens,
+                            self._scale if scale is None else scale, window, out, return_lse, _stream(stream))
 
     def status(self, stream=None) -> int:
         return proj_kv_device_status(self.handle, stream)

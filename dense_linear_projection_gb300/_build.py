@@ -2,14 +2,17 @@
 
 Each translation unit is compiled in parallel; the shared library lands next to
 this file as ``libproj_gb300.<machine>.so`` (the machine suffix keeps x86 and
-Arm builds apart).  Objects go to ``_build/<machine>/``.
+Arm builds apart).  Objects go to ``_build/<machine>/``.  Beside it lands
+``_bind.<machine>.so``, the calls that take PyTorch tensors (csrc/bind.cpp).
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import platform
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -40,6 +43,23 @@ def library_path() -> str:
     return os.path.join(PKG, f"libproj_gb300.{platform.machine()}.so")
 
 
+def bind_path() -> str:
+    return os.path.join(PKG, f"_bind.{platform.machine()}.so")
+
+
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("PyTorch not found: its headers are required to build _bind")
+    return spec.submodule_search_locations[0]
+
+
+def _run(cmd, what: str) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
 def _stale(target: str, deps) -> bool:
     if not os.path.exists(target):
         return True
@@ -49,32 +69,44 @@ def _stale(target: str, deps) -> bool:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile (if sources changed) and return the library path."""
-    out = library_path()
+    out, bind = library_path(), bind_path()
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    if not force and not _stale(out, srcs + HEADERS):
+    bind_src = os.path.join(CSRC, "bind.cpp")
+    bind_stale = force or _stale(bind, [bind_src, os.path.join(INCLUDE, "proj.h")])
+    lib_stale = force or _stale(out, srcs + HEADERS)
+    if not lib_stale and not bind_stale:
         return out
     objdir = os.path.join(PKG, "_build", platform.machine())
     os.makedirs(objdir, exist_ok=True)
-    cc = nvcc()
 
     def compile_one(src):
         obj = os.path.join(objdir, os.path.basename(src) + ".o")
-        cmd = [cc, *ARCH_FLAGS, *COMMON, "-c", src, "-o", obj]
+        if src == bind_src:
+            t = _torch_dir()
+            cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-I" + INCLUDE,
+                   "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(t, "include"),
+                   "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"),
+                   "-I" + os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), "-c", src, "-o", obj]
+        else:
+            cmd = [nvcc(), *ARCH_FLAGS, *COMMON, "-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd))
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+        _run(cmd, f"compiling {src}")
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(srcs)) as ex:
-        objs = list(ex.map(compile_one, srcs))
-    tmp = out + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH_FLAGS, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, out)
+    todo = (srcs if lib_stale else []) + ([bind_src] if bind_stale else [])
+    with ThreadPoolExecutor(max_workers=len(todo)) as ex:
+        objs = dict(zip(todo, ex.map(compile_one, todo)))
+    if lib_stale:
+        tmp = out + f".tmp{os.getpid()}"
+        _run([nvcc(), *ARCH_FLAGS, "-shared", "-o", tmp, *(objs[s] for s in srcs)], "linking libproj_gb300")
+        os.replace(tmp, out)
+    if bind_stale:
+        tmp = bind + f".tmp{os.getpid()}"
+        _run([shutil.which("g++") or "g++", "-shared", "-o", tmp, objs[bind_src], "-L" + PKG,
+              "-l:" + os.path.basename(out), "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(_torch_dir(), "lib"),
+              "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], "linking _bind")
+        os.replace(tmp, bind)
     return out
 
 
