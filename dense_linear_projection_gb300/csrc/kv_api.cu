@@ -126,15 +126,12 @@ proj_status_t proj_kv_create(proj_kv_handle_t *out, const proj_kv_desc_t *desc, 
     const int elem = d.kv_dtype == PROJ_E4M3 ? 1 : 2;
     if ((d.page_stride * elem) % 16 != 0 || (d.token_stride * elem) % 16 != 0 || (d.head_stride * elem) % 16 != 0)
         return PROJ_ERR_MISALIGNED;
-    int device = 0;
-    cudaDeviceProp prop;
-    if (cudaGetDevice(&device) != cudaSuccess || cudaGetDeviceProperties(&prop, device) != cudaSuccess)
-        return PROJ_ERR_CUDA;
-    if (prop.major != 10 || prop.minor != 3) return PROJ_ERR_UNSUPPORTED;  // built for sm_103a
+    const int sms = gb300_sm_count();
+    if (sms <= 0) return sms < 0 ? PROJ_ERR_CUDA : PROJ_ERR_UNSUPPORTED;
     proj_kv_s *h = new (std::nothrow) proj_kv_s();
     if (!h) return PROJ_ERR_OUT_OF_MEMORY;
     h->d = d;
-    h->sm_count = prop.multiProcessorCount;
+    h->sm_count = sms;
     h->elem = elem;
     const int group = d.q_heads / d.kv_heads, most = d.head_dim <= 128 ? 16 : 8;
     h->chunks = (group + most - 1) / most;

@@ -15,6 +15,21 @@ inline bool launch_faulted() { return (fault_mask() & kFaultLaunch) != 0; }
 // Every device allocation of the library goes through here.
 cudaError_t dev_malloc(void **p, size_t bytes);
 
+// The current device's SM count, 0 if it is not a GB300 (compute capability
+// 10.3), -1 if the runtime fails.  (Single attributes: the whole property
+// structure takes over 100 us to fill.)
+inline int gb300_sm_count() {
+    int device = 0, major = 0, minor = 0, sms = 0;
+    if (cudaGetDevice(&device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
+        cudaGetLastError();
+        return -1;
+    }
+    return major == 10 && minor == 3 ? sms : 0;
+}
+
 inline cudaStream_t as_stream(void *s) { return static_cast<cudaStream_t>(s); }
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -2,7 +2,6 @@
 // launches.  See include/proj.h for the contract.
 #include <cuda_runtime.h>
 
-#include <cstdlib>
 #include <new>
 
 #include "proj.h"
@@ -81,11 +80,8 @@ proj_status_t proj_q4_create(proj_q4_handle_t *out, int64_t max_tokens, int64_t 
     if (max_tokens < 0 || max_tokens > kMaxDim || (has_bias != 0 && has_bias != 1) ||
         (y_dtype != PROJ_BF16 && y_dtype != PROJ_F32))
         return PROJ_ERR_INVALID_ARG;
-    int device = 0;
-    cudaDeviceProp prop;
-    if (cudaGetDevice(&device) != cudaSuccess || cudaGetDeviceProperties(&prop, device) != cudaSuccess)
-        return PROJ_ERR_CUDA;
-    if (prop.major != 10 || prop.minor != 3) return PROJ_ERR_UNSUPPORTED;  // built for sm_103a
+    const int sms = gb300_sm_count();
+    if (sms <= 0) return sms < 0 ? PROJ_ERR_CUDA : PROJ_ERR_UNSUPPORTED;
     for (int64_t m = 8; m <= kQ4MaxTokens; m *= 2)
         if (cudaFuncSetAttribute(instance_for(m, group, has_zeros != 0).kernel,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOfSm - 1024) != cudaSuccess) {
@@ -101,7 +97,7 @@ proj_status_t proj_q4_create(proj_q4_handle_t *out, int64_t max_tokens, int64_t 
     h->has_zeros = has_zeros;
     h->y_dtype = y_dtype;
     h->has_bias = has_bias;
-    h->sm_count = prop.multiProcessorCount;
+    h->sm_count = sms;
     h->shape = q4_shape(N, K, group, has_zeros != 0);
     *out = h;
     return PROJ_OK;
@@ -157,19 +153,20 @@ proj_status_t proj_q4_run(proj_q4_handle_t h, int64_t M, const void *X, const vo
     const int64_t tiles = (p.row_tiles + q.row_tiles - 1) / q.row_tiles;
     const int64_t passes = (M + kQ4MaxTokens - 1) / kQ4MaxTokens;
     // CTAs of one K range: as many as stand on the GPU at once, while every
-    // warp has a step.
+    // warp has a step.  (31 tokens, 12300 rows, 97 tiles at two CTAs an SM: 3 a
+    // range 19.3 us, 2 a range 22, 4 a range, two waves, 27.  28672 rows, 448
+    // tiles: one 24.1 us, two 28.)
     const int64_t steps = (p.k_blocks + 1) / 2;
     int64_t splits = q.per_sm * int64_t(h->sm_count) / tiles;
     if (splits > steps / q.k_steps) splits = steps / q.k_steps;
     p.splits = static_cast<int32_t>(splits < 1 ? 1 : splits > kQ4MaxSplits ? kQ4MaxSplits : splits);
-    if (const char *e = getenv("Q4S")) p.splits = atoi(e);
+    // Two stages where 16 warps stand on an SM (64 KiB of codes are on their
+    // way then; three were 7 % slower), three where 8 do.
     const int tokens = static_cast<int>(M < kQ4MaxTokens ? M : kQ4MaxTokens);
     const int groups = static_cast<int>(128 / h->group);
     const int stage = q.warps * (4096 + groups * (128 + (h->has_zeros ? 32 : 0))) + q.k_steps * tokens * kQ4XPitch;
-    const int fit = (kSmemOfSm / q.per_sm - 1024) / stage;
-    const int most = q.warps * q.per_sm > 8 ? 2 : 3;
-    p.stages = fit < 2 ? 2 : fit < most ? fit : most;
-    if (const char *e = getenv("Q4T")) p.stages = atoi(e);
+    const int fit = (kSmemOfSm / q.per_sm - 1024) / stage, most = q.warps * q.per_sm > 8 ? 2 : 3;
+    p.stages = fit < 2 ? 2 : fit < most ? fit : most;  // (two of the largest leave room for one CTA an SM)
     int smem = p.stages * stage;
     if (smem < q.red) smem = q.red;
 

@@ -58,7 +58,7 @@ struct Q4Params {
     int32_t y_f32;
     int32_t y_vec;   // Y's rows start on four-element boundaries: four at a time
     int32_t splits;  // CTAs of a cluster
-    int32_t stages;  // of the ring: 2, 3 or 4
+    int32_t stages;  // of the ring: 2 or 3
     const uint16_t *X;
     const uint4 *codes;
     const uint32_t *scales;

@@ -73,14 +73,23 @@ __global__ void q4_pack_scales_kernel(const uint16_t *scales, const uint8_t *zer
 // multiplies X as it is by these; a group's fp32 sum is scaled into the row's
 // fp32 sum, and the 2^7 is taken back when the row is written.
 //
-// The product is swapped (weight rows are the 16-row operand, up to 8·kNT
-// tokens its columns).  What bounds it is the stream of codes, and for small
-// token counts the instructions per code.  A warp owns 64 rows × 128 K at a
-// time, in a ring of shared-memory stages filled by 16-byte asynchronous copies.
-// A CTA of four warps covers kRT row tiles × kKW K steps (more tokens: more rows
-// to a CTA, since the CTA's copies of X grow with them); the S CTAs of a cluster
-// share the K range of the same rows.  Sums join in a fixed order: the kKW warps
-// in shared memory, then the cluster's CTAs through distributed shared memory.
+// The product is swapped (weight rows are the 16-row operand of the warp-level
+// step, up to 8·kNT tokens its columns).  What bounds it: at up to 8 tokens the
+// stream of codes and, nearly as much, the 555 instructions that a warp spends on
+// 4 KiB of them (one token, 28672 × 8192: 24.1 us, 75 % of the copy bandwidth;
+// the loads alone 20.1); above that the instructions (16 tokens, 8192 × 8192:
+// 13.4 us, loads alone 8.8; 31 tokens, 12300 × 4128 in groups of 32: 19.3, 9.2).
+// A warp owns 64 rows × 128 K at a time, in a ring of shared-memory stages filled
+// by 16-byte asynchronous copies, with up to four row blocks' chains of
+// tensor-core steps interleaved.  A CTA covers kRT row tiles × kKW K steps (at
+// 32 tokens two tiles, since the CTA's copies of X grow with them); the CTAs of a
+// cluster share the K range of the same rows.  Sums join in a fixed order: the
+// kKW warps in shared memory, then the cluster's CTAs through distributed shared
+// memory.
+//
+// The tcgen05 tensor core is not faster here: with the operands stored to tensor
+// memory by the warps and the sums read back for each group, the same cases took
+// 50, 17.5 and 20.6 us.  The warps' own work stays, and hand-overs come to it.
 constexpr uint32_t kQ4Unit = 0x7E807E80u;      // 2^126, twice: codes that stand for q·2^-133
 constexpr uint32_t kQ4UnitHigh = 0x7C807C80u;  // 2^122: for q·2^-129
 constexpr uint32_t kQ4UnitMinus = 0xFE80FE80u;
@@ -237,10 +246,8 @@ __global__ void __launch_bounds__(Q4Tile<kNT>::kThreads, Q4Tile<kNT>::kPerSm) q4
     for (int step = step0; step < step1; step += kKW) {
         if (stages == 2)
             cp_async_wait<0>();
-        else if (stages == 3)
-            cp_async_wait<1>();
         else
-            cp_async_wait<2>();
+            cp_async_wait<1>();
         meet();
         load(step + (stages - 1) * kKW, slot_in);
         if (++slot_in == stages) slot_in = 0;
