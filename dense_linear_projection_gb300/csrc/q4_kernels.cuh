@@ -110,6 +110,14 @@ __device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t 
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
+// a0 += s·b0, a1 += s·b1 in one instruction.
+__device__ __forceinline__ void fma_pair(float &a0, float &a1, float s, float b0, float b1) {
+    asm("{\n\t.reg .b64 a, b, c;\n\t"
+        "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%3, %4};\n\tmov.b64 c, {%2, %2};\n\t"
+        "fma.rn.f32x2 a, b, c, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(a0), "+f"(a1)
+        : "f"(s), "f"(b0), "f"(b1));
+}
 __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -331,10 +339,8 @@ __global__ void __launch_bounds__(Q4Tile<kNT>::kThreads, Q4Tile<kNT>::kPerSm) q4
                 for (int r = 0; r < kTogether; ++r)
 #pragma unroll
                     for (int t = 0; t < kNT; ++t) {
-                        acc[r0 + r][t][0] += s[r][0] * part[r][t][0];
-                        acc[r0 + r][t][1] += s[r][0] * part[r][t][1];
-                        acc[r0 + r][t][2] += s[r][1] * part[r][t][2];
-                        acc[r0 + r][t][3] += s[r][1] * part[r][t][3];
+                        fma_pair(acc[r0 + r][t][0], acc[r0 + r][t][1], s[r][0], part[r][t][0], part[r][t][1]);
+                        fma_pair(acc[r0 + r][t][2], acc[r0 + r][t][3], s[r][1], part[r][t][2], part[r][t][3]);
                     }
             }
         }
