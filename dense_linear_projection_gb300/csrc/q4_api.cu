@@ -34,7 +34,7 @@ int pack_blocks(int64_t items, int sm_count) {
 using Q4Kernel = void (*)(Q4Params);
 struct Q4Instance {
     Q4Kernel kernel;
-    int warps, per_sm, row_tiles, k_steps, red;  // of a CTA; bytes of its join
+    int warps, row_blocks, per_sm, row_tiles, k_steps, red;  // row blocks of a warp; of a CTA; bytes of its join
 };
 
 template <int kNT>
@@ -47,7 +47,7 @@ Q4Instance instance_nt(int64_t group, bool zeros) {
         k = zeros ? dev::q4_kernel<kNT, 2, true> : dev::q4_kernel<kNT, 2, false>;
     else
         k = zeros ? dev::q4_kernel<kNT, 4, true> : dev::q4_kernel<kNT, 4, false>;
-    return {k, Tile::kWarps, Tile::kPerSm, Tile::kRT, Tile::kKW, Tile::kRed};
+    return {k, Tile::kWarps, Tile::kR, Tile::kPerSm, Tile::kRT, Tile::kKW, Tile::kRed};
 }
 
 Q4Instance instance_for(int64_t M, int64_t group, bool zeros) {
@@ -153,9 +153,9 @@ proj_status_t proj_q4_run(proj_q4_handle_t h, int64_t M, const void *X, const vo
     const int64_t tiles = (p.row_tiles + q.row_tiles - 1) / q.row_tiles;
     const int64_t passes = (M + kQ4MaxTokens - 1) / kQ4MaxTokens;
     // CTAs of one K range: as many as stand on the GPU at once, while every
-    // warp has a step.  (31 tokens, 12300 rows, 97 tiles at two CTAs an SM: 3 a
-    // range 19.3 us, 2 a range 22, 4 a range, two waves, 27.  28672 rows, 448
-    // tiles: one 24.1 us, two 28.)
+    // warp has a step.  (31 tokens, 12300 rows, 97 tiles at four CTAs an SM: 6 a
+    // range 17.5 us, 3 a range 22.  28672 rows, 448 tiles at two CTAs an SM: one
+    // 23.8 us, two, that is three waves, 28.)
     const int64_t steps = (p.k_blocks + 1) / 2;
     int64_t splits = q.per_sm * int64_t(h->sm_count) / tiles;
     if (splits > steps / q.k_steps) splits = steps / q.k_steps;
@@ -164,7 +164,7 @@ proj_status_t proj_q4_run(proj_q4_handle_t h, int64_t M, const void *X, const vo
     // way then; three were 7 % slower), three where 8 do.
     const int tokens = static_cast<int>(M < kQ4MaxTokens ? M : kQ4MaxTokens);
     const int groups = static_cast<int>(128 / h->group);
-    const int stage = q.warps * (4096 + groups * (128 + (h->has_zeros ? 32 : 0))) + q.k_steps * tokens * kQ4XPitch;
+    const int stage = q.warps * q.row_blocks * (1024 + groups * (32 + (h->has_zeros ? 8 : 0))) + q.k_steps * tokens * kQ4XPitch;
     const int fit = (kSmemOfSm / q.per_sm - 1024) / stage, most = q.warps * q.per_sm > 8 ? 2 : 3;
     p.stages = fit < 2 ? 2 : fit < most ? fit : most;  // (two of the largest leave room for one CTA an SM)
     int smem = p.stages * stage;

@@ -79,11 +79,10 @@ __global__ void q4_pack_scales_kernel(const uint16_t *scales, const uint8_t *zer
 // 4 KiB of them (one token, 28672 × 8192: 24.1 us, 75 % of the copy bandwidth;
 // the loads alone 20.1); above that the instructions (16 tokens, 8192 × 8192:
 // 13.4 us, loads alone 8.8; 31 tokens, 12300 × 4128 in groups of 32: 19.3, 9.2).
-// A warp owns 64 rows × 128 K at a time, in a ring of shared-memory stages filled
-// by 16-byte asynchronous copies, with up to four row blocks' chains of
-// tensor-core steps interleaved.  A CTA covers kRT row tiles × kKW K steps (at
-// 32 tokens two tiles, since the CTA's copies of X grow with them); the CTAs of a
-// cluster share the K range of the same rows.  Sums join in a fixed order: the
+// A warp owns 64 or 32 rows × 128 K at a time, in a ring of shared-memory stages
+// filled by 16-byte asynchronous copies.  A CTA covers kRT row tiles × kKW K steps
+// (at 32 tokens two tiles, since the CTA's copies of X grow with them); the CTAs of
+// a cluster share the K range of the same rows.  Sums join in a fixed order: the
 // kKW warps in shared memory, then the cluster's CTAs through distributed shared
 // memory.
 //
@@ -95,14 +94,22 @@ constexpr uint32_t kQ4UnitHigh = 0x7C807C80u;  // 2^122: for q·2^-129
 constexpr uint32_t kQ4UnitMinus = 0xFE80FE80u;
 constexpr float kQ4Restore = 128.f;
 
+// How a CTA is cut, measured over 1, 2 and 4 row tiles, 2 and 4 row blocks a warp
+// and 8 to 16 warps an SM.  Up to 8 tokens registers allow 16 warps of four row
+// blocks; 16 tokens run best on 8 (13.3 us against 14.0 to 14.6 for 16 warps, whose
+// copies of X leave room for fewer stages); 32 tokens on 16 warps of two row
+// blocks, four of them sharing X (17.5 us; 8 warps of four row blocks 18.1).
 template <int kNT>
 struct Q4Tile {
     static constexpr int kWarps = kNT == 4 ? 4 : 8, kThreads = 32 * kWarps;
-    static constexpr int kPerSm = kNT == 2 ? 1 : 2;  // CTAs an SM: 16 warps at 8 tokens, 8 above (registers)
-    static constexpr int kRT = kNT == 4 ? 2 : 1;     // row tiles of a CTA
-    static constexpr int kKW = kWarps / kRT;      // K steps at a time
-    static constexpr int kPitch = kRT * 64 + 4;   // floats of a token's rows while joining: conflict-free
+    static constexpr int kR = kNT == 4 ? 2 : 4;                         // row blocks of a warp
+    static constexpr int kRT = kNT == 4 ? 2 : 1;                        // row tiles of a CTA
+    static constexpr int kPerSm = kNT == 1 ? 2 : kNT == 2 ? 1 : 4;      // CTAs an SM
+    static constexpr int kShare = kRT * 4 / kR;      // warps that share a K step
+    static constexpr int kKW = kWarps / kShare;      // K steps at a time
+    static constexpr int kPitch = kRT * 64 + 4;      // floats of a token's rows while joining: conflict-free
     static constexpr int kRed = kKW * 8 * kNT * kPitch * 4;
+    static_assert(kKW * kShare == kWarps, "whole K steps");
 };
 
 __device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
@@ -157,22 +164,23 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
 template <int kNT, int kGroups, bool kZeros>
 __global__ void __launch_bounds__(Q4Tile<kNT>::kThreads, Q4Tile<kNT>::kPerSm) q4_kernel(const Q4Params p) {
     using Tile = Q4Tile<kNT>;
-    constexpr int kRT = Tile::kRT, kKW = Tile::kKW;
+    constexpr int kRT = Tile::kRT, kKW = Tile::kKW, kR = Tile::kR, kShare = Tile::kShare;
     extern __shared__ __align__(128) uint8_t smem[];
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rt = warp % kRT, kw = warp / kRT;
+    const int part_of = warp % kShare, kw = warp / kShare;  // which of the CTA's rows, which K steps
     const int g = lane >> 2, j = lane & 3;
     const int rank = static_cast<int>(blockIdx.x % p.splits);
     const int64_t tile0 = blockIdx.x / p.splits * kRT;  // the CTA's first row tile
-    const int64_t tile = tile0 + rt;
+    const int64_t tile = tile0 + part_of * kR / 4;
+    const int block0 = part_of * kR % 4;  // the warp's first row block of its tile
     const bool rows_there = tile < p.row_tiles;
     const int64_t m0 = blockIdx.y * int64_t(kQ4MaxTokens);
     const int M = static_cast<int>(p.M - m0 < kQ4MaxTokens ? p.M - m0 : kQ4MaxTokens);
 
     // A stage: each warp's codes, scales and zero points, then X for each K step.
-    constexpr int kScaleBytes = kGroups * 128, kZeroBytes = kZeros ? kGroups * 32 : 0;
-    constexpr int kWarpBytes = 4096 + kScaleBytes + kZeroBytes;
+    constexpr int kCodeBytes = kR * 1024, kScaleBytes = kGroups * kR * 32, kZeroBytes = kZeros ? kGroups * kR * 8 : 0;
+    constexpr int kWarpBytes = kCodeBytes + kScaleBytes + kZeroBytes;
     const int x_bytes = M * kQ4XPitch;
     const int stage_bytes = Tile::kWarps * kWarpBytes + kKW * x_bytes;
     const uint32_t base = smem_u32(smem);
@@ -185,19 +193,24 @@ __global__ void __launch_bounds__(Q4Tile<kNT>::kThreads, Q4Tile<kNT>::kPerSm) q4
 #pragma unroll
     for (int t = 0; t < kNT; ++t) x_row[t] = min(8 * t + g, M - 1) * kQ4XPitch + j * 16;
 
-    float acc[4][kNT][4];
+    float acc[kR][kNT][4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < kR; ++r)
 #pragma unroll
         for (int t = 0; t < kNT; ++t) acc[r][t][0] = acc[r][t][1] = acc[r][t][2] = acc[r][t][3] = 0.f;
 
-    // Loading: pointers to this lane's next step.
-    const uint8_t *codes = reinterpret_cast<const uint8_t *>(p.codes) + (tile * p.k_blocks + step0 * 2) * 2048 + lane * 16;
-    const uint8_t *scales = reinterpret_cast<const uint8_t *>(p.scales) + (tile * p.groups_padded + step0 * kGroups) * 128 + lane * 16;
-    const uint8_t *zeros = kZeros ? p.zeros + (tile * p.groups_padded + step0 * kGroups) * 32 + lane * 16 : nullptr;
-    const int x_first = (rt * 32 + lane) / 16, x_chunk = lane % 16;  // first of the tokens this lane copies; its 8 K of the step
+    // Loading: pointers to this lane's next step.  A group's scales are 2·kR
+    // copies of 16 bytes, its zero points kR / 2.
+    const uint8_t *codes = reinterpret_cast<const uint8_t *>(p.codes) + (tile * p.k_blocks + step0 * 2) * 2048 + block0 * 512 + lane * 16;
+    const int scale_group = lane / (2 * kR), zero_group = lane / (kR / 2);
+    const uint8_t *scales = reinterpret_cast<const uint8_t *>(p.scales) +
+                            (tile * p.groups_padded + step0 * kGroups + scale_group) * 128 + block0 * 32 + lane % (2 * kR) * 16;
+    const uint8_t *zeros = kZeros ? p.zeros + (tile * p.groups_padded + step0 * kGroups + zero_group) * 32 + block0 * 8 +
+                                        lane % (kR / 2) * 16
+                                  : nullptr;
+    const int x_first = (part_of * 32 + lane) / 16, x_chunk = lane % 16;  // first of the tokens this lane copies; its 8 K of the step
     const uint8_t *x = reinterpret_cast<const uint8_t *>(p.X + (m0 + x_first) * p.K + step0 * 128 + x_chunk * 8);
-    const int64_t x_next = 2 * kRT * p.K * 2;  // bytes to the lane's next token
+    const int64_t x_next = 2 * kShare * p.K * 2;  // bytes to the lane's next token
     const int whole = static_cast<int>((p.K / 128 < step1 ? p.K / 128 : step1));  // steps below it lie inside K
     auto load = [&](int step, int slot) {
         if (step < step1) {
@@ -207,44 +220,45 @@ __global__ void __launch_bounds__(Q4Tile<kNT>::kThreads, Q4Tile<kNT>::kPerSm) q4
             if (step < whole) {
                 if (rows_there) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) cp_async16(w + i * 512, codes + i * 512);
-                    if (lane < kGroups * 8) cp_async16(w + 4096, scales);
-                    if (kZeros && lane < kGroups * 2) cp_async16(w + 4096 + kScaleBytes, zeros);
+                    for (int i = 0; i < 2 * kR; ++i) cp_async16(w + i * 512, codes + i / kR * 2048 + i % kR * 512);
+                    if (scale_group < kGroups) cp_async16(w + kCodeBytes, scales);
+                    if (kZeros && zero_group < kGroups) cp_async16(w + kCodeBytes + kScaleBytes, zeros);
                 }
-                for (int m = x_first; m < M; m += 2 * kRT, to += 2 * kRT * kQ4XPitch, from += x_next) cp_async16(to, from);
+                for (int m = x_first; m < M; m += 2 * kShare, to += 2 * kShare * kQ4XPitch, from += x_next) cp_async16(to, from);
             } else {
                 // K ends inside the step: the blocks of codes and the groups
                 // that exist, and zeros for the rest.
-                const int blocks = step * 2 + 1 < p.k_blocks ? 8 : 4;
+                const int blocks = step * 2 + 1 < p.k_blocks ? 2 : 1;
                 if (rows_there) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) cp_async16(w + i * 512, i < blocks ? codes + i * 512 : codes, i < blocks);
-                    if (lane < kGroups * 8) {
-                        const bool in = step * kGroups + lane / 8 < p.groups_padded;
-                        cp_async16(w + 4096, in ? scales : codes, in);
+                    for (int i = 0; i < 2 * kR; ++i)
+                        cp_async16(w + i * 512, i / kR < blocks ? codes + i / kR * 2048 + i % kR * 512 : codes, i / kR < blocks);
+                    if (scale_group < kGroups) {
+                        const bool in = step * kGroups + scale_group < p.groups_padded;
+                        cp_async16(w + kCodeBytes, in ? scales : codes, in);
                     }
-                    if (kZeros && lane < kGroups * 2) {
-                        const bool in = step * kGroups + lane / 2 < p.groups_padded;
-                        cp_async16(w + 4096 + kScaleBytes, in ? zeros : codes, in);
+                    if (kZeros && zero_group < kGroups) {
+                        const bool in = step * kGroups + zero_group < p.groups_padded;
+                        cp_async16(w + kCodeBytes + kScaleBytes, in ? zeros : codes, in);
                     }
                 }
                 const bool in = step * 128 + x_chunk * 8 < p.K;
-                for (int m = x_first; m < M; m += 2 * kRT, to += 2 * kRT * kQ4XPitch, from += x_next)
+                for (int m = x_first; m < M; m += 2 * kShare, to += 2 * kShare * kQ4XPitch, from += x_next)
                     cp_async16(to, in ? from : codes, in);
             }
             codes += kKW * 4096;
-            scales += kKW * kScaleBytes;
-            if (kZeros) zeros += kKW * kZeroBytes;
+            scales += kKW * kGroups * 128;
+            if (kZeros) zeros += kKW * kGroups * 32;
             x += kKW * 256;
         }
         cp_async_commit();
     };
     // The warps that share a step's X.
     auto meet = [&]() {
-        if constexpr (kRT == 1)
+        if constexpr (kShare == 1)
             __syncwarp();
         else
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + kw), "n"(32 * kRT) : "memory");
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + kw), "n"(32 * kShare) : "memory");
     };
 
     griddep_wait();
@@ -262,86 +276,75 @@ __global__ void __launch_bounds__(Q4Tile<kNT>::kThreads, Q4Tile<kNT>::kPerSm) q4
         const uint32_t w = my_w + slot * stage_bytes, xs = my_x + slot * stage_bytes;
         if (++slot == stages) slot = 0;
 
-        // X as the second operand: column (token) g; columns past M repeat the
-        // last token and are dropped.
-        uint32_t b[kNT][16];
+        // A warp's row blocks go together: independent chains of tensor-core
+        // steps that cover their latency.
+        constexpr int kWords = 8 / kGroups;         // tensor-core steps of a group
+        constexpr int kPiece = kWords < 4 ? 2 : 4;  // steps whose operands are loaded at once
 #pragma unroll
-        for (int t = 0; t < kNT; ++t)
+        for (int group = 0; group < kGroups; ++group) {
+            float part[kR][kNT][4];
+            uint32_t z[kR][2];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const uint4 v = lds128(xs + x_row[t] + h * 64);
-                b[t][4 * h] = v.x, b[t][4 * h + 1] = v.y, b[t][4 * h + 2] = v.z, b[t][4 * h + 3] = v.w;
+            for (int r = 0; r < kR; ++r) {
+                if constexpr (kZeros) {
+                    const uint32_t both = lds8(w + kCodeBytes + kScaleBytes + group * kR * 8 + r * 8 + g);
+                    z[r][0] = bf16x2_mul((both & 15u) * 0x00010001u, kQ4UnitMinus);
+                    z[r][1] = bf16x2_mul((both >> 4) * 0x00010001u, kQ4UnitMinus);
+                } else {
+                    z[r][0] = z[r][1] = 0xBD80BD80u;  // −8·2^-7
+                }
             }
-        // Row blocks together: enough independent chains of tensor-core steps
-        // to cover their latency.
-        constexpr int kTogether = kNT == 1 ? 4 : kNT == 2 ? 2 : 1;
-        constexpr int kWords = 8 / kGroups;  // tensor-core steps of a group
 #pragma unroll
-        for (int r0 = 0; r0 < 4; r0 += kTogether) {
+            for (int i0 = 0; i0 < kWords; i0 += kPiece) {
+                const int at = group * kWords + i0;  // of the eight steps
+                // X as the second operand: column (token) g; columns past M
+                // repeat the last token and are dropped.
+                uint32_t b[kNT][2 * kPiece], word[kR][kPiece];
 #pragma unroll
-            for (int group = 0; group < kGroups; ++group) {
-                float part[kTogether][kNT][4];
-                uint32_t z[kTogether][2];
+                for (int t = 0; t < kNT; ++t)
 #pragma unroll
-                for (int r = 0; r < kTogether; ++r) {
-                    if constexpr (kZeros) {
-                        const uint32_t both = lds8(w + 4096 + kScaleBytes + group * 32 + (r0 + r) * 8 + g);
-                        z[r][0] = bf16x2_mul((both & 15u) * 0x00010001u, kQ4UnitMinus);
-                        z[r][1] = bf16x2_mul((both >> 4) * 0x00010001u, kQ4UnitMinus);
+                    for (int h = 0; h < kPiece / 2; ++h) {
+                        const uint4 v = lds128(xs + x_row[t] + (at / 2 + h) * 64);
+                        b[t][4 * h] = v.x, b[t][4 * h + 1] = v.y, b[t][4 * h + 2] = v.z, b[t][4 * h + 3] = v.w;
+                    }
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+                    const uint32_t from = w + (at / 4) * kR * 512 + r * 512 + lane * 16 + (at % 4) * 4;  // four steps: 16 bytes
+                    if constexpr (kPiece == 4) {
+                        const uint4 v = lds128(from);
+                        word[r][0] = v.x, word[r][1] = v.y, word[r][2] = v.z, word[r][3] = v.w;
                     } else {
-                        z[r][0] = z[r][1] = 0xBD80BD80u;  // −8·2^-7
+                        const uint2 v = lds64(from);
+                        word[r][0] = v.x, word[r][1] = v.y;
                     }
                 }
-                constexpr int kPiece = kWords < 4 ? 2 : 4;  // words of one load
 #pragma unroll
-                for (int i0 = 0; i0 < kWords; i0 += kPiece) {
-                    uint32_t word[kTogether][kPiece];
+                for (int i = 0; i < kPiece; ++i)
 #pragma unroll
-                    for (int r = 0; r < kTogether; ++r) {
-                        const int at = group * kWords + i0;  // steps 4·kb + (0..3) share 16 bytes
-                        const uint32_t from = w + (at / 4) * 2048 + (r0 + r) * 512 + lane * 16 + (at % 4) * 4;
-                        if constexpr (kPiece == 4) {
-                            const uint4 v = lds128(from);
-                            word[r][0] = v.x, word[r][1] = v.y, word[r][2] = v.z, word[r][3] = v.w;
-                        } else {
-                            const uint2 v = lds64(from);
-                            word[r][0] = v.x, word[r][1] = v.y;
+                    for (int r = 0; r < kR; ++r) {
+                        const uint32_t now = word[r][i], next = now >> 8;
+                        const uint32_t a0 = bf16x2_fma(now & 0x000f000fu, kQ4Unit, z[r][0]);
+                        const uint32_t a1 = bf16x2_fma(next & 0x000f000fu, kQ4Unit, z[r][1]);
+                        const uint32_t a2 = bf16x2_fma(now & 0x00f000f0u, kQ4UnitHigh, z[r][0]);
+                        const uint32_t a3 = bf16x2_fma(next & 0x00f000f0u, kQ4UnitHigh, z[r][1]);
+#pragma unroll
+                        for (int t = 0; t < kNT; ++t) {
+                            if (i0 + i == 0)
+                                mma16816_first<false>(part[r][t], a0, a1, a2, a3, b[t][2 * i], b[t][2 * i + 1]);
+                            else
+                                mma16816<false>(part[r][t], a0, a1, a2, a3, b[t][2 * i], b[t][2 * i + 1]);
                         }
                     }
+            }
 #pragma unroll
-                    for (int i = 0; i < kPiece; ++i) {
-                        const int at = group * kWords + i0 + i;
+            for (int r = 0; r < kR; ++r) {
+                const uint32_t two = lds32(w + kCodeBytes + group * kR * 32 + r * 32 + g * 4);
+                const float s0 = __uint_as_float(two << 16), s1 = __uint_as_float(two & 0xffff0000u);
 #pragma unroll
-                        for (int r = 0; r < kTogether; ++r) {
-                            const uint32_t now = word[r][i], next = now >> 8;
-                            const uint32_t a0 = bf16x2_fma(now & 0x000f000fu, kQ4Unit, z[r][0]);
-                            const uint32_t a1 = bf16x2_fma(next & 0x000f000fu, kQ4Unit, z[r][1]);
-                            const uint32_t a2 = bf16x2_fma(now & 0x00f000f0u, kQ4UnitHigh, z[r][0]);
-                            const uint32_t a3 = bf16x2_fma(next & 0x00f000f0u, kQ4UnitHigh, z[r][1]);
-#pragma unroll
-                            for (int t = 0; t < kNT; ++t) {
-                                if (i0 + i == 0)
-                                    mma16816_first<false>(part[r][t], a0, a1, a2, a3, b[t][2 * at], b[t][2 * at + 1]);
-                                else
-                                    mma16816<false>(part[r][t], a0, a1, a2, a3, b[t][2 * at], b[t][2 * at + 1]);
-                            }
-                        }
-                    }
+                for (int t = 0; t < kNT; ++t) {
+                    fma_pair(acc[r][t][0], acc[r][t][1], s0, part[r][t][0], part[r][t][1]);
+                    fma_pair(acc[r][t][2], acc[r][t][3], s1, part[r][t][2], part[r][t][3]);
                 }
-                float s[kTogether][2];
-#pragma unroll
-                for (int r = 0; r < kTogether; ++r) {
-                    const uint32_t two = lds32(w + 4096 + group * 128 + (r0 + r) * 32 + g * 4);
-                    s[r][0] = __uint_as_float(two << 16);
-                    s[r][1] = __uint_as_float(two & 0xffff0000u);
-                }
-#pragma unroll
-                for (int r = 0; r < kTogether; ++r)
-#pragma unroll
-                    for (int t = 0; t < kNT; ++t) {
-                        fma_pair(acc[r0 + r][t][0], acc[r0 + r][t][1], s[r][0], part[r][t][0], part[r][t][1]);
-                        fma_pair(acc[r0 + r][t][2], acc[r0 + r][t][3], s[r][1], part[r][t][2], part[r][t][3]);
-                    }
             }
         }
     }
@@ -352,10 +355,10 @@ __global__ void __launch_bounds__(Q4Tile<kNT>::kThreads, Q4Tile<kNT>::kPerSm) q4
     float *red = reinterpret_cast<float *>(smem);
     constexpr int kPitch = Tile::kPitch, kPlane = 8 * kNT * kPitch;
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < kR; ++r)
 #pragma unroll
         for (int t = 0; t < kNT; ++t) {
-            float *to = red + kw * kPlane + (8 * t + 2 * j) * kPitch + rt * 64 + r * 16 + g;
+            float *to = red + kw * kPlane + (8 * t + 2 * j) * kPitch + (part_of * kR + r) * 16 + g;
             to[0] = acc[r][t][0];
             to[kPitch] = acc[r][t][1];
             to[8] = acc[r][t][2];
