@@ -44,8 +44,9 @@ KvCacheView view_of(const proj_kv_s *h, const int32_t *table, int64_t table_widt
 // A bf16 row array: base and row stride whole 16-byte multiples.
 bool rows_aligned(const void *p, int64_t stride) { return aligned16(p) && stride % 8 == 0; }
 
+// Tokens are counted in 32 bits, with room for a tile past the last one.
 bool fits_table(int64_t table_width, int32_t page_size) {
-    return table_width >= 0 && table_width <= kMaxDim && table_width * page_size <= kMaxDim;
+    return table_width >= 0 && table_width <= kMaxDim && table_width * page_size <= kMaxDim - 4095;
 }
 
 // A launch whose set-up may overlap the preceding kernel's tail.

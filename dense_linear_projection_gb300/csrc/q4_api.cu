@@ -80,6 +80,7 @@ proj_status_t proj_q4_create(proj_q4_handle_t *out, int64_t max_tokens, int64_t 
     if (max_tokens < 0 || max_tokens > kMaxDim || (has_bias != 0 && has_bias != 1) ||
         (y_dtype != PROJ_BF16 && y_dtype != PROJ_F32))
         return PROJ_ERR_INVALID_ARG;
+    if (max_tokens > int64_t(65535) * kQ4MaxTokens) return PROJ_ERR_UNSUPPORTED;  // passes: the grid's second dimension
     const int sms = gb300_sm_count();
     if (sms <= 0) return sms < 0 ? PROJ_ERR_CUDA : PROJ_ERR_UNSUPPORTED;
     for (int64_t m = 8; m <= kQ4MaxTokens; m *= 2)

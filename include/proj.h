@@ -526,13 +526,13 @@ proj_status_t proj_selftest_wait_timeout(int64_t limit_ns, void *stream);
  *   lanes take them, then the scales, then the zero points.  It depends on N,
  *   K, group and has_zeros alone: every handle with those runs it.
  *
- * proj_q4_create: max_tokens is the largest M of a run (it sizes the scratch).
+ * proj_q4_create: max_tokens bounds M of a run (at most 2097120).
  *   group 32, 64 or 128 (else PROJ_ERR_UNSUPPORTED), K a multiple of it (else
  *   PROJ_ERR_INVALID_ARG); N of any size; K = 0 gives Y = bias or 0.
  * proj_q4_run: X [M, K] bf16 (16-byte aligned), bias [N] bf16 or NULL as
  *   created, Y [M, N] of y_dtype; 0 ≤ M ≤ max_tokens.  Asynchronous, no
- *   allocation, can be captured in a graph.  One handle must not run on two
- *   streams at the same time.
+ *   allocation, can be captured in a graph.  The handle owns no device memory
+ *   and may run on several streams at the same time.  Reruns are bit-identical.
  */
 typedef struct proj_q4_s *proj_q4_handle_t;
 
@@ -562,7 +562,8 @@ proj_status_t proj_q4_destroy(proj_q4_handle_t h);
  * proj_kv_create: head_dim a multiple of 16 up to 256, q_heads a multiple of
  *   kv_heads, page_size ≥ 1; strides whole 16-byte multiples (else
  *   PROJ_ERR_MISALIGNED).  max_sequences bounds the sequences of one
- *   proj_kv_attend.  A handle owns scratch for joining split sequences and a
+ *   proj_kv_attend, whose page tables may hold up to 2^31 − 4096 tokens a
+ *   sequence.  A handle owns scratch for joining split sequences and a
  *   status word; one handle may serve every layer whose cache has its
  *   geometry, but must not run on two streams at the same time.
  *

@@ -37,6 +37,14 @@ def test_cache_geometry_refusals(change, status):
     assert e.value.status == status
 
 
+def test_projection_refusals():
+    for args, status in [((2097121, 64, 64, 64), dlp.PROJ_ERR_UNSUPPORTED), ((1, 64, 64, 16), dlp.PROJ_ERR_UNSUPPORTED),
+                         ((1, 64, 65, 64), dlp.PROJ_ERR_INVALID_ARG), ((1, -1, 64, 64), dlp.PROJ_ERR_INVALID_ARG)]:
+        with pytest.raises(dlp.ProjError) as e:
+            dlp.proj_q4_create(*args)
+        assert e.value.status == status
+
+
 def test_null_handles():
     L = dlp.lib()
     assert L.proj_q4_run(None, 1, None, None, None, None, None) == dlp.PROJ_ERR_INVALID_ARG

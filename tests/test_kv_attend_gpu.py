@@ -236,6 +236,8 @@ def test_refusals():
                                     1.0, q, 512, None), misaligned),
         (lambda: dlp.proj_kv_attend(kv.handle, 2, q, 512, None, v, None, None, table, table.shape[1], lens, 0, 1.0, q,
                                     512, None), invalid),
+        (lambda: dlp.proj_kv_attend(kv.handle, 2, q, 512, k, v, None, None, table, (1 << 31) // 16, lens, 0, 1.0, q, 512,
+                                    None), invalid),                             # more tokens than 32 bits count
         (lambda: dlp.proj_kv_attend(None, 2, q, 512, k, v, None, None, table, table.shape[1], lens, 0, 1.0, q, 512,
                                     None), invalid),
     ]:
