@@ -36,7 +36,7 @@
 namespace projgb {
 namespace dev {
 
-template <bool kE4m3, int kDim, int kNT>
+template <bool kE4m3, int kDim, int kNT, int kKeyHeads>
 struct AttendShape {
     static constexpr int kElem = kE4m3 ? 1 : 2;
     static constexpr int kRow = kDim * kElem;         // bytes of a token's row in a stage
@@ -46,9 +46,13 @@ struct AttendShape {
     // (an 8-bit cache of 128-wide heads ran at 66 % of the copy bandwidth with one).
     static constexpr int kBlocks = kRow <= 128 ? 2 : 1;
     static constexpr int kStep = 16 * kBlocks;        // tokens of a warp's step
-    static constexpr int kTile = kKvWarps * kStep;    // unit of the work shared between CTAs
+    // A CTA's row is one key head with its warps on consecutive steps, or two key
+    // heads with two warps each.
+    static constexpr int kLanes = kKvWarps / kKeyHeads;
+    static constexpr int kTile = kLanes * kStep;      // unit of the work shared between CTAs
     static constexpr int kStage = 2 * kStep * kRow;   // keys, then values
-    static constexpr int kHeads = 8 * kNT;
+    static constexpr int kHeads = 8 * kNT;             // query heads of a warp
+    static constexpr int kRowHeads = kHeads * kKeyHeads;
     static constexpr int kJoin = kKvWarps * kHeads * (kDim + 4) * 4;  // the warps' sums, fp32
     static constexpr int kSmall = kKvWarps * kHeads * 8 + 64;   // their maxima and sums of weights; flags
     // Two CTAs an SM (one for 256-wide heads): while one joins its warps, the
@@ -126,7 +130,7 @@ struct AttendSegment {
     int64_t tiles;          // of the segment: 0 where it holds only the row's start
 };
 
-template <int kStep>
+template <typename Shape>
 __device__ __forceinline__ void read_length(const KvAttendParams &p, int b, AttendCursor &c) {
     const int64_t most = p.cache.table_width * p.cache.page_size;
     int n = p.seq_lens[b];
@@ -136,31 +140,30 @@ __device__ __forceinline__ void read_length(const KvAttendParams &p, int b, Atte
     }
     c.n = n;
     c.low = p.window > 0 && n > p.window ? n - static_cast<int>(p.window) : 0;
-    constexpr int kTile = kKvWarps * kStep;
-    c.tiles = (n - (c.low & ~(kStep - 1)) + kTile - 1) / kTile;
+    c.tiles = (n - (c.low & ~(Shape::kStep - 1)) + Shape::kTile - 1) / Shape::kTile;
     c.span = c.tiles > 0 ? c.tiles + kKvRowCost : 0;
 }
 
 // Moves the cursor to the sequence that holds place `pos` (which exists).
-template <int kStep>
+template <typename Shape>
 __device__ __forceinline__ void seek(const KvAttendParams &p, AttendCursor &c, int64_t pos) {
     while (pos >= c.base + c.span * p.units) {
         c.base += c.span * p.units;
         ++c.b;
-        read_length<kStep>(p, c.b, c);
+        read_length<Shape>(p, c.b, c);
     }
 }
 
 // The part of places [pos, end) that lies in pos's row.
-template <int kStep>
+template <typename Shape>
 __device__ __forceinline__ AttendSegment segment_at(const AttendCursor &c, int64_t pos, int64_t end) {
-    constexpr int kTile = kKvWarps * kStep;
+    constexpr int kTile = Shape::kTile;
     AttendSegment s;
     s.unit = static_cast<int>(divide(pos - c.base, c.span));
     s.row_begin = c.base + s.unit * c.span;
     const int64_t from = pos - s.row_begin, to = end - s.row_begin < c.span ? end - s.row_begin : c.span;
     const int64_t k0 = from > kKvRowCost ? from - kKvRowCost : 0, k1 = to > kKvRowCost ? to - kKvRowCost : 0;
-    const int start = c.low & ~(kStep - 1);
+    const int start = c.low & ~(Shape::kStep - 1);
     s.first = start + static_cast<int>(k0) * kTile;
     s.last = k1 == c.tiles ? c.n : start + static_cast<int>(k1) * kTile;
     s.places = to - from;
@@ -308,17 +311,22 @@ __device__ __forceinline__ bool leave_part(float *partials, int64_t at, uint32_t
     return last;
 }
 
-template <bool kE4m3, int kDim, int kNT>
-__global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPerSm) kv_attend_kernel(KvAttendParams p) {
-    using Shape = AttendShape<kE4m3, kDim, kNT>;
+template <bool kE4m3, int kDim, int kNT, int kKeyHeads>
+__global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKeyHeads>::kPerSm) kv_attend_kernel(KvAttendParams p) {
+    using Shape = AttendShape<kE4m3, kDim, kNT, kKeyHeads>;
     constexpr int kHeads = Shape::kHeads, kStages = Shape::kStages, kRow = Shape::kRow;
     constexpr int kSteps = kDim / 16;  // 16-wide steps over a head
     constexpr int kStep = Shape::kStep, kBlocks = Shape::kBlocks;
+    constexpr int kRowHeads = Shape::kRowHeads;  // head h of a row: query head h / kKeyHeads of its key head h % kKeyHeads
     extern __shared__ __align__(1024) uint8_t smem[];
     griddep_launch_dependents();
     const KvCacheView &cache = p.cache;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, j = lane & 3;
+    const int step_lane = warp / kKeyHeads, row_key = warp % kKeyHeads;  // which of a tile's steps, which key head
+    // Key head `key` of a row, and the chunk of its query heads.  (Two key heads: one chunk.)
+    auto key_head = [&](int unit, int key) { return kKeyHeads == 1 ? unit / p.chunks : unit * kKeyHeads + key; };
+    auto chunk_of = [&](int unit) { return kKeyHeads == 1 ? unit % p.chunks : 0; };
     const uint32_t ring = smem_u32(smem) + warp * kStages * Shape::kStage;
     float *join = reinterpret_cast<float *>(smem + kKvWarps * kStages * Shape::kStage);  // [warp][head][dim + 4]
     float *join_m = join + kKvWarps * kHeads * (kDim + 4);                                    // [warp][head]
@@ -345,7 +353,7 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
         int64_t incl = 0;
         for (int b = lane * run; b < B && b < (lane + 1) * run; ++b) {
             AttendCursor c;
-            read_length<kStep>(p, b, c);
+            read_length<Shape>(p, b, c);
             incl += c.span * p.units;
         }
 #pragma unroll
@@ -363,8 +371,8 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
             const int64_t before = __shfl_sync(0xffffffffu, incl, from > 0 ? from - 1 : 0);
             cur.base = from > 0 ? before : 0;
             cur.b = from * run;
-            read_length<kStep>(p, cur.b, cur);
-            seek<kStep>(p, cur, pos);
+            read_length<Shape>(p, cur.b, cur);
+            seek<Shape>(p, cur, pos);
         }
     }
 
@@ -373,8 +381,8 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
     int64_t lpos = pos;
     AttendSegment lseg{};
     bool lmore = pos < end;
-    if (lmore) lseg = segment_at<kStep>(lcur, lpos, end);
-    int ltok = lseg.first + warp * kStep;  // first token of the step to load next
+    if (lmore) lseg = segment_at<Shape>(lcur, lpos, end);
+    int ltok = lseg.first + step_lane * kStep;  // first token of the step to load next
     int64_t lhead = 0;  // the row's head in the cache
     int lpage = -1;     // page of token ltok + lane % kStep, -1: not attended
     int lplace = 0;
@@ -385,11 +393,11 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
                 lmore = false;
                 return;
             }
-            seek<kStep>(p, lcur, lpos);
-            lseg = segment_at<kStep>(lcur, lpos, end);
-            ltok = lseg.first + warp * kStep;
+            seek<Shape>(p, lcur, lpos);
+            lseg = segment_at<Shape>(lcur, lpos, end);
+            ltok = lseg.first + step_lane * kStep;
         }
-        lhead = static_cast<int64_t>(lseg.unit / p.chunks) * cache.head_stride;
+        lhead = static_cast<int64_t>(key_head(lseg.unit, row_key)) * cache.head_stride;
         const int t = ltok + (lane & (kStep - 1));
         lpage = -1;
         if (t >= lcur.low && t < lseg.last) {
@@ -444,7 +452,7 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
     // Sequences without tokens have no tiles: their rows are written here.
     for (int b = blockIdx.x; b < B; b += gridDim.x) {
         AttendCursor c;
-        read_length<kStep>(p, b, c);
+        read_length<Shape>(p, b, c);
         if (c.n > 0) continue;
         for (int i = tid; i < p.q_heads * cache.head_dim; i += kKvThreads) p.out[b * p.out_stride + i] = 0;
         if (p.lse)
@@ -461,14 +469,14 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
     AttendSegment seg;
     auto ask = [&]() {
         for (; pos < end; pos += seg.places) {
-            seek<kStep>(p, cur, pos);
-            seg = segment_at<kStep>(cur, pos, end);
+            seek<Shape>(p, cur, pos);
+            seg = segment_at<Shape>(cur, pos, end);
             if (seg.tiles > 0) break;
         }
         if (pos >= end) return;
-        const int chunk = seg.unit % p.chunks, key_head = seg.unit / p.chunks;
+        const int chunk = chunk_of(seg.unit), key = key_head(seg.unit, row_key);
         const int heads = min(p.chunk_heads, p.group - chunk * p.chunk_heads);
-        const int64_t head0 = key_head * p.group + chunk * p.chunk_heads;
+        const int64_t head0 = key * p.group + chunk * p.chunk_heads;
 #pragma unroll
         for (int t = 0; t < kNT; ++t) {
             const uint16_t *q = p.q + cur.b * p.q_stride + (head0 + 8 * t + g) * cache.head_dim;
@@ -483,13 +491,12 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
                 }
             }
         }
-        if (kE4m3 && p.k_scale) key_scale = p.k_scale[key_head];
+        if (kE4m3 && p.k_scale) key_scale = p.k_scale[key];
     };
     ask();
     while (pos < end) {
-        const int hk = seg.unit / p.chunks, chunk = seg.unit % p.chunks;
-        const int head0 = hk * p.group + chunk * p.chunk_heads;
-        const int heads = min(p.chunk_heads, p.group - chunk * p.chunk_heads);
+        const int chunk = chunk_of(seg.unit);
+        const int heads = kKeyHeads * min(p.chunk_heads, p.group - chunk * p.chunk_heads);  // of the row
         const int row_b = cur.b;
         const int64_t row_tiles = cur.tiles, seg_tiles = seg.tiles, row_begin = seg.row_begin;
         const int seg_unit = seg.unit;
@@ -540,7 +547,7 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
             for (int d = 0; d < kSteps; ++d) o[t][d][0] = o[t][d][1] = o[t][d][2] = o[t][d][3] = 0.f;
         }
 
-        for (int tok = seg.first + warp * kStep; tok < seg.last; tok += Shape::kTile) {
+        for (int tok = seg.first + step_lane * kStep; tok < seg.last; tok += Shape::kTile) {
             cp_async_wait<kStages - 2>();
             __syncwarp();
             uint32_t bits = 0;
@@ -686,7 +693,7 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
         ask();
 
         // Join the warps.
-        using Part = JoinPart<kHeads, kDim>;
+        using Part = JoinPart<kRowHeads, kDim>;
 #pragma unroll
         for (int t = 0; t < kNT; ++t) {
 #pragma unroll
@@ -720,18 +727,19 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
         for (int k = 0; k < Part::kPer; ++k) {
             const int h = h0 + k * Part::kHeadStep;
             if (h >= heads) break;
-            float warp_m[kKvWarps];
+            const int at = h % kKeyHeads * kHeads + h / kKeyHeads;  // in the first of its warps
+            float warp_m[Shape::kLanes];
 #pragma unroll
-            for (int i = 0; i < kKvWarps; ++i) {
-                warp_m[i] = join_m[i * kHeads + h];
+            for (int i = 0; i < Shape::kLanes; ++i) {
+                warp_m[i] = join_m[i * kRowHeads + at];
                 r.m[k] = fmaxf(r.m[k], warp_m[i]);
             }
             const float base = finite_or_zero(r.m[k]);
 #pragma unroll
-            for (int i = 0; i < kKvWarps; ++i) {
+            for (int i = 0; i < Shape::kLanes; ++i) {
                 const float w = exp2_fast(warp_m[i] - base);
-                const float4 v = *reinterpret_cast<const float4 *>(join + (i * kHeads + h) * Part::kPitch + d0);
-                r.l[k] += w * join_l[i * kHeads + h];
+                const float4 v = *reinterpret_cast<const float4 *>(join + (i * kRowHeads + at) * Part::kPitch + d0);
+                r.l[k] += w * join_l[i * kRowHeads + at];
                 r.o[k].x += w * v.x, r.o[k].y += w * v.y, r.o[k].z += w * v.z, r.o[k].w += w * v.w;
             }
         }
@@ -751,41 +759,43 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT>::kPe
             // A CTA that has no more to load joins by way of its ring.
             auto join_all = [&](int count, auto at) {
                 if (pos >= end)
-                    join_parts_in<kHeads, kDim>(smem, kKvWarps * kStages * Shape::kStage, p.partials, count, at, heads, r);
+                    join_parts_in<kRowHeads, kDim>(smem, kKvWarps * kStages * Shape::kStage, p.partials, count, at, heads, r);
                 else
-                    join_parts<kHeads, kDim>(p.partials, count, at, heads, r);
+                    join_parts<kRowHeads, kDim>(p.partials, count, at, heads, r);
             };
             if (parts <= kKvJoinOnce) {
-                write = leave_part<kHeads, kDim>(p.partials, slot(mine), counter, parts, heads, r, flag);
+                write = leave_part<kRowHeads, kDim>(p.partials, slot(mine), counter, parts, heads, r, flag);
                 if (write) join_all(parts, slot);
             } else {
                 // Many parts: in groups, each joined into its first part's
                 // slot by its own last arrival, and then the groups.
                 const int size = parts <= kKvJoinMany ? kKvJoinGroup : 2 * kKvJoinGroup;
                 const int g0 = mine / size * size, in_group = min(size, parts - g0);
-                write = leave_part<kHeads, kDim>(p.partials, slot(mine), p.group_counters + slot(g0), in_group, heads, r, flag);
+                write = leave_part<kRowHeads, kDim>(p.partials, slot(mine), p.group_counters + slot(g0), in_group, heads, r, flag);
                 if (write) {
                     join_all(in_group, [&](int i) { return slot(g0 + i); });
                     __syncthreads();  // every thread has read the slot that is written next
                     const int groups = (parts + size - 1) / size;
-                    write = leave_part<kHeads, kDim>(p.partials, slot(g0), counter, groups, heads, r, flag);
+                    write = leave_part<kRowHeads, kDim>(p.partials, slot(g0), counter, groups, heads, r, flag);
                     if (write) join_all(groups, [&](int i) { return slot(i * size); });
                 }
             }
         }
         if (write) {
-            const float by = kE4m3 && p.v_scale ? p.v_scale[hk] : 1.f;
-            uint16_t *out = p.out + row_b * p.out_stride + static_cast<int64_t>(head0) * cache.head_dim + d0;
-            float *lse = p.lse ? p.lse + static_cast<int64_t>(row_b) * p.q_heads + head0 : nullptr;
 #pragma unroll
             for (int k = 0; k < Part::kPer; ++k) {
                 const int h = h0 + k * Part::kHeadStep;
                 if (h >= heads) break;
+                const int key = key_head(seg_unit, h % kKeyHeads);
+                const int64_t head = static_cast<int64_t>(key) * p.group + chunk * p.chunk_heads + h / kKeyHeads;
+                const float by = kE4m3 && p.v_scale ? p.v_scale[key] : 1.f;
                 const float inv = r.l[k] > 0.f ? by / r.l[k] : 0.f;
                 if (d0 < cache.head_dim)
-                    *reinterpret_cast<uint2 *>(out + h * cache.head_dim) =
+                    *reinterpret_cast<uint2 *>(p.out + row_b * p.out_stride + head * cache.head_dim + d0) =
                         make_uint2(bf16_pair(r.o[k].x * inv, r.o[k].y * inv), bf16_pair(r.o[k].z * inv, r.o[k].w * inv));
-                if (lse && d0 == 0) lse[h] = r.l[k] > 0.f ? (r.m[k] + log2f(r.l[k])) * 0.6931471805599453f : -INFINITY;
+                if (p.lse && d0 == 0)
+                    p.lse[static_cast<int64_t>(row_b) * p.q_heads + head] =
+                        r.l[k] > 0.f ? (r.m[k] + log2f(r.l[k])) * 0.6931471805599453f : -INFINITY;
             }
         }
         __syncthreads();  // the join buffer is free again

@@ -65,8 +65,8 @@ struct KvAttendParams {
     int32_t group;        // query heads of a key head
     int32_t chunk_heads;  // of which a row takes this many at most
     int32_t chunks;       // rows of a key head
-    int32_t units;        // kv_heads · chunks: rows of a sequence
-    float *partials;      // [CTA][first, last row][2 + dim][heads]
+    int32_t units;        // rows of a sequence: kv_heads · chunks, or pairs of key heads
+    float *partials;      // [CTA][row begun by another, row begun last][maxima, sums, heads × dim]
     uint32_t *counters;        // [sequence][unit], zero between runs
     uint32_t *group_counters;  // [slot of a partial result], zero between runs
     uint16_t *out;
