@@ -297,12 +297,12 @@ __device__ __forceinline__ bool leave_part(float *partials, int64_t at, uint32_t
     }
     __syncthreads();
     if (threadIdx.x == 0) {
-        __threadfence();  // after the barrier: covers every thread's stores
-        const bool last = atomicAdd(counter, 1u) == static_cast<uint32_t>(expected - 1);
-        if (last) {
-            __threadfence();
-            *counter = 0;  // as every run finds it
-        }
+        // Releases every thread's stores (they happened before the barrier) and
+        // acquires those of the arrivals before it.
+        uint32_t before;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+        const bool last = before == static_cast<uint32_t>(expected - 1);
+        if (last) *counter = 0;  // as every run finds it
         *flag = last;
     }
     __syncthreads();
@@ -362,7 +362,9 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
             if (lane >= o) incl += other;
         }
         total = __shfl_sync(0xffffffffu, incl, 31);
-        ctas = total < gridDim.x ? static_cast<uint32_t>(total) : gridDim.x;  // those that have a place
+        // CTAs at work: each has kKvMinPlaces at least (but the first of few).
+        const int64_t worth = (total + kKvMinPlaces - 1) / kKvMinPlaces;
+        ctas = worth < gridDim.x ? static_cast<uint32_t>(worth) : gridDim.x;
         pos = blockIdx.x < ctas ? share_of(total, blockIdx.x, ctas) : total;
         end = blockIdx.x < ctas ? share_of(total, blockIdx.x + 1, ctas) : total;
         if (pos < end) {
@@ -789,13 +791,13 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
                 const int key = key_head(seg_unit, h % kKeyHeads);
                 const int64_t head = static_cast<int64_t>(key) * p.group + chunk * p.chunk_heads + h / kKeyHeads;
                 const float by = kE4m3 && p.v_scale ? p.v_scale[key] : 1.f;
-                const float inv = r.l[k] > 0.f ? by / r.l[k] : 0.f;
+                const float inv = r.l[k] == 0.f ? 0.f : by / r.l[k];  // (a NaN stays one)
                 if (d0 < cache.head_dim)
                     *reinterpret_cast<uint2 *>(p.out + row_b * p.out_stride + head * cache.head_dim + d0) =
                         make_uint2(bf16_pair(r.o[k].x * inv, r.o[k].y * inv), bf16_pair(r.o[k].z * inv, r.o[k].w * inv));
                 if (p.lse && d0 == 0)
                     p.lse[static_cast<int64_t>(row_b) * p.q_heads + head] =
-                        r.l[k] > 0.f ? (r.m[k] + log2f(r.l[k])) * 0.6931471805599453f : -INFINITY;
+                        r.l[k] == 0.f ? -INFINITY : (r.m[k] + log2f(r.l[k])) * 0.6931471805599453f;
             }
         }
         __syncthreads();  // the join buffer is free again

@@ -12,6 +12,7 @@ constexpr int kKvMaxDim = 256;
 constexpr int kKvWarps = 4;                        // warps of an attention CTA
 constexpr int kKvThreads = 32 * kKvWarps;
 constexpr int kKvRowCost = 2;  // a row's start and join, in tiles (64 ragged sequences: 0, 1, 2 gave 170, 163, 161 us)
+constexpr int kKvMinPlaces = 2;  // of a CTA (one head of 1000 tokens: 1, 2, 4 gave 11.7, 10.4, 11.7 us)
 // Parts of a row that one CTA joins at once; more are joined in groups first
 // (twice as large past kKvJoinMany parts).  A round trip to scratch takes about
 // 1.3 us while the other CTAs stream, and the early groups meet before the last:

@@ -49,6 +49,32 @@ def test_head_groups(heads, kv_heads, dtype):
     run([300, 5, 77], heads, kv_heads, 64, 16, dtype=dtype)
 
 
+@pytest.mark.parametrize("heads,kv_heads", [(32, 2), (24, 2), (4, 4), (18, 6), (16, 1)])
+@pytest.mark.parametrize("dtype,dim", [("e4m3", 128), ("e4m3", 96), ("bf16", 64), ("bf16", 128)])
+def test_pairs_of_key_heads(heads, kv_heads, dtype, dim):
+    # Short rows of memory are taken two key heads at a time, where those are even.
+    run([700, 1, 0, 130], heads, kv_heads, dim, 16, dtype=dtype)
+    run([2500], heads, kv_heads, dim, 16, dtype=dtype, window=900)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_nan_and_infinity_stay_with_their_heads(dtype):
+    # A NaN in one sequence's keys of one head makes that head's outputs and sums NaN, no others.
+    import torch
+    lens, page = [900, 40], 16
+    kv, q, table, lens_dev = case(lens, 8, 4, 64, page, dtype=dtype)
+    ref = ku.attention64(q, kv.k_cache, kv.v_cache, table, lens, page, 64 ** -0.5, 0, kv.k_scale, kv.v_scale)
+    raw = kv.k_cache.view(torch.uint8) if dtype == "e4m3" else kv.k_cache
+    raw[table[0, 20].long(), 3, 2, 5] = 0x7F if dtype == "e4m3" else math.nan
+    out, lse = kv.attend(q, table, lens_dev, return_lse=True)
+    hit = torch.zeros((2, 8), dtype=torch.bool, device="cuda")
+    hit[0, 4:6] = True  # two query heads to a key head
+    assert torch.equal(out.isnan().all(2), hit) and torch.equal(out.isnan().any(2), hit) and torch.equal(lse.isnan(), hit)
+    out, lse = out.masked_fill(hit[..., None], 0), lse.masked_fill(hit, 0)
+    want, want_lse, lim, lim_lse = ref
+    ku.check_attention(out, lse, (want.masked_fill(hit[..., None], 0), want_lse.masked_fill(hit, 0), lim, lim_lse), "others")
+
+
 @pytest.mark.parametrize("dim", [16, 32, 48, 64, 80, 96, 128, 144, 192, 256])
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_head_dims(dim, dtype):
