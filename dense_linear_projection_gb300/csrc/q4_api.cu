@@ -160,7 +160,7 @@ proj_status_t proj_q4_run(proj_q4_handle_t h, int64_t M, const void *X, const vo
     const int64_t steps = (p.k_blocks + 1) / 2;
     int64_t splits = q.per_sm * int64_t(h->sm_count) / tiles;
     if (splits > steps / q.k_steps) splits = steps / q.k_steps;
-    p.splits = static_cast<int32_t>(splits < 1 ? 1 : splits > kQ4MaxSplits ? kQ4MaxSplits : splits);
+    p.splits = static_cast<uint32_t>(splits < 1 ? 1 : splits > kQ4MaxSplits ? kQ4MaxSplits : splits);
     // Two stages where 16 warps stand on an SM (64 KiB of codes are on their
     // way then; three were 7 % slower), three where 8 do.
     const int tokens = static_cast<int>(M < kQ4MaxTokens ? M : kQ4MaxTokens);
@@ -180,7 +180,7 @@ proj_status_t proj_q4_run(proj_q4_handle_t h, int64_t M, const void *X, const vo
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(p.splits);
+    attr[1].val.clusterDim.x = p.splits;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;

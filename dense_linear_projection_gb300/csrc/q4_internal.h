@@ -57,7 +57,7 @@ struct Q4Params {
     int64_t M, N, K, row_tiles, k_blocks, groups_padded;
     int32_t y_f32;
     int32_t y_vec;   // Y's rows start on four-element boundaries: four at a time
-    int32_t splits;  // CTAs of a cluster
+    uint32_t splits;  // CTAs of a cluster
     int32_t stages;  // of the ring: 2 or 3
     const uint16_t *X;
     const uint4 *codes;

@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(Q4Tile<kNT>::kThreads, Q4Tile<kNT>::kPerSm) q4
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int part_of = warp % kShare, kw = warp / kShare;  // which of the CTA's rows, which K steps
     const int g = lane >> 2, j = lane & 3;
-    const int rank = static_cast<int>(blockIdx.x % p.splits);
+    const uint32_t rank = blockIdx.x % p.splits;
     const int64_t tile0 = blockIdx.x / p.splits * kRT;  // the CTA's first row tile
     const int64_t tile = tile0 + part_of * kR / 4;
     const int block0 = part_of * kR % 4;  // the warp's first row block of its tile
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(Q4Tile<kNT>::kThreads, Q4Tile<kNT>::kPerSm) q4
     const uint32_t base = smem_u32(smem);
     const uint32_t my_w = base + warp * kWarpBytes, my_x = base + Tile::kWarps * kWarpBytes + kw * x_bytes;
 
-    const int64_t steps = (p.k_blocks + 1) / 2;
+    const uint32_t steps = static_cast<uint32_t>((p.k_blocks + 1) / 2);  // at most 2^24: 32-bit divisions
     const int step0 = static_cast<int>(steps * rank / p.splits) + kw, step1 = static_cast<int>(steps * (rank + 1) / p.splits);
 
     uint32_t x_row[kNT];  // this lane's place in a step's X
@@ -394,18 +394,20 @@ __global__ void __launch_bounds__(Q4Tile<kNT>::kThreads, Q4Tile<kNT>::kPerSm) q4
             }
         }
     };
-    for (uint32_t e = tid; e < quads; e += Tile::kThreads) {
-        float4 *at = reinterpret_cast<float4 *>(red + (e / kQuads) * kPitch + (e % kQuads) * 4);
-        float4 y = *at;
+    if (kKW > 1 || p.splits == 1) {
+        for (uint32_t e = tid; e < quads; e += Tile::kThreads) {
+            float4 *at = reinterpret_cast<float4 *>(red + (e / kQuads) * kPitch + (e % kQuads) * 4);
+            float4 y = *at;
 #pragma unroll
-        for (int k = 1; k < kKW; ++k) {
-            const float4 o = at[k * kPlane / 4];
-            y.x += o.x, y.y += o.y, y.z += o.z, y.w += o.w;
+            for (int k = 1; k < kKW; ++k) {
+                const float4 o = at[k * kPlane / 4];
+                y.x += o.x, y.y += o.y, y.z += o.z, y.w += o.w;
+            }
+            if (p.splits == 1)
+                store(e, y);
+            else
+                *at = y;
         }
-        if (p.splits == 1)
-            store(e, y);
-        else
-            *at = y;
     }
     if (p.splits > 1) {
         cluster_arrive();
