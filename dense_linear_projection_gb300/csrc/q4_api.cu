@@ -11,11 +11,18 @@
 
 using namespace projgb;
 
+// How a run of up to 8, 16 or 32 tokens (and of more, in passes) is shared out.
+struct Q4Plan {
+    int splits = 1;  // CTAs of a cluster, that share a tile's K range
+    int per_sm = 1;  // CTAs that an SM takes at once
+};
+
 struct proj_q4_s {
     int64_t max_tokens = 0, N = 0, K = 0, group = 0;
     int has_zeros = 0, y_dtype = PROJ_BF16, has_bias = 0;
     int sm_count = 0;
     Q4Shape shape{};
+    Q4Plan plans[3];
 };
 
 namespace {
@@ -34,7 +41,7 @@ int pack_blocks(int64_t items, int sm_count) {
 using Q4Kernel = void (*)(Q4Params);
 struct Q4Instance {
     Q4Kernel kernel;
-    int warps, row_blocks, per_sm, row_tiles, k_steps, red;  // row blocks of a warp; of a CTA; bytes of its join
+    int warps, row_blocks, per_sm, k_steps, red;  // row blocks of a warp; of a CTA; bytes of its join
 };
 
 template <int kNT>
@@ -47,7 +54,7 @@ Q4Instance instance_nt(int64_t group, bool zeros) {
         k = zeros ? dev::q4_kernel<kNT, 2, true> : dev::q4_kernel<kNT, 2, false>;
     else
         k = zeros ? dev::q4_kernel<kNT, 4, true> : dev::q4_kernel<kNT, 4, false>;
-    return {k, Tile::kWarps, Tile::kR, Tile::kPerSm, Tile::kRT, Tile::kKW, Tile::kRed};
+    return {k, Tile::kWarps, Tile::kR, Tile::kPerSm, Tile::kKW, Tile::kRed};
 }
 
 Q4Instance instance_for(int64_t M, int64_t group, bool zeros) {
@@ -55,6 +62,54 @@ Q4Instance instance_for(int64_t M, int64_t group, bool zeros) {
 }
 
 constexpr int kSmemOfSm = 228 * 1024;  // shared memory of an SM, 1 KiB of it reserved for each CTA
+// So much shared memory for a CTA that one more of them does not fit on an SM.
+constexpr int smem_for_at_most(int per_sm) { return kSmemOfSm / (per_sm + 1) - 1024 + 256; }
+
+// Clusters that stand on the GPU at once, with `per_sm` CTAs an SM.
+int64_t clusters_at_once(const Q4Instance &q, int splits, int per_sm) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute cluster;
+    cfg.gridDim = dim3(static_cast<unsigned>(splits));
+    cfg.blockDim = dim3(static_cast<unsigned>(32 * q.warps));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem_for_at_most(per_sm));
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = static_cast<unsigned>(splits);
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cfg.attrs = &cluster;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, q.kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return clusters;
+}
+
+Q4Plan plan_for(const Q4Shape &shape, const Q4Instance &q, int sm_count) {
+    Q4Plan plan;
+    plan.per_sm = q.per_sm;
+    const int64_t tiles = shape.row_tiles, steps = (shape.k_blocks + 1) / 2;
+    if (tiles == 0 || steps == 0) return plan;
+    // CTAs of one K range: as many as stand on the GPU at once, while every
+    // warp has a step.  (31 tokens, 12300 rows, 193 tiles: 3 a range 16.2 us, 2
+    // 17.9, 1 21.9, and 6, that is two waves, 19.6.)
+    int64_t most = q.per_sm * int64_t(sm_count) / tiles;
+    if (most > steps / q.k_steps) most = steps / q.k_steps;
+    if (most > kQ4MaxSplits) most = kQ4MaxSplits;
+    int s = static_cast<int>(most);
+    while (s > 1 && clusters_at_once(q, s, q.per_sm) < tiles) --s;
+    // With four rounds of K steps or fewer, a join takes more than a split saves
+    // that takes no work off the busiest SM (one token, K 2048: 16384 rows 6.0 us
+    // whole, 7.1 split; 4096 rows, where it does take work off, 4.0 and 3.5).
+    const auto busiest = [&](int64_t ctas) { return (ctas + sm_count - 1) / sm_count; };
+    if (s > 1 && steps <= 4 * q.k_steps && busiest(tiles * s) >= s * busiest(tiles)) s = 1;
+    if (s > 1) plan.splits = s;
+    // As few CTAs an SM as hold them all at once: left to themselves, some SMs
+    // take four and others none (one token, 28672 × 8192, 448 tiles: 21.2 us
+    // instead of 26.2; 2048 rows, 32 clusters of 8, 4.3 instead of 5.4).
+    while (plan.per_sm > 1 && clusters_at_once(q, plan.splits, plan.per_sm - 1) >= tiles) --plan.per_sm;
+    return plan;
+}
 
 }  // namespace
 
@@ -100,6 +155,7 @@ proj_status_t proj_q4_create(proj_q4_handle_t *out, int64_t max_tokens, int64_t 
     h->has_bias = has_bias;
     h->sm_count = sms;
     h->shape = q4_shape(N, K, group, has_zeros != 0);
+    for (int i = 0; i < 3; ++i) h->plans[i] = plan_for(h->shape, instance_for(8 << i, group, has_zeros != 0), sms);
     *out = h;
     return PROJ_OK;
 }
@@ -151,29 +207,26 @@ proj_status_t proj_q4_run(proj_q4_handle_t h, int64_t M, const void *X, const vo
     p.Y = Y;
 
     const Q4Instance q = instance_for(M, h->group, h->has_zeros != 0);
-    const int64_t tiles = (p.row_tiles + q.row_tiles - 1) / q.row_tiles;
+    const Q4Plan &plan = h->plans[M <= 8 ? 0 : M <= 16 ? 1 : 2];
     const int64_t passes = (M + kQ4MaxTokens - 1) / kQ4MaxTokens;
-    // CTAs of one K range: as many as stand on the GPU at once, while every
-    // warp has a step.  (31 tokens, 12300 rows, 97 tiles at four CTAs an SM: 6 a
-    // range 17.5 us, 3 a range 22.  28672 rows, 448 tiles at two CTAs an SM: one
-    // 23.8 us, two, that is three waves, 28.)
-    const int64_t steps = (p.k_blocks + 1) / 2;
-    int64_t splits = q.per_sm * int64_t(h->sm_count) / tiles;
-    if (splits > steps / q.k_steps) splits = steps / q.k_steps;
-    p.splits = static_cast<uint32_t>(splits < 1 ? 1 : splits > kQ4MaxSplits ? kQ4MaxSplits : splits);
+    const int per_sm = passes == 1 ? plan.per_sm : q.per_sm;
+    p.splits = static_cast<uint32_t>(plan.splits);
     // Two stages where 16 warps stand on an SM (64 KiB of codes are on their
-    // way then; three were 7 % slower), three where 8 do.
+    // way then, and three are slower), three where fewer do (12 warps: 21.2 us
+    // against 21.7 for one token, 28672 × 8192).
     const int tokens = static_cast<int>(M < kQ4MaxTokens ? M : kQ4MaxTokens);
     const int groups = static_cast<int>(128 / h->group);
-    const int stage = q.warps * q.row_blocks * (1024 + groups * (32 + (h->has_zeros ? 8 : 0))) + q.k_steps * tokens * kQ4XPitch;
-    const int fit = (kSmemOfSm / q.per_sm - 1024) / stage, most = q.warps * q.per_sm > 8 ? 2 : 3;
-    p.stages = fit < 2 ? 2 : fit < most ? fit : most;  // (two of the largest leave room for one CTA an SM)
+    const int weights = q.warps * q.row_blocks * (1024 + groups * (32 + (h->has_zeros ? 8 : 0)));
+    const int stage = (weights + 255) / 256 * 256 + q.k_steps * tokens * kQ4XPitch;  // X on a 256-byte boundary
+    const int fit = (kSmemOfSm / per_sm - 1024) / stage, most = q.warps * per_sm > 12 ? 2 : 3;
+    p.stages = fit < 2 ? 2 : fit < most ? fit : most;
     int smem = p.stages * stage;
     if (smem < q.red) smem = q.red;
+    if (per_sm < q.per_sm && smem < smem_for_at_most(per_sm)) smem = smem_for_at_most(per_sm);
 
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[2];
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.splits), static_cast<unsigned>(passes));
+    cfg.gridDim = dim3(static_cast<unsigned>(p.row_tiles * p.splits), static_cast<unsigned>(passes));
     cfg.blockDim = dim3(static_cast<unsigned>(32 * q.warps));
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = as_stream(stream);

@@ -31,8 +31,9 @@ namespace projgb {
 constexpr int kQ4TileRows = 64;
 constexpr int kQ4MaxTokens = 32;  // tokens of one pass over the weights
 constexpr int kQ4MaxSplits = 8;   // CTAs of a cluster that share a K range (the portable cluster size)
-constexpr int kQ4XPitch = 320;    // bytes between tokens of X in a stage: 128 K, and 64 bytes that
-                                  // put the next token's 16-byte chunks on the other banks
+// Bytes between tokens of X in a stage: 128 K.  Odd tokens have the 64-byte
+// halves of each 128 bytes swapped: two tokens' chunks lie on different banks.
+constexpr int kQ4XPitch = 256;
 
 PROJ_HD int q4_k_of(int j, int i) { return (i >> 1) * 32 + j * 8 + (i & 1) * 4; }
 

@@ -76,13 +76,12 @@ __global__ void q4_pack_scales_kernel(const uint16_t *scales, const uint8_t *zer
 // The product is swapped (weight rows are the 16-row operand of the warp-level
 // step, up to 8·kNT tokens its columns).  What bounds it: at up to 8 tokens the
 // stream of codes and, nearly as much, the 555 instructions that a warp spends on
-// 4 KiB of them (one token, 28672 × 8192: 24.1 us, 75 % of the copy bandwidth;
-// the loads alone 20.1); above that the instructions (16 tokens, 8192 × 8192:
-// 13.4 us, loads alone 8.8; 31 tokens, 12300 × 4128 in groups of 32: 19.3, 9.2).
+// 4 KiB of them (one token, 28672 × 8192: 21.2 us, 85 % of the copy bandwidth);
+// above that the instructions (16 tokens, 8192 × 8192: 14.2 us, of 5.4 for the
+// bytes; 31 tokens, 12300 × 4128 in groups of 32: 16.2, of 4.4).
 // A warp owns 64 or 32 rows × 128 K at a time, in a ring of shared-memory stages
-// filled by 16-byte asynchronous copies.  A CTA covers kRT row tiles × kKW K steps
-// (at 32 tokens two tiles, since the CTA's copies of X grow with them); the CTAs of
-// a cluster share the K range of the same rows.  Sums join in a fixed order: the
+// filled by 16-byte asynchronous copies.  A CTA covers one row tile × kKW K steps;
+// the CTAs of a cluster share the K range of the same rows.  Sums join in a fixed order: the
 // kKW warps in shared memory, then the cluster's CTAs through distributed shared
 // memory.
 //
@@ -94,20 +93,22 @@ constexpr uint32_t kQ4UnitHigh = 0x7C807C80u;  // 2^122: for q·2^-129
 constexpr uint32_t kQ4UnitMinus = 0xFE80FE80u;
 constexpr float kQ4Restore = 128.f;
 
-// How a CTA is cut, measured over 1, 2 and 4 row tiles, 2 and 4 row blocks a warp
-// and 8 to 16 warps an SM.  Up to 8 tokens registers allow 16 warps of four row
-// blocks; 16 tokens run best on 8 (13.3 us against 14.0 to 14.6 for 16 warps, whose
-// copies of X leave room for fewer stages); 32 tokens on 16 warps of two row
-// blocks, four of them sharing X (17.5 us; 8 warps of four row blocks 18.1).
+// How a CTA is cut: four warps, so that CTAs of even size spread evenly over the
+// SMs at most row counts.  Measured at K = 8192 against CTAs of eight warps (two an
+// SM up to 8 tokens, one at 16): 1 token, 10240 rows 12.2 us against 14.9, 28672
+// rows 21.8 against 23.0, 2048 rows 4.8 against 4.7; 16 tokens, 12288 rows 17.1
+// against 23.6, 28672 rows 28.6 against 36.0, 8192 rows 13.4 against 12.8.  With 32
+// tokens two warps share the copies of X and have two row blocks each, as registers
+// allow; two row tiles a CTA copy X half as often, yet take 17.8 us against 12.9 at
+// 4096 rows, and 26.0 against 26.4 at 12288.
 template <int kNT>
 struct Q4Tile {
-    static constexpr int kWarps = kNT == 4 ? 4 : 8, kThreads = 32 * kWarps;
-    static constexpr int kR = kNT == 4 ? 2 : 4;                         // row blocks of a warp
-    static constexpr int kRT = kNT == 4 ? 2 : 1;                        // row tiles of a CTA
-    static constexpr int kPerSm = kNT == 1 ? 2 : kNT == 2 ? 1 : 4;      // CTAs an SM
-    static constexpr int kShare = kRT * 4 / kR;      // warps that share a K step
+    static constexpr int kWarps = 4, kThreads = 32 * kWarps;
+    static constexpr int kR = kNT == 4 ? 2 : 4;        // row blocks of a warp
+    static constexpr int kPerSm = kNT == 2 ? 3 : 4;    // CTAs an SM, by their registers
+    static constexpr int kShare = 4 / kR;            // warps that share a K step
     static constexpr int kKW = kWarps / kShare;      // K steps at a time
-    static constexpr int kPitch = kRT * 64 + 4;      // floats of a token's rows while joining: conflict-free
+    static constexpr int kPitch = 64 + 4;            // floats of a token's rows while joining: conflict-free
     static constexpr int kRed = kKW * 8 * kNT * kPitch * 4;
     static_assert(kKW * kShare == kWarps, "whole K steps");
 };
@@ -164,34 +165,36 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
 template <int kNT, int kGroups, bool kZeros>
 __global__ void __launch_bounds__(Q4Tile<kNT>::kThreads, Q4Tile<kNT>::kPerSm) q4_kernel(const Q4Params p) {
     using Tile = Q4Tile<kNT>;
-    constexpr int kRT = Tile::kRT, kKW = Tile::kKW, kR = Tile::kR, kShare = Tile::kShare;
-    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int kKW = Tile::kKW, kR = Tile::kR, kShare = Tile::kShare;
+    extern __shared__ __align__(256) uint8_t smem[];
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int part_of = warp % kShare, kw = warp / kShare;  // which of the CTA's rows, which K steps
     const int g = lane >> 2, j = lane & 3;
     const uint32_t rank = blockIdx.x % p.splits;
-    const int64_t tile0 = blockIdx.x / p.splits * kRT;  // the CTA's first row tile
-    const int64_t tile = tile0 + part_of * kR / 4;
-    const int block0 = part_of * kR % 4;  // the warp's first row block of its tile
-    const bool rows_there = tile < p.row_tiles;
+    const int64_t tile = blockIdx.x / p.splits;
+    const int block0 = part_of * kR;  // the warp's first row block of the tile
     const int64_t m0 = blockIdx.y * int64_t(kQ4MaxTokens);
     const int M = static_cast<int>(p.M - m0 < kQ4MaxTokens ? p.M - m0 : kQ4MaxTokens);
 
     // A stage: each warp's codes, scales and zero points, then X for each K step.
     constexpr int kCodeBytes = kR * 1024, kScaleBytes = kGroups * kR * 32, kZeroBytes = kZeros ? kGroups * kR * 8 : 0;
     constexpr int kWarpBytes = kCodeBytes + kScaleBytes + kZeroBytes;
+    constexpr int kWeights = (Tile::kWarps * kWarpBytes + 255) / 256 * 256;  // X begins on a 256-byte boundary
     const int x_bytes = M * kQ4XPitch;
-    const int stage_bytes = Tile::kWarps * kWarpBytes + kKW * x_bytes;
+    const int stage_bytes = kWeights + kKW * x_bytes;
     const uint32_t base = smem_u32(smem);
-    const uint32_t my_w = base + warp * kWarpBytes, my_x = base + Tile::kWarps * kWarpBytes + kw * x_bytes;
+    const uint32_t my_w = base + warp * kWarpBytes, my_x = base + kWeights + kw * x_bytes;
 
     const uint32_t steps = static_cast<uint32_t>((p.k_blocks + 1) / 2);  // at most 2^24: 32-bit divisions
     const int step0 = static_cast<int>(steps * rank / p.splits) + kw, step1 = static_cast<int>(steps * (rank + 1) / p.splits);
 
     uint32_t x_row[kNT];  // this lane's place in a step's X
 #pragma unroll
-    for (int t = 0; t < kNT; ++t) x_row[t] = min(8 * t + g, M - 1) * kQ4XPitch + j * 16;
+    for (int t = 0; t < kNT; ++t) {
+        const int m = min(8 * t + g, M - 1);
+        x_row[t] = m * kQ4XPitch + j * 16 + (m & 1) * 64;
+    }
 
     float acc[kR][kNT][4];
 #pragma unroll
@@ -210,37 +213,34 @@ __global__ void __launch_bounds__(Q4Tile<kNT>::kThreads, Q4Tile<kNT>::kPerSm) q4
                                   : nullptr;
     const int x_first = (part_of * 32 + lane) / 16, x_chunk = lane % 16;  // first of the tokens this lane copies; its 8 K of the step
     const uint8_t *x = reinterpret_cast<const uint8_t *>(p.X + (m0 + x_first) * p.K + step0 * 128 + x_chunk * 8);
+    const int x_to = (x_chunk * 16) ^ ((x_first & 1) * 64);  // all of a lane's tokens are odd, or even
     const int64_t x_next = 2 * kShare * p.K * 2;  // bytes to the lane's next token
     const int whole = static_cast<int>((p.K / 128 < step1 ? p.K / 128 : step1));  // steps below it lie inside K
     auto load = [&](int step, int slot) {
         if (step < step1) {
             const uint32_t w = my_w + slot * stage_bytes + lane * 16;
-            uint32_t to = my_x + slot * stage_bytes + x_first * kQ4XPitch + x_chunk * 16;
+            uint32_t to = my_x + slot * stage_bytes + x_first * kQ4XPitch + x_to;
             const uint8_t *from = x;
             if (step < whole) {
-                if (rows_there) {
 #pragma unroll
-                    for (int i = 0; i < 2 * kR; ++i) cp_async16(w + i * 512, codes + i / kR * 2048 + i % kR * 512);
-                    if (scale_group < kGroups) cp_async16(w + kCodeBytes, scales);
-                    if (kZeros && zero_group < kGroups) cp_async16(w + kCodeBytes + kScaleBytes, zeros);
-                }
+                for (int i = 0; i < 2 * kR; ++i) cp_async16(w + i * 512, codes + i / kR * 2048 + i % kR * 512);
+                if (scale_group < kGroups) cp_async16(w + kCodeBytes, scales);
+                if (kZeros && zero_group < kGroups) cp_async16(w + kCodeBytes + kScaleBytes, zeros);
                 for (int m = x_first; m < M; m += 2 * kShare, to += 2 * kShare * kQ4XPitch, from += x_next) cp_async16(to, from);
             } else {
                 // K ends inside the step: the blocks of codes and the groups
                 // that exist, and zeros for the rest.
                 const int blocks = step * 2 + 1 < p.k_blocks ? 2 : 1;
-                if (rows_there) {
 #pragma unroll
-                    for (int i = 0; i < 2 * kR; ++i)
-                        cp_async16(w + i * 512, i / kR < blocks ? codes + i / kR * 2048 + i % kR * 512 : codes, i / kR < blocks);
-                    if (scale_group < kGroups) {
-                        const bool in = step * kGroups + scale_group < p.groups_padded;
-                        cp_async16(w + kCodeBytes, in ? scales : codes, in);
-                    }
-                    if (kZeros && zero_group < kGroups) {
-                        const bool in = step * kGroups + zero_group < p.groups_padded;
-                        cp_async16(w + kCodeBytes + kScaleBytes, in ? zeros : codes, in);
-                    }
+                for (int i = 0; i < 2 * kR; ++i)
+                    cp_async16(w + i * 512, i / kR < blocks ? codes + i / kR * 2048 + i % kR * 512 : codes, i / kR < blocks);
+                if (scale_group < kGroups) {
+                    const bool in = step * kGroups + scale_group < p.groups_padded;
+                    cp_async16(w + kCodeBytes, in ? scales : codes, in);
+                }
+                if (kZeros && zero_group < kGroups) {
+                    const bool in = step * kGroups + zero_group < p.groups_padded;
+                    cp_async16(w + kCodeBytes + kScaleBytes, in ? zeros : codes, in);
                 }
                 const bool in = step * 128 + x_chunk * 8 < p.K;
                 for (int m = x_first; m < M; m += 2 * kShare, to += 2 * kShare * kQ4XPitch, from += x_next)
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(Q4Tile<kNT>::kThreads, Q4Tile<kNT>::kPerSm) q4
                 for (int t = 0; t < kNT; ++t)
 #pragma unroll
                     for (int h = 0; h < kPiece / 2; ++h) {
-                        const uint4 v = lds128(xs + x_row[t] + (at / 2 + h) * 64);
+                        const uint4 v = lds128((xs + x_row[t]) ^ ((at / 2 + h) * 64));
                         b[t][4 * h] = v.x, b[t][4 * h + 1] = v.y, b[t][4 * h + 2] = v.z, b[t][4 * h + 3] = v.w;
                     }
 #pragma unroll
@@ -366,9 +366,9 @@ __global__ void __launch_bounds__(Q4Tile<kNT>::kThreads, Q4Tile<kNT>::kPerSm) q4
         }
     __syncthreads();
     // Four rows at a time.
-    constexpr uint32_t kQuads = 16 * kRT;
+    constexpr uint32_t kQuads = 16;
     const uint32_t quads = M * kQuads;
-    const int64_t n0 = tile0 * 64;
+    const int64_t n0 = tile * 64;
     auto store = [&](uint32_t e, float4 v) {
         const int64_t n = n0 + (e % kQuads) * 4, at = (m0 + e / kQuads) * p.N + n;
         float y[4] = {v.x * kQ4Restore, v.y * kQ4Restore, v.z * kQ4Restore, v.w * kQ4Restore};
