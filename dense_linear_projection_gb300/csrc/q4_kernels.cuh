@@ -76,7 +76,7 @@ __global__ void q4_pack_scales_kernel(const uint16_t *scales, const uint8_t *zer
 // The product is swapped (weight rows are the 16-row operand of the warp-level
 // step, up to 8·kNT tokens its columns).  What bounds it: at up to 8 tokens the
 // stream of codes and, nearly as much, the 555 instructions that a warp spends on
-// 4 KiB of them (one token, 28672 × 8192: 21.2 us, 85 % of the copy bandwidth);
+// 4 KiB of them (one token, 28672 × 8192: 20.7 us, 87 % of the copy bandwidth);
 // above that the instructions (16 tokens, 8192 × 8192: 14.2 us, of 5.4 for the
 // bytes; 31 tokens, 12300 × 4128 in groups of 32: 16.2, of 4.4).
 // A warp owns 64 or 32 rows × 128 K at a time, in a ring of shared-memory stages
@@ -261,6 +261,14 @@ __global__ void __launch_bounds__(Q4Tile<kNT>::kThreads, Q4Tile<kNT>::kPerSm) q4
             asm volatile("bar.sync %0, %1;" ::"r"(1 + kw), "n"(32 * kShare) : "memory");
     };
 
+    // The first step's codes move to L2 while the kernel before this one ends (a
+    // prefetch returns nothing, so it may come before the wait): 20.7 us against
+    // 21.2 for one token, 28672 × 8192.  More steps, or 32 tokens, gain nothing.
+    if constexpr (kNT < 4) {
+        if (step0 < whole)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t *>(p.codes) +
+                                                          (tile * p.k_blocks + step0 * 2) * 2048 + lane * 128));
+    }
     griddep_wait();
     const int stages = p.stages;
     for (int s = 0; s < stages - 1; ++s) load(step0 + s * kKW, s);
