@@ -77,7 +77,7 @@ __global__ void q4_pack_scales_kernel(const uint16_t *scales, const uint8_t *zer
 // step, up to 8·kNT tokens its columns).  What bounds it: at up to 8 tokens the
 // stream of codes and, nearly as much, the 555 instructions that a warp spends on
 // 4 KiB of them (one token, 28672 × 8192: 20.7 us, 87 % of the copy bandwidth);
-// above that the instructions (16 tokens, 8192 × 8192: 14.2 us, of 5.4 for the
+// above that the instructions (16 tokens, 8192 × 8192: 13.9 us, of 5.4 for the
 // bytes; 31 tokens, 12300 × 4128 in groups of 32: 16.2, of 4.4).
 // A warp owns 64 or 32 rows × 128 K at a time, in a ring of shared-memory stages
 // filled by 16-byte asynchronous copies.  A CTA covers one row tile × kKW K steps;
@@ -423,6 +423,7 @@ __global__ void __launch_bounds__(Q4Tile<kNT>::kThreads, Q4Tile<kNT>::kPerSm) q4
         // Each CTA finishes a share of the elements, adding the ranks in order.
         const uint32_t e1 = quads * (rank + 1) / p.splits;
         for (uint32_t e = quads * rank / p.splits + tid; e < e1; e += Tile::kThreads) {
+            if (n0 + (e % kQuads) * 4 >= p.N) continue;  // what is read is stored
             const uint32_t at = base + ((e / kQuads) * kPitch + (e % kQuads) * 4) * 4;
             float4 part[kQ4MaxSplits];
 #pragma unroll
@@ -434,7 +435,10 @@ __global__ void __launch_bounds__(Q4Tile<kNT>::kThreads, Q4Tile<kNT>::kPerSm) q4
                 if (s < p.splits) y.x += part[s].x, y.y += part[s].y, y.z += part[s].z, y.w += part[s].w;
             store(e, y);
         }
-        cluster_arrive();  // no CTA leaves while another reads its sums
+        // No CTA leaves while another reads its sums.  This one's reads are over:
+        // its stores, issued before, took their values.  (A release would wait for
+        // the stores to be seen: 0.3 us.)
+        asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
         cluster_wait();
     }
 }
