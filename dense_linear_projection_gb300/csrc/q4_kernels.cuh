@@ -75,7 +75,7 @@ __global__ void q4_pack_scales_kernel(const uint16_t *scales, const uint8_t *zer
 //
 // The product is swapped (weight rows are the 16-row operand of the warp-level
 // step, up to 8·kNT tokens its columns).  What bounds it: at up to 8 tokens the
-// stream of codes and, nearly as much, the 555 instructions that a warp spends on
+// stream of codes and, nearly as much, the 500 instructions that a warp spends on
 // 4 KiB of them (one token, 28672 × 8192: 20.7 us, 87 % of the copy bandwidth);
 // above that the instructions (16 tokens, 8192 × 8192: 13.9 us, of 5.4 for the
 // bytes; 31 tokens, 12300 × 4128 in groups of 32: 16.2, of 4.4).
