@@ -435,10 +435,11 @@ __global__ void __launch_bounds__(Q4Tile<kNT>::kThreads, Q4Tile<kNT>::kPerSm) q4
                 if (s < p.splits) y.x += part[s].x, y.y += part[s].y, y.z += part[s].z, y.w += part[s].w;
             store(e, y);
         }
-        // No CTA leaves while another reads its sums.  This one's reads are over:
-        // its stores, issued before, took their values.  (A release would wait for
-        // the stores to be seen: 0.3 us.)
-        asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+        // No CTA leaves while another reads its sums: the arrival releases, so the
+        // reads come before it.  (It waits for the stores too, 0.2 us.  With all reads
+        // first and the stores after the arrival, 2048 rows take 4.15 us instead of
+        // 4.24, but 31 tokens in groups of 32 take 20.0 instead of 16.5.)
+        cluster_arrive();
         cluster_wait();
     }
 }

@@ -64,3 +64,16 @@ def test_rope_table():
         for j, rate in enumerate((1.0, 0.1)):
             assert abs(t[p, j].item() - math.cos(p * rate)) < 1e-7
             assert abs(t[p, 2 + j].item() - math.sin(p * rate)) < 1e-7
+
+
+def test_cluster_arrivals_are_ordered():
+    # A CTA of a cluster may leave once every other has arrived: an arrival without release does not
+    # order the reads of another CTA's shared memory that come before it, so no kernel has one.
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(dlp.__file__), "csrc")
+    arrivals = []
+    for name in sorted(os.listdir(csrc)):
+        with open(os.path.join(csrc, name), encoding="utf-8") as f:
+            arrivals += [(name, m) for m in re.findall(r"barrier\.cluster\.arrive[.\w]*", f.read())]
+    assert arrivals and all(m.endswith((".release", ".arrive", ".aligned")) and "relaxed" not in m for _, m in arrivals), arrivals

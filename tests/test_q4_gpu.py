@@ -220,3 +220,25 @@ def test_refusals():
         with pytest.raises(dlp.ProjError) as e:
             what()
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("M,N,K,group", [(1, 2048, 8192, 128), (8, 130, 8192, 64), (16, 4100, 8192, 64),
+                                         (16, 500, 4096, 128), (31, 12300, 4128, 32), (32, 6000, 2048, 128), (64, 1000, 2048, 64)])
+def test_clusters_that_leave_and_start_back_to_back(M, N, K, group):
+    # Shared K ranges: a cluster's sums are read by its other CTAs while the next launch's CTAs wait
+    # for the places that it leaves.  Integers below 2²⁴ come out exactly whenever all are read in time.
+    import torch
+    import dense_linear_projection_gb300 as dlp
+    codes, _, z = stored(N, K, group, True, 21)
+    scales = torch.ones((N, K // group), device="cuda", dtype=torch.bfloat16)
+    proj = dlp.Q4Projection(M, N, K, group, has_zeros=True, y_dtype=dlp.PROJ_F32)
+    P = proj.pack(codes, scales, z)
+    X = torch.randint(-3, 4, (4, M, K), device="cuda").to(torch.bfloat16)
+    out = torch.empty((24, M, N), device="cuda")
+    for i in range(24):
+        proj(X[i % 4], P, out=out[i])
+    W = dequantised(codes, scales, z, group)
+    for i in range(4):
+        ref = (X[i].double() @ W.t()).float()
+        for j in range(i, 24, 4):
+            assert torch.equal(out[j], ref), (i, j)
