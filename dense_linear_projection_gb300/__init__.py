@@ -508,7 +508,8 @@ class Q4Projection:
     the stored form: ``codes`` [N, K/2] uint8 (even k in the low four bits),
     ``scales`` [N, K/group] bf16 and, with ``has_zeros``, ``zeros`` [N, K/group]
     uint8.  Packed weights run with every handle of the same N, K, group and
-    ``has_zeros``.
+    ``has_zeros``.  The handle belongs to the device that is current when it is
+    made; tensors of another are refused.
     """
 
     def __init__(self, max_tokens: int, N: int, K: int, group: int = 128, has_zeros: bool = False,
@@ -538,7 +539,8 @@ class Q4Projection:
         packed = torch.empty(self._bytes, dtype=torch.uint8, device=codes.device)
         if stream is None:
             stream = torch.cuda.current_stream(codes.device)
-        proj_q4_pack(self.handle, codes, scales, zeros, packed, stream)
+        with torch.cuda.device(device):
+            proj_q4_pack(self.handle, codes, scales, zeros, packed, stream)
         return packed
 
     def __call__(self, X, packed, bias=None, out=None, stream=None):
@@ -574,8 +576,8 @@ class PagedKV:
     float8_e4m3fn CUDA tensors of the same strides; a view with heads before
     tokens in memory works as well, head_dim has to be contiguous.  With 8-bit
     elements ``k_scale``, ``v_scale`` ([kv_heads] fp32) say what one unit
-    stands for.  The tensors stay the caller's; the handle owns scratch for
-    sequences that several thread blocks share.
+    stands for.  The tensors stay the caller's; the handle, on their device, owns
+    scratch for sequences that several thread blocks share.
     """
 
     def __init__(self, k_cache, v_cache, q_heads: int, max_sequences: int, k_scale=None, v_scale=None, stream=None):
@@ -604,7 +606,8 @@ class PagedKV:
         self._append, self._attend = _bind().append, _bind().attend
         s = k_cache.stride()
         desc = KvDesc(pages, s[0], s[1], s[2], max_sequences, page_size, q_heads, kv_heads, head_dim, kv_dtype)
-        self.handle = proj_kv_create(desc, stream)
+        with torch.cuda.device(device):
+            self.handle = proj_kv_create(desc, stream)
 
     def append(self, q, k, v, positions, page_table, seq_ids=None, rope=None, interleaved: bool = False, q_out=None,
                stream=None):
@@ -631,7 +634,9 @@ class PagedKV:
                             self._scale if scale is None else scale, window, out, return_lse, _stream(stream))
 
     def status(self, stream=None) -> int:
-        return proj_kv_device_status(self.handle, stream)
+        import torch
+        with torch.cuda.device(self.k_cache.device):
+            return proj_kv_device_status(self.handle, stream)
 
     def close(self) -> None:
         if self.handle:

@@ -5,11 +5,14 @@
 // looking up shapes, types and pointers one by one and crossing ctypes took 9 to
 // 14 us on the Grace host, against 2 to 5 us on the GPU.  The functions here
 // compute nothing; each raises the library's ProjError for what it refuses.
+// Each makes the tensors' device current for the call, where the library refuses
+// a handle of another.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -104,6 +107,7 @@ PyObject *q4(PyObject *, PyObject *const *a, Py_ssize_t count) {
         const at::Tensor &X = needed(a[5], "X: a tensor");
         const int64_t device = X.is_cuda() ? X.get_device() : -1;
         if (!is(X, at::kBFloat16, device, 2) || X.size(1) != K || !X.is_contiguous()) refuse("X: contiguous bf16 CUDA [M, K]");
+        const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(device));
         const int64_t M = X.size(0);
         const at::Tensor &packed = needed(a[6], "packed: a tensor");
         if (!is(packed, at::kByte, device, 1) || packed.numel() != bytes || !packed.is_contiguous())
@@ -162,6 +166,7 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t count) {
     return guarded([&]() -> PyObject * {
         if (count != 18) refuse("append: eighteen arguments");
         const Cache c = cache_of(a);
+        const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(c.device));
         const at::Tensor *q = tensor(a[8], "q: a tensor");
         const at::Tensor &k = needed(a[9], "k: a tensor"), &v = needed(a[10], "v: a tensor");
         const char *kv_rows = "k, v: bf16 [tokens, kv_heads, head_dim] with contiguous heads and one row stride, on the cache's device";
@@ -209,6 +214,7 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t count) {
     return guarded([&]() -> PyObject * {
         if (count != 16) refuse("attend: sixteen arguments");
         const Cache c = cache_of(a);
+        const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(c.device));
         const at::Tensor &q = needed(a[8], "q: a tensor");
         const int64_t n = q.dim() > 0 ? q.size(0) : 0;
         const int64_t q_stride = rows(q, n, c.q_heads, c.dim, c.device,

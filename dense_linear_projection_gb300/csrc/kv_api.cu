@@ -15,7 +15,7 @@ using namespace projgb;
 
 struct proj_kv_s {
     proj_kv_desc_t d{};
-    int sm_count = 0;
+    int sm_count = 0, device = 0;
     int elem = 2;  // bytes of a cache element
     int chunk_heads = 0, chunks = 0;  // rows of a key head: query heads of each, and how many
     int key_heads = 1;                // key heads of a row: 1 or 2
@@ -143,6 +143,7 @@ proj_status_t proj_kv_create(proj_kv_handle_t *out, const proj_kv_desc_t *desc, 
     if (!h) return PROJ_ERR_OUT_OF_MEMORY;
     h->d = d;
     h->sm_count = sms;
+    h->device = device_of_handle();
     h->elem = elem;
     const int group = d.q_heads / d.kv_heads, most = d.head_dim <= 128 ? 16 : 8;
     h->chunks = (group + most - 1) / most;
@@ -190,7 +191,7 @@ proj_status_t proj_kv_append(proj_kv_handle_t h, int64_t tokens, const void *q, 
                              int64_t rope_positions, int32_t rot_dim, int interleaved, const float *k_scale,
                              const float *v_scale, void *k_cache, void *v_cache, void *q_out, int64_t q_out_stride,
                              void *stream) {
-    if (!h || tokens < 0 || tokens > kMaxDim || sequences < 0 || sequences > kMaxDim || rope_positions < 0 ||
+    if (!h || !is_current(h->device) || tokens < 0 || tokens > kMaxDim || sequences < 0 || sequences > kMaxDim || rope_positions < 0 ||
         (interleaved != 0 && interleaved != 1) || !fits_table(table_width, h->d.page_size))
         return PROJ_ERR_INVALID_ARG;
     const proj_kv_desc_t &d = h->d;
@@ -243,7 +244,7 @@ proj_status_t proj_kv_attend(proj_kv_handle_t h, int64_t sequences, const void *
                              const void *k_cache, const void *v_cache, const float *k_scale, const float *v_scale,
                              const int32_t *page_table, int64_t table_width, const int32_t *seq_lens, int64_t window,
                              float scale, void *out, int64_t out_stride, float *lse, void *stream) {
-    if (!h || sequences < 0 || sequences > h->d.max_sequences || window < 0 || !std::isfinite(scale) ||
+    if (!h || !is_current(h->device) || sequences < 0 || sequences > h->d.max_sequences || window < 0 || !std::isfinite(scale) ||
         !fits_table(table_width, h->d.page_size))
         return PROJ_ERR_INVALID_ARG;
     const proj_kv_desc_t &d = h->d;
@@ -289,7 +290,7 @@ proj_status_t proj_kv_attend(proj_kv_handle_t h, int64_t sequences, const void *
 }
 
 proj_status_t proj_kv_device_status(proj_kv_handle_t h, void *stream) {
-    if (!h) return PROJ_ERR_INVALID_ARG;
+    if (!h || !is_current(h->device)) return PROJ_ERR_INVALID_ARG;
     if (cudaStreamSynchronize(as_stream(stream)) != cudaSuccess) return PROJ_ERR_CUDA;
     int word = 0;
     if (cudaMemcpy(&word, h->status, sizeof word, cudaMemcpyDeviceToHost) != cudaSuccess) return PROJ_ERR_CUDA;

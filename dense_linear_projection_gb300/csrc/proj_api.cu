@@ -23,9 +23,10 @@ namespace projgb {
 
 // Host-side fault injection for tests (PROJ_FAULT, read once per process): a
 // comma-separated list of "alloc" (every device allocation of the library
-// fails as out of memory), "encode" (every tensor-map encoding fails) and
-// "launch" (every kernel launch fails before it is queued).  The failure is
-// made on the host: nothing faulty reaches the device.
+// fails as out of memory), "encode" (every tensor-map encoding fails),
+// "launch" (every kernel launch fails before it is queued) and "device" (every
+// handle is taken for another device's).  The failure is made on the host:
+// nothing faulty reaches the device.
 int fault_mask() {
     static const int mask = [] {
         int m = 0;
@@ -33,6 +34,7 @@ int fault_mask() {
             if (std::strstr(e, "alloc")) m |= kFaultAlloc;
             if (std::strstr(e, "encode")) m |= kFaultEncode;
             if (std::strstr(e, "launch")) m |= kFaultLaunch;
+            if (std::strstr(e, "device")) m |= kFaultDevice;
         }
         return m;
     }();

@@ -8,7 +8,7 @@
 namespace projgb {
 
 // Host-side fault injection (proj_api.cu): which kinds of calls fail.
-constexpr int kFaultAlloc = 1, kFaultEncode = 2, kFaultLaunch = 4;
+constexpr int kFaultAlloc = 1, kFaultEncode = 2, kFaultLaunch = 4, kFaultDevice = 8;
 int fault_mask();
 inline bool launch_faulted() { return (fault_mask() & kFaultLaunch) != 0; }
 
@@ -28,6 +28,23 @@ inline int gb300_sm_count() {
         return -1;
     }
     return major == 10 && minor == 3 ? sms : 0;
+}
+
+// The device that a handle made now belongs to: the current one, -1 if the
+// runtime fails.  Calls with the handle are refused while another is current:
+// its scratch and its kernels' attributes are that device's.
+inline int device_of_handle() {
+    int device = -1;
+    if (cudaGetDevice(&device) != cudaSuccess) {
+        cudaGetLastError();
+        return -1;
+    }
+    return (fault_mask() & kFaultDevice) ? device + 1 : device;
+}
+inline bool is_current(int device) {
+    int now = -1;
+    if (cudaGetDevice(&now) != cudaSuccess) cudaGetLastError();
+    return now == device && now >= 0;
 }
 
 inline cudaStream_t as_stream(void *s) { return static_cast<cudaStream_t>(s); }

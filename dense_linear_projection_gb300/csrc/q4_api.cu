@@ -20,7 +20,7 @@ struct Q4Plan {
 struct proj_q4_s {
     int64_t max_tokens = 0, N = 0, K = 0, group = 0;
     int has_zeros = 0, y_dtype = PROJ_BF16, has_bias = 0;
-    int sm_count = 0;
+    int sm_count = 0, device = 0;
     Q4Shape shape{};
     Q4Plan plans[3];
 };
@@ -154,6 +154,7 @@ proj_status_t proj_q4_create(proj_q4_handle_t *out, int64_t max_tokens, int64_t 
     h->y_dtype = y_dtype;
     h->has_bias = has_bias;
     h->sm_count = sms;
+    h->device = device_of_handle();
     h->shape = q4_shape(N, K, group, has_zeros != 0);
     for (int i = 0; i < 3; ++i) h->plans[i] = plan_for(h->shape, instance_for(8 << i, group, has_zeros != 0), sms);
     *out = h;
@@ -162,7 +163,7 @@ proj_status_t proj_q4_create(proj_q4_handle_t *out, int64_t max_tokens, int64_t 
 
 proj_status_t proj_q4_pack(proj_q4_handle_t h, const void *codes, const void *scales, const void *zeros, void *packed,
                            void *stream) {
-    if (!h) return PROJ_ERR_INVALID_ARG;
+    if (!h || !is_current(h->device)) return PROJ_ERR_INVALID_ARG;
     const Q4Shape &s = h->shape;
     if (s.codes_bytes == 0) return PROJ_OK;
     if (!codes || !scales || !packed || (zeros != nullptr) != (h->has_zeros != 0)) return PROJ_ERR_INVALID_ARG;
@@ -181,7 +182,7 @@ proj_status_t proj_q4_pack(proj_q4_handle_t h, const void *codes, const void *sc
 
 proj_status_t proj_q4_run(proj_q4_handle_t h, int64_t M, const void *X, const void *packed, const void *bias, void *Y,
                           void *stream) {
-    if (!h || M < 0 || M > h->max_tokens) return PROJ_ERR_INVALID_ARG;
+    if (!h || !is_current(h->device) || M < 0 || M > h->max_tokens) return PROJ_ERR_INVALID_ARG;
     if (M == 0 || h->N == 0) return PROJ_OK;
     if ((bias != nullptr) != (h->has_bias != 0) || !Y) return PROJ_ERR_INVALID_ARG;
     if (h->K > 0 && (!X || !packed)) return PROJ_ERR_INVALID_ARG;

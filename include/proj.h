@@ -533,6 +533,8 @@ proj_status_t proj_selftest_wait_timeout(int64_t limit_ns, void *stream);
  *   created, Y [M, N] of y_dtype; 0 ≤ M ≤ max_tokens.  Asynchronous, no
  *   allocation, can be captured in a graph.  The handle owns no device memory
  *   and may run on several streams at the same time.  Reruns are bit-identical.
+ *   A handle belongs to the device that is current when it is created: pack and
+ *   run return PROJ_ERR_INVALID_ARG while another is.
  */
 typedef struct proj_q4_s *proj_q4_handle_t;
 
@@ -566,6 +568,8 @@ proj_status_t proj_q4_destroy(proj_q4_handle_t h);
  *   sequence.  A handle owns scratch for joining split sequences and a
  *   status word; one handle may serve every layer whose cache has its
  *   geometry, but must not run on two streams at the same time.
+ *   It belongs to the device that is current when it is created: the other calls
+ *   return PROJ_ERR_INVALID_ARG while another is.
  *
  * proj_kv_append: for token i of `tokens`, at position p = positions[i] of
  *   sequence seq_ids[i] (i itself when seq_ids is NULL): the first rot_dim

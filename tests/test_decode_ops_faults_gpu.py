@@ -81,3 +81,17 @@ def test_faults(fault):
     if fault == "alloc":
         want = {"pack": ok, "run": ok, "create": dlp.PROJ_ERR_OUT_OF_MEMORY}
     assert got == want
+
+
+def test_handles_of_another_device():
+    # Every handle is taken for another device's: each call is refused before anything is launched.
+    # (The host's check alone: no launch with addresses of the wrong device is made.)
+    import dense_linear_projection_gb300 as dlp
+    dlp.build()
+    r = subprocess.run([sys.executable, "-c", CHILD], cwd=ROOT, env=dict(os.environ, PROJ_FAULT="device"), capture_output=True,
+                       text=True, timeout=300)
+    lines = [x for x in r.stdout.splitlines() if x.startswith("RESULT ")]
+    assert r.returncode == 0 and lines, r.stdout + r.stderr
+    got = json.loads(lines[-1][7:])
+    assert got.pop("alive") and got.pop("leak") == 0 and got.pop("create") == dlp.PROJ_OK
+    assert set(got) == {"pack", "run", "append", "attend", "status"} and set(got.values()) == {dlp.PROJ_ERR_INVALID_ARG}
