@@ -400,21 +400,28 @@ class Projection:
 
     ``X``: [M,K] bf16 CUDA tensor; ``W``: [N,K] (``PROJ_W_NK``) or [K,N]
     (``PROJ_W_KN``) bf16; ``bias``: [N] bf16 or None.  Returns ``Y`` [M,N] in
-    ``y_dtype`` (allocated with torch unless ``out`` is given).
+    ``y_dtype`` (allocated with torch unless ``out`` is given).  The handle
+    belongs to the device that is current when it is made; tensors of another
+    are refused.
     """
 
     def __init__(self, M: int, N: int, K: int, w_layout: int = PROJ_W_NK,
                  y_dtype: int = PROJ_BF16, has_bias: bool = False, stream=None,
                  overlap: Optional[int] = None, w_dtype: int = PROJ_BF16):
-        import torch  # noqa: F401  (PyTorch provides memory and streams only)
+        import torch  # (PyTorch provides memory and streams only)
         self.M, self.N, self.K = M, N, K
         self.w_layout, self.y_dtype, self.has_bias = w_layout, y_dtype, bool(has_bias)
         self.w_dtype = w_dtype
         self.act = PROJ_ACT_NONE
         self.handle = proj_create(M, N, K, w_layout, PROJ_BF16, w_dtype, y_dtype, has_bias,
                                   PROJ_BF16, stream)
+        self.device = torch.cuda.current_device()
         if overlap is not None:
             proj_set_overlap(self.handle, overlap)
+
+    def _check_device(self, x) -> None:
+        if x.get_device() != self.device:
+            raise ProjError(PROJ_ERR_INVALID_ARG, f"a tensor outside the handle's device, cuda:{self.device}")
 
     @property
     def plan(self) -> dict:
@@ -424,6 +431,7 @@ class Projection:
         """Y = act(X·Wᵀ + bias) + residual; ``packed=True`` takes weights from
         :meth:`pack`; the activation is set by :meth:`set_activation`."""
         import torch
+        self._check_device(X)
         if out is None:
             dt = torch.float32 if self.y_dtype == PROJ_F32 else torch.bfloat16
             n_out = self.N // 2 if self.act == PROJ_ACT_SWIGLU else self.N
@@ -448,6 +456,7 @@ class Projection:
         and low bf16 parts here); returns a new bf16 CUDA tensor to pass with
         ``packed=True``."""
         import torch
+        self._check_device(W)
         n = proj_packed_weight_bytes(self.handle)
         P = torch.empty(max(n // 2, 8), dtype=torch.bfloat16, device=W.device)
         if stream is None:

@@ -451,7 +451,7 @@ proj_status_t proj_create(proj_handle_t *out, int64_t M, int64_t N, int64_t K,
 
     proj_plan_s *h = new (std::nothrow) proj_plan_s();
     if (!h) return PROJ_ERR_OUT_OF_MEMORY;
-    h->device = device;
+    h->device = device_of_handle();
     h->sm_count = prop.multiProcessorCount;
     h->hilo = hilo ? 1 : 0;
     h->kt = kt;
@@ -566,7 +566,7 @@ proj_status_t proj_packed_weight_bytes(proj_handle_t h, size_t *bytes) {
 }
 
 proj_status_t proj_pack_weights(proj_handle_t h, const void *W, void *W_packed, void *stream) {
-    if (!h) return PROJ_ERR_INVALID_ARG;
+    if (!h || !is_current(h->device)) return PROJ_ERR_INVALID_ARG;
     const proj_plan_desc_t &plan = h->plan;
     if (plan.kernel != PROJ_KERNEL_TC) return PROJ_OK;
     if (!W || !W_packed) return PROJ_ERR_INVALID_ARG;
@@ -595,7 +595,7 @@ namespace {
 
 proj_status_t run_impl(proj_handle_t h, const void *X, const void *W, bool packed, const void *bias,
                        const void *residual, void *Y, void *stream) {
-    if (!h) return PROJ_ERR_INVALID_ARG;
+    if (!h || !is_current(h->device)) return PROJ_ERR_INVALID_ARG;
     if (h->hilo && !packed && h->plan.kernel == PROJ_KERNEL_TC) return PROJ_ERR_UNSUPPORTED;
     if ((bias != nullptr) != (h->has_bias != 0)) return PROJ_ERR_INVALID_ARG;
     const bool stored = !packed && h->has_plan_stored;  // weights as stored, plan of single CTAs
@@ -753,7 +753,7 @@ proj_status_t copy_host(void *dst_dev, const void *src_dev, void *dst, const voi
 
 proj_status_t run_host_impl(proj_handle_t h, const void *X_host, const void *W, bool packed,
                             const void *bias, void *Y_host, void *stream) {
-    if (!h) return PROJ_ERR_INVALID_ARG;
+    if (!h || !is_current(h->device)) return PROJ_ERR_INVALID_ARG;
     if (h->plan.kernel == PROJ_KERNEL_NONE) return PROJ_OK;
     if (!Y_host || (!X_host && h->K > 0)) return PROJ_ERR_INVALID_ARG;
     const size_t xb = static_cast<size_t>(h->M) * h->K * 2;
@@ -789,7 +789,7 @@ proj_status_t run_host_impl(proj_handle_t h, const void *X_host, const void *W, 
 extern "C" {
 
 proj_status_t proj_device_status(proj_handle_t h, void *stream) {
-    if (!h) return PROJ_ERR_INVALID_ARG;
+    if (!h || !is_current(h->device)) return PROJ_ERR_INVALID_ARG;
     if (cudaStreamSynchronize(as_stream(stream)) != cudaSuccess) return PROJ_ERR_CUDA;
     if (h->plan.kernel != PROJ_KERNEL_TC) return PROJ_OK;
     int word = 0;

@@ -220,7 +220,9 @@ proj_status_t proj_plan_reduction_order(const proj_plan_desc_t *plan, int64_t sp
                                         int64_t *count);
 
 /*
- * Create a handle for one problem shape on the current CUDA device.
+ * Create a handle for one problem shape on the current CUDA device.  While
+ * another device is current, runs, packing and proj_device_status with the
+ * handle return PROJ_ERR_INVALID_ARG.
  *   M, N, K ≥ 0 (a zero M or N plans nothing; K == 0 plans Y = bias or 0).
  *   x_dtype, bias_dtype: PROJ_BF16 only (else PROJ_ERR_UNSUPPORTED).
  *   w_dtype: PROJ_BF16, or PROJ_F32 for fp32 router weights, computed as the

@@ -146,3 +146,23 @@ def test_launch_fault(lib_built):
         assert r[k] == dlp.PROJ_ERR_CUDA, (k, r)
     assert r["status"] == dlp.PROJ_OK and r["noalloc_status"] == dlp.PROJ_OK, r
     assert r["destroy"] == dlp.PROJ_OK and r["context_ok"] and r["leak_bytes"] <= 0, r
+
+
+def test_handles_of_another_device(lib_built):
+    # Every handle is taken for another device's: refused on the host, nothing is launched with it.
+    import dense_linear_projection_gb300 as dlp
+    r = run_child("device")
+    for k in ("run", "run_again", "pack", "run_host", "status"):
+        assert r[k] == dlp.PROJ_ERR_INVALID_ARG, (k, r)
+    assert r["create"] == r["destroy"] == r["noalloc"] == dlp.PROJ_OK and r["context_ok"] and r["leak_bytes"] <= 0, r
+
+
+def test_tensors_outside_the_handles_device():
+    import torch
+    import dense_linear_projection_gb300 as dlp
+    proj = dlp.Projection(4, 64, 64)
+    X, W = torch.zeros((4, 64), dtype=torch.bfloat16), torch.zeros((64, 64), dtype=torch.bfloat16)
+    for call in (lambda: proj(X, W.cuda()), lambda: proj.pack(W)):
+        with pytest.raises(dlp.ProjError) as e:
+            call()
+        assert e.value.status == dlp.PROJ_ERR_INVALID_ARG
