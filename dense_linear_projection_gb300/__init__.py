@@ -395,6 +395,19 @@ def proj_kv_destroy(h: Optional[int]) -> None:
 
 
 # ---------------------------------------------------------------- convenience
+def _empty_on(stream, n, dtype, device):
+    """A new tensor of the memory of ``stream`` (a stream, a handle, or None for
+    the current one): what another stream gave back may still be in use there."""
+    import torch
+    if stream is None:
+        return torch.empty(n, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        # 0 and the runtime's other name for it, 1, are the default stream.
+        stream = torch.cuda.ExternalStream(stream, device) if stream > 1 else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=dtype, device=device)
+
+
 class Projection:
     """A planned projection for one shape; call it with PyTorch tensors.
 
@@ -435,7 +448,7 @@ class Projection:
         if out is None:
             dt = torch.float32 if self.y_dtype == PROJ_F32 else torch.bfloat16
             n_out = self.N // 2 if self.act == PROJ_ACT_SWIGLU else self.N
-            out = torch.empty((self.M, n_out), dtype=dt, device=X.device)
+            out = _empty_on(stream, (self.M, n_out), dt, X.device)
         if stream is None:
             stream = torch.cuda.current_stream(X.device)
         if residual is not None:
@@ -458,7 +471,7 @@ class Projection:
         import torch
         self._check_device(W)
         n = proj_packed_weight_bytes(self.handle)
-        P = torch.empty(max(n // 2, 8), dtype=torch.bfloat16, device=W.device)
+        P = _empty_on(stream, max(n // 2, 8), torch.bfloat16, W.device)
         if stream is None:
             stream = torch.cuda.current_stream(W.device)
         proj_pack_weights(self.handle, W, P, stream)
@@ -545,7 +558,7 @@ class Q4Projection:
         device = codes.get_device()
         _require(device >= 0 and scales.get_device() == device and (zeros is None or zeros.get_device() == device),
                  "codes, scales, zeros: on one CUDA device")
-        packed = torch.empty(self._bytes, dtype=torch.uint8, device=codes.device)
+        packed = _empty_on(stream, self._bytes, torch.uint8, codes.device)
         if stream is None:
             stream = torch.cuda.current_stream(codes.device)
         with torch.cuda.device(device):

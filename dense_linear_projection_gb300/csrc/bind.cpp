@@ -89,6 +89,18 @@ void *stream_of(PyObject *o, int64_t device) {
     return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
 }
 
+// A new tensor of the memory of the stream `o` that the call runs on: what another
+// stream gave back may still be in use there.
+at::Tensor fresh(PyObject *o, int64_t device, at::IntArrayRef sizes, const at::TensorOptions &options) {
+    if (o == Py_None) return at::empty(sizes, options);
+    const int64_t h = integer(o);
+    const auto index = static_cast<c10::DeviceIndex>(device);
+    // 0 and the runtime's other name for it, 1, are the default stream.
+    const c10::cuda::CUDAStreamGuard on(h == 0 || h == 1 ? c10::cuda::getDefaultCUDAStream(index)
+                                                         : c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(h), index));
+    return at::empty(sizes, options);
+}
+
 const void *data(const at::Tensor *t) { return t ? t->data_ptr() : nullptr; }
 
 PyObject *init(PyObject *, PyObject *error) {
@@ -118,7 +130,7 @@ PyObject *q4(PyObject *, PyObject *const *a, Py_ssize_t count) {
         at::Tensor made;
         const at::Tensor *out = tensor(a[8], "out: a tensor");
         if (!out) {
-            made = at::empty({M, N}, X.options().dtype(type));
+            made = fresh(a[9], device, {M, N}, X.options().dtype(type));
             out = &made;
         } else if (!is(*out, type, device, 2) || out->size(0) != M || out->size(1) != N || !out->is_contiguous()) {
             refuse("out: contiguous [M, N] of y_dtype, on X's device");
@@ -190,7 +202,7 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t count) {
             q_stride = rows(*q, tokens, c.q_heads, c.dim, c.device,
                             "q: bf16 [tokens, q_heads, head_dim] with contiguous heads, on the cache's device");
             if (!q_out) {
-                made = at::empty({tokens, c.q_heads, c.dim}, q->options());
+                made = fresh(a[17], c.device, {tokens, c.q_heads, c.dim}, q->options());
                 q_out = &made;
             }
             q_out_stride = rows(*q_out, tokens, c.q_heads, c.dim, c.device, "q_out: as q");
@@ -229,12 +241,12 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t count) {
         at::Tensor made, lse;
         const at::Tensor *out = tensor(a[13], "out: a tensor");
         if (!out) {
-            made = at::empty({n, c.q_heads, c.dim}, q.options());
+            made = fresh(a[15], c.device, {n, c.q_heads, c.dim}, q.options());
             out = &made;
         }
         const int64_t out_stride = rows(*out, n, c.q_heads, c.dim, c.device, "out: as q");
         const bool with_lse = PyObject_IsTrue(a[14]) == 1;
-        if (with_lse) lse = at::empty({n, c.q_heads}, q.options().dtype(at::kFloat));
+        if (with_lse) lse = fresh(a[15], c.device, {n, c.q_heads}, q.options().dtype(at::kFloat));
         check(proj_kv_attend(c.h, n, q.data_ptr(), q_stride, c.k->data_ptr(), c.v->data_ptr(),
                              static_cast<const float *>(data(c.k_scale)), static_cast<const float *>(data(c.v_scale)),
                              static_cast<const int32_t *>(table.data_ptr()), table.size(1),
