@@ -22,7 +22,9 @@
 //
 // Precision: fp32 logits, weights and sums.  The weights enter the second
 // product as two 16-bit parts (high + low): in one bf16 part their rounding
-// would double the error of a bf16 output.  An e4m3 cache is converted to fp16
+// would double the error of a bf16 output.  Two bf16 parts hold a weight to 2^-16
+// of itself; two fp16 parts (split2) too, down to weights of 2^-36 of the largest,
+// and to 2^-52 of the largest below.  An e4m3 cache is converted to fp16
 // (exact); the queries then are fp16 too, scaled by a power of two per head so
 // that no bf16 query overflows or vanishes.
 #pragma once
@@ -76,13 +78,28 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+// fp16 has no exponent below -24, so the weights (1 at most) are taken 2^15 times
+// as large, and what their high parts leave 2^12 times as large again, next to
+// values 2^12 times smaller (e4m3 times 2^-12 is exact in fp16): a weight loses
+// 2^-24 of itself or 2^-52, whichever is more.  (131071 tokens of 25 nats below one
+// whose value is zero are still all of the output.)
+constexpr float kHalfWeight = 32768.f, kHalfWeightBack = 1.f / 32768.f, kHalfRest = 4096.f;
+constexpr uint32_t kHalfRestBack = 0x0C000C00u;  // 2^-12, twice
+
+__device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // Two weights as 16-bit high parts and what the high parts leave.
 template <bool kHalf>
 __device__ __forceinline__ void split2(float a, float b, uint32_t &high, uint32_t &low) {
     if constexpr (kHalf) {
+        a *= kHalfWeight, b *= kHalfWeight;
         const __half2 h = __floats2half2_rn(a, b);
         const float2 f = __half22float2(h);
-        const __half2 r = __floats2half2_rn(a - f.x, b - f.y);
+        const __half2 r = __floats2half2_rn((a - f.x) * kHalfRest, (b - f.y) * kHalfRest);
         high = *reinterpret_cast<const uint32_t *>(&h);
         low = *reinterpret_cast<const uint32_t *>(&r);
     } else {
@@ -681,10 +698,12 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
                             const uint32_t lo8 = __byte_perm(a[2 * i], 0, 0x3120), hi8 = __byte_perm(a[2 * i + 1], 0, 0x3120);
                             const uint32_t a0 = e4m3x2_to_half2(lo8), a1 = e4m3x2_to_half2(lo8 >> 16);
                             const uint32_t a2 = e4m3x2_to_half2(hi8), a3 = e4m3x2_to_half2(hi8 >> 16);
+                            const uint32_t s0 = half2_mul(a0, kHalfRestBack), s1 = half2_mul(a1, kHalfRestBack);
+                            const uint32_t s2 = half2_mul(a2, kHalfRestBack), s3 = half2_mul(a3, kHalfRestBack);
 #pragma unroll
                             for (int t = 0; t < kNT; ++t) {
                                 mma16816<true>(o[t][d + i], a0, a1, a2, a3, high[n][t][0], high[n][t][1]);
-                                mma16816<true>(o[t][d + i], a0, a1, a2, a3, low[n][t][0], low[n][t][1]);
+                                mma16816<true>(o[t][d + i], s0, s1, s2, s3, low[n][t][0], low[n][t][1]);
                             }
                         }
                     }
@@ -790,7 +809,7 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
                 if (h >= heads) break;
                 const int key = key_head(seg_unit, h % kKeyHeads);
                 const int64_t head = static_cast<int64_t>(key) * p.group + chunk * p.chunk_heads + h / kKeyHeads;
-                const float by = kE4m3 && p.v_scale ? p.v_scale[key] : 1.f;
+                const float by = kE4m3 ? (p.v_scale ? p.v_scale[key] : 1.f) * kHalfWeightBack : 1.f;
                 const float inv = r.l[k] == 0.f ? 0.f : by / r.l[k];  // (a NaN stays one)
                 if (d0 < cache.head_dim)
                     *reinterpret_cast<uint2 *>(p.out + row_b * p.out_stride + head * cache.head_dim + d0) =

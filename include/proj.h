@@ -592,7 +592,9 @@ proj_status_t proj_q4_destroy(proj_q4_handle_t h);
  *   n = seq_lens[b] (window 0: all n):
  *     out[b,h] = Σ_t softmax_t(scale · q[b,h]·k_t) · v_t,
  *     lse[b,h] = log Σ_t e^(scale · q[b,h]·k_t)   (lse fp32 [B, q_heads], or NULL).
- *   n = 0 gives out = 0 and lse = −∞.  The weights and sums are fp32; out is bf16, rounded once.
+ *   n = 0 gives out = 0 and lse = −∞.  Logits, weights and sums are fp32; in the
+ *   product with v a weight is held to 2^-16 of itself (over e4m3: or to 2^-52 of
+ *   the largest weight, whichever is more); out is bf16, rounded once.
  *   The sequences' tokens are dealt out evenly over the GPU and joined in a
  *   fixed order: reruns are bit-identical.
  *

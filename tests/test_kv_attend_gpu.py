@@ -270,3 +270,28 @@ def test_refusals():
         with pytest.raises(dlp.ProjError) as e:
             what()
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("nats", [3, 8, 12, 15, 17.5, 20, 24])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_small_weights_count(dtype, nats):
+    # One token takes the largest weight and has the value 0; all others lie e^-nats below it and are all of
+    # the output.  The bound holds each weight to 2⁻¹⁶ of itself (e4m3: down to 2⁻³⁶ = e^-24.9 of the largest).
+    import torch
+    for lens, at, heads, kv_heads, dim in (([4000, 40], 0, 8, 2, 64), ([4000, 33], 3999, 16, 1, 128), ([9000], 100, 4, 1, 256)):
+        kv, q, table, lens_dev = case(lens, heads, kv_heads, dim, 16, dtype=dtype)
+        q.zero_()
+        q[..., 3] = 1
+        raw = lambda c: c.view(torch.uint8) if dtype == "e4m3" else c  # noqa: E731
+        raw(kv.k_cache).zero_()
+        key = torch.zeros((kv_heads, dim), device="cuda")
+        key[:, 3] = 16
+        for b, n in enumerate(lens):
+            page, place = table[b, min(at, n - 1) // 16].long(), min(at, n - 1) % 16
+            raw(kv.k_cache)[page, place] = raw(key.to(kv.k_cache.dtype))
+            raw(kv.v_cache)[page, place] = 0
+        if kv.k_scale is not None:
+            kv.k_scale.fill_(1.0)
+        out, lse = kv.attend(q, table, lens_dev, scale=nats / 16, return_lse=True)
+        ref = ku.attention64(q, kv.k_cache, kv.v_cache, table, lens, 16, nats / 16, 0, kv.k_scale, kv.v_scale)
+        ku.check_attention(out, lse, ref, f"{nats} nats, {lens}")
