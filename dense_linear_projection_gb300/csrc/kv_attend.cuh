@@ -25,8 +25,9 @@
 // would double the error of a bf16 output.  Two bf16 parts hold a weight to 2^-16
 // of itself; two fp16 parts (split2) too, down to weights of 2^-36 of the largest,
 // and to 2^-52 of the largest below.  An e4m3 cache is converted to fp16
-// (exact); the queries then are fp16 too, scaled by a power of two per head so
-// that no bf16 query overflows or vanishes.
+// (exact); the queries then are fp16 too, scaled by a power of two per head:
+// elements down to 2^-32 of the head's largest are exact, smaller ones are held to
+// 2^-40 of it (a logit's fp32 sum holds no more beside the largest).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -538,8 +539,9 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
                 }
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // 2^-e brings the largest to [1, 2): e within ±126 keeps both powers normal numbers.
-                const int e = min(126, max(-126, static_cast<int>(top >> 7) - 127));
+                // 2^-e brings the largest to [2^14, 2^15), so that fp16 holds elements
+                // down to 2^-32 of it exactly; e within ±126 keeps both powers normal numbers.
+                const int e = min(126, max(-126, static_cast<int>(top >> 7) - 127 - 14));
                 const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k) {

@@ -295,3 +295,30 @@ def test_small_weights_count(dtype, nats):
         out, lse = kv.attend(q, table, lens_dev, scale=nats / 16, return_lse=True)
         ref = ku.attention64(q, kv.k_cache, kv.v_cache, table, lens, 16, nats / 16, 0, kv.k_scale, kv.v_scale)
         ku.check_attention(out, lse, ref, f"{nats} nats, {lens}")
+
+
+@pytest.mark.parametrize("power", [10, 16, 22])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_queries_of_unequal_elements(dtype, power):
+    # One element of each query is 2^power, against keys that are 0 there: the others make the logits.
+    import torch
+    lens = [300, 20]
+    for dim in (64, 128, 256):
+        kv, q, table, lens_dev = case(lens, 8, 2, dim, 16, dtype=dtype)
+        q[..., 5] = 2.0 ** power
+        raw = kv.k_cache.view(torch.uint8) if dtype == "e4m3" else kv.k_cache
+        raw[..., 5] = 0
+        out, lse = kv.attend(q, table, lens_dev, return_lse=True)
+        ref = ku.attention64(q, kv.k_cache, kv.v_cache, table, lens, 16, dim ** -0.5, 0, kv.k_scale, kv.v_scale)
+        ku.check_attention(out, lse, ref, f"2^{power}, {dim}")
+
+
+def test_queries_at_the_ends_of_bf16_over_8_bits():
+    # The largest and the smallest bf16 queries, subnormal ones among them.
+    import torch
+    kv, q, table, lens = case([100] * 2, 4, 2, 64, 16, dtype="e4m3")
+    for size, scale in ((2.0 ** 125, 2.0 ** -126), (2.0 ** -124, 2.0 ** 121), (2.0 ** -130, 2.0 ** 122)):
+        x = (q.float() * size).to(torch.bfloat16)
+        out, lse = kv.attend(x, table, lens, scale=scale, return_lse=True)
+        ref = ku.attention64(x, kv.k_cache, kv.v_cache, table, [100] * 2, 16, scale, 0, kv.k_scale, kv.v_scale)
+        ku.check_attention(out, lse, ref, f"size={size}")
