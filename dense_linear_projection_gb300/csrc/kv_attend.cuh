@@ -104,11 +104,13 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &high, uint32_
         high = *reinterpret_cast<const uint32_t *>(&h);
         low = *reinterpret_cast<const uint32_t *>(&r);
     } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        const float2 f = __bfloat1622float2(h);
-        const __nv_bfloat162 r = __floats2bfloat162_rn(a - f.x, b - f.y);
-        high = *reinterpret_cast<const uint32_t *>(&h);
-        low = *reinterpret_cast<const uint32_t *>(&r);
+        // The high part is the upper half of the next float below, so that the
+        // low part of a positive weight is positive: an infinite value times 0, or
+        // times parts of both signs, would be NaN.
+        constexpr float kBelow = 0x1.fffffep-1f;
+        const uint32_t ha = __float_as_uint(__fmul_rz(a, kBelow)), hb = __float_as_uint(__fmul_rz(b, kBelow));
+        high = __byte_perm(ha, hb, 0x7632);
+        low = bf16_pair(a - __uint_as_float(ha & 0xffff0000u), b - __uint_as_float(hb & 0xffff0000u));
     }
 }
 

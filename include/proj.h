@@ -596,7 +596,8 @@ proj_status_t proj_q4_destroy(proj_q4_handle_t h);
  *   product with v a weight is held to 2^-16 of itself (over e4m3: or to 2^-52 of
  *   the largest weight, whichever is more); out is bf16, rounded once.  Over
  *   e4m3, elements of q are held to 2^-40 of their head's largest, exactly down
- *   to 2^-32 of it.
+ *   to 2^-32 of it.  An infinite value of v gives infinity where its weight is
+ *   above 2^-100 of the largest (below, NaN).
  *   The sequences' tokens are dealt out evenly over the GPU and joined in a
  *   fixed order: reruns are bit-identical.
  *

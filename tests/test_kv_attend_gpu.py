@@ -322,3 +322,43 @@ def test_queries_at_the_ends_of_bf16_over_8_bits():
         out, lse = kv.attend(x, table, lens, scale=scale, return_lse=True)
         ref = ku.attention64(x, kv.k_cache, kv.v_cache, table, [100] * 2, 16, scale, 0, kv.k_scale, kv.v_scale)
         ku.check_attention(out, lse, ref, f"size={size}")
+
+
+@pytest.mark.parametrize("lens", [[1, 17], [900, 40], [20000], [130] * 40], ids=lambda x: f"{len(x)}x{x[0]}")
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_infinite_values(lens, dim):
+    # An infinite value makes its element of its heads infinite, two of both signs or a NaN make it NaN.
+    import torch
+    kv, q, table, lens_dev = case(lens, 8, 4, dim, 16)
+    ref = ku.attention64(q, kv.k_cache, kv.v_cache, table, lens, 16, dim ** -0.5)
+    last = lens[0] - 1
+    kv.v_cache[table[0, last // 16].long(), last % 16, 2, 5:9] = torch.tensor([math.inf, -math.inf, math.nan, math.inf], device="cuda").to(torch.bfloat16)
+    kv.v_cache[table[0, 0].long(), 0, 2, 8] = -math.inf
+    out, lse = kv.attend(q, table, lens_dev, return_lse=True)
+    got = out[0, 4:6, 5:9].clone()
+    assert (got[:, 0] == math.inf).all() and (got[:, 1] == -math.inf).all() and got[:, 2].isnan().all()
+    assert got[:, 3].isnan().all() if lens[0] > 1 else (got[:, 3] == -math.inf).all()
+    out[0, 4:6, 5:9] = ref[0][0, 4:6, 5:9].to(torch.bfloat16)
+    ku.check_attention(out, lse, ref, "the others")
+
+
+def test_infinite_keys():
+    # A logit of -inf has no weight; one of +inf makes its heads' outputs NaN, as in the definition.
+    import torch
+    lens, dim = [700, 30], 64
+    kv, q, table, lens_dev = case(lens, 8, 4, dim, 16)
+    q[0, 4:6, 7] = 1
+    ref = ku.attention64(q, kv.k_cache, kv.v_cache, table, lens, 16, dim ** -0.5, keep=lambda b, t: (t != 650) | (b != 0))
+    whole = ku.attention64(q, kv.k_cache, kv.v_cache, table, lens, 16, dim ** -0.5)
+    page = table[0, 650 // 16].long()
+    kv.k_cache[page, 650 % 16, 2, 7] = -math.inf
+    out, lse = kv.attend(q, table, lens_dev, return_lse=True)
+    mixed = [w.clone() for w in whole]
+    for m, r in zip(mixed, ref):
+        m[0, 4:6] = r[0, 4:6]
+    ku.check_attention(out, lse, mixed, "-inf")
+    kv.k_cache[page, 650 % 16, 2, 7] = math.inf
+    out, lse = kv.attend(q, table, lens_dev, return_lse=True)
+    assert out[0, 4:6].isnan().all() and lse[0, 4:6].isnan().all()
+    out[0, 4:6], lse[0, 4:6] = whole[0][0, 4:6].to(torch.bfloat16), whole[1][0, 4:6].float()
+    ku.check_attention(out, lse, whole, "+inf")
