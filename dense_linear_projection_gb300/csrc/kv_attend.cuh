@@ -215,8 +215,19 @@ struct JoinPart {
 
 __device__ __forceinline__ float finite_or_zero(float top) { return top == -INFINITY ? 0.f : top; }
 
-// Joins the partial results in slots slot(0) .. slot(count - 1), in that order;
-// the loads of several are in flight at a time.  Heads past `heads` are unused.
+// One part, of maximum m, against the joint maximum: in the same operations
+// wherever a part is joined.
+template <int kHeads, int kDim>
+__device__ __forceinline__ void add_part(JoinPart<kHeads, kDim> &r, int k, float m, float l, float4 o) {
+    const float w = exp2_fast(m - finite_or_zero(r.m[k]));
+    r.l[k] = __fmaf_rn(w, l, r.l[k]);
+    r.o[k].x = __fmaf_rn(w, o.x, r.o[k].x), r.o[k].y = __fmaf_rn(w, o.y, r.o[k].y);
+    r.o[k].z = __fmaf_rn(w, o.z, r.o[k].z), r.o[k].w = __fmaf_rn(w, o.w, r.o[k].w);
+}
+
+// Joins the partial results in slots slot(0) .. slot(count - 1), in that order,
+// against the maximum of all; the loads of several are in flight at a time.  Heads
+// past `heads` are unused.
 template <int kHeads, int kDim, typename Slot>
 __device__ __forceinline__ void join_parts(const float *partials, int count, Slot slot, int heads, JoinPart<kHeads, kDim> &r) {
     using Part = JoinPart<kHeads, kDim>;
@@ -237,26 +248,25 @@ __device__ __forceinline__ void join_parts(const float *partials, int count, Slo
                 l[i] = __ldcg(from + kHeads + h);
                 o[i] = __ldcg(reinterpret_cast<const float4 *>(from + 2 * kHeads + h * kDim + d));
             }
-            float top = r.m[k];
+            if (c == 0) {
+                for (int x = kAtOnce; x < count; x += kAtOnce)
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) top = fmaxf(top, m[i]);
-            const float base = finite_or_zero(top), keep = exp2_fast(r.m[k] - base);
-            r.m[k] = top;
-            r.l[k] *= keep;
-            r.o[k].x *= keep, r.o[k].y *= keep, r.o[k].z *= keep, r.o[k].w *= keep;
+                    for (int i = 0; i < kAtOnce; ++i)
+                        r.m[k] = fmaxf(r.m[k], __ldcg(partials + slot(x + i < count ? x + i : x) * Part::kFloats + h));
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) r.m[k] = fmaxf(r.m[k], m[i]);
+            }
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i) {
                 if (c + i >= count) break;
-                const float w = exp2_fast(m[i] - base);
-                r.l[k] += w * l[i];
-                r.o[k].x += w * o[i].x, r.o[k].y += w * o[i].y, r.o[k].z += w * o[i].z, r.o[k].w += w * o[i].w;
+                add_part(r, k, m[i], l[i], o[i]);
             }
         }
     }
 }
 
-// The same by way of `ring` (shared memory of `bytes` that no copy is under way
-// to): one round trip for as many parts as it holds.
+// The same, bit for bit, by way of `ring` (shared memory of `bytes` that no copy is
+// under way to): one round trip for as many parts as it holds.
 template <int kHeads, int kDim, typename Slot>
 __device__ __forceinline__ void join_parts_in(uint8_t *ring, int bytes, const float *partials, int count, Slot slot, int heads,
                                               JoinPart<kHeads, kDim> &r) {
@@ -272,6 +282,15 @@ __device__ __forceinline__ void join_parts_in(uint8_t *ring, int bytes, const fl
             for (int x = threadIdx.x * 4; x < floats; x += kKvThreads * 4) cp_async16(to + (i * floats + x) * 4, from + x);
         }
         cp_async_commit();
+        if (c == 0) {  // the maxima of the parts that the ring does not hold yet
+#pragma unroll
+            for (int k = 0; k < Part::kPer; ++k) {
+                const int h = h0 + k * Part::kHeadStep;
+                if (h >= heads) break;
+#pragma unroll 4
+                for (int i = n; i < count; ++i) r.m[k] = fmaxf(r.m[k], __ldcg(partials + slot(i) * Part::kFloats + h));
+            }
+        }
         cp_async_wait<0>();
         __syncthreads();
         const float *part = reinterpret_cast<const float *>(ring);
@@ -279,19 +298,12 @@ __device__ __forceinline__ void join_parts_in(uint8_t *ring, int bytes, const fl
         for (int k = 0; k < Part::kPer; ++k) {
             const int h = h0 + k * Part::kHeadStep;
             if (h >= heads) break;
-            float top = r.m[k];
-            for (int i = 0; i < n; ++i) top = fmaxf(top, part[i * floats + h]);
-            const float base = finite_or_zero(top), keep = exp2_fast(r.m[k] - base);
-            r.m[k] = top;
-            r.l[k] *= keep;
-            r.o[k].x *= keep, r.o[k].y *= keep, r.o[k].z *= keep, r.o[k].w *= keep;
+            if (c == 0)
+                for (int i = 0; i < n; ++i) r.m[k] = fmaxf(r.m[k], part[i * floats + h]);
 #pragma unroll 4
-            for (int i = 0; i < n; ++i) {
-                const float w = exp2_fast(part[i * floats + h] - base);
-                const float4 o = *reinterpret_cast<const float4 *>(part + i * floats + 2 * kHeads + h * kDim + d);
-                r.l[k] += w * part[i * floats + kHeads + h];
-                r.o[k].x += w * o.x, r.o[k].y += w * o.y, r.o[k].z += w * o.z, r.o[k].w += w * o.w;
-            }
+            for (int i = 0; i < n; ++i)
+                add_part(r, k, part[i * floats + h], part[i * floats + kHeads + h],
+                         *reinterpret_cast<const float4 *>(part + i * floats + 2 * kHeads + h * kDim + d));
         }
         __syncthreads();
     }

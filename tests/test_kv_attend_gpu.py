@@ -362,3 +362,32 @@ def test_infinite_keys():
     assert out[0, 4:6].isnan().all() and lse[0, 4:6].isnan().all()
     out[0, 4:6], lse[0, 4:6] = whole[0][0, 4:6].to(torch.bfloat16), whole[1][0, 4:6].float()
     ku.check_attention(out, lse, whole, "+inf")
+
+
+@pytest.mark.parametrize("B,n,heads,kv_heads", [(3, 5000, 64, 8), (33, 9600, 8, 1), (4, 30000, 16, 1)])
+def test_reruns_beside_other_work(B, n, heads, kv_heads):
+    # Bit-identical whichever CTA joins a row: copies on another stream change the order of arrival, the
+    # second half's values are the first's with the other sign (what is left of the sums is their rounding),
+    # and the last token's logit is the largest, so that a later part has the maximum.
+    import torch
+    kv, q, table, lens = case([n] * B, heads, kv_heads, 128, 16)
+    t, half = torch.arange(n, device="cuda"), n // 2
+    for b in range(B):
+        pages = table[b].long()[t // 16]
+        k, v = kv.k_cache[pages, t % 16], kv.v_cache[pages, t % 16]
+        k[half:2 * half], v[half:2 * half] = k[:half], -v[:half]
+        k[..., 0] = k[-1] = 0
+        k[-1, :, 0] = 30
+        v[-1] = v[half - 1] = 0
+        kv.k_cache[pages, t % 16], kv.v_cache[pages, t % 16] = k, v
+    q[..., 0] = 2
+    first, lse0 = kv.attend(q, table, lens, return_lse=True)
+    side, a = torch.cuda.Stream(), torch.empty(1 << 28, device="cuda", dtype=torch.uint8)
+    c = torch.empty_like(a)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(400):
+        with torch.cuda.stream(side):
+            c[:1 << (20 + i % 9)].copy_(a[:1 << (20 + i % 9)])
+        out, lse = kv.attend(q, table, lens, return_lse=True)
+        differ += (out != first).any() | (lse != lse0).any()
+    assert differ.item() == 0
