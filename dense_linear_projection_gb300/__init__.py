@@ -656,7 +656,13 @@ class PagedKV:
                             self._scale if scale is None else scale, window, out, return_lse, _stream(stream))
 
     def status(self, stream=None) -> int:
+        """What the kernels found so far on ``stream`` (by default the current
+        one, as for the calls): PROJ_ERR_INVALID_ARG once after an index out of
+        range.  Waits for the stream; the word of another stream's calls may not
+        be there yet."""
         import torch
+        if stream is None:
+            stream = torch.cuda.current_stream(self.k_cache.device)
         with torch.cuda.device(self.k_cache.device):
             return proj_kv_device_status(self.handle, stream)
 

@@ -291,11 +291,21 @@ proj_status_t proj_kv_attend(proj_kv_handle_t h, int64_t sequences, const void *
 
 proj_status_t proj_kv_device_status(proj_kv_handle_t h, void *stream) {
     if (!h || !is_current(h->device)) return PROJ_ERR_INVALID_ARG;
-    if (cudaStreamSynchronize(as_stream(stream)) != cudaSuccess) return PROJ_ERR_CUDA;
+    // Read and cleared in the stream's order: a kernel launched after this call on
+    // any stream finds the word as this call leaves it.
     int word = 0;
-    if (cudaMemcpy(&word, h->status, sizeof word, cudaMemcpyDeviceToHost) != cudaSuccess) return PROJ_ERR_CUDA;
+    if (cudaMemcpyAsync(&word, h->status, sizeof word, cudaMemcpyDeviceToHost, as_stream(stream)) != cudaSuccess ||
+        cudaStreamSynchronize(as_stream(stream)) != cudaSuccess) {
+        cudaGetLastError();
+        return PROJ_ERR_CUDA;
+    }
     if (word == 0) return PROJ_OK;
-    return cudaMemset(h->status, 0, sizeof word) == cudaSuccess ? PROJ_ERR_INVALID_ARG : PROJ_ERR_CUDA;
+    if (cudaMemsetAsync(h->status, 0, sizeof word, as_stream(stream)) != cudaSuccess ||
+        cudaStreamSynchronize(as_stream(stream)) != cudaSuccess) {
+        cudaGetLastError();
+        return PROJ_ERR_CUDA;
+    }
+    return PROJ_ERR_INVALID_ARG;
 }
 
 proj_status_t proj_kv_destroy(proj_kv_handle_t h) {

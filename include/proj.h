@@ -605,7 +605,8 @@ proj_status_t proj_q4_destroy(proj_q4_handle_t h);
  * device can see is checked there: a position past the page table or the
  * rope table, a sequence id or a page outside its array, a length below zero
  * or past the page table.  Such a token is skipped (attention leaves it out)
- * and proj_kv_device_status then returns PROJ_ERR_INVALID_ARG once.
+ * and proj_kv_device_status then returns PROJ_ERR_INVALID_ARG once: it waits for
+ * `stream`, which has to be the one that the handle's calls ran on.
  */
 typedef struct proj_kv_s *proj_kv_handle_t;
 

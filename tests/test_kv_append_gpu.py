@@ -247,3 +247,24 @@ def test_refusals():
         with pytest.raises(dlp.ProjError) as e:
             what()
         assert e.value.status == status
+
+
+def test_status_follows_the_stream():
+    # status() waits for the stream that the calls run on, the current one by default.
+    import torch
+    import dense_linear_projection_gb300 as dlp
+    k_cache, v_cache = ku.make_cache(8, 16, 2, 64)
+    kv = dlp.PagedKV(k_cache, v_cache, 2, 1)
+    k, v = (torch.zeros((1, 2, 64), device="cuda").to(torch.bfloat16) for _ in "kv")
+    pos, table = torch.full((1,), 99, dtype=torch.int32, device="cuda"), torch.zeros((1, 2), dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            torch.cuda._sleep(100_000_000)
+            kv.append(None, k, v, pos, table)
+            assert kv.status() == dlp.PROJ_ERR_INVALID_ARG
+            assert kv.status() == dlp.PROJ_OK
+    torch.cuda._sleep(100_000_000)
+    kv.append(None, k, v, pos, table, stream=side)
+    assert kv.status(side) == dlp.PROJ_ERR_INVALID_ARG and kv.status(side.cuda_stream) == dlp.PROJ_OK
