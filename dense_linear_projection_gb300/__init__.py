@@ -478,6 +478,11 @@ class Projection:
         return P
 
     def status(self, stream=None) -> int:
+        """The handle's device status after the runs on ``stream`` (by default
+        the current one, as for the calls), which it waits for."""
+        if stream is None:
+            import torch
+            stream = torch.cuda.current_stream(self.device)
         return proj_device_status(self.handle, stream)
 
     def close(self) -> None:

@@ -790,10 +790,12 @@ extern "C" {
 
 proj_status_t proj_device_status(proj_handle_t h, void *stream) {
     if (!h || !is_current(h->device)) return PROJ_ERR_INVALID_ARG;
-    if (cudaStreamSynchronize(as_stream(stream)) != cudaSuccess) return PROJ_ERR_CUDA;
+    cudaStream_t s = as_stream(stream);
+    if (cudaStreamSynchronize(s) != cudaSuccess) return PROJ_ERR_CUDA;
     if (h->plan.kernel != PROJ_KERNEL_TC) return PROJ_OK;
     int word = 0;
-    if (cudaMemcpy(&word, h->params.status, sizeof word, cudaMemcpyDeviceToHost) != cudaSuccess)
+    if (cudaMemcpyAsync(&word, h->params.status, sizeof word, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
         return PROJ_ERR_CUDA;
     if (word == 0) return PROJ_OK;
     const proj_status_t what = (word & (kErrSmemTooSmall | kErrLaunchShape | kErrPairTmem))
@@ -801,8 +803,9 @@ proj_status_t proj_device_status(proj_handle_t h, void *stream) {
                                    : PROJ_ERR_DEVICE_TIMEOUT;
     // Clear the word and the split-K counters (a run that gave up may have
     // left some mid-count) so the handle is usable again.
-    if (cudaMemset(static_cast<uint8_t *>(h->scratch) + h->scratch_clear_from, 0,
-                   static_cast<size_t>(h->scratch_bytes - h->scratch_clear_from)) != cudaSuccess)
+    if (cudaMemsetAsync(static_cast<uint8_t *>(h->scratch) + h->scratch_clear_from, 0,
+                        static_cast<size_t>(h->scratch_bytes - h->scratch_clear_from), s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
         return PROJ_ERR_CUDA;
     return what;
 }

@@ -65,3 +65,17 @@ def test_paged_cache(as_handle):
           [((B, H, D), bf16)], as_handle)
     q = rows[:, :H].contiguous()
     check(lambda s: kv.attend(q, table, lens, return_lse=True, stream=s), [((B, H, D), bf16), ((B, H), torch.float32)], as_handle)
+
+
+def test_projection_status_waits_for_the_current_stream():
+    import torch
+    import dense_linear_projection_gb300 as dlp
+    X, W = (torch.randn(s, device="cuda").to(torch.bfloat16) for s in ((16, 1024), (2048, 1024)))
+    proj = dlp.Projection(16, 2048, 1024)
+    torch.cuda.synchronize()
+    done = torch.cuda.Event()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        torch.cuda._sleep(100_000_000)
+        proj(X, W)
+        done.record()
+        assert proj.status() == dlp.PROJ_OK and done.query()
