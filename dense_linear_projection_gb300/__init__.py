@@ -15,7 +15,7 @@ import json
 import os
 from typing import Optional
 
-from ._build import bind_path, build, library_path
+from ._build import bind_path, build, build_bind, library_path
 
 __all__ = [
     "PROJ_OK", "PROJ_ERR_INVALID_ARG", "PROJ_ERR_UNSUPPORTED", "PROJ_ERR_MISALIGNED",
@@ -510,7 +510,7 @@ _BIND = None
 
 
 def _bind():
-    """The native calls that take PyTorch tensors (csrc/bind.cpp), loaded once."""
+    """The native calls that take PyTorch tensors (csrc/bind.cpp), built on first use, loaded once."""
     global _BIND
     if _BIND is None:
         import importlib.machinery
@@ -519,7 +519,7 @@ def _bind():
         lib()
         path = bind_path()
         if not os.path.exists(path):
-            build()
+            path = build_bind()
         loader = importlib.machinery.ExtensionFileLoader("_bind", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_bind", loader))
         loader.exec_module(module)

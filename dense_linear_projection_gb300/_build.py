@@ -2,8 +2,9 @@
 
 Each translation unit is compiled in parallel; the shared library lands next to
 this file as ``libproj_gb300.<machine>.so`` (the machine suffix keeps x86 and
-Arm builds apart).  Objects go to ``_build/<machine>/``.  Beside it lands
-``_bind.<machine>.so``, the calls that take PyTorch tensors (csrc/bind.cpp).
+Arm builds apart).  Objects go to ``_build/<machine>/``.  The calls that take
+PyTorch tensors (csrc/bind.cpp) are a file of their own beside it, built on first
+use; the library and its C ABI need neither PyTorch nor g++.
 """
 from __future__ import annotations
 
@@ -44,7 +45,9 @@ def library_path() -> str:
 
 
 def bind_path() -> str:
-    return os.path.join(PKG, f"_bind.{platform.machine()}.so")
+    """Where _bind lies: one file for each Python and PyTorch, whose binary interfaces it uses."""
+    import torch
+    return os.path.join(PKG, f"_bind.{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}.so")
 
 
 def _torch_dir() -> str:
@@ -67,46 +70,58 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _objdir() -> str:
+    path = os.path.join(PKG, "_build", platform.machine())
+    os.makedirs(path, exist_ok=True)
+    return path
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile (if sources changed) and return the library path."""
-    out, bind = library_path(), bind_path()
+    """Compile the library (if sources changed) and return its path.  Needs nvcc alone."""
+    out = library_path()
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    bind_src = os.path.join(CSRC, "bind.cpp")
-    bind_stale = force or _stale(bind, [bind_src, os.path.join(INCLUDE, "proj.h")])
-    lib_stale = force or _stale(out, srcs + HEADERS)
-    if not lib_stale and not bind_stale:
+    if not force and not _stale(out, srcs + HEADERS):
         return out
-    objdir = os.path.join(PKG, "_build", platform.machine())
-    os.makedirs(objdir, exist_ok=True)
+    objdir = _objdir()
 
     def compile_one(src):
         obj = os.path.join(objdir, os.path.basename(src) + ".o")
-        if src == bind_src:
-            t = _torch_dir()
-            cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-I" + INCLUDE,
-                   "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(t, "include"),
-                   "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"),
-                   "-I" + os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), "-c", src, "-o", obj]
-        else:
-            cmd = [nvcc(), *ARCH_FLAGS, *COMMON, "-c", src, "-o", obj]
+        cmd = [nvcc(), *ARCH_FLAGS, *COMMON, "-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd))
         _run(cmd, f"compiling {src}")
         return obj
 
-    todo = (srcs if lib_stale else []) + ([bind_src] if bind_stale else [])
-    with ThreadPoolExecutor(max_workers=len(todo)) as ex:
-        objs = dict(zip(todo, ex.map(compile_one, todo)))
-    if lib_stale:
-        tmp = out + f".tmp{os.getpid()}"
-        _run([nvcc(), *ARCH_FLAGS, "-shared", "-o", tmp, *(objs[s] for s in srcs)], "linking libproj_gb300")
-        os.replace(tmp, out)
-    if bind_stale:
-        tmp = bind + f".tmp{os.getpid()}"
-        _run([shutil.which("g++") or "g++", "-shared", "-o", tmp, objs[bind_src], "-L" + PKG,
-              "-l:" + os.path.basename(out), "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(_torch_dir(), "lib"),
-              "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], "linking _bind")
-        os.replace(tmp, bind)
+    with ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+        objs = list(ex.map(compile_one, srcs))
+    tmp = out + f".tmp{os.getpid()}"
+    _run([nvcc(), *ARCH_FLAGS, "-shared", "-o", tmp, *objs], "linking libproj_gb300")
+    os.replace(tmp, out)
+    return out
+
+
+def build_bind(force: bool = False, verbose: bool = False) -> str:
+    """Compile the calls that take PyTorch tensors (if sources changed), next to
+    the library that they call, and return their path.  Needs PyTorch and g++."""
+    out, src = bind_path(), os.path.join(CSRC, "bind.cpp")
+    if not force and not _stale(out, [src, os.path.join(INCLUDE, "proj.h")]):
+        build(verbose=verbose)
+        return out
+    t, gxx = _torch_dir(), shutil.which("g++") or "g++"
+    obj = os.path.join(_objdir(), os.path.basename(out) + ".o")
+    cmd = [gxx, "-O2", "-std=c++17", "-fPIC", "-I" + INCLUDE, "-I" + sysconfig.get_paths()["include"],
+           "-I" + os.path.join(t, "include"), "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-I" + os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), "-c", src, "-o", obj]
+    if verbose:
+        print(" ".join(cmd))
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        compiled = ex.submit(_run, cmd, f"compiling {src}")
+        library = build(verbose=verbose)
+        compiled.result()
+    tmp = out + f".tmp{os.getpid()}"
+    _run([gxx, "-shared", "-o", tmp, obj, "-L" + PKG, "-l:" + os.path.basename(library), "-Wl,-rpath,$ORIGIN",
+          "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], "linking _bind")
+    os.replace(tmp, out)
     return out
 
 
