@@ -75,6 +75,12 @@ int64_t integer(PyObject *o) {
     return v;
 }
 
+bool truth(PyObject *o, const char *what) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) refuse(what);
+    return v != 0;
+}
+
 void *handle(PyObject *o) {
     if (o == Py_None) refuse("closed");
     return reinterpret_cast<void *>(integer(o));
@@ -194,7 +200,7 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t count) {
             refuse("seq_ids: contiguous int32 [tokens], on the cache's device");
         if (rope && (!is(*rope, at::kFloat, c.device, 2) || !rope->is_contiguous()))
             refuse("rope: contiguous fp32 [positions, rot_dim], on the cache's device");
-        const int interleaved = PyObject_IsTrue(a[15]);
+        const int interleaved = truth(a[15], "interleaved: a truth value");
         const at::Tensor *q_out = tensor(a[16], "q_out: a tensor");
         at::Tensor made;
         int64_t q_stride = 0, q_out_stride = 0;
@@ -245,7 +251,7 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t count) {
             out = &made;
         }
         const int64_t out_stride = rows(*out, n, c.q_heads, c.dim, c.device, "out: as q");
-        const bool with_lse = PyObject_IsTrue(a[14]) == 1;
+        const bool with_lse = truth(a[14], "return_lse: a truth value");
         if (with_lse) lse = fresh(a[15], c.device, {n, c.q_heads}, q.options().dtype(at::kFloat));
         check(proj_kv_attend(c.h, n, q.data_ptr(), q_stride, c.k->data_ptr(), c.v->data_ptr(),
                              static_cast<const float *>(data(c.k_scale)), static_cast<const float *>(data(c.v_scale)),

@@ -391,3 +391,20 @@ def test_reruns_beside_other_work(B, n, heads, kv_heads):
         out, lse = kv.attend(q, table, lens, return_lse=True)
         differ += (out != first).any() | (lse != lse0).any()
     assert differ.item() == 0
+
+
+def test_truth_values_that_have_none():
+    # What an argument's own test raises comes out, before anything is launched.
+    import torch
+
+    class Neither:
+        def __bool__(self):
+            raise ValueError("neither")
+
+    kv, q, table, lens = case([5, 5], 8, 2, 64, 16)
+    out = torch.full_like(q, 7.0)
+    with pytest.raises(ValueError, match="neither"):
+        kv.attend(q, table, lens, out=out, return_lse=Neither())
+    with pytest.raises(ValueError, match="neither"):
+        kv.append(q, q[:, :2], q[:, 2:4], lens, table, interleaved=Neither(), q_out=out)
+    assert (out == 7).all()
