@@ -21,13 +21,12 @@
 //     order, from fp32 partial results in scratch.
 //
 // Precision: fp32 logits, weights and sums.  The weights enter the second
-// product as two 16-bit parts (high + low): in one bf16 part their rounding
-// would double the error of a bf16 output.  Two bf16 parts hold a weight to 2^-16
-// of itself; two fp16 parts (split2) too, down to weights of 2^-36 of the largest,
-// and to 2^-52 of the largest below.  An e4m3 cache is converted to fp16
-// (exact); the queries then are fp16 too, scaled by a power of two per head:
-// elements down to 2^-32 of the head's largest are exact, smaller ones are held to
-// 2^-40 of it (a logit's fp32 sum holds no more beside the largest).
+// product as 16-bit parts that hold them as fp32 does (split): three of bf16, or
+// over e4m3 two of fp16, to 2^-23 of a weight or 2^-52 of the largest.  An e4m3
+// cache is converted to fp16 (exact); the queries then are fp16 too, scaled by a
+// power of two per head: elements down to 2^-32 of the head's largest are exact,
+// smaller ones are held to 2^-40 of it (a logit's fp32 sum holds no more beside
+// the largest).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -82,7 +81,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // fp16 has no exponent below -24, so the weights (1 at most) are taken 2^15 times
 // as large, and what their high parts leave 2^12 times as large again, next to
 // values 2^12 times smaller (e4m3 times 2^-12 is exact in fp16): a weight loses
-// 2^-24 of itself or 2^-52, whichever is more.  (131071 tokens of 25 nats below one
+// 2^-23 of itself or 2^-52, whichever is more.  (131071 tokens of 25 nats below one
 // whose value is zero are still all of the output.)
 constexpr float kHalfWeight = 32768.f, kHalfWeightBack = 1.f / 32768.f, kHalfRest = 4096.f;
 constexpr uint32_t kHalfRestBack = 0x0C000C00u;  // 2^-12, twice
@@ -93,25 +92,37 @@ __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
     return d;
 }
 
-// Two weights as 16-bit high parts and what the high parts leave.
+// Two weights as 16-bit parts, each of what the parts before it leave: three of
+// bf16 (24 bits) or two of fp16 (22).
 template <bool kHalf>
-__device__ __forceinline__ void split2(float a, float b, uint32_t &high, uint32_t &low) {
+struct WeightParts {
+    static constexpr int kCount = kHalf ? 2 : 3;
+    uint32_t part[kCount];
+};
+template <bool kHalf>
+__device__ __forceinline__ WeightParts<kHalf> split(float a, float b) {
+    WeightParts<kHalf> s;
     if constexpr (kHalf) {
         a *= kHalfWeight, b *= kHalfWeight;
         const __half2 h = __floats2half2_rn(a, b);
         const float2 f = __half22float2(h);
         const __half2 r = __floats2half2_rn((a - f.x) * kHalfRest, (b - f.y) * kHalfRest);
-        high = *reinterpret_cast<const uint32_t *>(&h);
-        low = *reinterpret_cast<const uint32_t *>(&r);
+        s.part[0] = *reinterpret_cast<const uint32_t *>(&h);
+        s.part[1] = *reinterpret_cast<const uint32_t *>(&r);
     } else {
-        // The high part is the upper half of the next float below, so that the
-        // low part of a positive weight is positive: an infinite value times 0, or
-        // times parts of both signs, would be NaN.
+        // A part is the upper half of the next float below, so that every part of
+        // a positive weight is positive: an infinite value times 0, or times parts
+        // of both signs, would be NaN.
         constexpr float kBelow = 0x1.fffffep-1f;
-        const uint32_t ha = __float_as_uint(__fmul_rz(a, kBelow)), hb = __float_as_uint(__fmul_rz(b, kBelow));
-        high = __byte_perm(ha, hb, 0x7632);
-        low = bf16_pair(a - __uint_as_float(ha & 0xffff0000u), b - __uint_as_float(hb & 0xffff0000u));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t ha = __float_as_uint(__fmul_rz(a, kBelow)), hb = __float_as_uint(__fmul_rz(b, kBelow));
+            s.part[i] = __byte_perm(ha, hb, 0x7632);
+            a -= __uint_as_float(ha & 0xffff0000u), b -= __uint_as_float(hb & 0xffff0000u);
+        }
+        s.part[2] = bf16_pair(a, b);
     }
+    return s;
 }
 
 // Byte offset of chunk c of row r in an operand of a stage: the chunks of
@@ -633,7 +644,8 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
             }
 
             // x: tokens g (0, 1) and g + 8 (2, 3) of each block, heads 2j and 2j + 1.
-            uint32_t high[kBlocks][kNT][2], low[kBlocks][kNT][2];
+            constexpr int kParts = WeightParts<kE4m3>::kCount;
+            uint32_t weight[kBlocks][kNT][2][kParts];
 #pragma unroll
             for (int t = 0; t < kNT; ++t) {
 #pragma unroll
@@ -680,10 +692,9 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
                 for (int n = 0; n < kBlocks; ++n)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        uint32_t hi, lo;
-                        split2<kE4m3>(x[n][t][2 * i], x[n][t][2 * i + 1], hi, lo);
-                        high[n][t][i] = transpose8x8(hi);
-                        low[n][t][i] = transpose8x8(lo);
+                        const WeightParts<kE4m3> s = split<kE4m3>(x[n][t][2 * i], x[n][t][2 * i + 1]);
+#pragma unroll
+                        for (int y = 0; y < kParts; ++y) weight[n][t][i][y] = transpose8x8(s.part[y]);
                     }
             }
             if constexpr (!kE4m3) {
@@ -694,10 +705,10 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
                         uint32_t a[4];
                         ldsm_x4_t(a, vs + chunk_at<kRow>(16 * n + (lane & 7) + ((lane >> 4) << 3), 2 * d + ((lane >> 3) & 1)));
 #pragma unroll
-                        for (int t = 0; t < kNT; ++t) {
-                            mma16816<false>(o[t][d], a[0], a[1], a[2], a[3], high[n][t][0], high[n][t][1]);
-                            mma16816<false>(o[t][d], a[0], a[1], a[2], a[3], low[n][t][0], low[n][t][1]);
-                        }
+                        for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                            for (int y = 0; y < kParts; ++y)
+                                mma16816<false>(o[t][d], a[0], a[1], a[2], a[3], weight[n][t][0][y], weight[n][t][1][y]);
                     }
             } else {
                 // Transposed in pairs of elements: a lane receives elements
@@ -718,8 +729,8 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
                             const uint32_t s2 = half2_mul(a2, kHalfRestBack), s3 = half2_mul(a3, kHalfRestBack);
 #pragma unroll
                             for (int t = 0; t < kNT; ++t) {
-                                mma16816<true>(o[t][d + i], a0, a1, a2, a3, high[n][t][0], high[n][t][1]);
-                                mma16816<true>(o[t][d + i], s0, s1, s2, s3, low[n][t][0], low[n][t][1]);
+                                mma16816<true>(o[t][d + i], a0, a1, a2, a3, weight[n][t][0][0], weight[n][t][1][0]);
+                                mma16816<true>(o[t][d + i], s0, s1, s2, s3, weight[n][t][0][1], weight[n][t][1][1]);
                             }
                         }
                     }

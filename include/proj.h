@@ -592,12 +592,12 @@ proj_status_t proj_q4_destroy(proj_q4_handle_t h);
  *   n = seq_lens[b] (window 0: all n):
  *     out[b,h] = Σ_t softmax_t(scale · q[b,h]·k_t) · v_t,
  *     lse[b,h] = log Σ_t e^(scale · q[b,h]·k_t)   (lse fp32 [B, q_heads], or NULL).
- *   n = 0 gives out = 0 and lse = −∞.  Logits, weights and sums are fp32; in the
- *   product with v a weight is held to 2^-16 of itself (over e4m3: or to 2^-52 of
- *   the largest weight, whichever is more); out is bf16, rounded once.  Over
- *   e4m3, elements of q are held to 2^-40 of their head's largest, exactly down
- *   to 2^-32 of it.  An infinite value of v gives infinity where its weight is
- *   above 2^-100 of the largest (below, NaN).
+ *   n = 0 gives out = 0 and lse = −∞.  Logits, weights and sums are fp32; out is
+ *   bf16, rounded once.  Over e4m3, in the product with v a weight is held to
+ *   2^-23 of itself or 2^-52 of the largest, whichever is more, and elements of q
+ *   are held to 2^-40 of their head's largest, exactly down to 2^-32 of it.  An
+ *   infinite value of v gives infinity where its weight is above 2^-100 of the
+ *   largest (below, NaN).
  *   The sequences' tokens are dealt out evenly over the GPU and joined in a
  *   fixed order: reruns are bit-identical.
  *

@@ -408,3 +408,33 @@ def test_truth_values_that_have_none():
     with pytest.raises(ValueError, match="neither"):
         kv.append(q, q[:, :2], q[:, 2:4], lens, table, interleaved=Neither(), q_out=out)
     assert (out == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_weights_are_held_as_fp32(dtype):
+    # Two tokens of nearly equal weight and opposite values: the output is their weights' difference.
+    # Logits are at most 2⁻³ and exact but for the scale (2⁻²³ of them); the exponential's 2⁻²¹, the weights'
+    # parts 2⁻²³, three 16-token products and a sum 2⁻²² each and the division 2⁻²³ stay below 2⁻¹⁹ of Σ w|v|,
+    # which is 1.  (With 16 bits a weight: 2⁻¹⁷.)
+    import torch
+    lens, heads, kv_heads, dim = [2] * 16, 64, 8, 64
+    kv, q, table, lens_dev = case(lens, heads, kv_heads, dim, 16, dtype=dtype)
+    raw = lambda c: c.view(torch.uint8) if dtype == "e4m3" else c  # noqa: E731
+    raw(kv.k_cache).zero_()
+    plus, minus = (raw(torch.full((), x, device="cuda").to(kv.k_cache.dtype)) for x in (1.0, -1.0))
+    step = 2.0 ** -6 if dtype == "e4m3" else 2.0 ** -11
+    if dtype == "e4m3":
+        kv.k_scale.fill_(2.0 ** -5)
+        kv.v_scale.fill_(1.0)
+    for b in range(16):
+        page = table[b, 0].long()
+        keys = torch.zeros((kv_heads, dim), device="cuda")
+        keys[:, 0] = (torch.arange(kv_heads, device="cuda") + 1 + b % 8) * step
+        raw(kv.k_cache)[page, 0] = raw(keys.to(kv.k_cache.dtype))
+        raw(kv.v_cache)[page, 0], raw(kv.v_cache)[page, 1] = plus, minus
+    q.zero_()
+    q[..., 0] = (1 + torch.arange(heads, device="cuda") / 64)[None]
+    out = kv.attend(q, table, lens_dev, scale=1.0)
+    want, _, _, _ = ku.attention64(q, kv.k_cache, kv.v_cache, table, lens, 16, 1.0, 0, kv.k_scale, kv.v_scale)
+    over = ku.beyond(out, want, 2.0 ** -19)
+    assert (over <= 0).all(), f"{int((over > 0).sum())} of {out.numel()} beyond the bound, by up to {over.max().item():.3e}"
