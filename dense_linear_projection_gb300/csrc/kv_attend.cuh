@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
         if (t >= lcur.low && t < lseg.last) {
             const uint32_t q = static_cast<uint32_t>(t) / static_cast<uint32_t>(cache.page_size);
             lplace = t - static_cast<int>(q) * cache.page_size;
-            lpage = __ldg(cache.table + lcur.b * cache.table_width + q);
+            lpage = cache.table[lcur.b * cache.table_width + q];
             if (lpage < 0 || lpage >= cache.num_pages) {
                 atomicOr(p.status, kKvErrPage);
                 lpage = -1;

@@ -77,3 +77,14 @@ def test_cluster_arrivals_are_ordered():
         with open(os.path.join(csrc, name), encoding="utf-8") as f:
             arrivals += [(name, m) for m in re.findall(r"barrier\.cluster\.arrive[.\w]*", f.read())]
     assert arrivals and all(m.endswith((".release", ".arrive", ".aligned")) and "relaxed" not in m for _, m in arrivals), arrivals
+
+
+def test_no_loads_past_the_coherent_path():
+    # The kernels may be resident while the kernel before them still writes their inputs (programmatic
+    # launches): a load that takes memory for unchanging over the kernel's life is not theirs to use.
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(dlp.__file__), "csrc")
+    for name in sorted(os.listdir(csrc)):
+        with open(os.path.join(csrc, name), encoding="utf-8") as f:
+            assert not re.search(r"__ldg\(|ld\.global\.nc|__ldlu", f.read()), name
