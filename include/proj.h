@@ -512,7 +512,7 @@ proj_status_t proj_selftest_wait_timeout(int64_t limit_ns, void *stream);
  *
  *   Y[m, n] = Σ_k X[m, k] · s[n, g] · (q[n, k] − z[n, g])  (+ bias[n]),  g = ⌊k / group⌋
  *
- * q are codes 0..15, s bf16 scales (below 2^90), z zero points 0..15 (8 everywhere when
+ * q are codes 0..15, s bf16 scales, z zero points 0..15 (8 everywhere when
  * the weights have none).  q − z is exact in bf16; products and sums are fp32
  * (the scale multiplies a group's fp32 sum, so the dequantised weight itself is
  * never rounded), and Y is rounded once.  For the token counts of a decode

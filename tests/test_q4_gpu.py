@@ -242,3 +242,17 @@ def test_clusters_that_leave_and_start_back_to_back(M, N, K, group):
         ref = (X[i].double() @ W.t()).float()
         for j in range(i, 24, 4):
             assert torch.equal(out[j], ref), (i, j)
+
+
+@pytest.mark.parametrize("powers", [(100, -100), (-100, 100), (120, -60), (-120, 118), (126, -100)], ids=str)
+@pytest.mark.parametrize("M", [1, 16, 32])
+def test_scales_of_any_size(M, powers):
+    # Scales and activations far from 1 whose products are not.
+    import torch
+    import dense_linear_projection_gb300 as dlp
+    N, K, group = 70, 512, 64
+    codes, _, z = stored(N, K, group, True, 13)
+    scales = (torch.rand((N, K // group), device="cuda").double().add(0.25) * 2.0 ** powers[0]).to(torch.bfloat16)
+    proj = dlp.Q4Projection(M, N, K, group, has_zeros=True, y_dtype=dlp.PROJ_F32)
+    X = (torch.randn((M, K), device="cuda").double() * 2.0 ** powers[1]).to(torch.bfloat16)
+    check(proj(X, proj.pack(codes, scales, z)), X, dequantised(codes, scales, z, group), None, str(powers))
