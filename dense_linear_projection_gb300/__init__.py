@@ -415,7 +415,7 @@ class Projection:
     (``PROJ_W_KN``) bf16; ``bias``: [N] bf16 or None.  Returns ``Y`` [M,N] in
     ``y_dtype`` (allocated with torch unless ``out`` is given).  The handle
     belongs to the device that is current when it is made; tensors of another
-    are refused.
+    are refused.  Results carry no gradients.
     """
 
     def __init__(self, M: int, N: int, K: int, w_layout: int = PROJ_W_NK,
@@ -536,7 +536,8 @@ class Q4Projection:
     ``scales`` [N, K/group] bf16 and, with ``has_zeros``, ``zeros`` [N, K/group]
     uint8.  Packed weights run with every handle of the same N, K, group and
     ``has_zeros``.  The handle belongs to the device that is current when it is
-    made; tensors of another are refused.
+    made; tensors of another are refused.  Results carry no gradients, and an
+    ``out`` is written without autograd's notice (no version count).
     """
 
     def __init__(self, max_tokens: int, N: int, K: int, group: int = 128, has_zeros: bool = False,
@@ -604,7 +605,9 @@ class PagedKV:
     tokens in memory works as well, head_dim has to be contiguous.  With 8-bit
     elements ``k_scale``, ``v_scale`` ([kv_heads] fp32) say what one unit
     stands for.  The tensors stay the caller's; the handle, on their device, owns
-    scratch for sequences that several thread blocks share.
+    scratch for sequences that several thread blocks share.  Results carry no
+    gradients; the caches, ``out`` and ``q_out`` are written without autograd's
+    notice (no version count).
     """
 
     def __init__(self, k_cache, v_cache, q_heads: int, max_sequences: int, k_scale=None, v_scale=None, stream=None):

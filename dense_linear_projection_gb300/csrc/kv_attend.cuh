@@ -93,7 +93,9 @@ __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
 }
 
 // Two weights as 16-bit parts, each of what the parts before it leave: three of
-// bf16 (24 bits) or two of fp16 (22).
+// bf16 (24 bits) or two of fp16 (22).  Measured against two bf16 parts: one sequence
+// of 131071 tokens 92.0 us instead of 91.4, 64 ragged ones 161.8 and 162.0; against
+// fp16 parts of unscaled weights: 16 ragged sequences in 8 bits 94 instead of 92.
 template <bool kHalf>
 struct WeightParts {
     static constexpr int kCount = kHalf ? 2 : 3;

@@ -74,11 +74,15 @@ __global__ void q4_pack_scales_kernel(const uint16_t *scales, const uint8_t *zer
 // fp32 sum, and the 2^7 is taken back when the row is written.
 //
 // The product is swapped (weight rows are the 16-row operand of the warp-level
-// step, up to 8·kNT tokens its columns).  What bounds it: at up to 8 tokens the
-// stream of codes and, nearly as much, the 500 instructions that a warp spends on
-// 4 KiB of them (one token, 28672 × 8192: 20.7 us, 87 % of the copy bandwidth);
-// above that the instructions (16 tokens, 8192 × 8192: 13.9 us, of 5.4 for the
-// bytes; 31 tokens, 12300 × 4128 in groups of 32: 16.2, of 4.4).
+// step, up to 8·kNT tokens its columns).  What bounds it: at up to 8 tokens, where
+// the row count fills the SMs, the stream of codes, with 60 % of the issue slots
+// spent on 500 instructions a warp for 4 KiB of them (one token, 28672 × 8192:
+// 20.7 us, 87 % of the copy bandwidth); above that waits.  At 16 and 31 tokens 39
+// and 41 % of the issue slots and 20 and 27 % of the tensor pipe are in use: two to
+// four warps a scheduler wait for results, the math pipe, memory and one another
+// (16 tokens, 8192 × 8192: 14.2 us, of 5.4 for the bytes; 31 tokens, 12300 × 4128 in
+// groups of 32: 16.5, of 4.4), and whole tiles a CTA leave SMs idle between the row
+// counts that fill them (one token, 20480 rows take as long as 28672).
 // A warp owns 64 or 32 rows × 128 K at a time, in a ring of shared-memory stages
 // filled by 16-byte asynchronous copies.  A CTA covers one row tile × kKW K steps;
 // the CTAs of a cluster share the K range of the same rows.  Sums join in a fixed order: the
