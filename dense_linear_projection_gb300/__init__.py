@@ -34,6 +34,8 @@ __all__ = [
     "Projection",
     "proj_q4_packed_bytes", "proj_q4_create", "proj_q4_pack", "proj_q4_run", "proj_q4_destroy",
     "proj_kv_create", "proj_kv_append", "proj_kv_attend", "proj_kv_device_status", "proj_kv_destroy",
+    "proj_kv_append_normed", "proj_kv_shared_workspace", "proj_kv_attend_shared", "proj_kv_scored_workspace",
+    "proj_kv_attend_scored", "proj_kv_evict",
     "Q4Projection", "PagedKV", "rope_table",
 ]
 
@@ -54,6 +56,8 @@ EXPORTED_SYMBOLS = (
     "proj_noalloc_selftest_wait_timeout",
     "proj_q4_packed_bytes", "proj_q4_create", "proj_q4_pack", "proj_q4_run", "proj_q4_destroy",
     "proj_kv_create", "proj_kv_append", "proj_kv_attend", "proj_kv_device_status", "proj_kv_destroy",
+    "proj_kv_append_normed", "proj_kv_shared_workspace", "proj_kv_attend_shared", "proj_kv_scored_workspace",
+    "proj_kv_attend_scored", "proj_kv_evict",
 )
 
 
@@ -150,6 +154,15 @@ def lib() -> ctypes.CDLL:
     L.proj_kv_append.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, vp, vp, i64, i64, vp, i64, ctypes.c_int32, i32,
                                  vp, vp, vp, vp, vp, i64, vp]
     L.proj_kv_attend.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, ctypes.c_float, vp, i64, vp, vp]
+    L.proj_kv_append_normed.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, vp, i32, ctypes.c_float, vp, vp, vp, i64, i64, vp,
+                                        vp, i64, ctypes.c_int32, i32, vp, vp, vp, vp, vp, i64, vp]
+    L.proj_kv_shared_workspace.argtypes = [vp, i64, i64, ctypes.POINTER(ctypes.c_size_t)]
+    L.proj_kv_attend_shared.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, i64, vp, i64, vp, ctypes.c_float, vp, vp,
+                                        i64, vp, vp]
+    L.proj_kv_scored_workspace.argtypes = [vp, i64, i64, ctypes.POINTER(ctypes.c_size_t)]
+    L.proj_kv_attend_scored.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, ctypes.c_float, vp, vp, i64, vp,
+                                        vp, i64, vp, vp]
+    L.proj_kv_evict.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, i64, i64, i64, vp, vp, vp, vp, vp, vp]
     L.proj_kv_device_status.argtypes = [vp, vp]
     L.proj_kv_destroy.argtypes = [vp]
     for name in EXPORTED_SYMBOLS:
@@ -385,6 +398,54 @@ def proj_kv_attend(h: int, sequences: int, q, q_stride: int, k_cache, v_cache, k
                                 _ptr(out), out_stride, _ptr(lse), _stream(stream)), "proj_kv_attend")
 
 
+def proj_kv_append_normed(h: int, tokens: int, q, q_stride: int, k, v, kv_stride: int, q_weight, k_weight, weight_dtype: int,
+                          eps: float, positions, seq_ids, page_table, sequences: int, table_width: int, rope_rows, rope,
+                          rope_positions: int, rot_dim: int, interleaved: bool, k_scale, v_scale, k_cache, v_cache, q_out,
+                          q_out_stride: int, stream=None) -> None:
+    _check(lib().proj_kv_append_normed(h, tokens, _ptr(q), q_stride, _ptr(k), _ptr(v), kv_stride, _ptr(q_weight), _ptr(k_weight),
+                                       weight_dtype, eps, _ptr(positions), _ptr(seq_ids), _ptr(page_table), sequences,
+                                       table_width, _ptr(rope_rows), _ptr(rope), rope_positions, rot_dim,
+                                       int(bool(interleaved)), _ptr(k_scale), _ptr(v_scale), _ptr(k_cache), _ptr(v_cache),
+                                       _ptr(q_out), q_out_stride, _stream(stream)), "proj_kv_append_normed")
+
+
+def proj_kv_shared_workspace(h: int, sequences: int, prefix_len: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().proj_kv_shared_workspace(h, sequences, prefix_len, ctypes.byref(out)), "proj_kv_shared_workspace")
+    return int(out.value)
+
+
+def proj_kv_attend_shared(h: int, sequences: int, q, q_stride: int, k_cache, v_cache, k_scale, v_scale, prefix_pages,
+                          prefix_width: int, prefix_len: int, page_table, table_width: int, seq_lens, scale: float,
+                          workspace, out, out_stride: int, lse, stream=None) -> None:
+    _check(lib().proj_kv_attend_shared(h, sequences, _ptr(q), q_stride, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                                       _ptr(v_scale), _ptr(prefix_pages), prefix_width, prefix_len, _ptr(page_table),
+                                       table_width, _ptr(seq_lens), scale, _ptr(workspace), _ptr(out), out_stride, _ptr(lse),
+                                       _stream(stream)), "proj_kv_attend_shared")
+
+
+def proj_kv_scored_workspace(h: int, sequences: int, table_width: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().proj_kv_scored_workspace(h, sequences, table_width, ctypes.byref(out)), "proj_kv_scored_workspace")
+    return int(out.value)
+
+
+def proj_kv_attend_scored(h: int, sequences: int, q, q_stride: int, k_cache, v_cache, k_scale, v_scale, page_table,
+                          table_width: int, seq_lens, window: int, scale: float, scores, scores_out, score_tokens: int,
+                          workspace, out, out_stride: int, lse, stream=None) -> None:
+    _check(lib().proj_kv_attend_scored(h, sequences, _ptr(q), q_stride, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                                       _ptr(v_scale), _ptr(page_table), table_width, _ptr(seq_lens), window, scale,
+                                       _ptr(scores), _ptr(scores_out), score_tokens, _ptr(workspace), _ptr(out), out_stride,
+                                       _ptr(lse), _stream(stream)), "proj_kv_attend_scored")
+
+
+def proj_kv_evict(h: int, sequences: int, page_table, table_width: int, seq_lens, scores, score_tokens: int, to_table,
+                  to_width: int, keep: int, recent: int, k_cache, v_cache, lens_out, scores_out, kept, stream=None) -> None:
+    _check(lib().proj_kv_evict(h, sequences, _ptr(page_table), table_width, _ptr(seq_lens), _ptr(scores), score_tokens,
+                               _ptr(to_table), to_width, keep, recent, _ptr(k_cache), _ptr(v_cache), _ptr(lens_out),
+                               _ptr(scores_out), _ptr(kept), _stream(stream)), "proj_kv_evict")
+
+
 def proj_kv_device_status(h: int, stream=None) -> int:
     """Raw status (PROJ_ERR_INVALID_ARG once after a kernel met an index out of range); does not raise."""
     return int(lib().proj_kv_device_status(h, _stream(stream)))
@@ -598,7 +659,9 @@ def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device="cuda
 
 
 class PagedKV:
-    """A paged key-value cache: :meth:`append` new tokens, :meth:`attend` over it.
+    """A paged key-value cache: :meth:`append` new tokens, :meth:`attend` over it,
+    :meth:`attend_shared` behind a common prefix, :meth:`attend_scored` and
+    :meth:`evict` by score.
 
     ``k_cache``, ``v_cache``: [pages, page_size, kv_heads, head_dim] bf16 or
     float8_e4m3fn CUDA tensors of the same strides; a view with heads before
@@ -634,23 +697,29 @@ class PagedKV:
         self.q_heads, self.kv_heads, self.head_dim, self.page_size = q_heads, kv_heads, head_dim, page_size
         self._scale = head_dim ** -0.5
         self._append, self._attend = _bind().append, _bind().attend
+        self._attend_shared, self._attend_scored, self._evict = _bind().attend_shared, _bind().attend_scored, _bind().evict
         s = k_cache.stride()
         desc = KvDesc(pages, s[0], s[1], s[2], max_sequences, page_size, q_heads, kv_heads, head_dim, kv_dtype)
         with torch.cuda.device(device):
             self.handle = proj_kv_create(desc, stream)
 
     def append(self, q, k, v, positions, page_table, seq_ids=None, rope=None, interleaved: bool = False, q_out=None,
-               stream=None):
+               stream=None, q_norm=None, k_norm=None, eps: float = 1e-6, rope_rows=None):
         """Rotate ``q`` and ``k`` ([tokens, heads, head_dim] bf16, rows of any
         stride) at ``positions`` (int32 [tokens], negative: padding) and write
         ``k`` and ``v`` to the cache; returns the rotated queries (``q_out``,
         which may be ``q``; None when ``q`` is None).  ``page_table``: int32
         [sequences, pages of a sequence]; ``seq_ids``: int32 [tokens], default
         0, 1, 2, …; ``rope``: :func:`rope_table`'s form, or None for no
-        rotation."""
+        rotation.
+
+        ``q_norm``, ``k_norm`` ([head_dim] bf16 or fp32): each head of the
+        queries or keys becomes ``x · weight / sqrt(mean(x²) + eps)`` first, in
+        fp32.  ``rope_rows`` (int32 [tokens]): the rope table's row of each
+        token where that is not its position, as after :meth:`evict`."""
         return self._append(self.handle, self.q_heads, self.kv_heads, self.head_dim, self.k_cache, self.v_cache,
                             self.k_scale, self.v_scale, q, k, v, positions, page_table, seq_ids, rope, interleaved,
-                            q_out, _stream(stream))
+                            q_out, _stream(stream), q_norm, k_norm, eps, rope_rows)
 
     def attend(self, q, page_table, seq_lens, scale: Optional[float] = None, window: int = 0, out=None,
                return_lse: bool = False, stream=None):
@@ -662,6 +731,41 @@ class PagedKV:
         return self._attend(self.handle, self.q_heads, self.kv_heads, self.head_dim, self.k_cache, self.v_cache,
                             self.k_scale, self.v_scale, q, page_table, seq_lens,
                             self._scale if scale is None else scale, window, out, return_lse, _stream(stream))
+
+    def attend_shared(self, q, prefix_pages, prefix_len: int, page_table, seq_lens, scale: Optional[float] = None, out=None,
+                      return_lse: bool = False, stream=None):
+        """:meth:`attend` for a batch whose sequences all begin with the same
+        ``prefix_len`` tokens, which lie in ``prefix_pages`` (int32 [pages]) and
+        are read once for all of them; ``page_table`` and ``seq_lens`` are of
+        each sequence's own tokens after them (0: none)."""
+        return self._attend_shared(self.handle, self.q_heads, self.kv_heads, self.head_dim, self.k_cache, self.v_cache,
+                                   self.k_scale, self.v_scale, q, prefix_pages, prefix_len, page_table, seq_lens,
+                                   self._scale if scale is None else scale, out, return_lse, _stream(stream))
+
+    def attend_scored(self, q, page_table, seq_lens, scores, scale: Optional[float] = None, window: int = 0, scores_out=None,
+                      out=None, return_lse: bool = False, stream=None):
+        """:meth:`attend` that adds each token's softmax weight, summed over the
+        query heads of a key head, to ``scores`` (fp32 [sequences, kv_heads,
+        tokens of the page table or more]), in place or into ``scores_out``.
+        Returns ``(out, scores)``, and the log sums when ``return_lse``."""
+        return self._attend_scored(self.handle, self.q_heads, self.kv_heads, self.head_dim, self.k_cache, self.v_cache,
+                                   self.k_scale, self.v_scale, q, page_table, seq_lens, scores,
+                                   self._scale if scale is None else scale, window, scores_out, out, return_lse,
+                                   _stream(stream))
+
+    def evict(self, page_table, seq_lens, scores, to_table, keep: int, recent: int = 0, stream=None):
+        """Bring sequences of more than ``keep`` tokens down to ``keep``: the last
+        ``recent`` and those of the highest ``scores`` (of :meth:`attend_scored`;
+        equal ones: the earlier), chosen for each key head, in their order.  What
+        stays (all of a shorter sequence) is copied to the pages of ``to_table``
+        (int32 [sequences, pages]), none of which may be in use, and the old pages
+        are the caller's again.  Returns ``(lens, scores, kept)``: the new lengths,
+        the kept tokens' scores [sequences, kv_heads, tokens of to_table] with
+        zeros after them, and their old places [sequences, kv_heads, keep], -1
+        past the end.  Keys stay rotated as they were: new tokens go to the next
+        places, with ``rope_rows`` for their positions."""
+        return self._evict(self.handle, self.q_heads, self.kv_heads, self.head_dim, self.k_cache, self.v_cache,
+                           self.k_scale, self.v_scale, page_table, seq_lens, scores, to_table, keep, recent, _stream(stream))
 
     def status(self, stream=None) -> int:
         """What the kernels found so far on ``stream`` (by default the current

@@ -21,12 +21,13 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 SOURCES = ["proj_api.cu", "planner.cpp", "kernel_tc_lean.cu", "kernel_tc_fused.cu", "kernel_tc_pair.cu",
-           "kernel_tc_pair_fused.cu", "q4_api.cu", "kv_api.cu"]
+           "kernel_tc_pair_fused.cu", "q4_api.cu", "kv_api.cu", "kv_scored.cu", "kv_shared.cu", "kv_evict.cu"]
 HEADERS = [os.path.join(CSRC, "proj_internal.h"), os.path.join(CSRC, "proj_kernel.cuh"),
            os.path.join(CSRC, "proj_aux.cuh"), os.path.join(CSRC, "proj_launch.h"),
            os.path.join(CSRC, "proj_host.h"), os.path.join(CSRC, "proj_warp.cuh"), os.path.join(CSRC, "q4_internal.h"),
            os.path.join(CSRC, "q4_kernels.cuh"), os.path.join(CSRC, "kv_internal.h"),
-           os.path.join(CSRC, "kv_append.cuh"), os.path.join(CSRC, "kv_attend.cuh"),
+           os.path.join(CSRC, "kv_append.cuh"), os.path.join(CSRC, "kv_attend.cuh"), os.path.join(CSRC, "kv_host.cuh"),
+           os.path.join(CSRC, "kv_scored.cuh"), os.path.join(CSRC, "kv_prefix.cuh"), os.path.join(CSRC, "kv_evict.cuh"),
            os.path.join(INCLUDE, "proj.h")]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -75,6 +75,12 @@ int64_t integer(PyObject *o) {
     return v;
 }
 
+double number(PyObject *o, const char *what) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) refuse(what);
+    return v;
+}
+
 bool truth(PyObject *o, const char *what) {
     const int v = PyObject_IsTrue(o);
     if (v < 0) refuse(what);
@@ -108,6 +114,24 @@ at::Tensor fresh(PyObject *o, int64_t device, at::IntArrayRef sizes, const at::T
 }
 
 const void *data(const at::Tensor *t) { return t ? t->data_ptr() : nullptr; }
+
+// The tensor made here, or the argument that was written.
+PyObject *result(at::Tensor &made, PyObject *given) { return made.defined() ? THPVariable_Wrap(std::move(made)) : Py_NewRef(given); }
+
+// A tuple of `count` new references, which it takes; nullptr where one of them is.
+PyObject *together(PyObject **results, int count) {
+    PyObject *all = PyTuple_New(count);
+    bool ok = all != nullptr;
+    for (int i = 0; i < count; ++i) {
+        if (ok && results[i])
+            PyTuple_SET_ITEM(all, i, results[i]);
+        else
+            Py_XDECREF(results[i]), ok = false;
+    }
+    if (ok) return all;
+    Py_XDECREF(all);
+    return nullptr;
+}
 
 PyObject *init(PyObject *, PyObject *error) {
     Py_XDECREF(proj_error);
@@ -179,10 +203,10 @@ Cache cache_of(PyObject *const *a) {
     return c;
 }
 
-// append(cache.., q, k, v, positions, page_table, seq_ids, rope, interleaved, q_out, stream) -> q_out
+// append(cache.., q, k, v, positions, page_table, seq_ids, rope, interleaved, q_out, stream, q_norm, k_norm, eps, rope_rows) -> q_out
 PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t count) {
     return guarded([&]() -> PyObject * {
-        if (count != 18) refuse("append: eighteen arguments");
+        if (count != 22) refuse("append: twenty-two arguments");
         const Cache c = cache_of(a);
         const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(c.device));
         const at::Tensor *q = tensor(a[8], "q: a tensor");
@@ -202,6 +226,16 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t count) {
             refuse("rope: contiguous fp32 [positions, rot_dim], on the cache's device");
         const int interleaved = truth(a[15], "interleaved: a truth value");
         const at::Tensor *q_out = tensor(a[16], "q_out: a tensor");
+        const at::Tensor *norms[2] = {tensor(a[18], "q_norm: a tensor"), tensor(a[19], "k_norm: a tensor")};
+        const at::Tensor *rope_rows = tensor(a[21], "rope_rows: a tensor");
+        const double eps = number(a[20], "eps: a number");
+        for (const at::Tensor *w : norms)
+            if (w && ((!is(*w, at::kBFloat16, c.device, 1) && !is(*w, at::kFloat, c.device, 1)) || w->size(0) != c.dim || !w->is_contiguous()))
+                refuse("q_norm, k_norm: contiguous bf16 or fp32 [head_dim], on the cache's device");
+        if (norms[0] && norms[1] && norms[0]->scalar_type() != norms[1]->scalar_type()) refuse("q_norm, k_norm: of one type");
+        if (norms[0] && !q) refuse("q_norm: only with q");
+        if (rope_rows && (!rope || !ints(*rope_rows, c.device, 1) || rope_rows->size(0) != tokens))
+            refuse("rope_rows: contiguous int32 [tokens], on the cache's device, with a rope table");
         at::Tensor made;
         int64_t q_stride = 0, q_out_stride = 0;
         if (q) {
@@ -214,6 +248,20 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t count) {
             q_out_stride = rows(*q_out, tokens, c.q_heads, c.dim, c.device, "q_out: as q");
         } else if (q_out) {
             refuse("q_out: only with q");
+        }
+        if (norms[0] || norms[1] || rope_rows) {
+            const at::Tensor *w = norms[0] ? norms[0] : norms[1];
+            check(proj_kv_append_normed(
+                      c.h, tokens, data(q), q_stride, k.data_ptr(), v.data_ptr(), kv_stride, data(norms[0]), data(norms[1]),
+                      w && w->scalar_type() == at::kFloat ? PROJ_F32 : PROJ_BF16, static_cast<float>(eps),
+                      static_cast<const int32_t *>(positions.data_ptr()), static_cast<const int32_t *>(data(seq)),
+                      static_cast<const int32_t *>(table.data_ptr()), table.size(0), table.size(1),
+                      static_cast<const int32_t *>(data(rope_rows)), static_cast<const float *>(data(rope)), rope ? rope->size(0) : 0,
+                      rope ? static_cast<int32_t>(rope->size(1)) : 0, interleaved, static_cast<const float *>(data(c.k_scale)),
+                      static_cast<const float *>(data(c.v_scale)), c.k->data_ptr(), c.v->data_ptr(),
+                      q_out ? q_out->data_ptr() : nullptr, q_out_stride, stream_of(a[17], c.device)),
+                  "proj_kv_append_normed");
+            return made.defined() ? THPVariable_Wrap(std::move(made)) : Py_NewRef(a[16]);
         }
         check(proj_kv_append(c.h, tokens, data(q), q_stride, k.data_ptr(), v.data_ptr(), kv_stride,
                              static_cast<const int32_t *>(positions.data_ptr()), static_cast<const int32_t *>(data(seq)),
@@ -241,8 +289,7 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t count) {
         if (!ints(table, c.device, 2) || table.size(0) != n)
             refuse("page_table: contiguous int32 [sequences, pages], on the cache's device");
         if (!ints(lens, c.device, 1) || lens.size(0) != n) refuse("seq_lens: contiguous int32 [sequences], on the cache's device");
-        const double scale = PyFloat_AsDouble(a[11]);
-        if (scale == -1.0 && PyErr_Occurred()) refuse("scale: a number");
+        const double scale = number(a[11], "scale: a number");
         const int64_t window = integer(a[12]);
         at::Tensor made, lse;
         const at::Tensor *out = tensor(a[13], "out: a tensor");
@@ -259,17 +306,144 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t count) {
                              static_cast<const int32_t *>(lens.data_ptr()), window, static_cast<float>(scale), out->data_ptr(),
                              out_stride, with_lse ? static_cast<float *>(lse.data_ptr()) : nullptr, stream_of(a[15], c.device)),
               "proj_kv_attend");
-        PyObject *first = made.defined() ? THPVariable_Wrap(std::move(made)) : Py_NewRef(a[13]);
-        if (!with_lse || !first) return first;
-        PyObject *second = THPVariable_Wrap(std::move(lse));
-        if (!second) {
-            Py_DECREF(first);
-            return nullptr;
+        PyObject *results[2] = {result(made, a[13]), with_lse ? THPVariable_Wrap(std::move(lse)) : nullptr};
+        return with_lse ? together(results, 2) : results[0];
+    });
+}
+
+// The queries, lengths and outputs that the two forms of attention below share with attend.
+struct Attention {
+    const at::Tensor *q, *table, *lens;
+    int64_t n, q_stride, out_stride;
+    float scale;
+    at::Tensor made, lse;  // where they are made here
+    const at::Tensor *out;
+    bool with_lse;
+    float *lse_ptr() { return with_lse ? static_cast<float *>(lse.data_ptr()) : nullptr; }
+};
+Attention attention_of(const Cache &c, PyObject *q, PyObject *table, PyObject *lens, PyObject *scale, PyObject *out, PyObject *return_lse,
+                       PyObject *stream) {
+    Attention x;
+    x.q = &needed(q, "q: a tensor");
+    x.n = x.q->dim() > 0 ? x.q->size(0) : 0;
+    x.q_stride = rows(*x.q, x.n, c.q_heads, c.dim, c.device,
+                      "q: bf16 [sequences, q_heads, head_dim] with contiguous heads, on the cache's device");
+    x.table = &needed(table, "page_table: a tensor");
+    x.lens = &needed(lens, "seq_lens: a tensor");
+    if (!ints(*x.table, c.device, 2) || x.table->size(0) != x.n)
+        refuse("page_table: contiguous int32 [sequences, pages], on the cache's device");
+    if (!ints(*x.lens, c.device, 1) || x.lens->size(0) != x.n) refuse("seq_lens: contiguous int32 [sequences], on the cache's device");
+    x.scale = static_cast<float>(number(scale, "scale: a number"));
+    x.out = tensor(out, "out: a tensor");
+    x.out_stride = x.out ? rows(*x.out, x.n, c.q_heads, c.dim, c.device, "out: as q") : c.q_heads * c.dim;
+    x.with_lse = truth(return_lse, "return_lse: a truth value");
+    if (!x.out) x.made = fresh(stream, c.device, {x.n, c.q_heads, c.dim}, x.q->options());
+    if (x.with_lse) x.lse = fresh(stream, c.device, {x.n, c.q_heads}, x.q->options().dtype(at::kFloat));
+    return x;
+}
+at::Tensor workspace_of(PyObject *stream, const Cache &c, size_t bytes, const at::Tensor &like) {
+    return fresh(stream, c.device, {static_cast<int64_t>(bytes)}, like.options().dtype(at::kByte));
+}
+
+// attend_shared(cache.., q, prefix_pages, prefix_len, page_table, seq_lens, scale, out, return_lse, stream) -> out or (out, lse)
+PyObject *attend_shared(PyObject *, PyObject *const *a, Py_ssize_t count) {
+    return guarded([&]() -> PyObject * {
+        if (count != 17) refuse("attend_shared: seventeen arguments");
+        const Cache c = cache_of(a);
+        const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(c.device));
+        const at::Tensor &prefix = needed(a[9], "prefix_pages: a tensor");
+        if (!ints(prefix, c.device, 1)) refuse("prefix_pages: contiguous int32 [pages], on the cache's device");
+        const int64_t prefix_len = integer(a[10]);
+        Attention x = attention_of(c, a[8], a[11], a[12], a[13], a[14], a[15], a[16]);
+        const at::Tensor &out = x.out ? *x.out : x.made;
+        size_t bytes = 0;
+        check(proj_kv_shared_workspace(c.h, x.n, prefix_len, &bytes), "proj_kv_shared_workspace");
+        const at::Tensor workspace = workspace_of(a[16], c, bytes, *x.q);
+        check(proj_kv_attend_shared(c.h, x.n, x.q->data_ptr(), x.q_stride, c.k->data_ptr(), c.v->data_ptr(),
+                                    static_cast<const float *>(data(c.k_scale)), static_cast<const float *>(data(c.v_scale)),
+                                    static_cast<const int32_t *>(prefix.data_ptr()), prefix.size(0), prefix_len,
+                                    static_cast<const int32_t *>(x.table->data_ptr()), x.table->size(1),
+                                    static_cast<const int32_t *>(x.lens->data_ptr()), x.scale, workspace.data_ptr(), out.data_ptr(),
+                                    x.out_stride, x.lse_ptr(), stream_of(a[16], c.device)),
+              "proj_kv_attend_shared");
+        PyObject *results[2] = {result(x.made, a[14]), x.with_lse ? THPVariable_Wrap(std::move(x.lse)) : nullptr};
+        return x.with_lse ? together(results, 2) : results[0];
+    });
+}
+
+// fp32 [sequences, kv_heads, tokens] with room for every token of the page table.
+void scores_fit(const at::Tensor &s, const Cache &c, int64_t n, int64_t tokens, const char *what) {
+    if (!is(s, at::kFloat, c.device, 3) || s.size(0) != n || s.size(1) != c.kv_heads || s.size(2) < tokens || !s.is_contiguous()) refuse(what);
+}
+
+// attend_scored(cache.., q, page_table, seq_lens, scores, scale, window, scores_out, out, return_lse, stream)
+//   -> (out, scores_out) or (out, scores_out, lse)
+PyObject *attend_scored(PyObject *, PyObject *const *a, Py_ssize_t count) {
+    return guarded([&]() -> PyObject * {
+        if (count != 18) refuse("attend_scored: eighteen arguments");
+        const Cache c = cache_of(a);
+        const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(c.device));
+        Attention x = attention_of(c, a[8], a[9], a[10], a[12], a[15], a[16], a[17]);
+        const at::Tensor &out = x.out ? *x.out : x.made;
+        const char *shape = "scores, scores_out: contiguous fp32 [sequences, kv_heads, tokens of the page table or more], of one shape, "
+                            "on the cache's device, one tensor or apart";
+        const at::Tensor &scores = needed(a[11], "scores: a tensor");
+        const int64_t tokens = x.table->size(1) * c.k->size(1);
+        scores_fit(scores, c, x.n, tokens, shape);
+        const at::Tensor *to = tensor(a[14], "scores_out: a tensor");
+        if (to) {
+            scores_fit(*to, c, x.n, tokens, shape);
+            const char *p0 = static_cast<const char *>(scores.data_ptr()), *p1 = static_cast<const char *>(to->data_ptr());
+            const int64_t bytes = scores.numel() * 4;
+            if (to->size(2) != scores.size(2) || (p0 != p1 && p0 < p1 + bytes && p1 < p0 + bytes)) refuse(shape);
         }
-        PyObject *both = PyTuple_Pack(2, first, second);
-        Py_DECREF(first);
-        Py_DECREF(second);
-        return both;
+        const int64_t window = integer(a[13]);
+        size_t bytes = 0;
+        check(proj_kv_scored_workspace(c.h, x.n, x.table->size(1), &bytes), "proj_kv_scored_workspace");
+        const at::Tensor workspace = workspace_of(a[17], c, bytes, *x.q);
+        check(proj_kv_attend_scored(c.h, x.n, x.q->data_ptr(), x.q_stride, c.k->data_ptr(), c.v->data_ptr(),
+                                    static_cast<const float *>(data(c.k_scale)), static_cast<const float *>(data(c.v_scale)),
+                                    static_cast<const int32_t *>(x.table->data_ptr()), x.table->size(1),
+                                    static_cast<const int32_t *>(x.lens->data_ptr()), window, x.scale,
+                                    static_cast<const float *>(scores.data_ptr()),
+                                    static_cast<float *>(to ? to->data_ptr() : scores.data_ptr()), scores.size(2), workspace.data_ptr(),
+                                    out.data_ptr(), x.out_stride, x.lse_ptr(), stream_of(a[17], c.device)),
+              "proj_kv_attend_scored");
+        PyObject *results[3] = {result(x.made, a[15]), Py_NewRef(to ? a[14] : a[11]),
+                                x.with_lse ? THPVariable_Wrap(std::move(x.lse)) : nullptr};
+        return together(results, x.with_lse ? 3 : 2);
+    });
+}
+
+// evict(cache.., page_table, seq_lens, scores, to_table, keep, recent, stream) -> (lens, scores, kept)
+PyObject *evict(PyObject *, PyObject *const *a, Py_ssize_t count) {
+    return guarded([&]() -> PyObject * {
+        if (count != 15) refuse("evict: fifteen arguments");
+        const Cache c = cache_of(a);
+        const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(c.device));
+        const at::Tensor &table = needed(a[8], "page_table: a tensor"), &lens = needed(a[9], "seq_lens: a tensor");
+        if (!ints(table, c.device, 2)) refuse("page_table: contiguous int32 [sequences, pages], on the cache's device");
+        const int64_t n = table.size(0), page = c.k->size(1);
+        if (!ints(lens, c.device, 1) || lens.size(0) != n) refuse("seq_lens: contiguous int32 [sequences], on the cache's device");
+        const at::Tensor &scores = needed(a[10], "scores: a tensor"), &to = needed(a[11], "to_table: a tensor");
+        scores_fit(scores, c, n, table.size(1) * page,
+                   "scores: contiguous fp32 [sequences, kv_heads, tokens of the page table or more], on the cache's device");
+        if (!ints(to, c.device, 2) || to.size(0) != n) refuse("to_table: contiguous int32 [sequences, pages], on the cache's device");
+        const int64_t keep = integer(a[12]), recent = integer(a[13]);
+        if (keep < 0 || recent < 0 || recent > keep || keep > to.size(1) * page)
+            refuse("keep, recent: 0 <= recent <= keep, and no more than to_table has room for");
+        at::Tensor lens_out = fresh(a[14], c.device, {n}, lens.options());
+        at::Tensor scores_out = fresh(a[14], c.device, {n, c.kv_heads, to.size(1) * page}, scores.options());
+        at::Tensor kept = fresh(a[14], c.device, {n, c.kv_heads, keep}, lens.options());
+        check(proj_kv_evict(c.h, n, static_cast<const int32_t *>(table.data_ptr()), table.size(1),
+                            static_cast<const int32_t *>(lens.data_ptr()), static_cast<const float *>(scores.data_ptr()), scores.size(2),
+                            static_cast<const int32_t *>(to.data_ptr()), to.size(1), keep, recent, c.k->data_ptr(), c.v->data_ptr(),
+                            static_cast<int32_t *>(lens_out.data_ptr()), static_cast<float *>(scores_out.data_ptr()),
+                            static_cast<int32_t *>(kept.data_ptr()), stream_of(a[14], c.device)),
+              "proj_kv_evict");
+        PyObject *results[3] = {THPVariable_Wrap(std::move(lens_out)), THPVariable_Wrap(std::move(scores_out)),
+                                THPVariable_Wrap(std::move(kept))};
+        return together(results, 3);
     });
 }
 
@@ -278,6 +452,11 @@ PyMethodDef methods[] = {
     {"q4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(q4)), METH_FASTCALL, "a 4-bit projection"},
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append)), METH_FASTCALL, "append to a paged cache"},
     {"attend", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attend)), METH_FASTCALL, "attention over a paged cache"},
+    {"attend_shared", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attend_shared)), METH_FASTCALL,
+     "attention over a shared prefix and a paged cache"},
+    {"attend_scored", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attend_scored)), METH_FASTCALL,
+     "attention over a paged cache that adds up weights"},
+    {"evict", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(evict)), METH_FASTCALL, "eviction from a paged cache"},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", "Native calls with PyTorch tensors.", -1, methods,

@@ -177,5 +177,197 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const KvAppen
     }
 }
 
+// Append with the norm of each head of q and k before the rotation, and a rotary
+// row of the token's own:
+//   y = x · w / sqrt(Σ x² / head_dim + eps),  then rotated at rope[rope_rows[token]].
+// The squares are summed in fp32 by the lanes that hold a head's units (a power of
+// two of them, idle ones past the last unit), so a head is read once and meets in
+// log2(lanes) shuffles; bytes bound it as they bound the append alone.
+// The norm of one head: Σ x² below 2^120, and above 2^-90 where eps is too small to
+// hide what squares below 2^-126 lose, is taken as it is; else the head is scaled by
+// a power of two of its largest element first, so that every bf16 head has its norm.
+struct HeadNorm {
+    float pre, by;  // y = (x · pre) · by · w
+};
+__device__ __forceinline__ float group_sum(float x, int lanes, uint32_t mask) {
+    for (int o = lanes / 2; o > 0; o >>= 1) x += __shfl_xor_sync(mask, x, o);
+    return x;
+}
+__device__ __forceinline__ HeadNorm head_norm(const float *a, const float *b, int head_dim, float eps, int lanes, uint32_t mask) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum = __fmaf_rn(a[i], a[i], __fmaf_rn(b[i], b[i], sum));
+    sum = group_sum(sum, lanes, mask);
+    const float dim = static_cast<float>(head_dim);
+    if (sum < 0x1p120f && (sum >= 0x1p-90f || eps >= 0x1p-60f)) return {1.f, 1.f / sqrtf(sum / dim + eps)};
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(fabsf(a[i]), fabsf(b[i])));
+    for (int o = lanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, o));
+    // 2^-e, e the exponent of the largest element, within ±126 (zeros and subnormals: -126).
+    const int e = min(126, max(-126, static_cast<int>(__float_as_uint(top) >> 23) - 127));
+    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = a[i] * down, y = b[i] * down;
+        sum = __fmaf_rn(x, x, __fmaf_rn(y, y, sum));
+    }
+    sum = group_sum(sum, lanes, mask) / dim;
+    const float root = sqrtf(eps) * down;  // its square may be out of range, and then is all there is
+    return {down, 1.f / (root > 0x1p60f ? root : sqrtf(__fmaf_rn(root, root, sum)))};
+}
+
+__device__ __forceinline__ float norm_weight(const void *w, int32_t f32, int at) {
+    return f32 ? static_cast<const float *>(w)[at] : bf16_bits_to_float(static_cast<const uint16_t *>(w)[at]);
+}
+
+// lanes: threads of a head, the power of two at or above its units (32 at most).
+template <bool kE4m3, bool kInterleaved, bool kVec>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_norm_kernel(const KvAppendParams p, const int lanes) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const KvCacheView &c = p.cache;
+    const int64_t token = blockIdx.x;
+    const int half = p.rot_dim / 2;
+    const int pair_units = (half + 7) / 8, units = pair_units + (c.head_dim - p.rot_dim + 15) / 16;
+    const int slots = kAppendThreads / lanes;
+    const int unit = threadIdx.x & (lanes - 1), slot = threadIdx.x / lanes;
+    // The lanes of this head: every branch around a shuffle is theirs together.
+    const uint32_t mask = lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1u) << (threadIdx.x & 31 & ~(lanes - 1));
+    const int heads = p.q_heads + 2 * c.kv_heads, stride = slots * gridDim.y;
+    const int first = slot + blockIdx.y * slots;
+    if (first >= heads) return;
+
+    const bool rotary = unit < pair_units;
+    const int j0 = 8 * unit;                              // first rotary pair
+    const int d0 = p.rot_dim + 16 * (unit - pair_units);  // first copied element
+    const int r0 = !rotary ? d0 : kInterleaved ? 2 * j0 : j0;  // first elements of the unit's two runs of eight
+    const int r1 = rotary && !kInterleaved ? half + j0 : r0 + 8;
+    // Pairs of this unit, and the elements of pair x.
+    const int pairs = unit >= units ? 0 : min(8, rotary ? half - j0 : (c.head_dim - d0) / 2);
+    auto e0 = [&](int x) { return !rotary ? d0 + 2 * x : kInterleaved ? 2 * (j0 + x) : j0 + x; };
+    auto e1 = [&](int x) { return rotary && !kInterleaved ? half + j0 + x : e0(x) + 1; };
+
+    auto source = [&](int h) {
+        const bool is_q = h < p.q_heads, is_v = h >= p.q_heads + c.kv_heads;
+        const int head = is_q ? h : h - p.q_heads - (is_v ? c.kv_heads : 0);
+        return (is_q ? p.q + token * p.q_stride : (is_v ? p.v : p.k) + token * p.kv_stride) + static_cast<int64_t>(head) * c.head_dim;
+    };
+    // The first head's elements and the weights are asked for beside the position.
+    uint4 ahead[2] = {};
+    auto ask = [&](int h) {
+        if constexpr (kVec)
+            if (pairs > 0) {
+                const uint16_t *from = source(h);
+                ahead[0] = *reinterpret_cast<const uint4 *>(from + r0);
+                ahead[1] = *reinterpret_cast<const uint4 *>(from + r1);
+            }
+    };
+    ask(first);
+    // Elements (a[x], b[x]) of a pair; with kVec the unit's two runs of eight.
+    auto at_a = [&](int x) { return kVec ? r0 + x : e0(x); };
+    auto at_b = [&](int x) { return kVec ? r1 + x : e1(x); };
+    float qa[8], qb[8], ka[8], kb[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+        const bool in = x < pairs;
+        qa[x] = in && p.q_weight ? norm_weight(p.q_weight, p.weight_f32, at_a(x)) : 0.f;
+        qb[x] = in && p.q_weight ? norm_weight(p.q_weight, p.weight_f32, at_b(x)) : 0.f;
+        ka[x] = in && p.k_weight ? norm_weight(p.k_weight, p.weight_f32, at_a(x)) : 0.f;
+        kb[x] = in && p.k_weight ? norm_weight(p.k_weight, p.weight_f32, at_b(x)) : 0.f;
+    }
+
+    const int64_t pos = p.positions[token];
+    if (pos < 0) return;
+    const int64_t seq = p.seq_ids ? p.seq_ids[token] : token;
+    const int64_t row = p.rope_rows ? p.rope_rows[token] : pos;
+    int bad = 0;
+    if (pos >= c.table_width * c.page_size) bad |= kKvErrPosition;
+    if (p.rope && (row < 0 || row >= p.rope_positions)) bad |= kKvErrRopeRow;
+    if (seq < 0 || seq >= p.sequences) bad |= kKvErrSequence;
+    int64_t page = 0;
+    if (!(bad & (kKvErrPosition | kKvErrSequence))) {
+        page = c.table[seq * c.table_width + pos / c.page_size];
+        if (page < 0 || page >= c.num_pages) bad |= kKvErrPage;
+    }
+    if (bad) {
+        if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.status, bad);
+        return;
+    }
+    float cos[8], sin[8];
+    if (rotary) {
+        const float *r = p.rope + row * p.rot_dim;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            cos[i] = j0 + i < half ? r[j0 + i] : 1.f;
+            sin[i] = j0 + i < half ? r[half + j0 + i] : 0.f;
+        }
+    }
+    const int64_t place = page * c.page_stride + (pos % c.page_size) * c.token_stride;
+    for (int h = first; h < heads; h += stride) {
+        if (h != first) ask(h);
+        const bool is_q = h < p.q_heads, is_v = h >= p.q_heads + c.kv_heads;
+        const int head = is_q ? h : h - p.q_heads - (is_v ? c.kv_heads : 0);
+        void *to = is_q ? p.q_out : is_v ? p.v_cache : p.k_cache;
+        const int64_t at = is_q ? token * p.q_out_stride + static_cast<int64_t>(head) * c.head_dim : place + head * c.head_stride;
+        const float *scales = is_v ? p.v_scale : p.k_scale;
+        const float scale = kE4m3 && !is_q && scales ? scales[head] : 1.f;
+        float a[8], b[8];
+        if constexpr (kVec) {
+            unpack8(ahead[0], a);
+            unpack8(ahead[1], b);
+        } else {
+            const uint16_t *from = source(h);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                a[x] = x < pairs ? bf16_bits_to_float(from[e0(x)]) : 0.f;
+                b[x] = x < pairs ? bf16_bits_to_float(from[e1(x)]) : 0.f;
+            }
+        }
+        if (is_q ? p.q_weight != nullptr : !is_v && p.k_weight != nullptr) {
+            const HeadNorm n = head_norm(a, b, c.head_dim, p.eps, lanes, mask);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                a[x] = a[x] * n.pre * n.by * (is_q ? qa[x] : ka[x]);
+                b[x] = b[x] * n.pre * n.by * (is_q ? qb[x] : kb[x]);
+            }
+        }
+        if (pairs == 0) continue;
+        if (rotary && !is_v) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                if constexpr (kVec && kInterleaved) {
+                    float *y = x < 4 ? a + 2 * x : b + 2 * (x - 4);
+                    rotate(y[0], y[1], cos[x], sin[x]);
+                } else {
+                    rotate(a[x], b[x], cos[x], sin[x]);
+                }
+            }
+        }
+        if constexpr (kVec) {
+            if (is_q) {
+                store8<false>(to, at + r0, a, 1.f);
+                store8<false>(to, at + r1, b, 1.f);
+            } else {
+                store8<kE4m3>(to, at + r0, a, scale);
+                store8<kE4m3>(to, at + r1, b, scale);
+            }
+        } else {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                if (x >= pairs) break;
+                if (is_q) {
+                    store1<false>(to, at + e0(x), a[x], 1.f);
+                    store1<false>(to, at + e1(x), b[x], 1.f);
+                } else {
+                    store1<kE4m3>(to, at + e0(x), a[x], scale);
+                    store1<kE4m3>(to, at + e1(x), b[x], scale);
+                }
+            }
+        }
+    }
+}
+
 }  // namespace dev
 }  // namespace projgb

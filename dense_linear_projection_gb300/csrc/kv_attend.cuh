@@ -356,7 +356,7 @@ __device__ __forceinline__ bool leave_part(float *partials, int64_t at, uint32_t
     return last;
 }
 
-template <bool kE4m3, int kDim, int kNT, int kKeyHeads>
+template <bool kE4m3, int kDim, int kNT, int kKeyHeads, int kLeaves = kAttendPlain>
 __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKeyHeads>::kPerSm) kv_attend_kernel(KvAttendParams p) {
     using Shape = AttendShape<kE4m3, kDim, kNT, kKeyHeads>;
     constexpr int kHeads = Shape::kHeads, kStages = Shape::kStages, kRow = Shape::kRow;
@@ -501,7 +501,11 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
         AttendCursor c;
         read_length<Shape>(p, b, c);
         if (c.n > 0) continue;
-        for (int i = tid; i < p.q_heads * cache.head_dim; i += kKvThreads) p.out[b * p.out_stride + i] = 0;
+        if constexpr (kLeaves != kAttendPart)
+            for (int i = tid; i < p.q_heads * cache.head_dim; i += kKvThreads) p.out[b * p.out_stride + i] = 0;
+        if constexpr (kLeaves != kAttendPlain)  // (the output of a part without weight is not read)
+            for (int h = tid; h < p.q_heads; h += kKvThreads)
+                p.top[static_cast<int64_t>(b) * p.q_heads + h] = make_float2(-INFINITY, 0.f);
         if (p.lse)
             for (int h = tid; h < p.q_heads; h += kKvThreads) p.lse[static_cast<int64_t>(b) * p.q_heads + h] = -INFINITY;
     }
@@ -546,7 +550,7 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
         const int heads = kKeyHeads * min(p.chunk_heads, p.group - chunk * p.chunk_heads);  // of the row
         const int row_b = cur.b;
         const int64_t row_tiles = cur.tiles, seg_tiles = seg.tiles, row_begin = seg.row_begin;
-        const int seg_unit = seg.unit;
+        const int seg_unit = seg.unit, seg_last = seg.last;
 
         uint32_t qf[kNT][kSteps][2];
         float factor[kNT][2];  // logit to exponent of two, of this lane's heads 2j, 2j + 1
@@ -660,6 +664,28 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             if (!((bits >> (16 * n + g + 8 * (i >> 1))) & 1u)) x[n][t][i] = -INFINITY;
+                }
+                if constexpr (kLeaves == kAttendLogits) {
+                    // The row's tokens tok .. of this segment, as the next kernel reads them: the
+                    // heads of a token side by side (8 tokens of 8 heads, 256 bytes, a store).
+                    const int key = key_head(seg_unit, row_key), head = chunk * p.chunk_heads + 8 * t + 2 * j;
+                    const int there = min(p.chunk_heads, p.group - chunk * p.chunk_heads) - (8 * t + 2 * j);
+                    float *to = p.logits + ((row_b * static_cast<int64_t>(cache.kv_heads) + key) * cache.table_width * cache.page_size + tok) * p.group + head;
+                    const bool pairs = ((p.group | p.chunk_heads) & 1) == 0;
+#pragma unroll
+                    for (int n = 0; n < kBlocks; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int at = 16 * n + g + 8 * i;
+                            if (tok + at >= seg_last || there <= 0) continue;
+                            float *y = to + static_cast<int64_t>(at) * p.group;
+                            if (pairs) {
+                                *reinterpret_cast<float2 *>(y) = make_float2(x[n][t][2 * i], x[n][t][2 * i + 1]);
+                            } else {
+                                y[0] = x[n][t][2 * i];
+                                if (there > 1) y[1] = x[n][t][2 * i + 1];
+                            }
+                        }
                 }
                 float keep[2];
 #pragma unroll
@@ -840,12 +866,18 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
                 const int64_t head = static_cast<int64_t>(key) * p.group + chunk * p.chunk_heads + h / kKeyHeads;
                 const float by = kE4m3 ? (p.v_scale ? p.v_scale[key] : 1.f) * kHalfWeightBack : 1.f;
                 const float inv = r.l[k] == 0.f ? 0.f : by / r.l[k];  // (a NaN stays one)
-                if (d0 < cache.head_dim)
+                const int64_t row = static_cast<int64_t>(row_b) * p.q_heads + head;
+                if constexpr (kLeaves == kAttendPart) {
+                    if (d0 < cache.head_dim)
+                        *reinterpret_cast<float4 *>(p.out32 + row * cache.head_dim + d0) =
+                            make_float4(r.o[k].x * inv, r.o[k].y * inv, r.o[k].z * inv, r.o[k].w * inv);
+                } else if (d0 < cache.head_dim)
                     *reinterpret_cast<uint2 *>(p.out + row_b * p.out_stride + head * cache.head_dim + d0) =
                         make_uint2(bf16_pair(r.o[k].x * inv, r.o[k].y * inv), bf16_pair(r.o[k].z * inv, r.o[k].w * inv));
+                if (kLeaves != kAttendPlain && d0 == 0)
+                    p.top[row] = make_float2(r.m[k], kLeaves == kAttendPart ? r.l[k] : r.l[k] == 0.f ? 0.f : 1.f / r.l[k]);
                 if (p.lse && d0 == 0)
-                    p.lse[static_cast<int64_t>(row_b) * p.q_heads + head] =
-                        r.l[k] == 0.f ? -INFINITY : (r.m[k] + log2f(r.l[k])) * 0.6931471805599453f;
+                    p.lse[row] = r.l[k] == 0.f ? -INFINITY : (r.m[k] + log2f(r.l[k])) * 0.6931471805599453f;
             }
         }
         __syncthreads();  // the join buffer is free again

@@ -25,6 +25,10 @@ constexpr int kKvErrPosition = 1 << 0;  // position past the page table or the r
 constexpr int kKvErrSequence = 1 << 1;  // sequence id outside the page table
 constexpr int kKvErrPage = 1 << 2;      // page outside the cache
 constexpr int kKvErrLength = 1 << 3;    // length below zero or past the page table
+constexpr int kKvErrRopeRow = 1 << 4;   // row outside the rope table
+constexpr int kKvErrWait = 1 << 5;      // a bounded wait of the prefix kernel ran out
+
+constexpr int kEvictMostBlocks = 32;  // of the eviction's copy, for each SM
 
 // Where a sequence's tokens lie; strides in elements.
 struct KvCacheView {
@@ -43,6 +47,10 @@ struct KvAppendParams {
     const uint16_t *q, *k, *v;
     int64_t q_stride, kv_stride, q_out_stride;
     const int32_t *positions, *seq_ids;
+    const int32_t *rope_rows;  // the rope table's row of each token, or NULL: its position
+    const void *q_weight, *k_weight;  // of the norms: bf16 or fp32 [head_dim], NULL: no norm
+    int32_t weight_f32;
+    float eps;
     const float *rope;
     int32_t q_heads;  // 0: keys and values only
     int32_t rot_dim;
@@ -73,6 +81,65 @@ struct KvAttendParams {
     uint16_t *out;
     float *lse;
     int *status;
+    // Scored attention and the own part of shared-prefix attention (kAttendLogits, kAttendPart):
+    float *logits;   // [sequence][kv head][token][query head of it], in units of log 2
+    float2 *top;     // [sequence][query head]: maximum of the logits; with logits 1 / Σ 2^(x − maximum), else the sum
+    float *out32;    // [sequence][query head][head_dim]: the output before rounding
+};
+
+// What an attention kernel leaves beside, or instead of, the rounded output.
+constexpr int kAttendPlain = 0;   // the output
+constexpr int kAttendLogits = 1;  // the output, every logit, and each row's maximum and sum
+constexpr int kAttendPart = 2;    // the unrounded output, and each row's maximum and sum
+
+struct KvScoreParams {
+    const float *logits;
+    const float2 *top;
+    const float *scores;
+    float *scores_out;
+    const int32_t *seq_lens;
+    int64_t sequences, table_tokens, score_tokens, window;
+    int32_t kv_heads, group;
+};
+
+struct KvEvictParams {
+    KvCacheView cache;  // with the sequences' present table
+    const int32_t *to_table;
+    int64_t to_width, sequences, score_tokens, keep, recent;
+    const int32_t *seq_lens;
+    const float *scores;
+    float *scores_out;  // [sequence][kv head][to_width · page_size]
+    int32_t *lens_out, *kept;
+    void *k_cache, *v_cache;
+    int32_t elem;  // bytes of a cache element
+    int *status;
+};
+
+// Shared-prefix attention: see kv_prefix.cuh.
+struct KvPrefixParams {
+    KvCacheView cache;  // its table: the prefix's pages, of which table_width are given
+    int64_t sequences, prefix;
+    const uint16_t *q;
+    int64_t q_stride;
+    const void *k_cache, *v_cache;
+    const float *k_scale, *v_scale;
+    float scale;
+    int32_t group;
+    int64_t row_tiles, tiles;  // of a key head's rows; of the prefix's tokens
+    float *partials;           // [unit + CTA][maxima, sums of either half, values]
+    int *status;
+};
+
+struct KvCombineParams {
+    const float *partials;
+    const float2 *top;   // the own tokens' part
+    const float *out32;
+    int64_t sequences, row_tiles, tiles;
+    int32_t ctas;        // of the prefix kernel
+    int32_t kv_heads, group, head_dim;
+    uint16_t *out;
+    int64_t out_stride;
+    float *lse;
 };
 
 }  // namespace projgb

@@ -638,6 +638,76 @@ proj_status_t proj_kv_attend(proj_kv_handle_t h, int64_t sequences, const void *
 proj_status_t proj_kv_device_status(proj_kv_handle_t h, void *stream);
 proj_status_t proj_kv_destroy(proj_kv_handle_t h);
 
+/*
+ * More on the same cache.  What proj_kv_append and proj_kv_attend say of layouts,
+ * alignment, streams, devices, captures and of what only the device sees holds here.
+ *
+ * proj_kv_append_normed: proj_kv_append with the norm of every head of q and k first,
+ *     y[e] = x[e] · w[e] / sqrt(Σ x² / head_dim + eps),
+ *   in fp32, then the rotation, then the one rounding.  q_weight, k_weight:
+ *   [head_dim] of weight_dtype (PROJ_BF16 or PROJ_F32), NULL for no norm of q or of k;
+ *   eps finite and at least 0.  Every bf16 head has its norm: sums of squares out
+ *   of fp32's range are scaled.  rope_rows: the rope table's row of each token
+ *   (int32 [tokens]), NULL for its position.  After an eviction a token's place in
+ *   the cache, which positions[i] names, is not its position in the text any more.
+ *
+ * proj_kv_attend_shared: proj_kv_attend where every sequence's tokens are the same
+ *   prefix_len tokens first, in the pages prefix_pages[0 .. prefix_width), and then the
+ *   n = seq_lens[b] tokens of its own in page_table (n = 0: the prefix alone; no
+ *   windows).  The prefix is read once for the whole batch, on the tensor cores.
+ *   Logits, weights and sums are fp32; a weight enters the product with the values
+ *   in parts of 24 bits.  An infinite value gives infinity where its weight is above
+ *   2^-90 of the largest (below, NaN).  prefix_len = 0 is proj_kv_attend.  workspace:
+ *   device memory of the size that proj_kv_shared_workspace gives (16-byte aligned),
+ *   the call's own until it is done.
+ *
+ * proj_kv_attend_scored: proj_kv_attend, and for each key head g and attended token t
+ *     scores_out[b,g,t] = scores[b,g,t] + Σ_h softmax weight of t for query head h of g;
+ *   the other scores are copied.  scores, scores_out: fp32 [sequences, kv_heads,
+ *   score_tokens], score_tokens at least the page table's tokens; the two may be one
+ *   array, and may not overlap otherwise.  Tokens left out for a bad page have weight 0.
+ *   workspace: as above, of proj_kv_scored_workspace's size (4 bytes for each query
+ *   head and token that the page table has room for).
+ *
+ * proj_kv_evict: which tokens of each sequence and key head stay, by score, and their
+ *   copy to other pages.  A sequence of n = seq_lens[b] tokens keeps all of them
+ *   where n ≤ keep, else the last `recent` and the keep − recent of the highest
+ *   scores among the others (equal scores: the earlier tokens; −0 is 0; NaN is above
+ *   every number), in their order.  Place i of its pages in to_table (int32
+ *   [sequences, to_width], room for keep tokens at least) gets the i-th kept token of
+ *   each key head, so key heads of one place may hold different tokens.
+ *     lens_out[b] = min(n, keep);   kept[b,g,i]: the place that token i had, −1 past
+ *     lens_out (int32 [sequences, kv_heads, keep]);   scores_out[b,g,i]: its score, 0
+ *     past lens_out (fp32 [sequences, kv_heads, to_width · page_size]).
+ *   scores: fp32 [sequences, kv_heads, score_tokens], as above.  The pages written may
+ *   not be among those read, nor twice among themselves; those read may be shared
+ *   between sequences.  No output may overlap another array of the call.  A token on a
+ *   bad page, old or new, is not copied (proj_kv_device_status tells).
+ */
+proj_status_t proj_kv_append_normed(proj_kv_handle_t h, int64_t tokens, const void *q, int64_t q_stride, const void *k,
+                                    const void *v, int64_t kv_stride, const void *q_weight, const void *k_weight,
+                                    proj_dtype_t weight_dtype, float eps, const int32_t *positions, const int32_t *seq_ids,
+                                    const int32_t *page_table, int64_t sequences, int64_t table_width,
+                                    const int32_t *rope_rows, const float *rope, int64_t rope_positions, int32_t rot_dim,
+                                    int interleaved, const float *k_scale, const float *v_scale, void *k_cache, void *v_cache,
+                                    void *q_out, int64_t q_out_stride, void *stream);
+proj_status_t proj_kv_shared_workspace(proj_kv_handle_t h, int64_t sequences, int64_t prefix_len, size_t *bytes);
+proj_status_t proj_kv_attend_shared(proj_kv_handle_t h, int64_t sequences, const void *q, int64_t q_stride,
+                                    const void *k_cache, const void *v_cache, const float *k_scale, const float *v_scale,
+                                    const int32_t *prefix_pages, int64_t prefix_width, int64_t prefix_len,
+                                    const int32_t *page_table, int64_t table_width, const int32_t *seq_lens, float scale,
+                                    void *workspace, void *out, int64_t out_stride, float *lse, void *stream);
+proj_status_t proj_kv_scored_workspace(proj_kv_handle_t h, int64_t sequences, int64_t table_width, size_t *bytes);
+proj_status_t proj_kv_attend_scored(proj_kv_handle_t h, int64_t sequences, const void *q, int64_t q_stride,
+                                    const void *k_cache, const void *v_cache, const float *k_scale, const float *v_scale,
+                                    const int32_t *page_table, int64_t table_width, const int32_t *seq_lens, int64_t window,
+                                    float scale, const float *scores, float *scores_out, int64_t score_tokens,
+                                    void *workspace, void *out, int64_t out_stride, float *lse, void *stream);
+proj_status_t proj_kv_evict(proj_kv_handle_t h, int64_t sequences, const int32_t *page_table, int64_t table_width,
+                            const int32_t *seq_lens, const float *scores, int64_t score_tokens, const int32_t *to_table,
+                            int64_t to_width, int64_t keep, int64_t recent, void *k_cache, void *v_cache, int32_t *lens_out,
+                            float *scores_out, int32_t *kept, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
