@@ -126,7 +126,8 @@ struct KvPrefixParams {
     float scale;
     int32_t group;
     int64_t row_tiles, tiles;  // of a key head's rows; of the prefix's tokens
-    float *partials;           // [unit + CTA][maxima, sums of either half, values]
+    int32_t box;               // tokens of a TMA box, 0: copies instead
+    float *partials;           // [unit + CTA][maxima, sums, values]
     int *status;
 };
 

@@ -14,12 +14,16 @@
 //   * X = Q·Kᵀ and o += P·V are tcgen05 products of 128 rows, accumulated in tensor
 //     memory: X of two token tiles, so that the one's softmax overlaps the other's
 //     products, and o.  P stays in tensor memory too, written over X.
-//   * warps 0..7 turn X into P: a thread has one row (tensor-memory lane) and half
-//     of a tile's tokens; two threads of a row meet over its maximum.
+//   * warps 0..15 turn X into P, in two groups that take every other tile, so that the one's
+//     waits lie under the other's arithmetic (which is what limits the kernel: splitting a
+//     weight takes 12 of the 20 instructions for two of them).  A thread has one row
+//     (tensor-memory lane) and half of a tile's tokens; the two threads of a row meet over its
+//     maximum, and the groups hand on what the weights are relative to.
 //   * o is rescaled only where the maximum grows by more than 2^8 (kLazy): a
 //     weight then is at most 2^8, which costs fp32 sums nothing.
-//   * warps 8..11 fill a ring of token tiles (16-byte asynchronous copies: a page may
-//     have any number of tokens and any strides), warp 12 issues the products.
+//   * warps 16..19 fill a ring of token tiles: pages of whole multiples of 8 tokens by TMA
+//     boxes of up to 32 tokens, others, and the prefix's end, by 16-byte asynchronous copies
+//     (which any page size and strides allow); warp 20 issues the products.
 //   * (key head, row tile, token tile) in this order are one line that the CTAs share
 //     evenly; each stretch of one row tile leaves a part in the workspace.
 //
@@ -33,7 +37,10 @@ namespace projgb {
 namespace dev {
 
 constexpr int kPrefixRows = 128;          // query rows of a tile
-constexpr int kPrefixSoftmaxWarps = 8, kPrefixLoadWarps = 4;
+constexpr int kPrefixGroups = 2;          // of softmax warps, for every other tile each
+constexpr int kPrefixPieces = 2;          // of a tile's tokens, a softmax thread's each
+constexpr int kPrefixSums = kPrefixGroups * kPrefixPieces;  // threads of a row
+constexpr int kPrefixSoftmaxWarps = 4 * kPrefixSums, kPrefixLoadWarps = 4;
 constexpr int kPrefixLoaders = 32 * kPrefixLoadWarps;
 constexpr int kPrefixThreads = 32 * (kPrefixSoftmaxWarps + kPrefixLoadWarps + 1);
 constexpr float kLazy = 8.f;
@@ -44,27 +51,32 @@ struct PrefixShape {
     static constexpr int kTokens = kDim > 128 ? 64 : 128;  // of a tile
     static constexpr int kTile = kTokens * kDim * 2;        // bytes of a tile of keys or values, bf16
     static constexpr int kRaw = kE4m3 ? kTile / 2 : 0;      // as they are in an 8-bit cache
-    static constexpr int kSlots = kE4m3 ? 4 : kDim > 128 ? 5 : 6;
+    static constexpr int kSlots = kDim <= 64 ? 6 : kE4m3 ? 3 : kDim <= 128 ? 5 : 4;  // (three: keys of two tiles, values of one)
     static constexpr int kRaws = kE4m3 ? (kDim > 128 ? 2 : 4) : 0;
     static constexpr int kQ = kPrefixRows * kDim * 2;
-    static constexpr int kCtl = 2048;
+    static constexpr int kCtl = 9216;
     static constexpr int kSmem = kQ + kSlots * kTile + kRaws * kRaw + kCtl;
-    // Tensor memory: o, then two buffers of X, each with room for P's three parts.
+    // Tensor memory: o, then two buffers of X, each with room for P's three parts: of 16 tokens
+    // the first two lie over their X, the third after X.  (A thread so overwrites only what it
+    // has read itself.)
     static constexpr int kBuffer = kTokens / 2 * 3;
     static constexpr int kColumns = kDim + 2 * kBuffer;
-    // A part: [maximum of a row][sum of either half of its tokens][kDim/4][row] float4.
-    static constexpr int kPart = 3 * kPrefixRows + kPrefixRows * kDim;
+    // A part: [maximum of a row][its threads' sums][kDim/4][row] float4.
+    static constexpr int kPart = (1 + kPrefixSums) * kPrefixRows + kPrefixRows * kDim;
     static_assert(kColumns <= 512 && kSmem <= 227 * 1024, "tensor memory and shared memory of an SM");
 };
 
 struct PrefixCtl {
-    uint64_t full[8], empty[8], q_full, q_empty, x_full[2], p_full[2], o_done[2], drain;
+    uint64_t full[8], empty[8], raw_full[4][kPrefixLoadWarps], q_full, q_empty, x_full[2], p_full[2], o_done[2], drain;
+    uint64_t base_full[2][4];  // [tile & 1][quarter of the rows]: the tile has left its base
     uint32_t tmem;
     int abort_flag;
     uint32_t valid[8][4];     // tokens of the last tiles that exist, a bit each
-    float top[2][kPrefixRows];  // a row's maximum over the other half of the tile, and of the next one
+    uint4 row[kPrefixLoadWarps][2][32];  // [tile & 1]: where a token lies in the cache (bytes), how many bytes of it to copy
+    float top[2][kPrefixPieces][kPrefixRows];  // [tile & 1]: a row's maximum
+    float base[2][kPrefixRows];                // [tile & 1]: what its weights are relative to
 };
-static_assert(sizeof(PrefixCtl) <= 2048, "PrefixShape::kCtl");
+static_assert(sizeof(PrefixCtl) <= 9216, "PrefixShape::kCtl");
 
 // D[tmem] (+)= A[tmem] · B[smem], bf16, fp32 accumulators.
 __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
@@ -73,6 +85,12 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *map, uint32_t bar, int32_t x, int32_t y, int32_t z, int32_t w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
         : "memory");
 }
 __device__ __forceinline__ void tmem_store8(uint32_t at, const uint32_t (&r)[8]) {
@@ -88,14 +106,97 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const float (&v)[16]) 
         "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
         : "memory");
 }
+// Columns of the thread's lane, as they are.
+__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void async_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// 16 bytes, of which `from` has the first `bytes` (16 or 0: then zeros).
+__device__ __forceinline__ void cp_async16n(uint32_t to, const void *from, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
 // Arrives on `bar` once the thread's copies so far are in shared memory.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(yes));
+    return yes != 0;
+}
 __device__ __forceinline__ void named_barrier(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    return p;
+}
+__device__ __forceinline__ float2 pair_to(uint64_t p) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2_rz(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// Two weights as three bf16 parts, the same as split<false>'s: each but the last the upper half of
+// the next float below, so that every part of a positive weight is positive.
+__device__ __forceinline__ void split3(uint64_t w, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+    const uint64_t below = pair_of(0x1.fffffep-1f, 0x1.fffffep-1f), minus = pair_of(-1.f, -1.f);
+    uint32_t *to[2] = {&hi, &mid};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float2 h = pair_to(mul2_rz(w, below));
+        const uint32_t a = __float_as_uint(h.x), b = __float_as_uint(h.y);
+        *to[i] = __byte_perm(a, b, 0x7632);
+        w = fma2(pair_of(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u)), minus, w);
+    }
+    const float2 r = pair_to(w);
+    lo = bf16_pair(r.x, r.y);
 }
 
 // kind::f16 instruction descriptor: fp32 accumulators, bf16 operands, M = 128.
@@ -129,10 +230,16 @@ struct PrefixWork {
 };
 
 template <bool kE4m3, int kDim>
-__global__ void __launch_bounds__(kPrefixThreads, 1) kv_prefix_kernel(const KvPrefixParams p) {
+__global__ void __launch_bounds__(kPrefixThreads, 1)
+    kv_prefix_kernel(const __grid_constant__ KvPrefixParams p, const __grid_constant__ CUtensorMap k_map,
+                     const __grid_constant__ CUtensorMap v_map) {
     using Shape = PrefixShape<kE4m3, kDim>;
     constexpr int kTokens = Shape::kTokens, kTile = Shape::kTile, kSlots = Shape::kSlots;
-    constexpr int kHalf = kTokens / 2;  // tokens of a softmax thread
+    constexpr int kPiece = kTokens / kPrefixPieces;        // tokens of a softmax thread
+    constexpr int kMine = kTokens / kPrefixLoadWarps;       // of a loading warp
+    constexpr int kOwn = kDim / kPrefixSums;                // elements of its row that a softmax thread writes
+    static_assert(kPiece == 2 * kMine, "a piece's tokens are two loading warps'");
+    constexpr uint32_t kAll = kMine == 32 ? 0xffffffffu : 0xffffu;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *ring = smem + Shape::kQ, *raws = ring + kSlots * kTile;
     PrefixCtl *ctl = reinterpret_cast<PrefixCtl *>(raws + Shape::kRaws * Shape::kRaw);
@@ -148,17 +255,21 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv_prefix_kernel(const KvPr
         tmem_relinquish<false>();
     }
     if (tid == 0) {
-        for (int i = 0; i < kSlots; ++i) {
+        static_assert(Shape::kRaws <= 4 && (!kE4m3 || kSlots >= 3), "barriers");
+        for (int i = 0; i < 8; ++i) {
             // (A copying loader arrives when its copies do; its warp once more, for `valid`.)
             mbar_init(smem_u32(&ctl->full[i]), kE4m3 ? kPrefixLoaders : kPrefixLoaders + kPrefixLoadWarps);
             mbar_init(smem_u32(&ctl->empty[i]), 1);
+            if (kE4m3 && i < Shape::kRaws)
+                for (int w = 0; w < kPrefixLoadWarps; ++w) mbar_init(smem_u32(&ctl->raw_full[i][w]), 33);
         }
         mbar_init(smem_u32(&ctl->q_full), kPrefixLoaders);
         mbar_init(smem_u32(&ctl->q_empty), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&ctl->x_full[i]), 1);
-            mbar_init(smem_u32(&ctl->p_full[i]), 32 * kPrefixSoftmaxWarps);
+            mbar_init(smem_u32(&ctl->p_full[i]), 32 * kPrefixSoftmaxWarps / kPrefixGroups);
             mbar_init(smem_u32(&ctl->o_done[i]), 1);
+            for (int q = 0; q < 4; ++q) mbar_init(smem_u32(&ctl->base_full[i][q]), 32 * kPrefixPieces);
         }
         mbar_init(smem_u32(&ctl->drain), 1);
         ctl->abort_flag = 0;
@@ -193,30 +304,61 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv_prefix_kernel(const KvPr
         const int loader = warp - kPrefixSoftmaxWarps;
         constexpr int kElem = kE4m3 ? 1 : 2;
         constexpr int kRowChunks = kDim * kElem / 16;            // 16-byte chunks of a token in the cache
-        constexpr int kMine = kTokens / kPrefixLoadWarps;        // tokens of a warp
         constexpr int kAtOnce = 32 / kRowChunks < 1 ? 1 : 32 / kRowChunks;  // of them a pass of the warp takes
         static_assert(kRowChunks <= 32, "a lane has one chunk of a row");
-        const int chunks = p.cache.head_dim * kElem / 16;
+        constexpr int kBatch = 4;  // rows whose places are read together (a copy is not moved past such a read)
         const int c = lane % kRowChunks, r_of = lane / kRowChunks;
-        const uint8_t *caches[2] = {static_cast<const uint8_t *>(p.k_cache), static_cast<const uint8_t *>(p.v_cache)};
-        // The places of this warp's tokens of a tile, asked for a tile ahead.
-        int64_t place = 0;
-        bool there = false;
-        auto look_up = [&](int64_t pos) {
-            there = false;
-            if (pos >= work.end) return;
-            const int64_t tile = pos % work.tiles, unit = pos / work.tiles;
-            const int64_t t = tile * kTokens + loader * kMine + lane;
-            if (lane < kMine && t < p.prefix) {
-                const uint32_t at = static_cast<uint32_t>(t), page_size = static_cast<uint32_t>(p.cache.page_size);
-                const int32_t page = p.cache.table[at / page_size];
-                there = page >= 0 && page < p.cache.num_pages;
-                if (!there) atomicOr(p.status, kKvErrPage);
-                place = page * p.cache.page_stride + (at % page_size) * p.cache.token_stride +
-                        unit / p.row_tiles * p.cache.head_stride;
+        const bool mine = c < p.cache.head_dim * kElem / 16;  // a chunk that the cache has
+        const uint8_t *k_from = static_cast<const uint8_t *>(p.k_cache) + c * 16, *v_from = static_cast<const uint8_t *>(p.v_cache) + c * 16;
+        // Where this lane's token of a tile lies.  Its page is asked for a tile ahead, and the
+        // page's number and the place in it go on by additions (a 64-bit division takes a third
+        // of a microsecond: with three of them a tile the loaders were what the rest waited for).
+        const uint32_t page_size = static_cast<uint32_t>(p.cache.page_size);
+        const uint32_t step_pages = kTokens / page_size, step_places = kTokens % page_size;
+        int64_t look_tile = work.pos % work.tiles, look_unit = work.pos / work.tiles, look_left = work.end - work.pos;
+        uint32_t look_page = 0, look_place = 0;  // of the lane's token of tile look_tile
+        auto look_at = [&]() {
+            const uint32_t t = static_cast<uint32_t>(look_tile) * kTokens + loader * kMine + lane;
+            look_page = t / page_size;
+            look_place = t - look_page * page_size;
+        };
+        int32_t page = -1;          // asked for, of the tile before look_tile
+        uint32_t place_of = 0;
+        bool inside = false;
+        int32_t look_head = static_cast<int32_t>(look_unit / p.row_tiles), head_index = look_head;
+        look_at();
+        auto ask_page = [&]() {
+            inside = look_left > 0 && lane < kMine && look_tile * kTokens + loader * kMine + lane < p.prefix;
+            page = inside ? p.cache.table[look_page] : -1;
+            place_of = look_place;
+            head_index = look_head;
+            --look_left;
+            look_page += step_pages;
+            look_place += step_places;
+            if (look_place >= page_size) look_place -= page_size, ++look_page;
+            if (++look_tile == work.tiles) {
+                look_tile = 0;
+                look_head = static_cast<int32_t>(++look_unit / p.row_tiles);
+                look_at();
             }
         };
-        look_up(work.pos);
+        // Leaves what was asked for to the warp, for the tile of number `n`, and asks for the next;
+        // returns which tokens exist.
+        int32_t box_page = 0, box_place = 0, box_head = 0;
+        auto take_page = [&](int64_t n) {
+            const bool there = page >= 0 && page < p.cache.num_pages;
+            if (inside && !there) atomicOr(p.status, kKvErrPage);
+            const int64_t at = there ? (page * p.cache.page_stride + place_of * p.cache.token_stride + head_index * p.cache.head_stride) * kElem : 0;
+            const uint32_t bits = __ballot_sync(0xffffffffu, there);
+            box_page = page, box_place = static_cast<int32_t>(place_of), box_head = head_index;
+            if (p.box == 0 || bits != kAll)
+                ctl->row[loader][n & 1][lane] =
+                    make_uint4(static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32), there ? 16u : 0u, 0u);
+            ask_page();
+            __syncwarp();
+            return bits;
+        };
+        ask_page();
         // Where a 16-byte chunk of a row lies in a tile of 64-element blocks, swizzled.
         auto chunk_to = [&](int rows_of, int r, int chunk) {
             return static_cast<uint32_t>((chunk >> 3) * rows_of * 128 + r * 128 + (((chunk & 7) ^ (r & 7)) << 4));
@@ -227,32 +369,51 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv_prefix_kernel(const KvPr
         int segment = 0;
         bool ok = true;
         // 8-bit: raw tiles are on their way kRaws - 1 ahead of the one that is converted.
-        int64_t raw_in = 0, raw_pos = work.pos;
+        int64_t raw_in = 0;
+        uint32_t raw_bits = 0;
         uint32_t raw_valid[kE4m3 ? Shape::kRaws / 2 : 1];
         const int64_t raw_tiles = 2 * (work.end - work.pos);
-        auto ask_raw = [&]() {  // the next raw tile: keys, then values, of raw_pos
+        // This warp's tokens by TMA, a box from each lane that has a box's first token; `block` bytes
+        // of a token go to each of `blocks` places `apart` bytes from one another.
+        auto load_boxes = [&](const CUtensorMap *map, uint32_t to, uint32_t bar, int blocks, int elements, uint32_t block, uint32_t apart) {
+            if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(blocks) * kMine * block);
+            __syncwarp();
+            if (lane < kMine && (lane & (p.box - 1)) == 0)
+                for (int j = 0; j < blocks; ++j)
+                    tma_load_4d(to + j * apart + static_cast<uint32_t>(lane) * block, map, bar, j * elements, box_place, box_head, box_page);
+        };
+        auto row_offset = [](uint4 row) { return static_cast<int64_t>(static_cast<uint64_t>(row.y) << 32 | row.x); };
+        auto ask_raw = [&]() {  // the next raw tile: keys, then values
             if constexpr (kE4m3) {
-                if (raw_in < raw_tiles) {
-                    const int which = static_cast<int>(raw_in & 1);
-                    const uint32_t bits = __ballot_sync(0xffffffffu, there);
-                    const uint32_t to = smem_u32(raws) + static_cast<uint32_t>(raw_in % Shape::kRaws) * Shape::kRaw;
+                if (raw_in >= raw_tiles) return;
+                const int which = static_cast<int>(raw_in & 1), at = static_cast<int>(raw_in % Shape::kRaws);
+                if (which == 0) {
+                    raw_bits = take_page(raw_in >> 1);
 #pragma unroll
-                    for (int i = 0; i < kMine / kAtOnce; ++i) {
-                        const int r = i * kAtOnce + r_of;
-                        const int64_t at = __shfl_sync(0xffffffffu, place, r) + c * 16;
-                        const bool fill = (bits >> r) & 1u;
-                        cp_async16(to + (loader * kMine + r) * kDim + c * 16, caches[which] + (fill && c < chunks ? at : 0), fill && c < chunks);
-                    }
-                    if (which == 0) {
-#pragma unroll
-                        for (int s = 0; s < Shape::kRaws / 2; ++s)
-                            if (static_cast<int>((raw_in / 2) % (Shape::kRaws / 2)) == s) raw_valid[s] = bits;
-                    } else {
-                        look_up(++raw_pos);
-                    }
-                    ++raw_in;
+                    for (int s = 0; s < Shape::kRaws / 2; ++s)
+                        if (at / 2 == s) raw_valid[s] = raw_bits;
                 }
-                cp_async_commit();
+                const uint32_t to = smem_u32(raws) + static_cast<uint32_t>(at * Shape::kRaw + loader * kMine * kDim);
+                const uint32_t bar = smem_u32(&ctl->raw_full[at][loader]);
+                if (p.box > 0 && raw_bits == kAll) {
+                    load_boxes(which ? &v_map : &k_map, to, bar, 1, 0, kDim, 0);
+                    mbar_arrive(bar);
+                } else {
+                    const uint8_t *from = which ? v_from : k_from;
+                    const uint4 *rows_of = ctl->row[loader][(raw_in >> 1) & 1] + r_of;
+#pragma unroll
+                    for (int i = 0; i < kMine / kAtOnce; i += kBatch) {
+                        uint4 row[kBatch];
+#pragma unroll
+                        for (int j = 0; j < kBatch; ++j) row[j] = rows_of[(i + j) * kAtOnce];
+#pragma unroll
+                        for (int j = 0; j < kBatch; ++j)
+                            if (mine) cp_async16n(to + ((i + j) * kAtOnce + r_of) * kDim + c * 16, from + row_offset(row[j]), row[j].z);
+                    }
+                    cp_async_arrive(bar);
+                    if (lane == 0) mbar_arrive(bar);
+                }
+                ++raw_in;
             }
         };
         if constexpr (kE4m3)
@@ -275,11 +436,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv_prefix_kernel(const KvPr
                                p.q + (fill ? b * p.q_stride + (head * p.group + g) * p.cache.head_dim + qc * 8 : 0), fill);
                 }
                 cp_async_arrive(smem_u32(&ctl->q_full));
-                if constexpr (kE4m3) cp_async_commit();
             }
             ++segment;
             for (; ok && pos < seg_end; ++pos, ++n) {
                 uint32_t bits = 0;
+                if constexpr (!kE4m3) bits = take_page(n);
                 for (int which = 0; which < 2; ++which) {
                     if (!warp_waited(&ctl->empty[slot], phase ^ 1u)) {
                         ok = false;
@@ -287,37 +448,47 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv_prefix_kernel(const KvPr
                     }
                     const uint32_t to = smem_u32(ring) + slot * kTile;
                     if constexpr (!kE4m3) {
-                        bits = __ballot_sync(0xffffffffu, there);
+                        const uint32_t bar = smem_u32(&ctl->full[slot]);
+                        if (lane == 0 && which == 0) ctl->valid[n & 7][loader] = bits;
+                        if (p.box > 0 && bits == kAll) {
+                            load_boxes(which ? &v_map : &k_map, to + loader * kMine * 128, bar, (p.cache.head_dim + 63) / 64, 64, 128,
+                                       kTokens * 128);
+                            mbar_arrive(bar);
+                        } else {
+                            const uint8_t *from = which ? v_from : k_from;
+                            const uint4 *rows_of = ctl->row[loader][n & 1] + r_of;
 #pragma unroll
-                        for (int i = 0; i < kMine / kAtOnce; ++i) {
-                            const int r = i * kAtOnce + r_of;
-                            const int64_t at = __shfl_sync(0xffffffffu, place, r) * 2 + c * 16;
-                            const bool fill = (bits >> r) & 1u;
-                            if (c < chunks)
-                                cp_async16(to + chunk_to(kTokens, loader * kMine + r, c), caches[which] + (fill ? at : 0), fill);
+                            for (int i = 0; i < kMine / kAtOnce; i += kBatch) {
+                                uint4 row[kBatch];
+#pragma unroll
+                                for (int j = 0; j < kBatch; ++j) row[j] = rows_of[(i + j) * kAtOnce];
+#pragma unroll
+                                for (int j = 0; j < kBatch; ++j)
+                                    if (mine)
+                                        cp_async16n(to + chunk_to(kTokens, loader * kMine + (i + j) * kAtOnce + r_of, c), from + row_offset(row[j]),
+                                                    row[j].z);
+                            }
+                            cp_async_arrive(bar);
+                            if (lane == 0) mbar_arrive(bar);
                         }
-                        cp_async_arrive(smem_u32(&ctl->full[slot]));
-                        if (lane == 0) {
-                            if (which == 0) ctl->valid[n & 7][loader] = bits;
-                            mbar_arrive(smem_u32(&ctl->full[slot]));
-                        }
-                        if (which == 1) look_up(pos + 1);
                     } else {
-                        // This lane's own chunks of the raw tile are in: every copy but the
-                        // kRaws - 1 asked for after it (a row tile's queries count as one more).
                         ask_raw();
-                        cp_async_wait<Shape::kRaws - 1>();
+                        const int at = static_cast<int>((2 * n + which) % Shape::kRaws);
+                        if (!warp_waited(&ctl->raw_full[at][loader], static_cast<uint32_t>((2 * n + which) / Shape::kRaws) & 1u)) {
+                            ok = false;
+                            break;
+                        }
                         if (which == 0) {
 #pragma unroll
                             for (int s = 0; s < Shape::kRaws / 2; ++s)
                                 if (static_cast<int>(n % (Shape::kRaws / 2)) == s) bits = raw_valid[s];
                             if (lane == 0) ctl->valid[n & 7][loader] = bits;
                         }
-                        const uint8_t *from = raws + (2 * n + which) % Shape::kRaws * Shape::kRaw;
+                        const uint8_t *from = raws + at * Shape::kRaw;
 #pragma unroll
                         for (int i = 0; i < kMine / kAtOnce; ++i) {
                             const int r = loader * kMine + i * kAtOnce + r_of;
-                            if (c >= chunks) continue;
+                            if (!mine) continue;
                             uint4 lo, hi;
                             e4m3_to_bf16(*reinterpret_cast<const uint4 *>(from + r * kDim + c * 16), lo, hi);
                             *reinterpret_cast<uint4 *>(ring + slot * kTile + chunk_to(kTokens, r, 2 * c)) = lo;
@@ -330,13 +501,24 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv_prefix_kernel(const KvPr
                 }
             }
         }
-        cp_async_wait<0>();
         asm volatile("cp.async.wait_all;" ::: "memory");
+        if (!ok) {
+            // A wait ran out: TMA copies of this warp may be on their way.  They end within
+            // microseconds; a barrier that other warps did not come to does not tell.
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 2000000u) {
+            }
+        }
     } else if (warp == kPrefixSoftmaxWarps + kPrefixLoadWarps) {
         // ------------------------------------------------------------ products
-        if (lane == 0) {
+        // The whole warp runs the loop, so that descriptors and addresses are the same in every
+        // lane and stay in uniform registers; one elected lane issues.  (From a branch of one lane
+        // each product took about 100 cycles to issue, whatever its width.)
+        {
             constexpr uint32_t kIdX = prefix_idesc(kTokens, false), kIdO = prefix_idesc(kDim, true);
-            const uint32_t q0 = smem_u32(smem), ring0 = smem_u32(ring);
+            // (The address field of a descriptor, in 16-byte units, holds every offset without a carry.)
+            const uint64_t q_desc = smem_desc_sw128(smem_u32(smem), 16, 1024), k_desc = smem_desc_sw128(smem_u32(ring), 16, 1024),
+                           v_desc = smem_desc_sw128(smem_u32(ring), kTokens * 128, 1024);
             int64_t pos = work.pos, seg_end = pos < work.end ? stretch_end(pos) : pos;
             int segment = 0, xslot = 0;  // the ring goes keys, values, keys, values ...
             uint32_t xphase = 0;
@@ -352,26 +534,30 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv_prefix_kernel(const KvPr
             // X of the next place; false once a wait ran out.
             auto issue_x = [&](int64_t n) {
                 if (x_first) {
-                    if (!waited(&ctl->q_full, static_cast<uint32_t>(segment) & 1u)) return false;
+                    if (!warp_waited(&ctl->q_full, static_cast<uint32_t>(segment) & 1u)) return false;
                     ++segment;
                     x_first = false;
                 }
-                if (!waited(&ctl->full[xslot], xphase)) return false;
+                if (!warp_waited(&ctl->full[xslot], xphase)) return false;
                 async_proxy_fence();
                 tc_fence_after_sync();
-                const uint32_t k0 = ring0 + xslot * kTile;
+                const uint64_t kd = k_desc + static_cast<uint64_t>(xslot) * (kTile >> 4);
                 const uint32_t d = tmem + kDim + static_cast<uint32_t>(n & 1) * Shape::kBuffer;
+                const bool last = ++xpos == x_seg_end && xpos < work.end;
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < kDim / 16; ++k) {
-                    const uint32_t block = static_cast<uint32_t>(k / 4), in = static_cast<uint32_t>(k % 4) * 32;
-                    tc_mma<false>(d, smem_desc_sw128(q0 + block * kPrefixRows * 128 + in, 16, 1024),
-                                  smem_desc_sw128(k0 + block * kTokens * 128 + in, 16, 1024), kIdX, k > 0);
+                    for (int k = 0; k < kDim / 16; ++k) {
+                        const uint64_t block = static_cast<uint64_t>(k / 4), in = static_cast<uint64_t>(k % 4) * 32;
+                        tc_mma<false>(d, q_desc + ((block * kPrefixRows * 128 + in) >> 4), kd + ((block * kTokens * 128 + in) >> 4), kIdX,
+                                      k > 0);
+                    }
+                    tc_commit<false>(smem_u32(&ctl->empty[xslot]));
+                    tc_commit<false>(smem_u32(&ctl->x_full[n & 1]));
+                    if (last) tc_commit<false>(smem_u32(&ctl->q_empty));
                 }
-                tc_commit<false>(smem_u32(&ctl->empty[xslot]));
-                tc_commit<false>(smem_u32(&ctl->x_full[n & 1]));
+                __syncwarp();
                 next(xslot, xphase);
-                if (++xpos == x_seg_end && xpos < work.end) {
-                    tc_commit<false>(smem_u32(&ctl->q_empty));
+                if (last) {
                     x_seg_end = stretch_end(xpos);
                     x_first = true;
                 }
@@ -387,149 +573,178 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) kv_prefix_kernel(const KvPr
                     seg_end = stretch_end(pos);
                 }
                 if (xpos < work.end && !issue_x(n + 1)) break;
-                if (!waited(&ctl->p_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u)) break;
-                if (!waited(&ctl->full[vslot], vphase)) break;
+                if (!warp_waited(&ctl->p_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u)) break;
+                if (!warp_waited(&ctl->full[vslot], vphase)) break;
                 async_proxy_fence();
                 tc_fence_after_sync();
-                const uint32_t v0 = ring0 + vslot * kTile;
+                const uint64_t vd = v_desc + static_cast<uint64_t>(vslot) * (kTile >> 4);
                 const uint32_t a = tmem + kDim + static_cast<uint32_t>(n & 1) * Shape::kBuffer;
+                const uint32_t more = pos > seg_begin;
+                if (elect_one()) {
 #pragma unroll
-                for (int y = 0; y < 3; ++y)
+                    for (int y = 0; y < 3; ++y)
 #pragma unroll
-                    for (int k = 0; k < kTokens / 16; ++k)
-                        tc_mma_ts(tmem, a + y * (kTokens / 2) + k * 8, smem_desc_sw128(v0 + k * 2048, kTokens * 128, 1024), kIdO,
-                                  pos > seg_begin || y > 0 || k > 0);
-                tc_commit<false>(smem_u32(&ctl->empty[vslot]));
-                tc_commit<false>(smem_u32(&ctl->o_done[n & 1]));
+                        for (int k = 0; k < kTokens / 16; ++k)
+                            tc_mma_ts(tmem, y < 2 ? a + 16 * k + 8 * y : a + kTokens + 8 * k, vd + k * (2048 >> 4), kIdO,
+                                      y > 0 || k > 0 ? 1u : more);
+                    tc_commit<false>(smem_u32(&ctl->empty[vslot]));
+                    tc_commit<false>(smem_u32(&ctl->o_done[n & 1]));
+                }
+                __syncwarp();
                 next(vslot, vphase);
             }
             // Every product is done before the tensor memory is given back, whatever happened.
-            tc_commit<false>(smem_u32(&ctl->drain));
-            const uint64_t t0 = globaltimer_ns();
-            while (!mbar_try_wait(smem_u32(&ctl->drain), 0) && static_cast<int64_t>(globaltimer_ns() - t0) < kPrefixWaitNs) {
+            if (elect_one()) {
+                tc_commit<false>(smem_u32(&ctl->drain));
+                const uint64_t t0 = globaltimer_ns();
+                while (!mbar_try_wait(smem_u32(&ctl->drain), 0) && static_cast<int64_t>(globaltimer_ns() - t0) < kPrefixWaitNs) {
+                }
             }
         }
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax
-        const int quarter = warp & 3, half = warp >> 2;
-        const int r = quarter * 32 + lane;
+        const int quarter = warp & 3, piece = (warp >> 2) % kPrefixPieces, group = warp / (4 * kPrefixPieces);
+        const int r = quarter * 32 + lane, share = group * kPrefixPieces + piece;
         const uint32_t at_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t buffer = at_lane + kDim + group * Shape::kBuffer, x0 = buffer + piece * kPiece;  // of the group's tiles
+        // Named barriers: the pieces of a group's rows; all softmax warps.  Every warp comes to the
+        // one for every tile of its group and to the other for every stretch, whatever ran out.
+        // (The hand-over between the groups is not one: they are not in step, and a barrier that
+        // one group had passed twice would take that for the other's arrival.)
+        const int own_barrier = 1 + group * 4 + quarter, all_barrier = 9;
         int64_t n = 0;
         bool ok = true;
         for (int64_t pos = work.pos; pos < work.end;) {
             const int64_t unit = pos / work.tiles, seg_begin = pos, seg_end = stretch_end(pos);
             const int64_t head = unit / p.row_tiles, row = unit % p.row_tiles * kPrefixRows + r;
             const float factor = p.scale * 1.4426950408889634f * (kE4m3 && p.k_scale ? p.k_scale[head] : 1.f);
-            float m = -INFINITY, l = 0.f;
+            const float none = factor < 0.f ? INFINITY : -INFINITY;
+            float m = -INFINITY, l = 0.f;  // what this thread's sum is relative to
             for (; pos < seg_end; ++pos, ++n) {
-                const int buf = static_cast<int>(n & 1);
-                const uint32_t x0 = at_lane + kDim + buf * Shape::kBuffer;
-                ok = ok && warp_waited(&ctl->x_full[buf], static_cast<uint32_t>(n >> 1) & 1u);
+                if (static_cast<int>(n & 1) != group) continue;
+                ok = ok && warp_waited(&ctl->x_full[group], static_cast<uint32_t>(n >> 1) & 1u);
                 tc_fence_after_sync();
-                float x[kHalf], top = -INFINITY;
+                float top = none;
+                uint32_t bits[2] = {kAll, kAll};  // tokens of the piece that exist, a loading warp's each
                 if (ok) {
-                    if constexpr (kHalf == 64) {
-                        tmem_load64(x0 + half * kHalf, x);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < kHalf / 16; ++i)
-                            tmem_load16(x0 + half * kHalf + 16 * i, *reinterpret_cast<float(*)[16]>(x + 16 * i));
-                    }
-#pragma unroll
-                    for (int i = 0; i < kHalf; ++i) x[i] *= factor;
-                    // Tokens of the half, in two words (of a loader warp's tokens each).
+                    bits[0] = ctl->valid[n & 7][2 * piece], bits[1] = ctl->valid[n & 7][2 * piece + 1];
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
-                        constexpr int kBits = kTokens / kPrefixLoadWarps;
-                        const uint32_t bits = ctl->valid[n & 7][half * 2 + w];
-                        if (bits != (kBits == 32 ? 0xffffffffu : 0xffffu)) {
+                        uint32_t x[kMine];
+                        tmem_load(x0 + w * kMine, x);
+                        if (bits[w] != kAll) {
 #pragma unroll
-                            for (int i = 0; i < kBits; ++i)
-                                if (!((bits >> i) & 1u)) x[w * kBits + i] = -INFINITY;
+                            for (int i = 0; i < kMine; ++i)
+                                if (!((bits[w] >> i) & 1u)) x[i] = __float_as_uint(none);
+                        }
+                        if (factor < 0.f) {
+#pragma unroll
+                            for (int i = 0; i < kMine; i += 2) top = fminf(fminf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), top);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < kMine; i += 2) top = fmaxf(fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), top);
                         }
                     }
-                    top = x[0];
-#pragma unroll
-                    for (int i = 1; i < kHalf; ++i) top = fmaxf(top, x[i]);
-                    ctl->top[half][r] = top;
+                    top *= factor;
+                    ctl->top[group][piece][r] = top;
                 }
-                // Both halves of a row have read X, which P overwrites, and left their
-                // maxima.  (Every warp comes here for every tile, whatever ran out.)
-                tc_fence_before_sync();
-                named_barrier(1 + quarter, 64);
-                tc_fence_after_sync();
-                top = fmaxf(top, ctl->top[half ^ 1][r]);
-                named_barrier(1 + quarter, 64);
+                named_barrier(own_barrier, 32 * kPrefixPieces);
+                if (pos > seg_begin)
+                    ok = ok && warp_waited(&ctl->base_full[(n - 1) & 1][quarter], static_cast<uint32_t>((n - 1) >> 1) & 1u);
+                const float before = pos > seg_begin ? ctl->base[(n - 1) & 1][r] : -INFINITY;
+                top = fmaxf(top, ctl->top[group][piece ^ 1][r]);
+                const bool grown = top > before + kLazy || (before == -INFINITY && top > before);
+                const float base_now = grown ? top : before;
+                if (piece == 0) ctl->base[n & 1][r] = base_now;
+                mbar_arrive(smem_u32(&ctl->base_full[n & 1][quarter]));
                 if (!ok) continue;
-                const bool grown = top > m + kLazy || (m == -INFINITY && top > m);
-                const float before = m;
-                if (grown) m = top;
-                if (__any_sync(0xffffffffu, grown)) {
+                if (base_now != m) {
+                    l *= exp2_fast(m - base_now);
+                    m = base_now;
+                }
+                if (pos > seg_begin && __any_sync(0xffffffffu, grown)) {
+                    // o of the tiles before is complete once the last one's product is.  (The
+                    // barrier's phase before that ended before X of this tile was there.)
+                    ok = warp_waited(&ctl->o_done[(n - 1) & 1], static_cast<uint32_t>((n - 1) >> 1) & 1u);
+                    if (!ok) continue;
+                    tc_fence_after_sync();
                     const float keep = grown ? exp2_fast(before - m) : 1.f;
-                    l *= keep;
-                    if (pos > seg_begin) {
-                        // o of the tiles before is complete once the last one's product is.  (The
-                        // barrier's phase before that ended two tiles ago, before X that was read then.)
-                        ok = warp_waited(&ctl->o_done[(n - 1) & 1], static_cast<uint32_t>((n - 1) >> 1) & 1u);
-                        if (!ok) continue;
-                        tc_fence_after_sync();
 #pragma unroll 1
-                        for (int d = 0; d < kDim / 2; d += 16) {
-                            float o[16];
-                            tmem_load16(at_lane + half * (kDim / 2) + d, o);
+                    for (int d = 0; d < kDim / kPrefixPieces; d += 16) {
+                        float o[16];
+                        tmem_load16(at_lane + piece * (kDim / kPrefixPieces) + d, o);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] *= keep;
-                            tmem_store16(at_lane + half * (kDim / 2) + d, o);
-                        }
+                        for (int i = 0; i < 16; ++i) o[i] *= keep;
+                        tmem_store16(at_lane + piece * (kDim / kPrefixPieces) + d, o);
                     }
                 }
                 const float base = finite_or_zero(m);
-                float sum[2] = {0.f, 0.f};  // of the tile: no long chain of additions
-#pragma unroll
-                for (int i = 0; i < kHalf; i += 16) {
-                    uint32_t part[3][8];
+                const uint64_t factors = pair_of(factor, factor), bases = pair_of(-base, -base);
+                uint64_t sum = pair_of(0.f, 0.f);  // of the tile: no long chain of additions
+                // X is read again, 16 tokens at a time in a loop: held in registers it would leave
+                // room for half as many warps, and unrolled over the tile the code of the three
+                // roles does not stay in the instruction cache (6600 cycles a tile).
+#pragma unroll 1
+                for (int i = 0; i < kPiece / 16; ++i) {
+                    uint32_t x[16], hi_mid[16], lo[8];
+                    tmem_load(x0 + 16 * i, x);
+                    const uint32_t there = (16 * i < kMine ? bits[0] : bits[1]) >> (16 * i % kMine);
+                    float w[16];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const float a = exp2_fast(x[i + 2 * j] - base), b = exp2_fast(x[i + 2 * j + 1] - base);
-                        sum[0] += a;
-                        sum[1] += b;
-                        const WeightParts<false> s = split<false>(a, b);
+                        const float2 v = pair_to(fma2(pair_of(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), factors, bases));
+                        w[2 * j] = exp2_fast(v.x), w[2 * j + 1] = exp2_fast(v.y);
+                    }
+                    if ((there & 0xffffu) != 0xffffu) {
 #pragma unroll
-                        for (int y = 0; y < 3; ++y) part[y][j] = s.part[y];
+                        for (int j = 0; j < 16; ++j)
+                            if (!((there >> j) & 1u)) w[j] = 0.f;
                     }
 #pragma unroll
-                    for (int y = 0; y < 3; ++y) tmem_store8(x0 + y * (kTokens / 2) + half * (kHalf / 2) + i / 2, part[y]);
+                    for (int j = 0; j < 8; ++j) {
+                        const uint64_t both = pair_of(w[2 * j], w[2 * j + 1]);
+                        sum = add2(sum, both);
+                        split3(both, hi_mid[j], hi_mid[8 + j], lo[j]);
+                    }
+                    tmem_store(x0 + 16 * i, hi_mid);
+                    tmem_store8(buffer + kTokens + piece * (kPiece / 2) + 8 * i, lo);
                 }
-                l += sum[0] + sum[1];
+                const float2 sums = pair_to(sum);
+                l += sums.x + sums.y;
                 tmem_store_wait();
                 tc_fence_before_sync();
-                mbar_arrive(smem_u32(&ctl->p_full[buf]));
+                mbar_arrive(smem_u32(&ctl->p_full[group]));
             }
-            // The part: o of every tile of the stretch.
+            // The part: o of every tile of the stretch, relative to the last base, from both groups.
+            named_barrier(all_barrier, 32 * kPrefixSoftmaxWarps);
+            const float last = ctl->base[(n - 1) & 1][r];
             ok = ok && warp_waited(&ctl->o_done[(n - 1) & 1], static_cast<uint32_t>((n - 1) >> 1) & 1u);
-            if (!ok) continue;
             tc_fence_after_sync();
-            float *part = p.partials + (unit + blockIdx.x) * Shape::kPart;
-            const bool mine = row < rows;
-            if (mine) {
-                if (half == 0) part[r] = m;
-                part[(1 + half) * kPrefixRows + r] = l;
-            }
-            const float by = kE4m3 && p.v_scale ? p.v_scale[head] : 1.f;
-            float4 *to = reinterpret_cast<float4 *>(part + 3 * kPrefixRows);
+            if (ok) {
+                float *part = p.partials + (unit + blockIdx.x) * Shape::kPart;
+                const bool mine = row < rows;
+                if (mine) {
+                    if (share == 0) part[r] = last;
+                    part[(1 + share) * kPrefixRows + r] = last != m ? l * exp2_fast(m - last) : l;
+                }
+                const float by = kE4m3 && p.v_scale ? p.v_scale[head] : 1.f;
+                float4 *to = reinterpret_cast<float4 *>(part + (1 + kPrefixSums) * kPrefixRows);
 #pragma unroll 1
-            for (int d = 0; d < kDim / 2; d += 16) {
-                const int at = half * (kDim / 2) + d;
-                float o[16];
-                tmem_load16(at_lane + at, o);
-                if (mine)
+                for (int d = 0; d < kOwn; d += 16) {
+                    const int at = share * kOwn + d;
+                    float o[16];
+                    tmem_load16(at_lane + at, o);
+                    if (mine)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        to[(at / 4 + i) * kPrefixRows + r] =
-                            make_float4(o[4 * i] * by, o[4 * i + 1] * by, o[4 * i + 2] * by, o[4 * i + 3] * by);
+                        for (int i = 0; i < 4; ++i)
+                            to[(at / 4 + i) * kPrefixRows + r] =
+                                make_float4(o[4 * i] * by, o[4 * i + 1] * by, o[4 * i + 2] * by, o[4 * i + 3] * by);
+                }
             }
+            // No product of the next stretch begins before all of o is read.
             tc_fence_before_sync();
+            named_barrier(all_barrier, 32 * kPrefixSoftmaxWarps);
         }
     }
     tc_fence_before_sync();
@@ -586,11 +801,14 @@ __global__ void __launch_bounds__(kCombineThreads) kv_combine_kernel(const KvCom
 #pragma unroll 4
         for (int x = group; x < parts; x += kCombineGroups) {
             const float *part = first + static_cast<int64_t>(x) * kPart;
-            const float4 *from = reinterpret_cast<const float4 *>(part + 3 * kPrefixRows);
+            const float4 *from = reinterpret_cast<const float4 *>(part + (1 + kPrefixSums) * kPrefixRows);
             float4 v[kPer];
 #pragma unroll
             for (int k = 0; k < kPer; ++k) v[k] = __ldcg(from + (c + k * kCombineLanes) * kPrefixRows + r);
-            add(__ldcg(part + r), __ldcg(part + kPrefixRows + r) + __ldcg(part + 2 * kPrefixRows + r), v);
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 1; k <= kPrefixSums; ++k) sum += __ldcg(part + k * kPrefixRows + r);
+            add(__ldcg(part + r), sum, v);
         }
     }
     if (group > 0) {

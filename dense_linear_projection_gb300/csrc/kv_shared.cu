@@ -1,5 +1,6 @@
 // C ABI of attention over a shared prefix (proj_kv_attend_shared): argument checks and launches.
 // See include/proj.h for the contract.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "kv_host.cuh"
@@ -10,7 +11,7 @@ using namespace projgb;
 
 namespace {
 
-using PrefixKernel = void (*)(KvPrefixParams);
+using PrefixKernel = void (*)(KvPrefixParams, CUtensorMap, CUtensorMap);
 using CombineKernel = void (*)(KvCombineParams);
 struct PrefixInstance {
     PrefixKernel kernel;
@@ -120,8 +121,22 @@ proj_status_t proj_kv_attend_shared(proj_kv_handle_t h, int64_t sequences, const
     x.tiles = s.tiles;
     x.partials = reinterpret_cast<float *>(at + s.tops + s.own);
     x.status = h->status;
+    // Boxes of whole 8-row groups of the swizzle, within a loading warp's tokens.  Without TMA
+    // (other page sizes, strides that a tensor map cannot have): 16-byte copies.
+    CUtensorMap maps[2] = {};
+    const int32_t most = s.instance.tokens / dev::kPrefixLoadWarps;
+    for (x.box = most; x.box >= 8 && h->d.page_size % x.box != 0;) x.box /= 2;
+    const proj_kv_desc_t &d = h->d;
+    const uint64_t dims[4] = {static_cast<uint64_t>(d.head_dim), static_cast<uint64_t>(d.page_size), static_cast<uint64_t>(d.kv_heads),
+                              static_cast<uint64_t>(d.num_pages)};
+    const uint64_t strides[3] = {static_cast<uint64_t>(d.token_stride) * h->elem, static_cast<uint64_t>(d.head_stride) * h->elem,
+                                 static_cast<uint64_t>(d.page_stride) * h->elem};
+    const uint32_t inner = h->elem == 2 ? 64 : s.instance.columns;
+    if (x.box < 8 || !encode_4d(&maps[0], k_cache, h->elem, dims, strides, inner, x.box) ||
+        !encode_4d(&maps[1], v_cache, h->elem, dims, strides, inner, x.box))
+        x.box = 0;
     const proj_status_t first = launch(s.instance.kernel, dim3(static_cast<unsigned>(s.ctas)), dev::kPrefixThreads,
-                                       static_cast<size_t>(s.instance.smem), stream, x);
+                                       static_cast<size_t>(s.instance.smem), stream, x, maps[0], maps[1]);
     if (first != PROJ_OK) return first;
 
     p.top = reinterpret_cast<float2 *>(at);

@@ -328,6 +328,23 @@ proj_status_t check_launch() {
 
 }  // namespace
 
+namespace projgb {
+
+bool encode_4d(void *map, const void *ptr, int elem, const uint64_t (&dims)[4], const uint64_t (&strides)[3], uint32_t b0,
+               uint32_t b1) {
+    if (fault_mask() & kFaultEncode) return false;
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]}, s[3] = {strides[0], strides[1], strides[2]};
+    const cuuint32_t box[4] = {b0, b1, 1, 1}, estr[4] = {1, 1, 1, 1};
+    return fn(static_cast<CUtensorMap *>(map), elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
+              const_cast<void *>(ptr), d, s, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              elem == 2 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace projgb
+
 extern "C" {
 
 const char *proj_status_string(proj_status_t s) {

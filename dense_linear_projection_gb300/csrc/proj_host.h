@@ -47,6 +47,11 @@ inline bool is_current(int device) {
     return now == device && now >= 0;
 }
 
+// A 4-D tensor map (a CUtensorMap at `map`) of 2- or 1-byte elements, boxes of b0 × b1 of the inner two
+// dimensions; strides in bytes.  Two-byte rows are 128-byte swizzled.  False where the driver refuses it.
+bool encode_4d(void *map, const void *ptr, int elem, const uint64_t (&dims)[4], const uint64_t (&strides)[3], uint32_t b0,
+               uint32_t b1);
+
 inline cudaStream_t as_stream(void *s) { return static_cast<cudaStream_t>(s); }
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
