@@ -67,7 +67,7 @@ struct PrefixShape {
 };
 
 struct PrefixCtl {
-    uint64_t full[8], empty[8], raw_full[4][kPrefixLoadWarps], q_full, q_empty, x_full[2], p_full[2], o_done[2], drain;
+    uint64_t full[8], empty[8], raw_full[4][kPrefixLoadWarps], q_full, q_empty, x_full[2], p_full[2][2], o_done[2], drain;
     uint64_t base_full[2][4];  // [tile & 1][quarter of the rows]: the tile has left its base
     uint32_t tmem;
     int abort_flag;
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         mbar_init(smem_u32(&ctl->q_empty), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&ctl->x_full[i]), 1);
-            mbar_init(smem_u32(&ctl->p_full[i]), 32 * kPrefixSoftmaxWarps / kPrefixGroups);
+            for (int h = 0; h < 2; ++h) mbar_init(smem_u32(&ctl->p_full[i][h]), 32 * kPrefixSoftmaxWarps / kPrefixGroups);
             mbar_init(smem_u32(&ctl->o_done[i]), 1);
             for (int q = 0; q < 4; ++q) mbar_init(smem_u32(&ctl->base_full[i][q]), 32 * kPrefixPieces);
         }
@@ -363,6 +363,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         auto chunk_to = [&](int rows_of, int r, int chunk) {
             return static_cast<uint32_t>((chunk >> 3) * rows_of * 128 + r * 128 + (((chunk & 7) ^ (r & 7)) << 4));
         };
+        // This thread's copies are in shared memory, where the tensor core reads them (what TMA
+        // brings needs no fence).
+        auto copies_done = []() {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            async_proxy_fence();
+        };
         int64_t n = 0, pos = work.pos;  // tiles loaded; their line
         int slot = 0;                   // of the ring
         uint32_t phase = 0;
@@ -435,7 +441,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     cp_async16(smem_u32(smem) + chunk_to(kPrefixRows, r, qc),
                                p.q + (fill ? b * p.q_stride + (head * p.group + g) * p.cache.head_dim + qc * 8 : 0), fill);
                 }
-                cp_async_arrive(smem_u32(&ctl->q_full));
+                copies_done();
+                mbar_arrive(smem_u32(&ctl->q_full));
             }
             ++segment;
             for (; ok && pos < seg_end; ++pos, ++n) {
@@ -468,7 +475,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                                         cp_async16n(to + chunk_to(kTokens, loader * kMine + (i + j) * kAtOnce + r_of, c), from + row_offset(row[j]),
                                                     row[j].z);
                             }
-                            cp_async_arrive(bar);
+                            copies_done();
+                            mbar_arrive(bar);
                             if (lane == 0) mbar_arrive(bar);
                         }
                     } else {
@@ -539,7 +547,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     x_first = false;
                 }
                 if (!warp_waited(&ctl->full[xslot], xphase)) return false;
-                async_proxy_fence();
                 tc_fence_after_sync();
                 const uint64_t kd = k_desc + static_cast<uint64_t>(xslot) * (kTile >> 4);
                 const uint32_t d = tmem + kDim + static_cast<uint32_t>(n & 1) * Shape::kBuffer;
@@ -573,23 +580,35 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     seg_end = stretch_end(pos);
                 }
                 if (xpos < work.end && !issue_x(n + 1)) break;
-                if (!warp_waited(&ctl->p_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u)) break;
                 if (!warp_waited(&ctl->full[vslot], vphase)) break;
-                async_proxy_fence();
-                tc_fence_after_sync();
                 const uint64_t vd = v_desc + static_cast<uint64_t>(vslot) * (kTile >> 4);
                 const uint32_t a = tmem + kDim + static_cast<uint32_t>(n & 1) * Shape::kBuffer;
                 const uint32_t more = pos > seg_begin;
-                if (elect_one()) {
+                // The first half of each piece's tokens, then the second, as P of them is there: the
+                // tensor core works on the one while the other is made.
 #pragma unroll
-                    for (int y = 0; y < 3; ++y)
+                for (int h = 0; ok && h < 2; ++h) {
+                    ok = warp_waited(&ctl->p_full[n & 1][h], static_cast<uint32_t>(n >> 1) & 1u);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < kTokens / 16; ++k)
-                            tc_mma_ts(tmem, y < 2 ? a + 16 * k + 8 * y : a + kTokens + 8 * k, vd + k * (2048 >> 4), kIdO,
-                                      y > 0 || k > 0 ? 1u : more);
-                    tc_commit<false>(smem_u32(&ctl->empty[vslot]));
-                    tc_commit<false>(smem_u32(&ctl->o_done[n & 1]));
+                        for (int y = 0; y < 3; ++y)
+#pragma unroll
+                            for (int i = 0; i < kTokens / 32; ++i) {
+                                constexpr int kSteps = kPiece / 32;  // 16-token steps of a half
+                                const int k = i / kSteps * 2 * kSteps + h * kSteps + i % kSteps;
+                                tc_mma_ts(tmem, y < 2 ? a + 16 * k + 8 * y : a + kTokens + 8 * k, vd + k * (2048 >> 4), kIdO,
+                                          h > 0 || y > 0 || i > 0 ? 1u : more);
+                            }
+                        if (h == 1) {
+                            tc_commit<false>(smem_u32(&ctl->empty[vslot]));
+                            tc_commit<false>(smem_u32(&ctl->o_done[n & 1]));
+                        }
+                    }
+                    __syncwarp();
                 }
+                if (!ok) break;
                 __syncwarp();
                 next(vslot, vphase);
             }
@@ -709,12 +728,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     }
                     tmem_store(x0 + 16 * i, hi_mid);
                     tmem_store8(buffer + kTokens + piece * (kPiece / 2) + 8 * i, lo);
+                    if (i % (kPiece / 32) == kPiece / 32 - 1) {
+                        tmem_store_wait();
+                        tc_fence_before_sync();
+                        mbar_arrive(smem_u32(&ctl->p_full[group][i / (kPiece / 32)]));
+                    }
                 }
                 const float2 sums = pair_to(sum);
                 l += sums.x + sums.y;
-                tmem_store_wait();
-                tc_fence_before_sync();
-                mbar_arrive(smem_u32(&ctl->p_full[group]));
             }
             // The part: o of every tile of the stretch, relative to the last base, from both groups.
             named_barrier(all_barrier, 32 * kPrefixSoftmaxWarps);
