@@ -67,9 +67,7 @@ proj_status_t append(proj_kv_handle_t h, const Norms *norms, int64_t tokens, con
         reinterpret_cast<uintptr_t>(rope) % 4 != 0 || reinterpret_cast<uintptr_t>(positions) % 4 != 0 ||
         reinterpret_cast<uintptr_t>(seq_ids) % 4 != 0 || reinterpret_cast<uintptr_t>(page_table) % 4 != 0)
         return PROJ_ERR_MISALIGNED;
-    const uintptr_t weight_bytes = norms && norms->dtype == PROJ_F32 ? 4 : 2;
-    if (norms && (reinterpret_cast<uintptr_t>(norms->q) % weight_bytes != 0 || reinterpret_cast<uintptr_t>(norms->k) % weight_bytes != 0 ||
-                  reinterpret_cast<uintptr_t>(norms->rope_rows) % 4 != 0))
+    if (norms && (!aligned16(norms->q) || !aligned16(norms->k) || reinterpret_cast<uintptr_t>(norms->rope_rows) % 4 != 0))
         return PROJ_ERR_MISALIGNED;
     KvAppendParams p{};
     p.cache = view_of(h, page_table, table_width);

@@ -65,7 +65,8 @@ proj_status_t proj_kv_evict(proj_kv_handle_t h, int64_t sequences, const int32_t
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, dev::kv_evict_select_kernel, p) != cudaSuccess) {
+    const bool held = table_width * d.page_size <= int64_t(ranks) * dev::kEvictHeld * dev::kEvictSlab;
+    if (cudaLaunchKernelEx(&cfg, held ? dev::kv_evict_select_kernel<true> : dev::kv_evict_select_kernel<false>, p) != cudaSuccess) {
         cudaGetLastError();
         return PROJ_ERR_CUDA;
     }

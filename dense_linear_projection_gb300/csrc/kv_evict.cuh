@@ -17,15 +17,17 @@ namespace dev {
 // some are taken: a token's place among the kept ones is then
 //   (keys above the border before it) + min(keys at the border before it, rest).
 //
-// What bounds it: the few short passes, one after another (the scores come from
-// memory once; the later passes find them in the L1 cache).  A cluster shares a
-// long row, its counts meet in distributed shared memory, and every CTA of it does
-// the same search on the sums.
+// What bounds it: the few short passes, one after another.  The scores come from
+// memory once and stay in registers (kHeld; longer rows are read again by every
+// pass).  A cluster shares a long row, its counts meet in distributed shared memory,
+// and every CTA of it does the same search on the sums.
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictBins = 2048;
 constexpr int kEvictSpan = 8192;    // scores of a CTA, where a cluster of at most kEvictCluster gives that
 constexpr int kEvictCluster = 8;
-constexpr int kEvictPer = 4;        // consecutive scores of a thread, when their places are counted
+constexpr int kEvictPer = 4;        // consecutive scores of a thread: its places are counted over these
+constexpr int kEvictSlab = kEvictThreads * kEvictPer;
+constexpr int kEvictHeld = 4;       // slabs in registers
 
 __device__ __forceinline__ uint32_t score_key(float s) {
     const uint32_t u = __float_as_uint(s + 0.f);  // −0 becomes 0
@@ -50,6 +52,7 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *warps) {
     return x + before;
 }
 
+template <bool kHeld>
 __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const KvEvictParams p) {
     __shared__ uint32_t bins[3][kEvictBins];
     __shared__ uint32_t warps[32], found[2], counts[2];
@@ -68,52 +71,88 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
         n = n < 0 ? 0 : table_tokens;
     }
     const int64_t stay = n < p.keep ? n : p.keep;
-    if (rank == 0 && tid == 0 && row % p.cache.kv_heads == 0) p.lens_out[b] = static_cast<int32_t>(stay);
+    // The last ones (all, where they fit) keep their order; `want` of the first m are chosen.
+    const int64_t want = n > p.keep ? p.keep - p.recent : 0, m = n > p.keep ? n - p.recent : 0;
+    const int64_t span = ((m + ranks - 1) / ranks + kEvictPer - 1) / kEvictPer * kEvictPer;
+    const int64_t low = span * rank < m ? span * rank : m, high = low + span < m ? low + span : m;
     const float *in = p.scores + row * p.score_tokens;
+    float held[kHeld ? kEvictHeld : 1][kEvictPer];
+    if (kHeld && want > 0) {
+#pragma unroll
+        for (int k = 0; k < kEvictHeld; ++k)
+#pragma unroll
+            for (int j = 0; j < kEvictPer; ++j) {
+                const int64_t i = low + k * kEvictSlab + tid * kEvictPer + j;
+                held[k][j] = i < high ? in[i] : 0.f;
+            }
+    }
     float *out = p.scores_out + row * wide;
     int32_t *kept = p.kept + row * p.keep;
     const int64_t step = int64_t(ranks) * kEvictThreads, mine = int64_t(rank) * kEvictThreads + tid;
+    if (rank == 0 && tid == 0 && row % p.cache.kv_heads == 0) p.lens_out[b] = static_cast<int32_t>(stay);
     for (int64_t i = stay + mine; i < wide; i += step) out[i] = 0.f;
     for (int64_t i = stay + mine; i < p.keep; i += step) kept[i] = -1;
-    // The last ones (all, where they fit) keep their order.
-    const int64_t want = n > p.keep ? p.keep - p.recent : 0, m = n > p.keep ? n - p.recent : 0;
     for (int64_t i = m + mine; i < n; i += step) {
         kept[want + i - m] = static_cast<int32_t>(i);
         out[want + i - m] = in[i];
     }
     if (want == 0) return;  // (every CTA of the cluster)
 
-    const int64_t span = ((m + ranks - 1) / ranks + kEvictPer - 1) / kEvictPer * kEvictPer;
-    const int64_t low = span * rank < m ? span * rank : m, high = low + span < m ? low + span : m;
+    // f(first place, scores) for each of this thread's runs of kEvictPer scores; every thread of
+    // the block comes to each, with places at or past `high` where it has none.
+    auto each_run = [&](auto f) {
+        if constexpr (kHeld) {
+#pragma unroll
+            for (int k = 0; k < kEvictHeld; ++k)
+                if (low + k * kEvictSlab < high) f(low + k * kEvictSlab + tid * kEvictPer, held[k]);
+        } else {
+            for (int64_t base = low; base < high; base += kEvictSlab) {
+                float s[kEvictPer];
+#pragma unroll
+                for (int j = 0; j < kEvictPer; ++j) s[j] = base + tid * kEvictPer + j < high ? in[base + tid * kEvictPer + j] : 0.f;
+                f(base + tid * kEvictPer, s);
+            }
+        }
+    };
+    // The whole row's CTAs have come here.
+    auto all_here = [&]() {
+        if (ranks > 1) {
+            cluster_arrive();
+            cluster_wait();
+        } else {
+            __syncthreads();
+        }
+    };
+    __syncthreads();
     uint32_t border = 0, rest = static_cast<uint32_t>(want);
 #pragma unroll
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const uint32_t digits = pass == 2 ? 1023u : 2047u;
-        __syncthreads();
-        for (int64_t base = low; base < high; base += kEvictThreads) {
-            const int64_t i = base + tid;
-            const uint32_t key = i < high ? score_key(in[i]) : 0u;
-            const bool counted = i < high && (pass == 0 || (key >> (shift + (pass == 2 ? 10 : 11))) == border);
-            const uint32_t digit = (key >> shift) & digits;
-            // One addition for a warp whose digits are all alike (scores that are all zero).
-            const uint32_t who = __ballot_sync(0xffffffffu, counted);
-            if (who == 0) continue;
-            const int lead = __ffs(who) - 1;
-            const uint32_t first = __shfl_sync(0xffffffffu, digit, lead);
-            if (__all_sync(0xffffffffu, !counted || digit == first)) {
-                if ((tid & 31) == lead) atomicAdd(&bins[pass][first], __popc(who));
-            } else if (counted) {
-                atomicAdd(&bins[pass][digit], 1u);
+        each_run([&](int64_t i0, const float(&s)[kEvictPer]) {
+#pragma unroll
+            for (int j = 0; j < kEvictPer; ++j) {
+                const uint32_t key = score_key(s[j]);
+                const bool counted = i0 + j < high && (pass == 0 || (key >> (shift + (pass == 2 ? 10 : 11))) == border);
+                const uint32_t digit = (key >> shift) & digits;
+                // One addition for a warp whose digits are all alike (scores that are all zero).
+                const uint32_t who = __ballot_sync(0xffffffffu, counted);
+                if (who == 0) continue;
+                const int lead = __ffs(who) - 1;
+                const uint32_t first = __shfl_sync(0xffffffffu, digit, lead);
+                if (__all_sync(0xffffffffu, !counted || digit == first)) {
+                    if ((tid & 31) == lead) atomicAdd(&bins[pass][first], __popc(who));
+                } else if (counted) {
+                    atomicAdd(&bins[pass][digit], 1u);
+                }
             }
-        }
-        cluster_arrive();
-        cluster_wait();
+        });
+        all_here();
         // Two digits a thread, the highest first, over all CTAs of the cluster.
         const uint32_t d1 = kEvictBins - 1 - 2 * tid, d0 = d1 - 1;
-        uint32_t c1 = 0, c0 = 0;
-        for (uint32_t r = 0; r < ranks; ++r) {
-            const uint32_t at = map_to_rank(smem_u32(&bins[pass][0]), r);
+        uint32_t c1 = bins[pass][d1], c0 = bins[pass][d0];
+        for (uint32_t o = 1; o < ranks; ++o) {
+            const uint32_t at = map_to_rank(smem_u32(&bins[pass][0]), rank + o < ranks ? rank + o : rank + o - ranks);
             c1 += ld_cluster_u32(at + d1 * 4);
             c0 += ld_cluster_u32(at + d0 * 4);
         }
@@ -132,18 +171,20 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
     uint32_t above = 0, equal = 0;
     if (ranks > 1) {
         uint32_t a = 0, e = 0;
-        for (int64_t i = low + tid; i < high; i += kEvictThreads) {
-            const uint32_t key = score_key(in[i]);
-            a += key > border;
-            e += key == border;
-        }
+        each_run([&](int64_t i0, const float(&s)[kEvictPer]) {
+#pragma unroll
+            for (int j = 0; j < kEvictPer; ++j) {
+                const uint32_t key = score_key(s[j]);
+                a += i0 + j < high && key > border;
+                e += i0 + j < high && key == border;
+            }
+        });
         a = __reduce_add_sync(0xffffffffu, a), e = __reduce_add_sync(0xffffffffu, e);
         if ((tid & 31) == 0) {
             if (a) atomicAdd(&counts[0], a);
             if (e) atomicAdd(&counts[1], e);
         }
-        cluster_arrive();
-        cluster_wait();
+        all_here();
         for (uint32_t r = 0; r < rank; ++r) {
             const uint32_t at = map_to_rank(smem_u32(&counts[0]), r);
             above += ld_cluster_u32(at);
@@ -151,13 +192,10 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
         }
         cluster_arrive();  // no CTA leaves while another reads its counts
     }
-    for (int64_t base = low; base < high; base += kEvictThreads * kEvictPer) {
-        const int64_t i0 = base + tid * kEvictPer;
-        float s[kEvictPer];
-        uint32_t key[kEvictPer], mine_of = 0;  // (above << 16) + equal: 4096 at most of each
+    each_run([&](int64_t i0, const float(&s)[kEvictPer]) {
+        uint32_t key[kEvictPer], mine_of = 0;  // (above << 16) + equal: kEvictSlab at most of each
 #pragma unroll
         for (int j = 0; j < kEvictPer; ++j) {
-            s[j] = i0 + j < high ? in[i0 + j] : 0.f;
             key[j] = score_key(s[j]);
             if (i0 + j < high) mine_of += key[j] > border ? 0x10000u : key[j] == border ? 1u : 0u;
         }
@@ -177,7 +215,7 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
         if (tid == kEvictThreads - 1) found[0] = upto;
         __syncthreads();
         above += found[0] >> 16, equal += found[0] & 0xffffu;
-    }
+    });
     if (ranks > 1) cluster_wait();
 }
 

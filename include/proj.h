@@ -645,8 +645,8 @@ proj_status_t proj_kv_destroy(proj_kv_handle_t h);
  * proj_kv_append_normed: proj_kv_append with the norm of every head of q and k first,
  *     y[e] = x[e] · w[e] / sqrt(Σ x² / head_dim + eps),
  *   in fp32, then the rotation, then the one rounding.  q_weight, k_weight:
- *   [head_dim] of weight_dtype (PROJ_BF16 or PROJ_F32), NULL for no norm of q or of k;
- *   eps finite and at least 0.  Every bf16 head has its norm: sums of squares out
+ *   [head_dim] of weight_dtype (PROJ_BF16 or PROJ_F32), 16-byte aligned, NULL for no
+ *   norm of q or of k; eps finite and at least 0.  Every bf16 head has its norm: sums of squares out
  *   of fp32's range are scaled.  rope_rows: the rope table's row of each token
  *   (int32 [tokens]), NULL for its position.  After an eviction a token's place in
  *   the cache, which positions[i] names, is not its position in the text any more.

@@ -77,7 +77,7 @@ def test_lengths_and_budgets(lens, keep, recent):
     run(lens, 2, 64, 16, keep, recent)
 
 
-@pytest.mark.parametrize("n", [1023, 4096, 4097, 8192, 8193, 20000, 70001])
+@pytest.mark.parametrize("n", [1023, 4096, 4097, 8192, 8193, 20000, 70001, 140001])
 @pytest.mark.parametrize("part", [0.01, 0.5, 0.999])
 def test_long_rows(n, part):
     run([n, n // 3], 2, 16, 64, max(2, int(n * part)), 1)
