@@ -151,7 +151,7 @@ proj_status_t proj_kv_create(proj_kv_handle_t *out, const proj_kv_desc_t *desc, 
     const int row_bytes = (d.head_dim <= 64 ? 64 : d.head_dim <= 128 ? 128 : 256) * elem;
     if (row_bytes <= 128 && d.kv_heads % 2 == 0 && h->chunks == 1) h->key_heads = 2;
     const AttendInstance a = instance_for<kAttendPlain>(h);
-    if (!prepare_attend<kAttendPlain>(h) || !prepare_scored(h) || !prepare_shared(h)) {
+    if (!prepare_attend<kAttendPlain>(h) || !prepare_scored(h) || !prepare_shared(h) || !prepare_evict()) {
         delete h;
         return PROJ_ERR_CUDA;
     }

@@ -8,6 +8,16 @@
 
 using namespace projgb;
 
+namespace projgb {
+bool prepare_evict() {
+    if (cudaFuncSetAttribute(dev::kv_evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, dev::kEvictSlab * 4) ==
+        cudaSuccess)
+        return true;
+    cudaGetLastError();
+    return false;
+}
+}  // namespace projgb
+
 extern "C" {
 
 proj_status_t proj_kv_evict(proj_kv_handle_t h, int64_t sequences, const int32_t *page_table, int64_t table_width,
@@ -65,17 +75,23 @@ proj_status_t proj_kv_evict(proj_kv_handle_t h, int64_t sequences, const int32_t
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const bool held = table_width * d.page_size <= int64_t(ranks) * dev::kEvictHeld * dev::kEvictSlab;
+    // Its scores in shared memory, where they fit (65 KiB at most).
+    const int64_t span = ((table_width * d.page_size + ranks - 1) / ranks + 3) / 4 * 4;
+    const bool held = span <= dev::kEvictSlab;
+    cfg.dynamicSmemBytes = held ? static_cast<size_t>(span) * 4 : 0;
     if (cudaLaunchKernelEx(&cfg, held ? dev::kv_evict_select_kernel<true> : dev::kv_evict_select_kernel<false>, p) != cudaSuccess) {
         cudaGetLastError();
         return PROJ_ERR_CUDA;
     }
     if (keep == 0) return PROJ_OK;
-    const int64_t at_once = int64_t(dev::kEvictCopyThreads / (d.head_dim * h->elem / 16)) * dev::kEvictAhead;
+    // Tokens of a block: 256, or fewer where that leaves SMs without one; blocks of a row: enough
+    // for every SM to have kEvictMostBlocks.
+    int tokens = dev::kEvictCopyThreads;
+    while (tokens > 32 && rows * ((keep + tokens - 1) / tokens) < 2 * int64_t(h->sm_count)) tokens /= 2;
     int64_t of_row = (int64_t(h->sm_count) * kEvictMostBlocks + rows - 1) / rows;
-    if (of_row > (keep + at_once - 1) / at_once) of_row = (keep + at_once - 1) / at_once;
+    if (of_row > (keep + tokens - 1) / tokens) of_row = (keep + tokens - 1) / tokens;
     return launch(dev::kv_evict_copy_kernel, dim3(static_cast<unsigned>(rows * of_row)), dev::kEvictCopyThreads, 0, stream, p,
-                  static_cast<int>(of_row));
+                  static_cast<int>(of_row), tokens);
 }
 
 }  // extern "C"

@@ -183,7 +183,9 @@ bool prepare_attend(const proj_kv_s *h) {
     return false;
 }
 
-// The same for the kernels of scored and of shared-prefix attention (kv_scored.cu, kv_shared.cu).
+// The same for the kernels of scored and shared-prefix attention and of eviction (kv_scored.cu,
+// kv_shared.cu, kv_evict.cu).
+bool prepare_evict();
 bool prepare_scored(const proj_kv_s *h);
 bool prepare_shared(const proj_kv_s *h);
 
