@@ -11,7 +11,7 @@ using namespace projgb;
 namespace projgb {
 bool prepare_evict() {
     if (cudaFuncSetAttribute(dev::kv_evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, dev::kEvictSlab * 4) ==
-        cudaSuccess)
+            cudaSuccess)
         return true;
     cudaGetLastError();
     return false;
@@ -58,7 +58,7 @@ proj_status_t proj_kv_evict(proj_kv_handle_t h, int64_t sequences, const int32_t
     p.elem = h->elem;
     p.status = h->status;
 
-    // CTAs of a row: as many as give each kEvictSpan scores, within a portable cluster.
+    // CTAs of a row: as many as give each kEvictSpan scores, within a cluster.
     const int64_t rows = sequences * d.kv_heads;
     unsigned ranks = 1;
     while (ranks < dev::kEvictCluster && table_width * d.page_size > int64_t(ranks) * dev::kEvictSpan) ranks *= 2;

@@ -18,15 +18,16 @@ namespace dev {
 //   (keys above the border before it) + min(keys at the border before it, rest).
 //
 // What bounds it: the few short passes, one after another.  The scores come from
-// memory once and stay in shared memory as keys (kHeld; rows of more than 16384 a CTA
+// memory once and stay in shared memory (kHeld; rows of more than 16384 a CTA
 // are read again by every pass), and the passes are loops of little code: unrolled
 // over scores held in registers they waited for instructions.  A cluster shares a long
-// row: each CTA adds what it counted to the sums of all (mostly a few of the digits
-// occur), and does the same search on them.
+// row and does the same search on the sums of its CTAs' counts, in each of them: of the
+// first digit, of which few values occur, a CTA adds its own to everyone's sums; of the
+// others everyone reads all counts.
 constexpr int kEvictThreads = 512, kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictBins = 2048;
 constexpr int kEvictSpan = 8192;    // scores of a CTA, where a cluster of at most kEvictCluster gives that
-constexpr int kEvictCluster = 8;
+constexpr int kEvictCluster = 8;    // (16, with half the scores each: 61 us instead of 57 for one row of 131071)
 constexpr int kEvictRun = 128;      // scores of a warp at a time, four a lane
 constexpr int kEvictSlab = 16384;   // scores of a CTA at a time: places within them take 16 bits
 
@@ -49,21 +50,26 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *warps) {
     __syncthreads();
     return x + __reduce_add_sync(0xffffffffu, lane < warp ? warps[lane] : 0u);
 }
+__device__ __forceinline__ uint4 ld_cluster_u4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
 __device__ __forceinline__ void add_cluster(uint32_t cluster_addr, uint32_t x) {
     asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(cluster_addr), "r"(x) : "memory");
 }
 
 template <bool kHeld>
 __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const KvEvictParams p) {
-    __shared__ __align__(16) uint32_t bins[kEvictBins], sums[3][kEvictBins];  // of this CTA's keys in a pass; of the row's
+    __shared__ __align__(16) uint32_t bins[3][kEvictBins], sums[kEvictBins];  // of this CTA's keys; of the row's first digits
     __shared__ uint32_t warps[kEvictWarps], found[2], totals[2];
-    extern __shared__ __align__(16) uint32_t held[];  // this CTA's keys
+    extern __shared__ __align__(16) float held[];  // this CTA's scores
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_ctarank(), ranks = cluster_nctarank();
     static_assert(kEvictBins == 4 * kEvictThreads, "four digits a thread");
-    reinterpret_cast<uint4 *>(bins)[tid] = make_uint4(0u, 0u, 0u, 0u);
-    for (int i = 0; i < 3; ++i) reinterpret_cast<uint4 *>(sums[i])[tid] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < 3; ++i) reinterpret_cast<uint4 *>(bins[i])[tid] = make_uint4(0u, 0u, 0u, 0u);
+    reinterpret_cast<uint4 *>(sums)[tid] = make_uint4(0u, 0u, 0u, 0u);
     if (tid < 2) totals[tid] = 0;
     if (ranks > 1) cluster_arrive();  // the sums are clear
     griddep_wait();
@@ -83,23 +89,11 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
     const int mine = static_cast<int>(low + span < m ? span : m - low);  // scores low, low + 1 ... of this CTA
     const float *row_scores = p.scores + row * p.score_tokens, *in = row_scores + low;
     const bool vec = (reinterpret_cast<uintptr_t>(in) & 15u) == 0;
-    // Keys of scores i .. i + 3 of this CTA, i a multiple of four; zeros at and past `mine`.
-    auto load_keys = [&](int i, uint32_t(&x)[4]) {
-        if (vec && i + 4 <= mine) {
-            const float4 v = *reinterpret_cast<const float4 *>(in + i);
-            x[0] = score_key(v.x), x[1] = score_key(v.y), x[2] = score_key(v.z), x[3] = score_key(v.w);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = i + j < mine ? score_key(in[i + j]) : 0u;
-        }
-    };
     if (kHeld && want > 0) {
+        const int whole = vec ? mine / 4 : 0;
+        for (int i = tid; i < whole; i += kEvictThreads) cp_async16(smem_u32(held + 4 * i), in + 4 * i);
 #pragma unroll 4
-        for (int i = 4 * tid; i < mine; i += 4 * kEvictThreads) {
-            uint32_t x[4];
-            load_keys(i, x);
-            *reinterpret_cast<uint4 *>(held + i) = make_uint4(x[0], x[1], x[2], x[3]);
-        }
+        for (int i = 4 * whole + tid; i < mine; i += kEvictThreads) held[i] = in[i];
     }
     float *out = p.scores_out + row * wide;
     int32_t *kept = p.kept + row * p.keep;
@@ -115,12 +109,14 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
     if (ranks > 1) cluster_wait();
     if (want == 0) return;  // (every CTA of the cluster)
 
-    auto four = [&](int i, uint32_t(&x)[4]) {
-        if constexpr (kHeld) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(held + i);  // (the last four may be past `mine`: zeros)
+    // Scores i .. i + 3 of this CTA, i a multiple of four below `mine`; what is at and past `mine` is not used.
+    auto four = [&](int i, float(&x)[4]) {
+        if (kHeld || (vec && i + 4 <= mine)) {
+            const float4 v = kHeld ? *reinterpret_cast<const float4 *>(held + i) : *reinterpret_cast<const float4 *>(in + i);
             x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
         } else {
-            load_keys(i, x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = i + j < mine ? in[i + j] : 0.f;
         }
     };
     // The whole row's CTAs have come here.
@@ -132,6 +128,7 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
             __syncthreads();
         }
     };
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     uint32_t border = 0, rest = static_cast<uint32_t>(want);
     uint32_t more = 0, level_here = 0;  // this thread's digits' keys of this CTA above the border; at it
@@ -141,30 +138,43 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
         const uint32_t digits = pass == 2 ? 1023u : 2047u;
 #pragma unroll 2
         for (int i = 4 * tid; i < mine; i += 4 * kEvictThreads) {
-            uint32_t key[4];
-            four(i, key);
+            float x[4];
+            four(i, x);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (i + j < mine && (pass == 0 || key[j] >> known == border)) atomicAdd(&bins[(key[j] >> shift) & digits], 1u);
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t key = score_key(x[j]);
+                if (i + j < mine && (pass == 0 || key >> known == border)) atomicAdd(&bins[pass][(key >> shift) & digits], 1u);
+            }
         }
         __syncthreads();
         // Four digits a thread, the highest first.
         const uint32_t d0 = kEvictBins - 4 - 4 * tid;
-        const uint4 local = *reinterpret_cast<const uint4 *>(bins + d0);
+        const uint4 local = *reinterpret_cast<const uint4 *>(&bins[pass][d0]);
         uint4 c = local;
         if (ranks > 1) {
-            const uint32_t has[4] = {local.x, local.y, local.z, local.w};
+            if (pass == 0) {
+                const uint32_t has[4] = {local.x, local.y, local.z, local.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (has[j])
-                    for (uint32_t r = 0; r < ranks; ++r) add_cluster(map_to_rank(smem_u32(&sums[pass][d0 + j]), r), has[j]);
-            all_here();
-            c = *reinterpret_cast<const uint4 *>(&sums[pass][d0]);
+                for (int j = 0; j < 4; ++j)
+                    if (has[j])
+                        for (uint32_t r = 0; r < ranks; ++r) add_cluster(map_to_rank(smem_u32(&sums[d0 + j]), r), has[j]);
+                all_here();
+                c = *reinterpret_cast<const uint4 *>(sums + d0);
+            } else {
+                all_here();
+                uint4 other[kEvictCluster - 1];  // (asked for together)
+#pragma unroll
+                for (uint32_t o = 1; o < kEvictCluster; ++o) {
+                    other[o - 1] = make_uint4(0u, 0u, 0u, 0u);
+                    if (o < ranks) other[o - 1] = ld_cluster_u4(map_to_rank(smem_u32(&bins[pass][d0]), rank + o < ranks ? rank + o : rank + o - ranks));
+                }
+#pragma unroll
+                for (int o = 0; o < kEvictCluster - 1; ++o) c.x += other[o].x, c.y += other[o].y, c.z += other[o].z, c.w += other[o].w;
+            }
         }
         const uint32_t all = c.x + c.y + c.z + c.w;
-        uint32_t before = block_scan(all, warps) - all;  // (its barriers: every thread has read its bins)
+        uint32_t before = block_scan(all, warps) - all;
         const uint32_t counts[4] = {c.w, c.z, c.y, c.x}, here[4] = {local.w, local.z, local.y, local.x};
-        *reinterpret_cast<uint4 *>(bins + d0) = make_uint4(0u, 0u, 0u, 0u);
         level_here = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -186,12 +196,18 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
         const int left = mine - base < kEvictSlab ? mine - base : kEvictSlab;
         return (left + kEvictWarps * kEvictRun - 1) / (kEvictWarps * kEvictRun);
     };
+    // Kept places and scores of a run, together: over the first two digits' counts, which the
+    // other CTAs have read by the last one's.
+    uint2 *stage = reinterpret_cast<uint2 *>(bins[0]) + warp * kEvictRun;
+    static_assert(kEvictWarps * kEvictRun * sizeof(uint2) <= 2 * sizeof(bins[0]), "room");
     // (keys above the border << 16) + (keys at it), of four.
-    auto weigh = [&](int i, const uint32_t(&key)[4]) {
+    auto weigh = [&](int i, const float(&x)[4]) {
         uint32_t sum = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (i + j < mine) sum += key[j] > border ? 0x10000u : key[j] == border ? 1u : 0u;
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t key = score_key(x[j]);
+            if (i + j < mine) sum += key > border ? 0x10000u : key == border ? 1u : 0u;
+        }
         return sum;
     };
     uint32_t above = 0, equal = 0;  // before the slab, first of the CTAs before this one
@@ -213,10 +229,10 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
 #pragma unroll 2
         for (int k = 0; k < runs; ++k) {
             const int i = base + (warp * runs + k) * kEvictRun + lane * 4;
-            uint32_t key[4];
+            float x[4];
             if (i < mine) {
-                four(i, key);
-                of_warp += weigh(i, key);
+                four(i, x);
+                of_warp += weigh(i, x);
             }
         }
         of_warp = __reduce_add_sync(0xffffffffu, of_warp);
@@ -230,9 +246,9 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
 #pragma unroll 1
         for (int k = 0; k < runs; ++k) {
             const int i = base + (warp * runs + k) * kEvictRun + lane * 4;
-            uint32_t key[4] = {0u, 0u, 0u, 0u};
-            if (i < mine) four(i, key);
-            const uint32_t sum = weigh(i, key);
+            float x[4] = {0.f, 0.f, 0.f, 0.f};
+            if (i < mine) four(i, x);
+            const uint32_t sum = weigh(i, x);
             uint32_t upto = sum;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -240,18 +256,26 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
                 if (lane >= o) upto += other;
             }
             uint32_t a = a0 + ((upto - sum) >> 16), e = e0 + ((upto - sum) & 0xffffu);
+            // The kept ones are next to each other: gathered in shared memory, and then written
+            // in whole rows of the warp (stores of the few of each lane took half the time).
+            const uint32_t begin = a0 + (e0 < rest ? e0 : rest);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bool there = i + j < mine, up = there && key[j] > border, level = there && key[j] == border;
-                if (up || (level && e < rest)) {
-                    const uint32_t to = a + (e < rest ? e : rest);
-                    kept[to] = static_cast<int32_t>(low) + i + j;
-                    out[to] = in[i + j];
-                }
+                const uint32_t key = score_key(x[j]);
+                const bool there = i + j < mine, up = there && key > border, level = there && key == border;
+                if (up || (level && e < rest))
+                    stage[a + (e < rest ? e : rest) - begin] = make_uint2(static_cast<uint32_t>(low) + i + j, __float_as_uint(x[j]));
                 a += up, e += level;
             }
             const uint32_t run = __shfl_sync(0xffffffffu, upto, 31);
             a0 += run >> 16, e0 += run & 0xffffu;
+            __syncwarp();
+            for (uint32_t o = lane; o < a0 + (e0 < rest ? e0 : rest) - begin; o += 32) {
+                const uint2 v = stage[o];
+                kept[begin + o] = static_cast<int32_t>(v.x);
+                out[begin + o] = __uint_as_float(v.y);
+            }
+            __syncwarp();
         }
         above += slab >> 16, equal += slab & 0xffffu;
     }
