@@ -72,6 +72,13 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
     return h;
 }
+__device__ __forceinline__ void cp_async16_hint(uint32_t to, const void *from, bool fill, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(to), "l"(from), "r"(fill ? 16 : 0), "l"(policy)
+                 : "memory");
+}
+__device__ __forceinline__ void store_hint(float *to, float2 v, uint64_t policy) {
+    asm volatile("st.global.L2::cache_hint.v2.f32 [%0], {%1, %2}, %3;" ::"l"(to), "f"(v.x), "f"(v.y), "l"(policy) : "memory");
+}
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -384,7 +391,9 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
             *reinterpret_cast<uint4 *>(smem + at) = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
     }
-    griddep_wait();
+    // (A part's kernel is launched once everything before the prefix's kernel is complete: it waits
+    // for the prefix's own at its end, so that the join, which waits for this one, finds both.)
+    if constexpr (kLeaves != kAttendPart) griddep_wait();
 
     // The line of work: every lane sums a run of sequences, and a scan over
     // the lanes (the same in every warp: no barrier) gives the total and where
@@ -463,6 +472,16 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
 #pragma unroll
     for (int s = 0; s < kStages; ++s) valid[s] = 0;
     const int row_chunks = cache.head_dim * Shape::kElem / 16;
+    // Logits are read again by the next kernel and keys and values are not: with these two hints
+    // more of the logits are still in the L2 cache then.
+    const uint64_t keep_policy = kLeaves == kAttendLogits ? l2_policy_evict_last() : 0;
+    const uint64_t pass_policy = kLeaves == kAttendLogits ? l2_policy_evict_first() : 0;
+    auto copy16 = [&](uint32_t to, const void *from, bool fill) {
+        if constexpr (kLeaves == kAttendLogits)
+            cp_async16_hint(to, from, fill, pass_policy);
+        else
+            cp_async16(to, from, fill);
+    };
     auto load = [&](int slot) {
         uint32_t bits = 0;
         if (lmore) {
@@ -480,8 +499,8 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
                 const bool fill = (bits >> r) & 1u;
                 if (c < row_chunks) {
                     const uint32_t d = to + chunk_at<kRow>(r, c);
-                    cp_async16(d, kc + (fill ? at : 0), fill);
-                    cp_async16(d + kStep * kRow, vc + (fill ? at : 0), fill);
+                    copy16(d, kc + (fill ? at : 0), fill);
+                    copy16(d + kStep * kRow, vc + (fill ? at : 0), fill);
                 }
             }
             ltok += Shape::kTile;
@@ -509,7 +528,10 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
         if (p.lse)
             for (int h = tid; h < p.q_heads; h += kKvThreads) p.lse[static_cast<int64_t>(b) * p.q_heads + h] = -INFINITY;
     }
-    if (pos >= end) return;
+    if (pos >= end) {
+        if constexpr (kLeaves == kAttendPart) griddep_wait();
+        return;
+    }
 
     // ---- computing, row by row.  The queries of a row are asked for before
     // the row ahead of it is joined.
@@ -680,7 +702,7 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
                             if (tok + at >= seg_last || there <= 0) continue;
                             float *y = to + static_cast<int64_t>(at) * p.group;
                             if (pairs) {
-                                *reinterpret_cast<float2 *>(y) = make_float2(x[n][t][2 * i], x[n][t][2 * i + 1]);
+                                store_hint(y, make_float2(x[n][t][2 * i], x[n][t][2 * i + 1]), keep_policy);
                             } else {
                                 y[0] = x[n][t][2 * i];
                                 if (there > 1) y[1] = x[n][t][2 * i + 1];
@@ -883,6 +905,7 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
         __syncthreads();  // the join buffer is free again
     }
     cp_async_wait<0>();
+    if constexpr (kLeaves == kAttendPart) griddep_wait();
 }
 
 }  // namespace dev

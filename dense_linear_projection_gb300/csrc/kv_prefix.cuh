@@ -249,7 +249,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         if (tid == 0) atomicOr(p.status, kKvErrWait);
         return;
     }
-    griddep_launch_dependents();
     if (warp == kPrefixSoftmaxWarps + kPrefixLoadWarps) {
         tmem_alloc<false>(smem_u32(&ctl->tmem), 512);
         tmem_relinquish<false>();
@@ -285,6 +284,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     tc_fence_after_sync();
     const uint32_t tmem = ctl->tmem;
     griddep_wait();
+    // Only now: the own tokens' attention, launched after this kernel, does not wait for its results
+    // and reads what the kernels before this one wrote (64 CTAs of a small call leave 88 SMs to it).
+    griddep_launch_dependents();
 
     const PrefixWork work(p);
     auto waited = [&](uint64_t *bar, uint32_t parity) {

@@ -15,6 +15,15 @@ namespace dev {
 // scores.  Computing x again from the keys would read 256 bytes for those 64.
 constexpr int kScoreThreads = 256;
 
+// Four logits, not needed again.
+__device__ __forceinline__ float4 load_once(const float *from, uint64_t policy) {
+    float4 v;
+    asm volatile("ld.global.L2::cache_hint.v4.f32 {%0, %1, %2, %3}, [%4], %5;"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "l"(from), "l"(policy));
+    return v;
+}
+
 template <bool kVec>  // the heads of a token in whole float4s
 __global__ void __launch_bounds__(kScoreThreads) kv_score_kernel(const KvScoreParams p, const int blocks_of_row) {
     griddep_launch_dependents();
@@ -28,6 +37,7 @@ __global__ void __launch_bounds__(kScoreThreads) kv_score_kernel(const KvScorePa
     float *out = p.scores_out + row * p.score_tokens;
     const float *x = p.logits + row * p.table_tokens * p.group;
     const float2 *top = p.top + row * p.group;  // row · group: the first of the key head's query heads
+    const uint64_t policy = l2_policy_evict_first();
     const bool in_place = p.scores == p.scores_out;
     const int64_t from = in_place ? low : 0, to = in_place ? n : p.score_tokens;
     for (int64_t t = from + part * kScoreThreads + threadIdx.x; t < to; t += int64_t(blocks_of_row) * kScoreThreads) {
@@ -37,7 +47,7 @@ __global__ void __launch_bounds__(kScoreThreads) kv_score_kernel(const KvScorePa
             const float *xt = x + t * p.group;
             if constexpr (kVec) {
                 for (int g = 0; g < p.group; g += 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(xt + g);
+                    const float4 v = load_once(xt + g, policy);
                     const float y[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
