@@ -19,8 +19,12 @@
 //     weight takes 12 of the 20 instructions for two of them).  A thread has one row
 //     (tensor-memory lane) and half of a tile's tokens; the two threads of a row meet over its
 //     maximum, and the groups hand on what the weights are relative to.
-//   * o is rescaled only where the maximum grows by more than 2^8 (kLazy): a
-//     weight then is at most 2^8, which costs fp32 sums nothing.
+//   * weights are relative to the maximum of the first tile of a CTA's stretch, so that a
+//     later tile's X is read once and nothing is handed on: fp32 sums and bf16 parts are as
+//     exact at 2^60 as at 1.  Where a tile's sum comes to 2^64, or o is not finite, the
+//     stretch is done again with running maxima, o rescaled where they grow by more than
+//     2^8 (kLazy).  (With running maxima throughout, 128 sequences behind 32768 tokens took
+//     237 us.)
 //   * warps 16..19 fill a ring of token tiles: pages of whole multiples of 8 tokens by TMA
 //     boxes of up to 32 tokens, others, and the prefix's end, by 16-byte asynchronous copies
 //     (which any page size and strides allow); warp 20 issues the products.
@@ -44,6 +48,7 @@ constexpr int kPrefixSoftmaxWarps = 4 * kPrefixSums, kPrefixLoadWarps = 4;
 constexpr int kPrefixLoaders = 32 * kPrefixLoadWarps;
 constexpr int kPrefixThreads = 32 * (kPrefixSoftmaxWarps + kPrefixLoadWarps + 1);
 constexpr float kLazy = 8.f;
+constexpr float kMostSum = 0x1p64f;  // of a tile's weights, relative to the first tile's maximum
 constexpr int64_t kPrefixWaitNs = 1000000000;
 
 template <bool kE4m3, int kDim>
@@ -68,13 +73,14 @@ struct PrefixShape {
 
 struct PrefixCtl {
     uint64_t full[8], empty[8], raw_full[4][kPrefixLoadWarps], q_full, q_empty, x_full[2], p_full[2][2], o_done[2], drain;
-    uint64_t base_full[2][4];  // [tile & 1][quarter of the rows]: the tile has left its base
+    uint64_t base_full[2][4];  // [quarter of the rows]: a base has been left
     uint32_t tmem;
     int abort_flag;
     uint32_t valid[8][4];     // tokens of the last tiles that exist, a bit each
     uint4 row[kPrefixLoadWarps][2][32];  // [tile & 1]: where a token lies in the cache (bytes), how many bytes of it to copy
     float top[2][kPrefixPieces][kPrefixRows];  // [tile & 1]: a row's maximum
-    float base[2][kPrefixRows];                // [tile & 1]: what its weights are relative to
+    float base[2][kPrefixRows];                // what weights are relative to, the last two left
+    uint32_t redo[2];                          // stretches to be done again, a bit each (the last for all from it on)
 };
 static_assert(sizeof(PrefixCtl) <= 9216, "PrefixShape::kCtl");
 
@@ -272,6 +278,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         }
         mbar_init(smem_u32(&ctl->drain), 1);
         ctl->abort_flag = 0;
+        ctl->redo[0] = ctl->redo[1] = 0;
         fence_barrier_init();
     }
     // Elements past head_dim stay zero: no copy ever writes them.
@@ -300,6 +307,29 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         return unit_end < work.end ? unit_end : work.end;
     };
     const int rows = static_cast<int>(p.sequences) * p.group;  // of a key head
+    // What each role does: all stretches with weights relative to their first tile's maxima; then,
+    // once every role is there, the stretches in which that did not do, one by one, with maxima kept
+    // tile by tile.  `begin` and `end`: what is done now; false once there is no more.
+    const int64_t first_unit = work.pos / work.tiles;
+    auto flag_of = [&](int64_t pos) {
+        const int64_t at = pos / work.tiles - first_unit;
+        return at < 63 ? static_cast<int>(at) : 63;
+    };
+    auto more_work = [&](int64_t &begin, int64_t &end, bool &kept) {
+        if (!kept) {
+            named_barrier(10, kPrefixThreads);
+            if (!(ctl->redo[0] | ctl->redo[1])) return false;
+            kept = true;
+            end = work.pos;
+        }
+        for (begin = end; begin < work.end; begin = stretch_end(begin)) {
+            const int at = flag_of(begin);
+            if (!((ctl->redo[at >> 5] >> (at & 31)) & 1u)) continue;
+            end = stretch_end(begin);
+            return true;
+        }
+        return false;
+    };
 
     if (warp >= kPrefixSoftmaxWarps && warp < kPrefixSoftmaxWarps + kPrefixLoadWarps) {
         // ------------------------------------------------------------ loaders
@@ -317,7 +347,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         // of a microsecond: with three of them a tile the loaders were what the rest waited for).
         const uint32_t page_size = static_cast<uint32_t>(p.cache.page_size);
         const uint32_t step_pages = kTokens / page_size, step_places = kTokens % page_size;
-        int64_t look_tile = work.pos % work.tiles, look_unit = work.pos / work.tiles, look_left = work.end - work.pos;
+        int64_t look_tile = 0, look_unit = 0, look_left = 0;
         uint32_t look_page = 0, look_place = 0;  // of the lane's token of tile look_tile
         auto look_at = [&]() {
             const uint32_t t = static_cast<uint32_t>(look_tile) * kTokens + loader * kMine + lane;
@@ -327,8 +357,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         int32_t page = -1;          // asked for, of the tile before look_tile
         uint32_t place_of = 0;
         bool inside = false;
-        int32_t look_head = static_cast<int32_t>(look_unit / p.row_tiles), head_index = look_head;
-        look_at();
+        int32_t look_head = 0, head_index = 0;
         auto ask_page = [&]() {
             inside = look_left > 0 && lane < kMine && look_tile * kTokens + loader * kMine + lane < p.prefix;
             page = inside ? p.cache.table[look_page] : -1;
@@ -346,6 +375,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         };
         // Leaves what was asked for to the warp, for the tile of number `n`, and asks for the next;
         // returns which tokens exist.
+        auto look_from = [&](int64_t begin, int64_t end) {
+            look_tile = begin % work.tiles, look_unit = begin / work.tiles, look_left = end - begin;
+            look_head = static_cast<int32_t>(look_unit / p.row_tiles);
+            look_at();
+            ask_page();
+        };
         int32_t box_page = 0, box_place = 0, box_head = 0;
         auto take_page = [&](int64_t n) {
             const bool there = page >= 0 && page < p.cache.num_pages;
@@ -360,7 +395,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             __syncwarp();
             return bits;
         };
-        ask_page();
         // Where a 16-byte chunk of a row lies in a tile of 64-element blocks, swizzled.
         auto chunk_to = [&](int rows_of, int r, int chunk) {
             return static_cast<uint32_t>((chunk >> 3) * rows_of * 128 + r * 128 + (((chunk & 7) ^ (r & 7)) << 4));
@@ -371,7 +405,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             asm volatile("cp.async.wait_all;" ::: "memory");
             async_proxy_fence();
         };
-        int64_t n = 0, pos = work.pos;  // tiles loaded; their line
+        int64_t n = 0;  // tiles loaded
         int slot = 0;                   // of the ring
         uint32_t phase = 0;
         int segment = 0;
@@ -380,7 +414,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         int64_t raw_in = 0;
         uint32_t raw_bits = 0;
         uint32_t raw_valid[kE4m3 ? Shape::kRaws / 2 : 1];
-        const int64_t raw_tiles = 2 * (work.end - work.pos);
+        int64_t raw_tiles = 0;
         // This warp's tokens by TMA, a box from each lane that has a box's first token; `block` bytes
         // of a token go to each of `blocks` places `apart` bytes from one another.
         auto load_boxes = [&](const CUtensorMap *map, uint32_t to, uint32_t bar, int blocks, int elements, uint32_t block, uint32_t apart) {
@@ -424,13 +458,20 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 ++raw_in;
             }
         };
+        int64_t begin = work.pos, end = work.end;
+        bool kept = false;
+        do {
+        look_from(begin, end);
+        raw_tiles += 2 * (end - begin);
         if constexpr (kE4m3)
             for (int i = 0; i < Shape::kRaws - 1; ++i) ask_raw();
-
-        while (ok && pos < work.end) {
+        for (int64_t pos = begin; ok && pos < end;) {
             // A row tile's queries, once its predecessor's products are done with the buffer.
             const int64_t unit = pos / work.tiles, seg_end = stretch_end(pos);
-            if (segment > 0 && !warp_waited(&ctl->q_empty, static_cast<uint32_t>(segment - 1) & 1u)) break;
+            if (segment > 0 && !warp_waited(&ctl->q_empty, static_cast<uint32_t>(segment - 1) & 1u)) {
+                ok = false;
+                break;
+            }
             {
                 const int64_t head = unit / p.row_tiles, row0 = unit % p.row_tiles * kPrefixRows;
                 constexpr int kQChunks = kDim / 8;
@@ -511,6 +552,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 }
             }
         }
+        } while (more_work(begin, end, kept));
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (!ok) {
             // A wait ran out: TMA copies of this warp may be on their way.  They end within
@@ -529,7 +571,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             // (The address field of a descriptor, in 16-byte units, holds every offset without a carry.)
             const uint64_t q_desc = smem_desc_sw128(smem_u32(smem), 16, 1024), k_desc = smem_desc_sw128(smem_u32(ring), 16, 1024),
                            v_desc = smem_desc_sw128(smem_u32(ring), kTokens * 128, 1024);
-            int64_t pos = work.pos, seg_end = pos < work.end ? stretch_end(pos) : pos;
+            int64_t begin = work.pos, end = work.end, xpos = 0, x_seg_end = 0;
+            bool kept = false;
             int segment = 0, xslot = 0;  // the ring goes keys, values, keys, values ...
             uint32_t xphase = 0;
             auto next = [&](int &slot, uint32_t &phase) {
@@ -538,21 +581,18 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     phase ^= 1u;
                 }
             };
-            int64_t xpos = pos;
-            int64_t x_seg_end = seg_end;
-            bool x_first = true;
             // X of the next place; false once a wait ran out.
             auto issue_x = [&](int64_t n) {
-                if (x_first) {
+                if (xpos == x_seg_end) {
                     if (!warp_waited(&ctl->q_full, static_cast<uint32_t>(segment) & 1u)) return false;
                     ++segment;
-                    x_first = false;
+                    x_seg_end = stretch_end(xpos);
                 }
                 if (!warp_waited(&ctl->full[xslot], xphase)) return false;
                 tc_fence_after_sync();
                 const uint64_t kd = k_desc + static_cast<uint64_t>(xslot) * (kTile >> 4);
                 const uint32_t d = tmem + kDim + static_cast<uint32_t>(n & 1) * Shape::kBuffer;
-                const bool last = ++xpos == x_seg_end && xpos < work.end;
+                ++xpos;
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kDim / 16; ++k) {
@@ -562,27 +602,27 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     }
                     tc_commit<false>(smem_u32(&ctl->empty[xslot]));
                     tc_commit<false>(smem_u32(&ctl->x_full[n & 1]));
-                    if (last) tc_commit<false>(smem_u32(&ctl->q_empty));
+                    if (xpos == x_seg_end) tc_commit<false>(smem_u32(&ctl->q_empty));
                 }
                 __syncwarp();
                 next(xslot, xphase);
-                if (last) {
-                    x_seg_end = stretch_end(xpos);
-                    x_first = true;
-                }
                 return true;
             };
             int vslot = 1;
             uint32_t vphase = 0;
-            int64_t n = 0, seg_begin = pos;
-            bool ok = pos < work.end && issue_x(0);
-            for (; ok && pos < work.end; ++pos, ++n) {
+            int64_t n = 0;
+            bool ok = true;
+            do {
+            int64_t seg_begin = begin, seg_end = stretch_end(begin);
+            xpos = x_seg_end = begin;
+            ok = ok && issue_x(n);
+            for (int64_t pos = begin; ok && pos < end; ++pos, ++n) {
                 if (pos == seg_end) {
                     seg_begin = pos;
                     seg_end = stretch_end(pos);
                 }
-                if (xpos < work.end && !issue_x(n + 1)) break;
-                if (!warp_waited(&ctl->full[vslot], vphase)) break;
+                if (xpos < end) ok = issue_x(n + 1);
+                ok = ok && warp_waited(&ctl->full[vslot], vphase);
                 const uint64_t vd = v_desc + static_cast<uint64_t>(vslot) * (kTile >> 4);
                 const uint32_t a = tmem + kDim + static_cast<uint32_t>(n & 1) * Shape::kBuffer;
                 const uint32_t more = pos > seg_begin;
@@ -610,10 +650,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     }
                     __syncwarp();
                 }
-                if (!ok) break;
-                __syncwarp();
                 next(vslot, vphase);
             }
+            } while (more_work(begin, end, kept));
             // Every product is done before the tensor memory is given back, whatever happened.
             if (elect_one()) {
                 tc_commit<false>(smem_u32(&ctl->drain));
@@ -634,72 +673,84 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         // (The hand-over between the groups is not one: they are not in step, and a barrier that
         // one group had passed twice would take that for the other's arrival.)
         const int own_barrier = 1 + group * 4 + quarter, all_barrier = 9;
-        int64_t n = 0;
-        bool ok = true;
-        for (int64_t pos = work.pos; pos < work.end;) {
-            const int64_t unit = pos / work.tiles, seg_begin = pos, seg_end = stretch_end(pos);
+        int64_t n = 0, left = 0;  // tiles; bases left before the stretch
+        bool ok = true, kept = false;
+        int64_t begin = work.pos, end = work.end;
+        do {
+        for (int64_t pos = begin; pos < end;) {
+            const int64_t unit = pos / work.tiles, seg_first = n, seg_begin = pos, seg_end = stretch_end(pos);
             const int64_t head = unit / p.row_tiles, row = unit % p.row_tiles * kPrefixRows + r;
             const float factor = p.scale * 1.4426950408889634f * (kE4m3 && p.k_scale ? p.k_scale[head] : 1.f);
             const float none = factor < 0.f ? INFINITY : -INFINITY;
             float m = -INFINITY, l = 0.f;  // what this thread's sum is relative to
+            bool bad = false;
             for (; pos < seg_end; ++pos, ++n) {
                 if (static_cast<int>(n & 1) != group) continue;
                 ok = ok && warp_waited(&ctl->x_full[group], static_cast<uint32_t>(n >> 1) & 1u);
                 tc_fence_after_sync();
-                float top = none;
                 uint32_t bits[2] = {kAll, kAll};  // tokens of the piece that exist, a loading warp's each
-                if (ok) {
-                    bits[0] = ctl->valid[n & 7][2 * piece], bits[1] = ctl->valid[n & 7][2 * piece + 1];
+                if (ok) bits[0] = ctl->valid[n & 7][2 * piece], bits[1] = ctl->valid[n & 7][2 * piece + 1];
+                if (kept || pos == seg_begin) {
+                    // The tile's maxima: of the first tile, or of each where they are kept.
+                    float top = none;
+                    if (ok) {
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        uint32_t x[kMine];
-                        tmem_load(x0 + w * kMine, x);
-                        if (bits[w] != kAll) {
+                        for (int w = 0; w < 2; ++w) {
+                            uint32_t x[kMine];
+                            tmem_load(x0 + w * kMine, x);
+                            if (bits[w] != kAll) {
 #pragma unroll
-                            for (int i = 0; i < kMine; ++i)
-                                if (!((bits[w] >> i) & 1u)) x[i] = __float_as_uint(none);
+                                for (int i = 0; i < kMine; ++i)
+                                    if (!((bits[w] >> i) & 1u)) x[i] = __float_as_uint(none);
+                            }
+                            if (factor < 0.f) {
+#pragma unroll
+                                for (int i = 0; i < kMine; i += 2) top = fminf(fminf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), top);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < kMine; i += 2) top = fmaxf(fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), top);
+                            }
                         }
-                        if (factor < 0.f) {
-#pragma unroll
-                            for (int i = 0; i < kMine; i += 2) top = fminf(fminf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), top);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < kMine; i += 2) top = fmaxf(fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), top);
-                        }
+                        top *= factor;
+                        ctl->top[group][piece][r] = top;
                     }
-                    top *= factor;
-                    ctl->top[group][piece][r] = top;
-                }
-                named_barrier(own_barrier, 32 * kPrefixPieces);
-                if (pos > seg_begin)
-                    ok = ok && warp_waited(&ctl->base_full[(n - 1) & 1][quarter], static_cast<uint32_t>((n - 1) >> 1) & 1u);
-                const float before = pos > seg_begin ? ctl->base[(n - 1) & 1][r] : -INFINITY;
-                top = fmaxf(top, ctl->top[group][piece ^ 1][r]);
-                const bool grown = top > before + kLazy || (before == -INFINITY && top > before);
-                const float base_now = grown ? top : before;
-                if (piece == 0) ctl->base[n & 1][r] = base_now;
-                mbar_arrive(smem_u32(&ctl->base_full[n & 1][quarter]));
-                if (!ok) continue;
-                if (base_now != m) {
-                    l *= exp2_fast(m - base_now);
-                    m = base_now;
-                }
-                if (pos > seg_begin && __any_sync(0xffffffffu, grown)) {
-                    // o of the tiles before is complete once the last one's product is.  (The
-                    // barrier's phase before that ended before X of this tile was there.)
-                    ok = warp_waited(&ctl->o_done[(n - 1) & 1], static_cast<uint32_t>((n - 1) >> 1) & 1u);
+                    named_barrier(own_barrier, 32 * kPrefixPieces);
+                    const int64_t at = left + (n - seg_first);  // of the bases left
+                    if (pos > seg_begin)
+                        ok = ok && warp_waited(&ctl->base_full[(at - 1) & 1][quarter], static_cast<uint32_t>((at - 1) >> 1) & 1u);
+                    const float before = pos > seg_begin ? ctl->base[(at - 1) & 1][r] : -INFINITY;
+                    top = fmaxf(top, ctl->top[group][piece ^ 1][r]);
+                    const bool grown = top > before + kLazy || (before == -INFINITY && top > before);
+                    const float base_now = grown ? top : before;
+                    if (piece == 0) ctl->base[at & 1][r] = base_now;
+                    mbar_arrive(smem_u32(&ctl->base_full[at & 1][quarter]));
                     if (!ok) continue;
-                    tc_fence_after_sync();
-                    const float keep = grown ? exp2_fast(before - m) : 1.f;
-#pragma unroll 1
-                    for (int d = 0; d < kDim / kPrefixPieces; d += 16) {
-                        float o[16];
-                        tmem_load16(at_lane + piece * (kDim / kPrefixPieces) + d, o);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] *= keep;
-                        tmem_store16(at_lane + piece * (kDim / kPrefixPieces) + d, o);
+                    if (base_now != m) {
+                        l *= exp2_fast(m - base_now);
+                        m = base_now;
                     }
+                    bad = bad || m == -INFINITY;  // (no token in the first tile: nothing to be relative to)
+                    if (pos > seg_begin && __any_sync(0xffffffffu, grown)) {
+                        // o of the tiles before is complete once the last one's product is.  (The
+                        // barrier's phase before that ended before X of this tile was there.)
+                        ok = warp_waited(&ctl->o_done[(n - 1) & 1], static_cast<uint32_t>((n - 1) >> 1) & 1u);
+                        if (!ok) continue;
+                        tc_fence_after_sync();
+                        const float keep = grown ? exp2_fast(before - m) : 1.f;
+#pragma unroll 1
+                        for (int d = 0; d < kDim / kPrefixPieces; d += 16) {
+                            float o[16];
+                            tmem_load16(at_lane + piece * (kDim / kPrefixPieces) + d, o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] *= keep;
+                            tmem_store16(at_lane + piece * (kDim / kPrefixPieces) + d, o);
+                        }
+                    }
+                } else if (n == seg_first + 1) {  // the other group's first tile of the stretch
+                    ok = ok && warp_waited(&ctl->base_full[left & 1][quarter], static_cast<uint32_t>(left >> 1) & 1u);
+                    if (ok) m = ctl->base[left & 1][r];
                 }
+                if (!ok) continue;
                 const float base = finite_or_zero(m);
                 const uint64_t factors = pair_of(factor, factor), bases = pair_of(-base, -base);
                 uint64_t sum = pair_of(0.f, 0.f);  // of the tile: no long chain of additions
@@ -737,16 +788,19 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     }
                 }
                 const float2 sums = pair_to(sum);
+                bad = bad || !(sums.x + sums.y < kMostSum);
                 l += sums.x + sums.y;
             }
             // The part: o of every tile of the stretch, relative to the last base, from both groups.
+            left += kept ? n - seg_first : 1;
             named_barrier(all_barrier, 32 * kPrefixSoftmaxWarps);
-            const float last = ctl->base[(n - 1) & 1][r];
+            const float last = ctl->base[(left - 1) & 1][r];
             ok = ok && warp_waited(&ctl->o_done[(n - 1) & 1], static_cast<uint32_t>((n - 1) >> 1) & 1u);
             tc_fence_after_sync();
             if (ok) {
                 float *part = p.partials + (unit + blockIdx.x) * Shape::kPart;
                 const bool mine = row < rows;
+                float none_of = 0.f;  // 0 · o: NaN where o is not finite
                 if (mine) {
                     if (share == 0) part[r] = last;
                     part[(1 + share) * kPrefixRows + r] = last != m ? l * exp2_fast(m - last) : l;
@@ -758,17 +812,27 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     const int at = share * kOwn + d;
                     float o[16];
                     tmem_load16(at_lane + at, o);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) none_of = __fmaf_rn(0.f, o[i], none_of);
                     if (mine)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             to[(at / 4 + i) * kPrefixRows + r] =
                                 make_float4(o[4 * i] * by, o[4 * i + 1] * by, o[4 * i + 2] * by, o[4 * i + 3] * by);
                 }
+                // Weights that come to 2^64 relative to the first tile's maximum, or none to be relative
+                // to, or a sum that is not finite, as it may then be of large values: once more, with
+                // maxima kept.
+                if (!kept && __any_sync(0xffffffffu, mine && (bad || none_of != 0.f)) && lane == 0) {
+                    const int at = flag_of(seg_begin);
+                    atomicOr(&ctl->redo[at >> 5], 1u << (at & 31));
+                }
             }
             // No product of the next stretch begins before all of o is read.
             tc_fence_before_sync();
             named_barrier(all_barrier, 32 * kPrefixSoftmaxWarps);
         }
+        } while (more_work(begin, end, kept));
     }
     tc_fence_before_sync();
     __syncthreads();

@@ -229,6 +229,36 @@ def test_bad_pages_are_reported_and_left_out():
     ku.check_attention(out, lse, shared64(q, kv.k_cache, kv.v_cache, good, 700, table, [20, 0], 16, 0.125, keep=lambda t: t < 0))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("size", [1.0, 30.0])
+def test_beginnings_on_bad_pages(dtype, size):
+    # No token in the first tiles of a CTA's stretch, and logits far below and above 0 in the others.
+    import torch
+    import dense_linear_projection_gb300 as dlp
+    for prefix_len, batch in ((2000, 5), (30000, 40)):
+        kv, q, prefix, table, n, scales = case(prefix_len, [3] * batch, 8, 1, 128, 16, dtype=dtype, size=size)
+        good = prefix.clone()
+        prefix[:20] = -1
+        prefix[60:70] = 2 ** 30
+        out, lse = kv.attend_shared(q, prefix, prefix_len, table, n, return_lse=True)
+        assert kv.status() == dlp.PROJ_ERR_INVALID_ARG
+        ref = shared64(q, kv.k_cache, kv.v_cache, good, prefix_len, table, [3] * batch, 16, 128 ** -0.5, *scales,
+                       keep=lambda t: (t // 16 >= 20) & ((t // 16 < 60) | (t // 16 >= 70)))
+        ku.check_attention(out, lse, ref)
+
+
+@pytest.mark.parametrize("shift", [-300.0, 300.0])
+def test_logits_far_from_zero(shift):
+    # Every logit shifted by one element that all queries and keys share: far beyond what 2^x holds.
+    kv, q, prefix, table, n, _ = case(5000, [40, 0, 7], 8, 2, 64, 16)
+    q[..., 0] = 16
+    kv.k_cache[..., 0] = shift / 2
+    kv.k_cache[prefix[100].item(), 3, :, 0] = 0
+    for scale in (0.125, 1.0):
+        out, lse = kv.attend_shared(q, prefix, 5000, table, n, scale=scale, return_lse=True)
+        ku.check_attention(out, lse, shared64(q, kv.k_cache, kv.v_cache, prefix, 5000, table, [40, 0, 7], 16, scale))
+
+
 def test_strided_queries_and_outputs():
     import torch
     kv, q, prefix, table, n, _ = case(600, [20, 0, 9], 8, 2, 64, 16)
