@@ -869,6 +869,21 @@ __global__ void __launch_bounds__(kCombineThreads) kv_combine_kernel(const KvCom
     const int64_t c0 = ((unit * p.tiles + 1) * p.ctas - 1) / total, c1 = ((unit + 1) * p.tiles * p.ctas - 1) / total;
     const float *first = p.partials + (unit + c0) * kPart;
     const int parts = static_cast<int>(c1 - c0) + 1;
+    // The own tokens' part, asked for beside the prefix's.
+    const uint32_t b = in ? static_cast<uint32_t>(row) / p.group : 0u, g = in ? static_cast<uint32_t>(row) % p.group : 0u;
+    const int64_t q_head = head * p.group + g, at = static_cast<int64_t>(b) * p.kv_heads * p.group + q_head;
+    float2 own = make_float2(-INFINITY, 0.f);
+    float4 own_values[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) own_values[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (in && group == 0) {
+        own = p.top[at];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int d = 4 * (c + k * kCombineLanes);
+            if (d < p.head_dim) own_values[k] = *reinterpret_cast<const float4 *>(p.out32 + at * p.head_dim + d);
+        }
+    }
     float m = -INFINITY, l = 0.f;
     float4 o[kPer];
 #pragma unroll
@@ -912,19 +927,11 @@ __global__ void __launch_bounds__(kCombineThreads) kv_combine_kernel(const KvCom
         for (int k = 0; k < kPer; ++k) v[k] = values[x - 1][c + k * kCombineLanes][i];
         add(tops[x][i], sums[x][i], v);
     }
-    const uint32_t b = static_cast<uint32_t>(row) / p.group, g = static_cast<uint32_t>(row) % p.group;
-    const int64_t q_head = head * p.group + g, at = static_cast<int64_t>(b) * p.kv_heads * p.group + q_head;
-    const float2 own = p.top[at];
-    if (own.y != 0.f) {  // (the own tokens' values are divided by their sum)
-        float4 v[kPer];
+    if (own.y != 0.f) {  // (the own tokens' values are divided by their sum; without tokens they are not written)
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const int d = 4 * (c + k * kCombineLanes);
-            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (d < p.head_dim) v[k] = *reinterpret_cast<const float4 *>(p.out32 + at * p.head_dim + d);
-            v[k].x *= own.y, v[k].y *= own.y, v[k].z *= own.y, v[k].w *= own.y;
-        }
-        add(own.x, own.y, v);
+        for (int k = 0; k < kPer; ++k)
+            own_values[k].x *= own.y, own_values[k].y *= own.y, own_values[k].z *= own.y, own_values[k].w *= own.y;
+        add(own.x, own.y, own_values);
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
