@@ -842,17 +842,21 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     }
 }
 
-// The join: eight rows of a key head a block, its four groups of threads on every
-// fourth part each; then the sequences' own part.  Bytes bound it (the parts).
-constexpr int kCombineRows = 8, kCombineLanes = 16, kCombineGroups = 4;
-constexpr int kCombineThreads = kCombineRows * kCombineLanes * kCombineGroups;
+// The join: eight rows of a key head a block, 128 threads on every kGroups-th part each; then
+// the sequences' own part.  Bytes bound it (the parts), and the few loads one after another:
+// with a few parts a unit one group of threads has them all on their way, and eight blocks an
+// SM (128 sequences behind 32768 tokens, up to four parts a unit, whole call: 224 us and 236
+// with four groups; 64 behind 8192, up to six: 81 and 78).
+constexpr int kCombineRows = 8, kCombineLanes = 16, kCombineMost = 4;
+constexpr int kCombineThreads = kCombineRows * kCombineLanes;  // of a group
+constexpr int kCombineFew = 4;  // parts of a unit, at most, for one group
 
-template <int kDim>
-__global__ void __launch_bounds__(kCombineThreads) kv_combine_kernel(const KvCombineParams p) {
+template <int kDim, int kGroups>
+__global__ void __launch_bounds__(kCombineThreads *kGroups) kv_combine_kernel(const KvCombineParams p) {
     constexpr int kPart = PrefixShape<false, kDim>::kPart;
     constexpr int kPer = kDim / 4 / kCombineLanes;  // float4s of a thread
-    __shared__ float tops[kCombineGroups][kCombineRows], sums[kCombineGroups][kCombineRows];
-    __shared__ float4 values[kCombineGroups - 1][kDim / 4][kCombineRows];
+    __shared__ float tops[kGroups][kCombineRows], sums[kGroups][kCombineRows];
+    __shared__ float4 values[kGroups > 1 ? kGroups - 1 : 1][kDim / 4][kCombineRows];
     griddep_launch_dependents();
     griddep_wait();
     const int tid = threadIdx.x;
@@ -901,7 +905,7 @@ __global__ void __launch_bounds__(kCombineThreads) kv_combine_kernel(const KvCom
     };
     if (in) {
 #pragma unroll 4
-        for (int x = group; x < parts; x += kCombineGroups) {
+        for (int x = group; x < parts; x += kGroups) {
             const float *part = first + static_cast<int64_t>(x) * kPart;
             const float4 *from = reinterpret_cast<const float4 *>(part + (1 + kPrefixSums) * kPrefixRows);
             float4 v[kPer];
@@ -921,7 +925,7 @@ __global__ void __launch_bounds__(kCombineThreads) kv_combine_kernel(const KvCom
     __syncthreads();
     if (group > 0 || !in) return;
 #pragma unroll
-    for (int x = 1; x < kCombineGroups; ++x) {
+    for (int x = 1; x < kGroups; ++x) {
         float4 v[kPer];
 #pragma unroll
         for (int k = 0; k < kPer; ++k) v[k] = values[x - 1][c + k * kCombineLanes][i];

@@ -62,13 +62,17 @@ proj_status_t proj_kv_attend_scored(proj_kv_handle_t h, int64_t sequences, const
     s.kv_heads = h->d.kv_heads;
     s.group = p.group;
     // Blocks enough for every SM, no more of a row than it has tokens for.
-    const int64_t rows = sequences * h->d.kv_heads, most = (score_tokens + dev::kScoreThreads - 1) / dev::kScoreThreads;
+    const bool ahead = p.group == 8 || p.group == 4;
+    const int64_t at_once = int64_t(dev::kScoreThreads) * (ahead ? dev::kScoreAhead : 1);
+    const int64_t rows = sequences * h->d.kv_heads, most = (score_tokens + at_once - 1) / at_once;
     int64_t of_row = (int64_t(h->sm_count) * 32 + rows - 1) / rows;
     if (of_row > most) of_row = most;
     if (rows * of_row > kMaxDim) return PROJ_ERR_UNSUPPORTED;
     const dim3 grid(static_cast<unsigned>(rows * of_row));
-    return p.group % 4 == 0 ? launch(dev::kv_score_kernel<true>, grid, dev::kScoreThreads, 0, stream, s, static_cast<int>(of_row))
-                            : launch(dev::kv_score_kernel<false>, grid, dev::kScoreThreads, 0, stream, s, static_cast<int>(of_row));
+    const int blocks = static_cast<int>(of_row), t = dev::kScoreThreads;
+    if (p.group == 8) return launch(dev::kv_score_kernel<8>, grid, t, 0, stream, s, blocks);
+    if (p.group == 4) return launch(dev::kv_score_kernel<4>, grid, t, 0, stream, s, blocks);
+    return launch(dev::kv_score_kernel<0>, grid, t, 0, stream, s, blocks);
 }
 
 }  // extern "C"

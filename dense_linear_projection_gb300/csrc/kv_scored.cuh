@@ -24,7 +24,12 @@ __device__ __forceinline__ float4 load_once(const float *from, uint64_t policy) 
     return v;
 }
 
-template <bool kVec>  // the heads of a token in whole float4s
+// kGroup: query heads of a key head where these are 4 or 8, whose maxima and sums stay in registers
+// and whose logits of kScoreAhead tokens are asked for together; 0 for other numbers.  (64 ragged
+// sequences: 20.6 us for 100 MB, of 197 with the attention.)
+constexpr int kScoreAhead = 4;
+
+template <int kGroup>
 __global__ void __launch_bounds__(kScoreThreads) kv_score_kernel(const KvScoreParams p, const int blocks_of_row) {
     griddep_launch_dependents();
     griddep_wait();
@@ -40,29 +45,44 @@ __global__ void __launch_bounds__(kScoreThreads) kv_score_kernel(const KvScorePa
     const uint64_t policy = l2_policy_evict_first();
     const bool in_place = p.scores == p.scores_out;
     const int64_t from = in_place ? low : 0, to = in_place ? n : p.score_tokens;
-    for (int64_t t = from + part * kScoreThreads + threadIdx.x; t < to; t += int64_t(blocks_of_row) * kScoreThreads) {
-        const float before = in[t];
-        float sum = 0.f;
-        if (t >= low && t < n) {
-            const float *xt = x + t * p.group;
-            if constexpr (kVec) {
-                for (int g = 0; g < p.group; g += 4) {
-                    const float4 v = load_once(xt + g, policy);
-                    const float y[4] = {v.x, v.y, v.z, v.w};
+    const int64_t step = int64_t(blocks_of_row) * kScoreThreads;
+    auto weight = [&](float y, float2 r) { return exp2_fast(y - finite_or_zero(r.x)) * r.y; };
+    if constexpr (kGroup > 0) {
+        float2 held[kGroup];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 r = top[g + i];
-                        sum += exp2_fast(y[i] - finite_or_zero(r.x)) * r.y;
-                    }
+        for (int g = 0; g < kGroup; ++g) held[g] = top[g];
+        for (int64_t t0 = from + part * kScoreThreads + threadIdx.x; t0 < to; t0 += kScoreAhead * step) {
+            float before[kScoreAhead];
+            float4 v[kScoreAhead][kGroup / 4];
+#pragma unroll
+            for (int k = 0; k < kScoreAhead; ++k) {
+                const int64_t t = t0 + k * step;
+                before[k] = t < to ? in[t] : 0.f;
+#pragma unroll
+                for (int g = 0; g < kGroup / 4; ++g)
+                    v[k][g] = t >= low && t < n ? load_once(x + t * kGroup + 4 * g, policy) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            }
+#pragma unroll
+            for (int k = 0; k < kScoreAhead; ++k) {
+                const int64_t t = t0 + k * step;
+                if (t >= to) break;
+                float sum = 0.f;
+                if (t >= low && t < n) {
+#pragma unroll
+                    for (int g = 0; g < kGroup / 4; ++g)
+                        sum += weight(v[k][g].x, held[4 * g]) + weight(v[k][g].y, held[4 * g + 1]) + weight(v[k][g].z, held[4 * g + 2]) +
+                               weight(v[k][g].w, held[4 * g + 3]);
                 }
-            } else {
-                for (int g = 0; g < p.group; ++g) {
-                    const float2 r = top[g];
-                    sum += exp2_fast(xt[g] - finite_or_zero(r.x)) * r.y;
-                }
+                out[t] = before[k] + sum;
             }
         }
-        out[t] = before + sum;
+    } else {
+        for (int64_t t = from + part * kScoreThreads + threadIdx.x; t < to; t += step) {
+            float sum = 0.f;
+            if (t >= low && t < n)
+                for (int g = 0; g < p.group; ++g) sum += weight(x[t * p.group + g], top[g]);
+            out[t] = in[t] + sum;
+        }
     }
 }
 

@@ -15,14 +15,14 @@ using PrefixKernel = void (*)(KvPrefixParams, CUtensorMap, CUtensorMap);
 using CombineKernel = void (*)(KvCombineParams);
 struct PrefixInstance {
     PrefixKernel kernel;
-    CombineKernel combine;
+    CombineKernel combine, combine_many;  // for a few parts of a unit, for many
     int smem, tokens, part, columns;  // shared memory, tokens of a tile, floats of a part, elements of a row in it
 };
 
 template <bool kE4m3, int kDim>
 PrefixInstance prefix_of() {
     using Shape = dev::PrefixShape<kE4m3, kDim>;
-    return {dev::kv_prefix_kernel<kE4m3, kDim>, dev::kv_combine_kernel<kDim>, Shape::kSmem, Shape::kTokens, Shape::kPart, kDim};
+    return {dev::kv_prefix_kernel<kE4m3, kDim>, dev::kv_combine_kernel<kDim, 1>, dev::kv_combine_kernel<kDim, dev::kCombineMost>, Shape::kSmem, Shape::kTokens, Shape::kPart, kDim};
 }
 
 template <bool kE4m3>
@@ -161,7 +161,10 @@ proj_status_t proj_kv_attend_shared(proj_kv_handle_t h, int64_t sequences, const
     c.lse = lse;
     const int64_t blocks = h->d.kv_heads * ((sequences * p.group + dev::kCombineRows - 1) / dev::kCombineRows);
     if (blocks > kMaxDim) return PROJ_ERR_UNSUPPORTED;
-    return launch(s.instance.combine, dim3(static_cast<unsigned>(blocks)), dev::kCombineThreads, 0, stream, c);
+    const int64_t units = h->d.kv_heads * s.row_tiles;
+    const bool few = (s.ctas + units - 1) / units + 1 <= dev::kCombineFew;
+    return launch(few ? s.instance.combine : s.instance.combine_many, dim3(static_cast<unsigned>(blocks)),
+                  dev::kCombineThreads * (few ? 1 : dev::kCombineMost), 0, stream, c);
 }
 
 }  // extern "C"
