@@ -669,8 +669,8 @@ class PagedKV:
     elements ``k_scale``, ``v_scale`` ([kv_heads] fp32) say what one unit
     stands for.  The tensors stay the caller's; the handle, on their device, owns
     scratch for sequences that several thread blocks share.  Results carry no
-    gradients; the caches, ``out`` and ``q_out`` are written without autograd's
-    notice (no version count).
+    gradients; the caches, ``out``, ``q_out`` and ``scores_out`` are written
+    without autograd's notice (no version count).
     """
 
     def __init__(self, k_cache, v_cache, q_heads: int, max_sequences: int, k_scale=None, v_scale=None, stream=None):
@@ -713,7 +713,7 @@ class PagedKV:
         0, 1, 2, …; ``rope``: :func:`rope_table`'s form, or None for no
         rotation.
 
-        ``q_norm``, ``k_norm`` ([head_dim] bf16 or fp32): each head of the
+        ``q_norm``, ``k_norm`` ([head_dim] bf16 or fp32, 16-byte aligned): each head of the
         queries or keys becomes ``x · weight / sqrt(mean(x²) + eps)`` first, in
         fp32.  ``rope_rows`` (int32 [tokens]): the rope table's row of each
         token where that is not its position, as after :meth:`evict`."""

@@ -196,10 +196,14 @@ __device__ __forceinline__ float group_sum(float x, int lanes, uint32_t mask) {
 }
 // 1 / sqrt(Σ x² / head_dim + eps) of elements a, b, which it scales where it has to.
 __device__ __forceinline__ float head_norm(float *a, float *b, float of_dim, float eps, int lanes, uint32_t mask) {
-    float sum = 0.f;
+    uint64_t squares = pair_of(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum = __fmaf_rn(a[i], a[i], __fmaf_rn(b[i], b[i], sum));
-    sum = group_sum(sum, lanes, mask);
+    for (int i = 0; i < 8; i += 2) {
+        const uint64_t x = pair_of(a[i], a[i + 1]), y = pair_of(b[i], b[i + 1]);
+        squares = fma2(x, x, fma2(y, y, squares));
+    }
+    const float2 both = pair_to(squares);
+    float sum = group_sum(both.x + both.y, lanes, mask);
     if (sum < 0x1p120f && (sum >= 0x1p-90f || eps >= 0x1p-60f)) return rsqrtf(__fmaf_rn(sum, of_dim, eps));
     float top = 0.f;
 #pragma unroll
@@ -352,17 +356,31 @@ __global__ void __launch_bounds__(kAppendThreads, kE4m3 ? 5 : 6) kv_append_norm_
         if (weight) {
             const float by = head_norm(a, b, of_dim, p.eps, lanes, mask);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) a[x] = a[x] * by * wa[x], b[x] = b[x] * by * wb[x];
+            for (int x = 0; x < 8; x += 2) {
+                const uint64_t scale2 = pair_of(by, by);
+                const float2 u = pair_to(mul2(mul2(pair_of(a[x], a[x + 1]), scale2), pair_of(wa[x], wa[x + 1])));
+                const float2 v = pair_to(mul2(mul2(pair_of(b[x], b[x + 1]), scale2), pair_of(wb[x], wb[x + 1])));
+                a[x] = u.x, a[x + 1] = u.y, b[x] = v.x, b[x + 1] = v.y;
+            }
         }
         if (pairs == 0) continue;
         if (rotary && !is_v) {
+            if constexpr (kVec && kInterleaved) {
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                if constexpr (kVec && kInterleaved) {
+                for (int x = 0; x < 8; ++x) {
                     float *y = x < 4 ? a + 2 * x : b + 2 * (x - 4);
                     rotate(y[0], y[1], cos[x], sin[x]);
-                } else {
-                    rotate(a[x], b[x], cos[x], sin[x]);
+                }
+            } else {
+                // Two pairs an instruction, in rotate()'s operations (a difference as x − 1 · y is
+                // the same number).
+#pragma unroll
+                for (int x = 0; x < 8; x += 2) {
+                    const uint64_t a2 = pair_of(a[x], a[x + 1]), b2 = pair_of(b[x], b[x + 1]);
+                    const uint64_t c2 = pair_of(cos[x], cos[x + 1]), s2 = pair_of(sin[x], sin[x + 1]);
+                    const float2 u = pair_to(fma2(mul2(b2, s2), pair_of(-1.f, -1.f), mul2(a2, c2)));
+                    const float2 v = pair_to(add2(mul2(b2, c2), mul2(a2, s2)));
+                    a[x] = u.x, a[x + 1] = u.y, b[x] = v.x, b[x + 1] = v.y;
                 }
             }
         }

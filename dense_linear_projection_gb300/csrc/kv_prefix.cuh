@@ -163,32 +163,6 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t pair_of(float x, float y) {
-    uint64_t p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
-    return p;
-}
-__device__ __forceinline__ float2 pair_to(uint64_t p) {
-    float2 v;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
-    return v;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t mul2_rz(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 // Two weights as three bf16 parts, the same as split<false>'s: each but the last the upper half of
 // the next float below, so that every part of a positive weight is positive.
 __device__ __forceinline__ void split3(uint64_t w, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
@@ -252,6 +226,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int *abort_flag = &ctl->abort_flag;
     if (smem_u32(smem) & 1023u) {  // (128-byte swizzled tiles; the same in every thread)
+        griddep_wait();  // (the next kernel counts on what came before this one)
         if (tid == 0) atomicOr(p.status, kKvErrWait);
         return;
     }
