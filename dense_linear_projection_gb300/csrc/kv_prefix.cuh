@@ -15,10 +15,9 @@
 //     memory: X of two token tiles, so that the one's softmax overlaps the other's
 //     products, and o.  P stays in tensor memory too, written over X.
 //   * warps 0..15 turn X into P, in two groups that take every other tile, so that the one's
-//     waits lie under the other's arithmetic (which is what limits the kernel: splitting a
-//     weight takes 12 of the 20 instructions for two of them).  A thread has one row
-//     (tensor-memory lane) and half of a tile's tokens; the two threads of a row meet over its
-//     maximum, and the groups hand on what the weights are relative to.
+//     waits lie under the other's arithmetic (splitting a weight takes 12 of the 20
+//     instructions for two of them).  A thread has one row (tensor-memory lane) and half of
+//     a tile's tokens.
 //   * weights are relative to the maximum of the first tile of a CTA's stretch, so that a
 //     later tile's X is read once and nothing is handed on: fp32 sums and bf16 parts are as
 //     exact at 2^60 as at 1.  Where a tile's sum comes to 2^64, or o is not finite, the
@@ -30,6 +29,14 @@
 //     (which any page size and strides allow); warp 20 issues the products.
 //   * (key head, row tile, token tile) in this order are one line that the CTAs share
 //     evenly; each stretch of one row tile leaves a part in the workspace.
+//
+// Measured: 1024 rows a key head, 8 key heads, 32768 tokens: 193 us, 712 TFLOP/s of the
+// formula's operations and 1424 of those carried out, 74 % of what a library product
+// reaches; 512 rows, 8192 tokens: 40 us (a third of it the start and end of the 13 tiles
+// that a CTA has).  Of a tile's 3000 cycles the products take 2100.  Tiles of 64 tokens in
+// four buffers, a group of warps each: 294 us for the first where two of 128 took 258
+// (every change between the two products costs about 300 cycles); the products issued from
+// a branch of one lane: 418; X held in registers by 16 warps: spills.
 //
 // Every wait is bounded; one that runs out records itself, and the CTA drains its
 // copies, frees its tensor memory and returns.
