@@ -259,6 +259,38 @@ def test_logits_far_from_zero(shift):
         ku.check_attention(out, lse, shared64(q, kv.k_cache, kv.v_cache, prefix, 5000, table, [40, 0, 7], 16, scale))
 
 
+def test_many_stretches_a_block():
+    # More than 63 stretches of row tiles a thread block, of which those of a growing prefix are done again.
+    import torch
+    import dense_linear_projection_gb300 as dlp
+    B, hk, D, page, prefix_len = 39500, 32, 16, 16, 200
+    k_cache, v_cache = ku.make_cache(20, page, hk, D)
+    prefix = torch.randperm(20).to(torch.int32).cuda()
+    at = torch.arange(prefix_len, device="cuda")
+    k_cache[prefix.long()[at[128:] // page], at[128:] % page, ::3] *= 60  # past the first tile, every third key head
+    q = torch.randn((B, hk, D), device="cuda").to(torch.bfloat16)
+    kv = dlp.PagedKV(k_cache, v_cache, hk, B)
+    n, table = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros((B, 0), dtype=torch.int32, device="cuda")
+    out, lse = kv.attend_shared(q, prefix, prefix_len, table, n, return_lse=True)
+    assert kv.status() == dlp.PROJ_OK
+    k, v = (ku.tokens_of(c, prefix[None], 0, 0, prefix_len, page) for c in (k_cache, v_cache))
+    for j in range(hk):
+        x = q[:, j].double()
+        s = x @ k[:, j].t() / 4
+        a = (x.abs() @ k[:, j].abs().t()).amax(1) / 4
+        p = torch.softmax(s, 1)
+        rel = 2 * (D / 16 + 8) * 2.0 ** -22 * a + 2.0 ** -20 + (prefix_len / 8 + 64) * 2.0 ** -22
+        over = ku.beyond(out[:, j], p @ v[:, j], (p @ v[:, j].abs()) * rel[:, None] + 1e-38)
+        assert (over <= 0).all(), (j, over.max().item())
+        want = torch.logsumexp(s, 1)
+        assert ((lse[:, j].double() - want).abs() <= rel + 2.0 ** -22 * want.abs()).all(), j
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_a_million_tokens(dtype):
+    run(1000003, [0, 70], 4, 1, 64, 16, dtype=dtype)
+
+
 def test_strided_queries_and_outputs():
     import torch
     kv, q, prefix, table, n, _ = case(600, [20, 0, 9], 8, 2, 64, 16)
