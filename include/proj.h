@@ -657,10 +657,11 @@ proj_status_t proj_kv_destroy(proj_kv_handle_t h);
  *   n = seq_lens[b] tokens of its own in page_table (n = 0: the prefix alone; no
  *   windows).  The prefix is read once for the whole batch, on the tensor cores.
  *   Logits, weights and sums are fp32; a weight enters the product with the values
- *   in parts of 24 bits.  An infinite value gives infinity where its weight is above
- *   2^-90 of the largest (below, NaN).  prefix_len = 0 is proj_kv_attend.  workspace:
- *   device memory of the size that proj_kv_shared_workspace gives (16-byte aligned),
- *   the call's own until it is done.
+ *   in parts of 24 bits (of the own tokens over e4m3: as proj_kv_attend says).  An
+ *   infinite value gives infinity where its weight is above 2^-90 of the largest
+ *   (below, NaN).  prefix_len = 0 is proj_kv_attend.  workspace: device memory of the
+ *   size that proj_kv_shared_workspace gives (16-byte aligned), the call's own until
+ *   it is done.
  *
  * proj_kv_attend_scored: proj_kv_attend, and for each key head g and attended token t
  *     scores_out[b,g,t] = scores[b,g,t] + Σ_h softmax weight of t for query head h of g;
