@@ -207,12 +207,13 @@ __device__ __forceinline__ void e4m3_to_bf16(uint4 raw, uint4 &lo, uint4 &hi) {
 
 // The stretch of the line that is CTA c's, and its part of one (key head, row tile).
 struct PrefixWork {
-    int64_t pos, end, tiles;  // places; token tiles of a unit
+    int64_t pos, end, tiles, unit;  // places; token tiles of a unit; unit of place `pos`
     __device__ __forceinline__ PrefixWork(const KvPrefixParams &p) {
         const int64_t total = p.cache.kv_heads * p.row_tiles * p.tiles;
         pos = total * blockIdx.x / gridDim.x;
         end = total * (blockIdx.x + 1) / gridDim.x;
         tiles = p.tiles;
+        unit = pos / tiles;
     }
 };
 
@@ -272,43 +273,45 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = ctl->tmem;
+    const PrefixWork work(p);
     griddep_wait();
     // Only now: the own tokens' attention, launched after this kernel, does not wait for its results
     // and reads what the kernels before this one wrote (64 CTAs of a small call leave 88 SMs to it).
     griddep_launch_dependents();
 
-    const PrefixWork work(p);
     auto waited = [&](uint64_t *bar, uint32_t parity) {
         return wait_phase(smem_u32(bar), parity, abort_flag, p.status, kKvErrWait, kPrefixWaitNs);
     };
     // The same for a whole warp, whose lanes go on or stop together.
     auto warp_waited = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, waited(bar, parity)) != 0; };
-    // Places [pos, end) in stretches of one unit.
-    auto stretch_end = [&](int64_t pos) {
-        const int64_t unit_end = (pos / work.tiles + 1) * work.tiles;
+    // Places [pos, end) in stretches of one unit each, which is counted on (a 64-bit division
+    // takes a third of a microsecond, and each role would have several before its first tile).
+    auto stretch_end = [&](int64_t unit) {
+        const int64_t unit_end = (unit + 1) * work.tiles;
         return unit_end < work.end ? unit_end : work.end;
     };
+    const uint32_t row_tiles = static_cast<uint32_t>(p.row_tiles);  // (units stay below 2^31)
     const int rows = static_cast<int>(p.sequences) * p.group;  // of a key head
     // What each role does: all stretches with weights relative to their first tile's maxima; then,
     // once every role is there, the stretches in which that did not do, one by one, with maxima kept
-    // tile by tile.  `begin` and `end`: what is done now; false once there is no more.
-    const int64_t first_unit = work.pos / work.tiles;
-    auto flag_of = [&](int64_t pos) {
-        const int64_t at = pos / work.tiles - first_unit;
+    // tile by tile.  `begin`, its unit and `end`: what is done now; false once there is no more.
+    auto flag_of = [&](int64_t unit) {
+        const int64_t at = unit - work.unit;
         return at < 63 ? static_cast<int>(at) : 63;
     };
-    auto more_work = [&](int64_t &begin, int64_t &end, bool &kept) {
+    auto more_work = [&](int64_t &begin, int64_t &unit, int64_t &end, bool &kept) {
         if (!kept) {
             named_barrier(10, kPrefixThreads);
             if (!(ctl->redo[0] | ctl->redo[1])) return false;
             kept = true;
             end = work.pos;
+            unit = work.unit - 1;
         }
-        for (begin = end; begin < work.end; begin = stretch_end(begin)) {
-            const int at = flag_of(begin);
-            if (!((ctl->redo[at >> 5] >> (at & 31)) & 1u)) continue;
-            end = stretch_end(begin);
-            return true;
+        while (end < work.end) {
+            begin = end;
+            end = stretch_end(++unit);
+            const int at = flag_of(unit);
+            if ((ctl->redo[at >> 5] >> (at & 31)) & 1u) return true;
         }
         return false;
     };
@@ -329,7 +332,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         // of a microsecond: with three of them a tile the loaders were what the rest waited for).
         const uint32_t page_size = static_cast<uint32_t>(p.cache.page_size);
         const uint32_t step_pages = kTokens / page_size, step_places = kTokens % page_size;
-        int64_t look_tile = 0, look_unit = 0, look_left = 0;
+        int64_t look_tile = 0, look_left = 0;
+        uint32_t look_unit = 0;
         uint32_t look_page = 0, look_place = 0;  // of the lane's token of tile look_tile
         auto look_at = [&]() {
             const uint32_t t = static_cast<uint32_t>(look_tile) * kTokens + loader * kMine + lane;
@@ -351,19 +355,20 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             if (look_place >= page_size) look_place -= page_size, ++look_page;
             if (++look_tile == work.tiles) {
                 look_tile = 0;
-                look_head = static_cast<int32_t>(++look_unit / p.row_tiles);
+                look_head = static_cast<int32_t>(++look_unit / row_tiles);
                 look_at();
             }
         };
-        // Leaves what was asked for to the warp, for the tile of number `n`, and asks for the next;
-        // returns which tokens exist.
-        auto look_from = [&](int64_t begin, int64_t end) {
-            look_tile = begin % work.tiles, look_unit = begin / work.tiles, look_left = end - begin;
-            look_head = static_cast<int32_t>(look_unit / p.row_tiles);
+        // The first of places [begin, end), which begin in `unit`.
+        auto look_from = [&](int64_t begin, int64_t unit, int64_t end) {
+            look_tile = begin - unit * work.tiles, look_unit = static_cast<uint32_t>(unit), look_left = end - begin;
+            look_head = static_cast<int32_t>(look_unit / row_tiles);
             look_at();
             ask_page();
         };
         int32_t box_page = 0, box_place = 0, box_head = 0;
+        // Leaves what was asked for to the warp, for the tile of number `n`, and asks for the next;
+        // returns which tokens exist.
         auto take_page = [&](int64_t n) {
             const bool there = page >= 0 && page < p.cache.num_pages;
             if (inside && !there) atomicOr(p.status, kKvErrPage);
@@ -440,36 +445,38 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 ++raw_in;
             }
         };
-        int64_t begin = work.pos, end = work.end;
+        int64_t begin = work.pos, first_unit = work.unit, end = work.end;
         bool kept = false;
         do {
-        look_from(begin, end);
+        look_from(begin, first_unit, end);
         raw_tiles += 2 * (end - begin);
         if constexpr (kE4m3)
             for (int i = 0; i < Shape::kRaws - 1; ++i) ask_raw();
-        for (int64_t pos = begin; ok && pos < end;) {
+        for (int64_t pos = begin, unit = first_unit; ok && pos < end; ++unit) {
             // A row tile's queries, once its predecessor's products are done with the buffer.
-            const int64_t unit = pos / work.tiles, seg_end = stretch_end(pos);
+            const int64_t seg_end = stretch_end(unit);
             if (segment > 0 && !warp_waited(&ctl->q_empty, static_cast<uint32_t>(segment - 1) & 1u)) {
                 ok = false;
                 break;
             }
             {
-                const int64_t head = unit / p.row_tiles, row0 = unit % p.row_tiles * kPrefixRows;
-                constexpr int kQChunks = kDim / 8;
-                for (int i = tid - 32 * kPrefixSoftmaxWarps; i < kPrefixRows * kQChunks; i += kPrefixLoaders) {
-                    const int r = i / kQChunks, qc = i % kQChunks;
-                    const int64_t row = row0 + r;
-                    if (qc * 8 >= p.cache.head_dim) continue;
-                    const bool fill = row < rows;
-                    const uint32_t b = static_cast<uint32_t>(row) / p.group, g = static_cast<uint32_t>(row) % p.group;
-                    cp_async16(smem_u32(smem) + chunk_to(kPrefixRows, r, qc),
-                               p.q + (fill ? b * p.q_stride + (head * p.group + g) * p.cache.head_dim + qc * 8 : 0), fill);
-                }
-                copies_done();
-                mbar_arrive(smem_u32(&ctl->q_full));
+                constexpr int kQChunks = kDim / 8, kStep = kPrefixLoaders / kQChunks;  // chunks of a row; rows between a thread's
+                const uint32_t head = static_cast<uint32_t>(unit) / row_tiles, group = p.group;
+                const int qc = (tid - 32 * kPrefixSoftmaxWarps) % kQChunks, r0 = (tid - 32 * kPrefixSoftmaxWarps) / kQChunks;
+                uint32_t row = (static_cast<uint32_t>(unit) - head * row_tiles) * kPrefixRows + r0, b = row / group, g = row - b * group;
+                const uint32_t step_b = kStep / group, step_g = kStep - step_b * group;
+                if (qc * 8 < p.cache.head_dim)
+#pragma unroll 4
+                    for (int r = r0; r < kPrefixRows; r += kStep) {
+                        const bool fill = row < static_cast<uint32_t>(rows);
+                        cp_async16(smem_u32(smem) + chunk_to(kPrefixRows, r, qc),
+                                   p.q + (fill ? b * p.q_stride + (static_cast<int64_t>(head) * group + g) * p.cache.head_dim + qc * 8 : 0), fill);
+                        row += kStep, b += step_b, g += step_g;
+                        if (g >= group) g -= group, ++b;
+                    }
             }
             ++segment;
+            bool asked = true;  // the queries are on their way
             for (; ok && pos < seg_end; ++pos, ++n) {
                 uint32_t bits = 0;
                 if constexpr (!kE4m3) bits = take_page(n);
@@ -530,11 +537,18 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                         async_proxy_fence();
                         mbar_arrive(smem_u32(&ctl->full[slot]));
                     }
+                    // (Only now: the first keys are asked for before the queries are waited for.  Their
+                    // slot is freed by products before this stretch's, which no queries hold up.)
+                    if (asked) {
+                        copies_done();
+                        mbar_arrive(smem_u32(&ctl->q_full));
+                        asked = false;
+                    }
                     if (++slot == kSlots) slot = 0, phase ^= 1u;
                 }
             }
         }
-        } while (more_work(begin, end, kept));
+        } while (more_work(begin, first_unit, end, kept));
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (!ok) {
             // A wait ran out: TMA copies of this warp may be on their way.  They end within
@@ -553,7 +567,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             // (The address field of a descriptor, in 16-byte units, holds every offset without a carry.)
             const uint64_t q_desc = smem_desc_sw128(smem_u32(smem), 16, 1024), k_desc = smem_desc_sw128(smem_u32(ring), 16, 1024),
                            v_desc = smem_desc_sw128(smem_u32(ring), kTokens * 128, 1024);
-            int64_t begin = work.pos, end = work.end, xpos = 0, x_seg_end = 0;
+            int64_t begin = work.pos, first_unit = work.unit, end = work.end, xpos = 0, x_seg_end = 0, x_unit = 0;
             bool kept = false;
             int segment = 0, xslot = 0;  // the ring goes keys, values, keys, values ...
             uint32_t xphase = 0;
@@ -568,7 +582,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 if (xpos == x_seg_end) {
                     if (!warp_waited(&ctl->q_full, static_cast<uint32_t>(segment) & 1u)) return false;
                     ++segment;
-                    x_seg_end = stretch_end(xpos);
+                    x_seg_end = stretch_end(x_unit++);
                 }
                 if (!warp_waited(&ctl->full[xslot], xphase)) return false;
                 tc_fence_after_sync();
@@ -595,13 +609,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             int64_t n = 0;
             bool ok = true;
             do {
-            int64_t seg_begin = begin, seg_end = stretch_end(begin);
+            int64_t unit = first_unit, seg_begin = begin, seg_end = stretch_end(unit);
             xpos = x_seg_end = begin;
+            x_unit = first_unit;
             ok = ok && issue_x(n);
             for (int64_t pos = begin; ok && pos < end; ++pos, ++n) {
                 if (pos == seg_end) {
                     seg_begin = pos;
-                    seg_end = stretch_end(pos);
+                    seg_end = stretch_end(++unit);
                 }
                 if (xpos < end) ok = issue_x(n + 1);
                 ok = ok && warp_waited(&ctl->full[vslot], vphase);
@@ -634,7 +649,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 }
                 next(vslot, vphase);
             }
-            } while (more_work(begin, end, kept));
+            } while (more_work(begin, first_unit, end, kept));
             // Every product is done before the tensor memory is given back, whatever happened.
             if (elect_one()) {
                 tc_commit<false>(smem_u32(&ctl->drain));
@@ -657,11 +672,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         const int own_barrier = 1 + group * 4 + quarter, all_barrier = 9;
         int64_t n = 0, left = 0;  // tiles; bases left before the stretch
         bool ok = true, kept = false;
-        int64_t begin = work.pos, end = work.end;
+        int64_t begin = work.pos, first_unit = work.unit, end = work.end;
         do {
-        for (int64_t pos = begin; pos < end;) {
-            const int64_t unit = pos / work.tiles, seg_first = n, seg_begin = pos, seg_end = stretch_end(pos);
-            const int64_t head = unit / p.row_tiles, row = unit % p.row_tiles * kPrefixRows + r;
+        for (int64_t pos = begin, unit = first_unit; pos < end; ++unit) {
+            const int64_t seg_first = n, seg_begin = pos, seg_end = stretch_end(unit);
+            const uint32_t head = static_cast<uint32_t>(unit) / row_tiles, row = (static_cast<uint32_t>(unit) - head * row_tiles) * kPrefixRows + r;
             const float factor = p.scale * 1.4426950408889634f * (kE4m3 && p.k_scale ? p.k_scale[head] : 1.f);
             const float none = factor < 0.f ? INFINITY : -INFINITY;
             float m = -INFINITY, l = 0.f;  // what this thread's sum is relative to
@@ -781,7 +796,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             tc_fence_after_sync();
             if (ok) {
                 float *part = p.partials + (unit + blockIdx.x) * Shape::kPart;
-                const bool mine = row < rows;
+                const bool mine = row < static_cast<uint32_t>(rows);
                 float none_of = 0.f;  // 0 · o: NaN where o is not finite
                 if (mine) {
                     if (share == 0) part[r] = last;
@@ -806,7 +821,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 // to, or a sum that is not finite, as it may then be of large values: once more, with
                 // maxima kept.
                 if (!kept && __any_sync(0xffffffffu, mine && (bad || none_of != 0.f)) && lane == 0) {
-                    const int at = flag_of(seg_begin);
+                    const int at = flag_of(unit);
                     atomicOr(&ctl->redo[at >> 5], 1u << (at & 31));
                 }
             }
@@ -814,7 +829,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             tc_fence_before_sync();
             named_barrier(all_barrier, 32 * kPrefixSoftmaxWarps);
         }
-        } while (more_work(begin, end, kept));
+        } while (more_work(begin, first_unit, end, kept));
     }
     tc_fence_before_sync();
     __syncthreads();

@@ -38,17 +38,19 @@ PrefixInstance prefix_for(const proj_kv_s *h) {
 // every row's own maximum and sum, its own output, then the prefix's parts.
 struct SharedPlan {
     PrefixInstance instance;
-    int64_t row_tiles = 0, tiles = 0;
+    int64_t row_tiles = 0, tiles = 0, combine_blocks = 0;
     int ctas = 0;
     size_t tops = 0, own = 0, parts = 0;
 };
 
-// False where the rows of a key head are too many.
+// False where the rows of a key head are too many, or all of them for the join's grid (and for
+// the prefix's 32-bit numbers of units, of 128 rows where a block of the join has 8).
 bool shared_plan(const proj_kv_s *h, int64_t sequences, int64_t prefix_len, SharedPlan &s) {
     const proj_kv_desc_t &d = h->d;
     s.instance = prefix_for(h);
     const int64_t rows = sequences * (d.q_heads / d.kv_heads);
-    if (rows > kMaxDim - 256) return false;
+    s.combine_blocks = d.kv_heads * ((rows + dev::kCombineRows - 1) / dev::kCombineRows);
+    if (rows > kMaxDim - 256 || s.combine_blocks > kMaxDim) return false;
     s.row_tiles = (rows + dev::kPrefixRows - 1) / dev::kPrefixRows;
     s.tiles = (prefix_len + s.instance.tokens - 1) / s.instance.tokens;
     const int64_t units = d.kv_heads * s.row_tiles;
@@ -159,11 +161,9 @@ proj_status_t proj_kv_attend_shared(proj_kv_handle_t h, int64_t sequences, const
     c.out = p.out;
     c.out_stride = out_stride;
     c.lse = lse;
-    const int64_t blocks = h->d.kv_heads * ((sequences * p.group + dev::kCombineRows - 1) / dev::kCombineRows);
-    if (blocks > kMaxDim) return PROJ_ERR_UNSUPPORTED;
     const int64_t units = h->d.kv_heads * s.row_tiles;
     const bool few = (s.ctas + units - 1) / units + 1 <= dev::kCombineFew;
-    return launch(few ? s.instance.combine : s.instance.combine_many, dim3(static_cast<unsigned>(blocks)),
+    return launch(few ? s.instance.combine : s.instance.combine_many, dim3(static_cast<unsigned>(s.combine_blocks)),
                   dev::kCombineThreads * (few ? 1 : dev::kCombineMost), 0, stream, c);
 }
 
