@@ -855,7 +855,6 @@ __global__ void __launch_bounds__(kCombineThreads *kGroups) kv_combine_kernel(co
     __shared__ float tops[kGroups][kCombineRows], sums[kGroups][kCombineRows];
     __shared__ float4 values[kGroups > 1 ? kGroups - 1 : 1][kDim / 4][kCombineRows];
     griddep_launch_dependents();
-    griddep_wait();
     const int tid = threadIdx.x;
     const int i = tid % kCombineRows, c = tid / kCombineRows % kCombineLanes, group = tid / (kCombineRows * kCombineLanes);
     const int rows = static_cast<int>(p.sequences) * p.group;
@@ -877,6 +876,7 @@ __global__ void __launch_bounds__(kCombineThreads *kGroups) kv_combine_kernel(co
     float4 own_values[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) own_values[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    griddep_wait();
     if (in && group == 0) {
         own = p.top[at];
 #pragma unroll
