@@ -72,9 +72,9 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
     reinterpret_cast<uint4 *>(sums)[tid] = make_uint4(0u, 0u, 0u, 0u);
     if (tid < 2) totals[tid] = 0;
     if (ranks > 1) cluster_arrive();  // the sums are clear
+    const uint32_t row_of = cluster_id_x(), kv_heads = p.cache.kv_heads;  // sequence · kv_heads + key head
+    const int64_t row = row_of, b = row_of / kv_heads;
     griddep_wait();
-    const int64_t row = cluster_id_x();  // sequence · kv_heads + key head
-    const int64_t b = row / p.cache.kv_heads;
     const int64_t table_tokens = p.cache.table_width * p.cache.page_size, wide = p.to_width * p.cache.page_size;
     int64_t n = p.seq_lens[b];
     if (n < 0 || n > table_tokens) {
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
     const int64_t stay = n < p.keep ? n : p.keep;
     // The last ones (all, where they fit) keep their order; `want` of the first m are chosen.
     const int64_t want = n > p.keep ? p.keep - p.recent : 0, m = n > p.keep ? n - p.recent : 0;
-    const int64_t span = ((m + ranks - 1) / ranks + 3) / 4 * 4;
+    const int64_t span = ((static_cast<uint32_t>(m) + ranks - 1) / ranks + 3) / 4 * 4;  // (a row's tokens fit 31 bits)
     const int64_t low = span * rank < m ? span * rank : m;
     const int mine = static_cast<int>(low + span < m ? span : m - low);  // scores low, low + 1 ... of this CTA
     const float *row_scores = p.scores + row * p.score_tokens, *in = row_scores + low;
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select_kernel(const Kv
     float *out = p.scores_out + row * wide;
     int32_t *kept = p.kept + row * p.keep;
     const int64_t step = int64_t(ranks) * kEvictThreads, at = int64_t(rank) * kEvictThreads + tid;
-    if (rank == 0 && tid == 0 && row % p.cache.kv_heads == 0) p.lens_out[b] = static_cast<int32_t>(stay);
+    if (rank == 0 && tid == 0 && row_of - static_cast<uint32_t>(b) * kv_heads == 0) p.lens_out[b] = static_cast<int32_t>(stay);
     for (int64_t i = stay + at; i < wide; i += step) out[i] = 0.f;
     for (int64_t i = stay + at; i < p.keep; i += step) kept[i] = -1;
 #pragma unroll 4
@@ -293,8 +293,9 @@ __global__ void __launch_bounds__(kEvictCopyThreads) kv_evict_copy_kernel(const 
     __shared__ int64_t from_of[kEvictCopyThreads], to_of[kEvictCopyThreads];  // bytes, of the token's row; −1: not copied
     griddep_launch_dependents();
     const KvCacheView &c = p.cache;
-    const int64_t row = blockIdx.x / blocks_of_row, part = blockIdx.x % blocks_of_row;
-    const int64_t b = row / c.kv_heads, head = row % c.kv_heads;
+    const uint32_t row_of = blockIdx.x / static_cast<uint32_t>(blocks_of_row), kv_heads = c.kv_heads;
+    const int64_t row = row_of, part = blockIdx.x % static_cast<uint32_t>(blocks_of_row);
+    const int64_t b = row_of / kv_heads, head = row_of % kv_heads;
     const int chunks = c.head_dim * p.elem / 16, pass = kEvictCopyThreads / chunks;  // tokens of a pass of the block
     const int chunk = threadIdx.x % chunks, first = threadIdx.x / chunks;
     const uint32_t page_size = static_cast<uint32_t>(c.page_size);
