@@ -32,8 +32,8 @@
 //
 // Measured: 1024 rows a key head, 8 key heads, 32768 tokens: 193 us, 712 TFLOP/s of the
 // formula's operations and 1424 of those carried out, 74 % of what a library product
-// reaches; 512 rows, 8192 tokens: 40 us (a third of it the start and end of the 13 tiles
-// that a CTA has).  Of a tile's 3000 cycles the products take 2100.  Tiles of 64 tokens in
+// reaches; 512 rows, 8192 tokens: 36 us (a quarter of it the start and end of the 13
+// tiles that a CTA has).  Of a tile's 3000 cycles the products take 2100.  Tiles of 64 tokens in
 // four buffers, a group of warps each: 294 us for the first where two of 128 took 258
 // (every change between the two products costs about 300 cycles); the products issued from
 // a branch of one lane: 418; X held in registers by 16 warps: spills.
@@ -843,7 +843,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
 // the sequences' own part.  Bytes bound it (the parts), and the few loads one after another:
 // with a few parts a unit one group of threads has them all on their way, and eight blocks an
 // SM (128 sequences behind 32768 tokens, up to four parts a unit, whole call: 224 us and 236
-// with four groups; 64 behind 8192, up to six: 81 and 78).
+// with four groups; 64 behind 8192, up to six: 81 and 78; the
+// prefix's kernel has since become 4 us shorter).
 constexpr int kCombineRows = 8, kCombineLanes = 16, kCombineMost = 4;
 constexpr int kCombineThreads = kCombineRows * kCombineLanes;  // of a group
 constexpr int kCombineFew = 4;  // parts of a unit, at most, for one group
