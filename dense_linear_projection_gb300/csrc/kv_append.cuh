@@ -365,22 +365,15 @@ __global__ void __launch_bounds__(kAppendThreads, kE4m3 ? 5 : 6) kv_append_norm_
         }
         if (pairs == 0) continue;
         if (rotary && !is_v) {
-            if constexpr (kVec && kInterleaved) {
+            // (rotate()'s separate operations: as packed products and sums the compiler fused them, and a call
+            // without norms had other bits than the append.)
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {
+            for (int x = 0; x < 8; ++x) {
+                if constexpr (kVec && kInterleaved) {
                     float *y = x < 4 ? a + 2 * x : b + 2 * (x - 4);
                     rotate(y[0], y[1], cos[x], sin[x]);
-                }
-            } else {
-                // Two pairs an instruction, in rotate()'s operations (a difference as x − 1 · y is
-                // the same number).
-#pragma unroll
-                for (int x = 0; x < 8; x += 2) {
-                    const uint64_t a2 = pair_of(a[x], a[x + 1]), b2 = pair_of(b[x], b[x + 1]);
-                    const uint64_t c2 = pair_of(cos[x], cos[x + 1]), s2 = pair_of(sin[x], sin[x + 1]);
-                    const float2 u = pair_to(fma2(mul2(b2, s2), pair_of(-1.f, -1.f), mul2(a2, c2)));
-                    const float2 v = pair_to(add2(mul2(b2, c2), mul2(a2, s2)));
-                    a[x] = u.x, a[x + 1] = u.y, b[x] = v.x, b[x + 1] = v.y;
+                } else {
+                    rotate(a[x], b[x], cos[x], sin[x]);
                 }
             }
         }
