@@ -223,20 +223,6 @@ __device__ __forceinline__ float head_norm(float *a, float *b, float of_dim, flo
     return 1.f / (root > 0x1p60f ? root : sqrtf(__fmaf_rn(root, root, sum)));
 }
 
-// Elements [at, at + 8) of a head in 8 bits, x · by with by = 1 / scale: a rounding more than the
-// division, and two values an instruction (256 tokens of 64 + 8 heads: 6.9 us with the division).
-__device__ __forceinline__ void store8_e4m3(void *to, int64_t at, const float *x, float by) {
-    uint32_t w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        // (Saturates: infinities and what is beyond ±448 become ±448; NaN stays one.)
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * by, x[4 * i + 1] * by), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * by, x[4 * i + 3] * by), __NV_SATFINITE, __NV_E4M3);
-        w[i] = lo | hi << 16;
-    }
-    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(to) + at) = make_uint2(w[0], w[1]);
-}
-
 // Eight weights from `at` on (aligned to 16 bytes).
 __device__ __forceinline__ void load_weights(const void *w, int32_t f32, int at, float *x) {
     if (f32) {
@@ -381,10 +367,6 @@ __global__ void __launch_bounds__(kAppendThreads, kE4m3 ? 5 : 6) kv_append_norm_
             if (is_q) {
                 store8<false>(to, at + r0, a, 1.f);
                 store8<false>(to, at + r1, b, 1.f);
-            } else if (kE4m3 && scale >= 0x1p-100f && scale <= 0x1p100f) {
-                const float by = 1.f / scale;
-                store8_e4m3(to, at + r0, a, by);
-                store8_e4m3(to, at + r1, b, by);
             } else {
                 store8<kE4m3>(to, at + r0, a, scale);
                 store8<kE4m3>(to, at + r1, b, scale);

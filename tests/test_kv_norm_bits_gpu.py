@@ -47,3 +47,35 @@ def test_rotation(dim, rot, interleaved):
         assert kv.status() == dlp.PROJ_OK
         assert torch.equal(q, want[:, :8]), given
         assert torch.equal(k_cache.flatten(0, 1)[:tokens], want[:, 8:]) and torch.equal(v_cache.flatten(0, 1)[:tokens], x[:, 10:])
+
+
+@pytest.mark.parametrize("dim,rot", [(128, 16), (128, 20), (64, 64), (48, 2)])
+def test_8_bits(dim, rot):
+    # Every bf16 value as an element of a value head and of a key head, at scales whose quotients come
+    # to the middle between two e4m3 numbers: x / scale, rounded once in fp32 and once to e4m3, whichever
+    # of the calls stores it.
+    import torch
+    import dense_linear_projection_gb300 as dlp
+    page, scales = 16, torch.tensor([2.06, 0.3, 1 / 3, 1.0, 0.0117, 3.0, 2.0 ** -101, 2.0 ** 101], device="cuda")
+    heads = scales.shape[0]
+    tokens = -(-65536 // dim)
+    every = torch.arange(-32768, 32768, dtype=torch.int32, device="cuda").to(torch.int16).view(torch.bfloat16)
+    every = torch.cat([every, every[:tokens * dim - 65536]]).view(tokens, 1, dim).expand(tokens, heads, dim)
+    q = rows((tokens, heads, dim), 3)
+    x = torch.cat([q, every, every], 1)
+    pos = torch.arange(tokens, dtype=torch.int32, device="cuda")
+    table = torch.arange(-(-tokens // page), dtype=torch.int32, device="cuda")[None]
+    seq, rope, w = torch.zeros_like(pos), dlp.rope_table(tokens, rot), torch.ones(dim, device="cuda")
+    divided = torch.div(every.float(), scales[:, None]).clamp(-448, 448)
+    finite = torch.isfinite(every)
+    first = None
+    for more in (dict(), dict(rope_rows=pos), dict(q_norm=w), dict(q_norm=w, rope_rows=pos), dict(k_norm=w)):
+        k_cache, v_cache = (c.view(torch.uint8).fill_(0x7f).view(c.dtype) for c in ku.make_cache(table.shape[1], page, heads, dim, "e4m3"))
+        kv = dlp.PagedKV(k_cache, v_cache, heads, 1, k_scale=scales, v_scale=scales)
+        kv.append(x[:, :heads], x[:, heads:2 * heads], x[:, 2 * heads:], pos, table, seq_ids=seq, rope=rope, **more)
+        assert kv.status() == dlp.PROJ_OK
+        got = [c.view(torch.uint8).flatten(0, 1)[:tokens].clone() for c in (k_cache, v_cache)]
+        first = first or got
+        assert torch.equal(got[1], first[1]), more
+        assert torch.equal(got[0], first[0]) or "k_norm" in more, more
+        assert torch.equal(got[1][finite], divided.to(torch.float8_e4m3fn).view(torch.uint8)[finite]), more
