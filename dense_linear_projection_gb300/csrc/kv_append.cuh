@@ -219,8 +219,9 @@ __device__ __forceinline__ float head_norm(float *a, float *b, float of_dim, flo
         sum = __fmaf_rn(a[i], a[i], __fmaf_rn(b[i], b[i], sum));
     }
     sum = group_sum(sum, lanes, mask) * of_dim;
-    const float root = sqrtf(eps) * down;  // its square may be out of range, and then is all there is
-    return 1.f / (root > 0x1p60f ? root : sqrtf(__fmaf_rn(root, root, sum)));
+    // (Its square may be out of range, and then is all there is.  `top` does not know of a NaN; the sum does.)
+    const float root = sqrtf(eps) * down;
+    return 1.f / (root > 0x1p60f && sum == sum ? root : sqrtf(__fmaf_rn(root, root, sum)));
 }
 
 // Eight weights from `at` on (aligned to 16 bytes).
