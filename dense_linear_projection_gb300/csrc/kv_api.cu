@@ -141,6 +141,7 @@ proj_status_t proj_kv_create(proj_kv_handle_t *out, const proj_kv_desc_t *desc, 
     h->sm_count = sms;
     h->device = device_of_handle();
     h->elem = elem;
+    h->fault_place = fault_wait_place();
     const int group = d.q_heads / d.kv_heads, most = d.head_dim <= 128 ? 16 : 8;
     h->chunks = (group + most - 1) / most;
     h->chunk_heads = (group + h->chunks - 1) / h->chunks;

@@ -22,6 +22,7 @@ struct proj_kv_s {
     int *status = nullptr;
     uint32_t *counters = nullptr, *group_counters = nullptr;
     float *partials = nullptr;
+    int64_t fault_place = -1;         // where the next prefix kernel's wait runs out (fault injection)
 };
 
 namespace projgb {

@@ -129,6 +129,8 @@ struct KvPrefixParams {
     int32_t box;               // tokens of a TMA box, 0: copies instead
     float *partials;           // [unit + CTA][maxima, sums, values]
     int *status;
+    int64_t wait_limit_ns;     // bounded waits give up after this long
+    int64_t fault_place;       // fault injection: of a CTA's places, where a wait runs out; −1: none
 };
 
 struct KvCombineParams {

@@ -38,8 +38,8 @@
 // (every change between the two products costs about 300 cycles); the products issued from
 // a branch of one lane: 418; X held in registers by 16 warps: spills.
 //
-// Every wait is bounded; one that runs out records itself, and the CTA drains its
-// copies, frees its tensor memory and returns.
+// Every wait is bounded (wait_limit_ns); one that runs out records itself, and the CTA drains its
+// products and copies, frees its tensor memory and returns.
 #pragma once
 
 #include "kv_attend.cuh"
@@ -57,6 +57,8 @@ constexpr int kPrefixThreads = 32 * (kPrefixSoftmaxWarps + kPrefixLoadWarps + 1)
 constexpr float kLazy = 8.f;
 constexpr float kMostSum = 0x1p64f;  // of a tile's weights, relative to the first tile's maximum
 constexpr int64_t kPrefixWaitNs = 1000000000;
+constexpr int64_t kPrefixFaultNs = 100000;   // instead, where one is to run out
+constexpr uint64_t kPrefixLandNs = 2000000;  // for copies on their way
 
 template <bool kE4m3, int kDim>
 struct PrefixShape {
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     griddep_launch_dependents();
 
     auto waited = [&](uint64_t *bar, uint32_t parity) {
-        return wait_phase(smem_u32(bar), parity, abort_flag, p.status, kKvErrWait, kPrefixWaitNs);
+        return wait_phase(smem_u32(bar), parity, abort_flag, p.status, kKvErrWait, p.wait_limit_ns);
     };
     // The same for a whole warp, whose lanes go on or stop together.
     auto warp_waited = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, waited(bar, parity)) != 0; };
@@ -451,7 +453,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         look_from(begin, first_unit, end);
         raw_tiles += 2 * (end - begin);
         if constexpr (kE4m3)
-            for (int i = 0; i < Shape::kRaws - 1; ++i) ask_raw();
+            for (int i = 0; ok && i < Shape::kRaws - 1; ++i) ask_raw();
         for (int64_t pos = begin, unit = first_unit; ok && pos < end; ++unit) {
             // A row tile's queries, once its predecessor's products are done with the buffer.
             const int64_t seg_end = stretch_end(unit);
@@ -550,13 +552,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         }
         } while (more_work(begin, first_unit, end, kept));
         asm volatile("cp.async.wait_all;" ::: "memory");
-        if (!ok) {
-            // A wait ran out: TMA copies of this warp may be on their way.  They end within
-            // microseconds; a barrier that other warps did not come to does not tell.
-            const uint64_t t0 = globaltimer_ns();
-            while (globaltimer_ns() - t0 < 2000000u) {
-            }
-        }
     } else if (warp == kPrefixSoftmaxWarps + kPrefixLoadWarps) {
         // ------------------------------------------------------------ products
         // The whole warp runs the loop, so that descriptors and addresses are the same in every
@@ -579,6 +574,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             };
             // X of the next place; false once a wait ran out.
             auto issue_x = [&](int64_t n) {
+                // (Fault injection: nobody arrives on that barrier.  As any wait that runs out, wherever.)
+                if (n == p.fault_place && !warp_waited(&ctl->drain, 0)) return false;
                 if (xpos == x_seg_end) {
                     if (!warp_waited(&ctl->q_full, static_cast<uint32_t>(segment) & 1u)) return false;
                     ++segment;
@@ -834,6 +831,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     tc_fence_before_sync();
     __syncthreads();
     if (warp == kPrefixSoftmaxWarps + kPrefixLoadWarps) {
+        if (*abort_flag) {
+            // A wait ran out, in whichever role: TMA copies that nobody has waited for may be on their
+            // way to this block's memory, those of loaders that came to their end among them.  They
+            // land within microseconds; a barrier that not everyone came to does not tell.
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < kPrefixLandNs) {
+            }
+        }
         tc_fence_after_sync();
         tmem_dealloc<false>(tmem, 512);
     }

@@ -123,6 +123,9 @@ proj_status_t proj_kv_attend_shared(proj_kv_handle_t h, int64_t sequences, const
     x.tiles = s.tiles;
     x.partials = reinterpret_cast<float *>(at + s.tops + s.own);
     x.status = h->status;
+    x.wait_limit_ns = h->fault_place < 0 ? dev::kPrefixWaitNs : dev::kPrefixFaultNs;
+    x.fault_place = h->fault_place;
+    h->fault_place = -1;
     // Boxes of whole 8-row groups of the swizzle, within a loading warp's tokens.  Without TMA
     // (other page sizes, strides that a tensor map cannot have): 16-byte copies.
     CUtensorMap maps[2] = {};

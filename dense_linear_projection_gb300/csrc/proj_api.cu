@@ -24,9 +24,11 @@ namespace projgb {
 // Host-side fault injection for tests (PROJ_FAULT, read once per process): a
 // comma-separated list of "alloc" (every device allocation of the library
 // fails as out of memory), "encode" (every tensor-map encoding fails),
-// "launch" (every kernel launch fails before it is queued) and "device" (every
-// handle is taken for another device's).  The failure is made on the host:
-// nothing faulty reaches the device.
+// "launch" (every kernel launch fails before it is queued), "device" (every
+// handle is taken for another device's).  The failure is made on the host: nothing
+// faulty reaches the device.  "wait<n>": in the first call of a cache handle that has
+// bounded waits, every block waits at its place n for a barrier that nobody arrives
+// on, and gives up.
 int fault_mask() {
     static const int mask = [] {
         int m = 0;
@@ -39,6 +41,15 @@ int fault_mask() {
         return m;
     }();
     return mask;
+}
+
+int64_t fault_wait_place() {
+    static const int64_t place = [] {
+        const char *e = std::getenv("PROJ_FAULT");
+        const char *at = e ? std::strstr(e, "wait") : nullptr;
+        return at ? std::strtoll(at + 4, nullptr, 10) : -1ll;
+    }();
+    return place;
 }
 
 cudaError_t dev_malloc(void **p, size_t bytes) {

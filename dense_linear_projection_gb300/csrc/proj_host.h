@@ -11,6 +11,7 @@ namespace projgb {
 constexpr int kFaultAlloc = 1, kFaultEncode = 2, kFaultLaunch = 4, kFaultDevice = 8;
 int fault_mask();
 inline bool launch_faulted() { return (fault_mask() & kFaultLaunch) != 0; }
+int64_t fault_wait_place();  // of "wait<n>", −1 without
 
 // Every device allocation of the library goes through here.
 cudaError_t dev_malloc(void **p, size_t bytes);
