@@ -39,7 +39,8 @@
 // a branch of one lane: 418; X held in registers by 16 warps: spills.
 //
 // Every wait is bounded (wait_limit_ns); one that runs out records itself, and the CTA drains its
-// products and copies, frees its tensor memory and returns.
+// products and copies, frees its tensor memory and returns; the rows whose parts it had not
+// computed then come out as NaN.
 #pragma once
 
 #include "kv_attend.cuh"
@@ -219,6 +220,13 @@ struct PrefixWork {
     }
 };
 
+// The part of a CTA that has not computed it: NaN in the sums of thread t of the sums' kPrefixSums ·
+// kPrefixRows, so that the rows' outputs and log sums are NaN and not what the memory held before.
+template <class Shape>
+__device__ __forceinline__ void leave_nan(const KvPrefixParams &p, int64_t unit, int t) {
+    if (t < kPrefixSums * kPrefixRows) p.partials[(unit + blockIdx.x) * Shape::kPart + kPrefixRows + t] = NAN;
+}
+
 template <bool kE4m3, int kDim>
 __global__ void __launch_bounds__(kPrefixThreads, 1)
     kv_prefix_kernel(const __grid_constant__ KvPrefixParams p, const __grid_constant__ CUtensorMap k_map,
@@ -238,6 +246,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     if (smem_u32(smem) & 1023u) {  // (128-byte swizzled tiles; the same in every thread)
         griddep_wait();  // (the next kernel counts on what came before this one)
         if (tid == 0) atomicOr(p.status, kKvErrWait);
+        const PrefixWork work(p);
+        for (int64_t unit = work.unit; unit * work.tiles < work.end; ++unit) leave_nan<Shape>(p, unit, tid);
         return;
     }
     if (warp == kPrefixSoftmaxWarps + kPrefixLoadWarps) {
@@ -821,6 +831,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     const int at = flag_of(unit);
                     atomicOr(&ctl->redo[at >> 5], 1u << (at & 31));
                 }
+            } else {
+                leave_nan<Shape>(p, unit, share * kPrefixRows + r);
             }
             // No product of the next stretch begins before all of o is read.
             tc_fence_before_sync();

@@ -1,7 +1,7 @@
 """Attention behind a shared prefix when a bounded wait runs out (PROJ_FAULT=wait<n>, read once per process:
 in a handle's first such call every block waits at its n-th tile for a barrier that nobody arrives on).  The
 kernel gives up by itself, with its copies and products landed: the call returns, the status tells once,
-and the handle's next call is right."""
+the rows that were not computed are NaN, and the handle's next call is right."""
 import json
 import os
 import subprocess
@@ -39,6 +39,35 @@ CASES = [(prefix_len, lens, 8, 2, dim, page, dtype)
          for dim in (64, 128, 256) for page, dtype in ((16, "bf16"), (3, "bf16"), (16, "e4m3"), (17, "e4m3"))]
 
 
+# An earlier call's results in the memory that the workspace comes from: other values, as plausible.
+STALE = r"""
+import json, sys, torch
+sys.path.insert(0, "tests")
+import dense_linear_projection_gb300 as dlp
+import kv_util as ku
+from test_kv_shared_gpu import case, shared64
+
+result = []
+for prefix_len, lens, heads, kv_heads, dim, page, dtype in json.loads(sys.argv[1]):
+    kv, q, prefix, table, n, scales = case(prefix_len, lens, heads, kv_heads, dim, page, dtype=dtype)
+    before, _, lim, lim_lse = shared64(q, kv.k_cache, kv.v_cache, prefix, prefix_len, table, lens, page, dim ** -0.5, *scales)
+    kv.attend_shared(-q, prefix, prefix_len, table, n)   # gives up
+    kv.attend_shared(-q, prefix, prefix_len, table, n)
+    assert kv.status() == dlp.PROJ_ERR_DEVICE_TIMEOUT
+    late = dlp.PagedKV(kv.k_cache, kv.v_cache, heads, len(lens), k_scale=scales[0], v_scale=scales[1])
+    out, lse = late.attend_shared(q, prefix, prefix_len, table, n, return_lse=True)  # gives up
+    assert late.status() == dlp.PROJ_ERR_DEVICE_TIMEOUT
+    good, good_lse = late.attend_shared(q, prefix, prefix_len, table, n, return_lse=True)
+    assert late.status() == dlp.PROJ_OK
+    # Each row is the right one, bit for bit, or NaN.
+    nan = out.isnan().all(-1)
+    assert torch.equal(nan, out.isnan().any(-1)) and torch.equal(nan, lse.isnan())
+    assert torch.equal(out[~nan], good[~nan]) and torch.equal(lse[~nan], good_lse[~nan]) and not good.isnan().any()
+    result.append(int(nan.sum()) / nan.numel())
+print("RESULT " + json.dumps(result))
+"""
+
+
 def child(cases, fault, code=CHILD):
     import dense_linear_projection_gb300 as dlp
     dlp.build()
@@ -58,6 +87,16 @@ def test_gives_up_and_goes_on(place):
     for case, r in zip(CASES, child(CASES, f"wait{place}")):
         gives_up = place == 0 or case[0] == 40000
         assert r == {"gave_up": [dlp.PROJ_ERR_DEVICE_TIMEOUT if gives_up else dlp.PROJ_OK, dlp.PROJ_OK], "after": dlp.PROJ_OK}, case
+
+
+@pytest.mark.parametrize("place", [0, 2])
+def test_rows_that_were_not_computed_are_nan(place):
+    # At the first tile every row lacks something, and so does every row whose tiles are shared by blocks
+    # of more; five row tiles a key head, of 313 or 625 tiles each.
+    cases = [(40000, [9] * 160, 8, 2, dim, page, dtype) for dim in (64, 128, 256) for page, dtype in ((16, "bf16"), (3, "bf16"), (16, "e4m3"))]
+    assert child(cases, f"wait{place}", STALE) == [1.0] * len(cases)
+    if place == 0:
+        assert child([CASES[i] for i in range(0, len(CASES), 3)], "wait0", STALE) == [1.0] * -(-len(CASES) // 3)
 
 
 def test_nothing_is_injected_without_the_variable():
