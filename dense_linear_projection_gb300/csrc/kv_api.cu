@@ -224,7 +224,10 @@ proj_status_t proj_kv_device_status(proj_kv_handle_t h, void *stream) {
         return PROJ_ERR_CUDA;
     }
     if (word == 0) return PROJ_OK;
-    if (cudaMemsetAsync(h->status, 0, sizeof word, as_stream(stream)) != cudaSuccess ||
+    // A wait that ran out is told first; what else was found stays for the next call.  (The bits are in
+    // the word's first byte.)
+    const int rest = (word & kKvErrWait) ? word & ~kKvErrWait : 0;
+    if (cudaMemsetAsync(h->status, rest, 1, as_stream(stream)) != cudaSuccess ||
         cudaStreamSynchronize(as_stream(stream)) != cudaSuccess) {
         cudaGetLastError();
         return PROJ_ERR_CUDA;

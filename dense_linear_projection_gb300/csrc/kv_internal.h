@@ -20,7 +20,7 @@ constexpr int kKvMinPlaces = 2;  // of a CTA (one head of 1000 tokens: 1, 2, 4 g
 // in groups of 16 and 90.5 in groups of 8.
 constexpr int kKvJoinOnce = 16, kKvJoinGroup = 8, kKvJoinMany = 128;
 
-// Bits of the cache handle's status word: what a kernel found out of range.
+// Bits of the cache handle's status word, below 2^8: what a kernel found out of range.
 constexpr int kKvErrPosition = 1 << 0;  // position past the page table or the rope table
 constexpr int kKvErrSequence = 1 << 1;  // sequence id outside the page table
 constexpr int kKvErrPage = 1 << 2;      // page outside the cache

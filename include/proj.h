@@ -608,7 +608,7 @@ proj_status_t proj_q4_destroy(proj_q4_handle_t h);
  * and proj_kv_device_status then returns PROJ_ERR_INVALID_ARG once: it waits for
  * `stream`, which has to be the one that the handle's calls ran on.  It returns
  * PROJ_ERR_DEVICE_TIMEOUT once where a bounded wait of proj_kv_attend_shared ran out
- * (1 s; the rows that it was for are NaN in out and lse).
+ * (1 s; the rows that it was for are NaN in out and lse), before anything else that was found.
  */
 typedef struct proj_kv_s *proj_kv_handle_t;
 

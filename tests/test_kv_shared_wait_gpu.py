@@ -103,3 +103,14 @@ def test_nothing_is_injected_without_the_variable():
     import dense_linear_projection_gb300 as dlp
     for case, r in zip(CASES[:4], child(CASES[:4], "")):
         assert r == {"gave_up": [dlp.PROJ_OK, dlp.PROJ_OK], "after": dlp.PROJ_OK}, case
+
+
+def test_what_else_was_found_is_told_after_the_wait():
+    import dense_linear_projection_gb300 as dlp
+    code = CHILD[:CHILD.index("result = []")] + r"""
+kv, q, prefix, table, n, _ = case(1000, [20, 20], 8, 2, 64, 16)
+table[0, 1] = -1
+kv.attend_shared(q, prefix, 1000, table, n)
+print("RESULT " + json.dumps([kv.status() for _ in range(3)]))
+"""
+    assert child([], "wait0", code) == [dlp.PROJ_ERR_DEVICE_TIMEOUT, dlp.PROJ_ERR_INVALID_ARG, dlp.PROJ_OK]
