@@ -473,8 +473,11 @@ __global__ void __launch_bounds__(kKvThreads, AttendShape<kE4m3, kDim, kNT, kKey
     for (int s = 0; s < kStages; ++s) valid[s] = 0;
     const int row_chunks = cache.head_dim * Shape::kElem / 16;
     // Logits are read again by the next kernel and keys and values are not: with these two hints
-    // more of the logits are still in the L2 cache then.
-    const uint64_t keep_policy = kLeaves == kAttendLogits ? l2_policy_evict_last() : 0;
+    // more of the logits are still in the L2 cache then (64 ragged sequences to 8192: 205 and 200 us
+    // with 8 query heads a key head, 189 and 184 with 4; 270 and 275 with 16, whose logits are more
+    // than the cache holds).  Only where that kernel's read says that they are done with: kept lines
+    // would else stay in the cache before everyone's (6 heads: 200 us, 196.5 with them kept).
+    const uint64_t keep_policy = kLeaves != kAttendLogits ? 0 : scored_in_fours(p.group) ? l2_policy_evict_last() : l2_policy_evict_normal();
     const uint64_t pass_policy = kLeaves == kAttendLogits ? l2_policy_evict_first() : 0;
     auto copy16 = [&](uint32_t to, const void *from, bool fill) {
         if constexpr (kLeaves == kAttendLogits)

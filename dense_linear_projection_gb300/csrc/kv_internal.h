@@ -87,6 +87,10 @@ struct KvAttendParams {
     float *out32;    // [sequence][query head][head_dim]: the output before rounding
 };
 
+// Scored attention: numbers of query heads of a key head whose logits the second kernel reads four at a
+// time, and for the last time.
+__host__ __device__ constexpr bool scored_in_fours(int group) { return group % 4 == 0 && group <= 16; }
+
 // What an attention kernel leaves beside, or instead of, the rounded output.
 constexpr int kAttendPlain = 0;   // the output
 constexpr int kAttendLogits = 1;  // the output, every logit, and each row's maximum and sum

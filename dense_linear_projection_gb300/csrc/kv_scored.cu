@@ -17,6 +17,18 @@ namespace {
 // The workspace: every row's maximum and sum, then the logits.
 size_t tops_bytes(const proj_kv_s *h, int64_t sequences) { return rounded(static_cast<size_t>(sequences) * h->d.q_heads * sizeof(float2)); }
 
+// Blocks enough for every SM, no more of a row than it has tokens for.
+template <int kGroup>
+proj_status_t launch_score(const proj_kv_s *h, const KvScoreParams &s, void *stream) {
+    const int64_t at_once = int64_t(dev::kScoreThreads) * dev::kScoreAhead<kGroup>;
+    const int64_t rows = s.sequences * s.kv_heads, most = (s.score_tokens + at_once - 1) / at_once;
+    int64_t of_row = (int64_t(h->sm_count) * 32 + rows - 1) / rows;
+    if (of_row > most) of_row = most;
+    if (rows * of_row > kMaxDim) return PROJ_ERR_UNSUPPORTED;
+    return launch(dev::kv_score_kernel<kGroup>, dim3(static_cast<unsigned>(rows * of_row)), dev::kScoreThreads, 0, stream, s,
+                  static_cast<int>(of_row));
+}
+
 }  // namespace
 
 extern "C" {
@@ -61,18 +73,14 @@ proj_status_t proj_kv_attend_scored(proj_kv_handle_t h, int64_t sequences, const
     s.window = window;
     s.kv_heads = h->d.kv_heads;
     s.group = p.group;
-    // Blocks enough for every SM, no more of a row than it has tokens for.
-    const bool ahead = p.group == 8 || p.group == 4;
-    const int64_t at_once = int64_t(dev::kScoreThreads) * (ahead ? dev::kScoreAhead : 1);
-    const int64_t rows = sequences * h->d.kv_heads, most = (score_tokens + at_once - 1) / at_once;
-    int64_t of_row = (int64_t(h->sm_count) * 32 + rows - 1) / rows;
-    if (of_row > most) of_row = most;
-    if (rows * of_row > kMaxDim) return PROJ_ERR_UNSUPPORTED;
-    const dim3 grid(static_cast<unsigned>(rows * of_row));
-    const int blocks = static_cast<int>(of_row), t = dev::kScoreThreads;
-    if (p.group == 8) return launch(dev::kv_score_kernel<8>, grid, t, 0, stream, s, blocks);
-    if (p.group == 4) return launch(dev::kv_score_kernel<4>, grid, t, 0, stream, s, blocks);
-    return launch(dev::kv_score_kernel<0>, grid, t, 0, stream, s, blocks);
+    static_assert(scored_in_fours(4) && scored_in_fours(8) && scored_in_fours(12) && scored_in_fours(16) && !scored_in_fours(20));
+    switch (p.group) {
+        case 4: return launch_score<4>(h, s, stream);
+        case 8: return launch_score<8>(h, s, stream);
+        case 12: return launch_score<12>(h, s, stream);
+        case 16: return launch_score<16>(h, s, stream);
+        default: return launch_score<0>(h, s, stream);
+    }
 }
 
 }  // extern "C"

@@ -24,10 +24,13 @@ __device__ __forceinline__ float4 load_once(const float *from, uint64_t policy) 
     return v;
 }
 
-// kGroup: query heads of a key head where these are 4 or 8, whose maxima and sums stay in registers
-// and whose logits of kScoreAhead tokens are asked for together; 0 for other numbers.  (64 ragged
-// sequences: 20.6 us for 100 MB, of 197 with the attention.)
-constexpr int kScoreAhead = 4;
+// kGroup: query heads of a key head where these are a multiple of four up to 16: the maxima and sums stay
+// in registers, the logits come in fours, of kScoreAhead tokens together.  (64 ragged sequences to 8192, 8
+// key heads, whole call: 16 heads 275 us, 312 as below; over 8 bits, 4 key heads, 129 and 147; 12 heads of
+// 4 key heads 135.5 and 142.5; 8 heads 20.6 us for 100 MB.)  0: other numbers, a token and a head at a
+// time (1: 182, 2: 184, 3: 189, 6: 200, 7: 204; 1 and 2 in the way of the fours 178 and 180).
+template <int kGroup>
+constexpr int kScoreAhead = kGroup == 0 ? 1 : kGroup <= 8 ? 4 : 2;  // tokens
 
 template <int kGroup>
 __global__ void __launch_bounds__(kScoreThreads) kv_score_kernel(const KvScoreParams p, const int blocks_of_row) {
@@ -48,14 +51,15 @@ __global__ void __launch_bounds__(kScoreThreads) kv_score_kernel(const KvScorePa
     const int64_t step = int64_t(blocks_of_row) * kScoreThreads;
     auto weight = [&](float y, float2 r) { return exp2_fast(y - finite_or_zero(r.x)) * r.y; };
     if constexpr (kGroup > 0) {
+        constexpr int kAhead = kScoreAhead<kGroup>;
         float2 held[kGroup];
 #pragma unroll
         for (int g = 0; g < kGroup; ++g) held[g] = top[g];
-        for (int64_t t0 = from + part * kScoreThreads + threadIdx.x; t0 < to; t0 += kScoreAhead * step) {
-            float before[kScoreAhead];
-            float4 v[kScoreAhead][kGroup / 4];
+        for (int64_t t0 = from + part * kScoreThreads + threadIdx.x; t0 < to; t0 += kAhead * step) {
+            float before[kAhead];
+            float4 v[kAhead][kGroup / 4];
 #pragma unroll
-            for (int k = 0; k < kScoreAhead; ++k) {
+            for (int k = 0; k < kAhead; ++k) {
                 const int64_t t = t0 + k * step;
                 before[k] = t < to ? in[t] : 0.f;
 #pragma unroll
@@ -63,7 +67,7 @@ __global__ void __launch_bounds__(kScoreThreads) kv_score_kernel(const KvScorePa
                     v[k][g] = t >= low && t < n ? load_once(x + t * kGroup + 4 * g, policy) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
             }
 #pragma unroll
-            for (int k = 0; k < kScoreAhead; ++k) {
+            for (int k = 0; k < kAhead; ++k) {
                 const int64_t t = t0 + k * step;
                 if (t >= to) break;
                 float sum = 0.f;
