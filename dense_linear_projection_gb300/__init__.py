@@ -737,7 +737,9 @@ class PagedKV:
         """:meth:`attend` for a batch whose sequences all begin with the same
         ``prefix_len`` tokens, which lie in ``prefix_pages`` (int32 [pages]) and
         are read once for all of them; ``page_table`` and ``seq_lens`` are of
-        each sequence's own tokens after them (0: none)."""
+        each sequence's own tokens after them (0: none).  Allocates a workspace
+        (:func:`proj_kv_shared_workspace`; 128 sequences of 64 heads of 128
+        behind 32768 tokens: 19 MB) from the stream's memory."""
         return self._attend_shared(self.handle, self.q_heads, self.kv_heads, self.head_dim, self.k_cache, self.v_cache,
                                    self.k_scale, self.v_scale, q, prefix_pages, prefix_len, page_table, seq_lens,
                                    self._scale if scale is None else scale, out, return_lse, _stream(stream))
@@ -747,7 +749,13 @@ class PagedKV:
         """:meth:`attend` that adds each token's softmax weight, summed over the
         query heads of a key head, to ``scores`` (fp32 [sequences, kv_heads,
         tokens of the page table or more]), in place or into ``scores_out``.
-        Returns ``(out, scores)``, and the log sums when ``return_lse``."""
+        Returns ``(out, scores)``, and the log sums when ``return_lse``.  The
+        weights are those among ``page_table``'s tokens (after
+        :meth:`attend_shared`'s prefix: not the whole text's).  Allocates a
+        workspace of 4 bytes for each query head and token that the page table
+        has room for, whatever the lengths are (64 sequences of 64 heads and a
+        table for 131072 tokens: 2.1 GB): keep the table as wide as the longest
+        sequence needs."""
         return self._attend_scored(self.handle, self.q_heads, self.kv_heads, self.head_dim, self.k_cache, self.v_cache,
                                    self.k_scale, self.v_scale, q, page_table, seq_lens, scores,
                                    self._scale if scale is None else scale, window, scores_out, out, return_lse,

@@ -184,8 +184,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const KvAppen
 // two of them, idle ones past the last unit), so a head is read once and meets in
 // log2(lanes) shuffles, while its next head is on the way; bytes bound it as they
 // bound the append alone.  8191 tokens of 96 heads: 80 us (75 % of the copy
-// bandwidth) with six blocks an SM, 85 with five (over 8 bits those are quicker, 6.3
-// us and 6.9 for 256 tokens), 92 without the next head, 114 with the weights held in
+// bandwidth) with six blocks an SM, 85 with five (over 8 bits, 256 tokens of 64 + 16
+// heads: 6.9 and 6.3; 8191 of 96: 86 and 88.5), 92 without the next head, 114 with the weights held in
 // registers, which leave room for fewer warps than reading them from the L1 cache.
 // The norm of one head: Σ x² below 2^120, and above 2^-90 where eps is too small to
 // hide what squares below 2^-126 lose, is taken as it is; else the head is scaled by
@@ -228,7 +228,8 @@ __device__ __forceinline__ float head_norm(float *a, float *b, float of_dim, flo
 // 1 / scale (within[0] and within[1]).  Rounding is monotonic: the quotient, rounded to fp32 and then to
 // e4m3, is between the two products' e4m3 numbers, and where these are one it is that one.  Else, near the
 // middle between two e4m3 numbers, the division (a few values in a million; more where scales have few
-// bits, whose quotients come to the very middle).  8191 tokens of 96 heads: 106 us with divisions alone.
+// bits, whose quotients come to the very middle).  8191 tokens of 96 heads: 88.5 us, 106 with divisions
+// alone; 103 where every scale is 3.
 __device__ __forceinline__ void store8_between(void *to, int64_t at, const float *x, float scale, const float (&within)[2]) {
     uint32_t w[2][2];  // [product][word]
 #pragma unroll

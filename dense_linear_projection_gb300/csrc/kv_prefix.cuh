@@ -23,7 +23,8 @@
 //     exact at 2^60 as at 1.  Where a tile's sum comes to 2^64, or o is not finite, the
 //     stretch is done again with running maxima, o rescaled where they grow by more than
 //     2^8 (kLazy).  (With running maxima throughout, 128 sequences behind 32768 tokens took
-//     237 us.)
+//     237 us.  Nearly every stretch done again, with keys that rise so far or infinite values
+//     everywhere: 226 -> 415 us; 64 sequences behind 8192 73.5 -> 107; over 8 bits 74 -> 128.)
 //   * warps 16..19 fill a ring of token tiles: pages of whole multiples of 8 tokens by TMA
 //     boxes of up to 32 tokens, others, and the prefix's end, by 16-byte asynchronous copies
 //     (which any page size and strides allow); warp 20 issues the products.
@@ -288,7 +289,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     const PrefixWork work(p);
     griddep_wait();
     // Only now: the own tokens' attention, launched after this kernel, does not wait for its results
-    // and reads what the kernels before this one wrote (64 CTAs of a small call leave 88 SMs to it).
+    // and reads what the kernels before this one wrote (64 CTAs of a small call leave 88 SMs to it; on an
+    // SM with a CTA of this kernel there is no room for one of it, so that with a CTA on every SM it
+    // follows, as these end).
     griddep_launch_dependents();
 
     auto waited = [&](uint64_t *bar, uint32_t parity) {

@@ -641,8 +641,10 @@ proj_status_t proj_kv_device_status(proj_kv_handle_t h, void *stream);
 proj_status_t proj_kv_destroy(proj_kv_handle_t h);
 
 /*
- * More on the same cache.  What proj_kv_append and proj_kv_attend say of layouts,
- * alignment, streams, devices, captures and of what only the device sees holds here.
+ * More on the same cache.  Their kernels are made ready by proj_kv_create, so that a capture need not
+ * do it: the first handle of a process takes 47 ms (15 without them), later ones 0.2 to 0.3.
+ * What proj_kv_append and proj_kv_attend say of layouts, alignment, streams, devices, captures
+ * and of what only the device sees holds here.
  *
  * proj_kv_append_normed: proj_kv_append with the norm of every head of q and k first,
  *     y[e] = x[e] · w[e] / sqrt(Σ x² / head_dim + eps),
@@ -660,15 +662,19 @@ proj_status_t proj_kv_destroy(proj_kv_handle_t h);
  *   Logits, weights and sums are fp32; a weight enters the product with the values
  *   in parts of 24 bits (of the own tokens over e4m3: as proj_kv_attend says).  An
  *   infinite value gives infinity where its weight is above 2^-90 of the largest
- *   (below, NaN).  prefix_len = 0 is proj_kv_attend.  workspace: device memory of the
- *   size that proj_kv_shared_workspace gives (16-byte aligned), the call's own until
- *   it is done.
+ *   (below, NaN).  The prefix's sums are the tensor core's, fp32 and cut off rather than
+ *   rounded.  Tokens whose weights come to 2^64 times those that a block begins with, and
+ *   values that are not finite, make it go over its tokens twice.  prefix_len = 0 is
+ *   proj_kv_attend.  workspace: device memory of the size that proj_kv_shared_workspace
+ *   gives (16-byte aligned), the call's own until it is done.
  *
  * proj_kv_attend_scored: proj_kv_attend, and for each key head g and attended token t
  *     scores_out[b,g,t] = scores[b,g,t] + Σ_h softmax weight of t for query head h of g;
- *   the other scores are copied.  scores, scores_out: fp32 [sequences, kv_heads,
- *   score_tokens], score_tokens at least the page table's tokens; the two may be one
- *   array, and may not overlap otherwise.  Tokens left out for a bad page have weight 0.
+ *   the other scores are copied.  The weights are those among the tokens of page_table:
+ *   behind a shared prefix, whose attention leaves no scores, they are not the whole
+ *   text's.  scores, scores_out: fp32 [sequences, kv_heads, score_tokens], score_tokens at
+ *   least the page table's tokens; the two may be one array, and may not overlap
+ *   otherwise.  Tokens left out for a bad page have weight 0.
  *   workspace: as above, of proj_kv_scored_workspace's size (4 bytes for each query
  *   head and token that the page table has room for).
  *
