@@ -778,7 +778,9 @@ class PagedKV:
     def status(self, stream=None) -> int:
         """What the kernels found so far on ``stream`` (by default the current
         one, as for the calls): PROJ_ERR_INVALID_ARG once after an index out of
-        range.  Waits for the stream; the word of another stream's calls may not
+        range, and before it PROJ_ERR_DEVICE_TIMEOUT once after a bounded wait of
+        :meth:`attend_shared` ran out (rows that lack a part are NaN then).
+        Waits for the stream; the word of another stream's calls may not
         be there yet."""
         import torch
         if stream is None:

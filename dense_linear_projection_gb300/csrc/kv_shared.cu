@@ -123,9 +123,13 @@ proj_status_t proj_kv_attend_shared(proj_kv_handle_t h, int64_t sequences, const
     x.tiles = s.tiles;
     x.partials = reinterpret_cast<float *>(at + s.tops + s.own);
     x.status = h->status;
-    x.wait_limit_ns = h->fault_place < 0 ? dev::kPrefixWaitNs : dev::kPrefixFaultNs;
-    x.fault_place = h->fault_place;
-    h->fault_place = -1;
+    x.wait_limit_ns = dev::kPrefixWaitNs;
+    x.fault_place = -1;
+    if (h->fault_place >= 0) {
+        x.wait_limit_ns = dev::kPrefixFaultNs;
+        x.fault_place = h->fault_place;
+        h->fault_place = -1;  // (the next calls are as ever)
+    }
     // Boxes of whole 8-row groups of the swizzle, within a loading warp's tokens.  Without TMA
     // (other page sizes, strides that a tensor map cannot have): 16-byte copies.
     CUtensorMap maps[2] = {};
