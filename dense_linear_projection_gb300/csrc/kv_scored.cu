@@ -17,14 +17,15 @@ namespace {
 // The workspace: every row's maximum and sum, then the logits.
 size_t tops_bytes(const proj_kv_s *h, int64_t sequences) { return rounded(static_cast<size_t>(sequences) * h->d.q_heads * sizeof(float2)); }
 
+constexpr int kScoreBlocks = 32;  // of an SM, at least
+
 // Blocks enough for every SM, no more of a row than it has tokens for.
 template <int kGroup>
 proj_status_t launch_score(const proj_kv_s *h, const KvScoreParams &s, void *stream) {
     const int64_t at_once = int64_t(dev::kScoreThreads) * dev::kScoreAhead<kGroup>;
     const int64_t rows = s.sequences * s.kv_heads, most = (s.score_tokens + at_once - 1) / at_once;
-    int64_t of_row = (int64_t(h->sm_count) * 32 + rows - 1) / rows;
+    int64_t of_row = (int64_t(h->sm_count) * kScoreBlocks + rows - 1) / rows;
     if (of_row > most) of_row = most;
-    if (rows * of_row > kMaxDim) return PROJ_ERR_UNSUPPORTED;
     return launch(dev::kv_score_kernel<kGroup>, dim3(static_cast<unsigned>(rows * of_row)), dev::kScoreThreads, 0, stream, s,
                   static_cast<int>(of_row));
 }
@@ -56,6 +57,8 @@ proj_status_t proj_kv_attend_scored(proj_kv_handle_t h, int64_t sequences, const
     if (!workspace || (score_tokens > 0 && (!scores || !scores_out))) return PROJ_ERR_INVALID_ARG;
     if (!aligned16(workspace) || reinterpret_cast<uintptr_t>(scores) % 4 != 0 || reinterpret_cast<uintptr_t>(scores_out) % 4 != 0)
         return PROJ_ERR_MISALIGNED;
+    // (Before anything is launched: the scores' grid has at most a block a row more than this.)
+    if (sequences > (kMaxDim - int64_t(h->sm_count) * kScoreBlocks) / h->d.kv_heads) return PROJ_ERR_UNSUPPORTED;
     p.top = static_cast<float2 *>(workspace);
     p.logits = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + tops_bytes(h, sequences));
     const proj_status_t first = launch_attend<kAttendLogits>(h, p, stream);
